@@ -73,6 +73,8 @@ typedef enum {
 #define NS_STATUS_AT_ITERATE (1 << 10) /* an intermediate X (between steps, or at a restart) */
 #define NS_STATUS_AT_OUTPUT (1 << 11)  /* the result written to the caller's matrix */
 #define NS_STATUS_AT_SPLIT (1 << 12)   /* soft-threshold split: lambda, B or O */
+#define NS_STATUS_BAD_INDEX (1 << 13)  /* a token id or a target outside the table or vocabulary; not an
+                                          error code: the call goes on as its description says */
 #define NS_STATUS_GUARD_RESTART (1 << 16)
 /* With NS_STATUS_GUARD_RESTART: the guard restarted before step k, 2 <= k <= 16. */
 #define NS_STATUS_GUARD_STEP(k) ((int32_t)(1u << (15 + (k))))
@@ -361,6 +363,150 @@ ns_status ns_muon_step(void* W, const void* G, float* M, int64_t batch,
                        const float* a, const float* b, const float* c,
                        ns_mode mode, const ns_options* opt, void* workspace,
                        size_t workspace_bytes, ns_stream_t stream);
+
+/*
+ * The two ends of a training step
+ * -------------------------------
+ * Muon updates a model's hidden matrices; the embedding table, the output
+ * projection and the norm vectors are left to another optimizer (Muon /
+ * NanoGPT article, "From SGD to Muon").  The calls below compute those
+ * parameters' gradients: embedding, layer norm, and the output projection
+ * with its softmax cross entropy, each forward and backward.
+ *
+ * Common to them: device pointers, row-major matrices with the stated row
+ * stride in elements (>= the row's length); data in NS_BF16, NS_FP16 or
+ * NS_FP32, statistics and sums in fp32, each result rounded once; any
+ * alignment of at least one element (rows on 16-byte boundaries are faster);
+ * no floating-point atomics, so equal calls give equal bits; rows == 0 is
+ * allowed.  d_status is the optional status word: non-finite results OR in
+ * NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT, ids outside their range
+ * NS_STATUS_BAD_INDEX.  Outputs must not overlap inputs except where
+ * stated.
+ *
+ * Layer norm over the rows of X:
+ *     mean_i = sum_j X_ij / cols,  rstd_i = 1 / sqrt(sum_j (X_ij - mean_i)^2 / cols + eps)
+ *     Y_ij = (X_ij - mean_i) rstd_i weight_j + bias_j
+ *   rows < 2^31, 1 <= cols <= 2^24; eps >= 0 and finite.
+ *   weight, bias   cols elements of param_dtype (dtype or NS_FP32), either
+ *                  may be NULL (ones, zeros).
+ *   mean, rstd     rows floats each, for the backward pass; either may be
+ *                  NULL.
+ *   Y may be X (with ldy == ldx).
+ */
+ns_status ns_layer_norm(const void* X, int64_t rows, int64_t cols, int64_t ldx,
+                        ns_dtype dtype, const void* weight, const void* bias,
+                        ns_dtype param_dtype, float eps, void* Y, int64_t ldy,
+                        float* mean, float* rstd, int32_t* d_status,
+                        ns_stream_t stream);
+
+/*
+ * Its gradients, with xhat = (X - mean) rstd and a = weight dY:
+ *     dX = rstd (a - mean_j(a) - xhat mean_j(a xhat))
+ *     dweight_j = sum_i dY_ij xhat_ij,   dbias_j = sum_i dY_ij
+ *   mean, rstd   as written by ns_layer_norm.
+ *   dweight, dbias   cols elements of param_dtype, either may be NULL.  With
+ *                no rows they are zeros.
+ *   dX may be dY (with lddx == lddy).
+ *   workspace    ns_layer_norm_workspace_size(rows, cols) bytes, 256-byte
+ *                aligned; not used (and may be NULL) when dweight and dbias
+ *                are both NULL.
+ */
+size_t ns_layer_norm_workspace_size(int64_t rows, int64_t cols);
+
+ns_status ns_layer_norm_backward(const void* dY, int64_t lddy, const void* X,
+                                 int64_t ldx, int64_t rows, int64_t cols,
+                                 ns_dtype dtype, const float* mean,
+                                 const float* rstd, const void* weight,
+                                 ns_dtype param_dtype, void* dX, int64_t lddx,
+                                 void* dweight, void* dbias, int32_t* d_status,
+                                 void* workspace, size_t workspace_bytes,
+                                 ns_stream_t stream);
+
+/*
+ * Embedding lookup: out_i = scale * table[ids_i].
+ *   ids      n ids, int64 (ids64 == 1) or int32 (ids64 == 0).  An id
+ *            outside [0, vocab) reads nothing: its row of out is zero and
+ *            NS_STATUS_BAD_INDEX is set.
+ *   table    vocab x cols, row stride ldt; out n x cols, row stride ldo.
+ *   n < 2^31, 1 <= vocab <= 2^28, 1 <= cols <= 2^24; scale finite.
+ */
+ns_status ns_embedding(const void* ids, int32_t ids64, int64_t n,
+                       const void* table, int64_t vocab, int64_t cols,
+                       int64_t ldt, ns_dtype dtype, float scale, void* out,
+                       int64_t ldo, int32_t* d_status, ns_stream_t stream);
+
+/*
+ * Its gradient: dT[v] = scale * sum of dY's rows i with ids_i == v, added up
+ * in the order of i.
+ *   accumulate == 0: every row of dT is written, rows without an id as
+ *            zeros.  accumulate == 1: dT <- dT + that (tied embeddings: dT
+ *            holds the output projection's gradient); rows without an id
+ *            are not touched.
+ *   Ids outside [0, vocab) contribute nothing and set NS_STATUS_BAD_INDEX.
+ *   workspace   ns_embedding_workspace_size(n, vocab, cols) bytes, 256-byte
+ *            aligned.
+ */
+size_t ns_embedding_workspace_size(int64_t n, int64_t vocab, int64_t cols);
+
+ns_status ns_embedding_backward(const void* ids, int32_t ids64, int64_t n,
+                                const void* dY, int64_t lddy, int64_t vocab,
+                                int64_t cols, ns_dtype dtype, float scale,
+                                void* dT, int64_t ldt, int32_t accumulate,
+                                int32_t* d_status, void* workspace,
+                                size_t workspace_bytes, ns_stream_t stream);
+
+/*
+ * Softmax cross entropy of an output projection, the logits z = H W^T
+ * (rows x vocab) never stored:
+ *     lse_i = log sum_j exp z_ij,   loss_i = lse_i - z_{i, targets_i}
+ *   H        rows x cols hidden states, row stride ldh; W vocab x cols
+ *            weights, row stride ldw.
+ *   targets  rows ids, int64 (targets64 == 1) or int32.  A row whose target
+ *            is ignore_index has loss 0 (its lse is still computed); any
+ *            other target outside [0, vocab) gives loss NaN and sets
+ *            NS_STATUS_BAD_INDEX.
+ *   loss, lse   rows floats each.  A row of logits that holds a NaN or
+ *            +Inf gives NaN; -Inf logits count as probability 0.
+ *   rows, vocab <= 2^23, cols <= 2^20, ldh and ldw <= 2^23.
+ *   workspace   ns_linear_cross_entropy_workspace_size(rows, cols, vocab,
+ *            dtype, aligned, 0) bytes, 256-byte aligned; aligned is 1 when H
+ *            and W start on 16-byte boundaries and their row strides are
+ *            multiples of 128 bytes, else 0 (the operands are then copied,
+ *            as they are when cols is not a multiple of 64, or 32 in fp32).
+ */
+size_t ns_linear_cross_entropy_workspace_size(int64_t rows, int64_t cols,
+                                              int64_t vocab, ns_dtype dtype,
+                                              int32_t aligned, int32_t backward);
+
+ns_status ns_linear_cross_entropy(const void* H, int64_t ldh, const void* W,
+                                  int64_t ldw, const void* targets,
+                                  int32_t targets64, int64_t rows, int64_t cols,
+                                  int64_t vocab, ns_dtype dtype,
+                                  int64_t ignore_index, float* loss, float* lse,
+                                  int32_t* d_status, void* workspace,
+                                  size_t workspace_bytes, ns_stream_t stream);
+
+/*
+ * Its gradients.  With dz_ij = dloss_i (exp(z_ij - lse_i) - [j == targets_i]):
+ *     dH = dz W,   dW = dz^T H
+ * The logits are made again, one piece of the vocabulary at a time.
+ *   lse      as written by ns_linear_cross_entropy.
+ *   dloss    rows floats: the gradients of the losses.
+ *   dH       rows x cols, row stride lddh; dW vocab x cols, row stride lddw;
+ *            dtype.  Either may be NULL.
+ * Rows whose target is ignored or out of range, and rows with dloss 0,
+ * contribute exact zeros.  dz is rounded to dtype (fp16: scaled by
+ * 2^15 / max|dloss| first, so dloss may span about 2^24 between rows); both
+ * products accumulate in fp32.
+ *   workspace   ns_linear_cross_entropy_workspace_size(..., aligned, 1)
+ *            bytes.
+ */
+ns_status ns_linear_cross_entropy_backward(
+    const void* H, int64_t ldh, const void* W, int64_t ldw, const void* targets,
+    int32_t targets64, int64_t rows, int64_t cols, int64_t vocab,
+    ns_dtype dtype, int64_t ignore_index, const float* lse, const float* dloss,
+    void* dH, int64_t lddh, void* dW, int64_t lddw, int32_t* d_status,
+    void* workspace, size_t workspace_bytes, ns_stream_t stream);
 
 /*
  * The kernel builds one call would launch, for inspection (host only;

@@ -5,7 +5,9 @@ Newton-Schulz (Muon's approximate polar factor), a batched launcher for
 equal-shape expert matrices, the ROOT soft-threshold split, ROOT's per-shape
 coefficient schedules (fitted on the host, run through the per-step
 coefficient arrays) and a whole Muon step (momentum, orthogonalization,
-weight update).  The HIP
+weight update).  Beside it stand the operators that give the parameters Muon
+leaves out their gradients: embedding, layer norm and the output projection's
+softmax cross entropy, forward and backward.  The HIP
 library does all the work; this package only marshals arguments.
 """
 
@@ -17,6 +19,11 @@ from ._binding import (NS_MAX_STEPS, TUNED_ABC, NSError, lib, muon_step,
                        plan_kernels,
                        soft_threshold_split, status_code, status_string,
                        workspace_size)
+from ._training import (embedding, embedding_backward,
+                        embedding_workspace_size, layer_norm,
+                        layer_norm_backward, layer_norm_workspace_size,
+                        linear_cross_entropy, linear_cross_entropy_backward,
+                        linear_cross_entropy_workspace_size)
 from .coeffs import fit_coefficients, root_coefficients
 
 __all__ = [
@@ -25,6 +32,10 @@ __all__ = [
     "orthogonalize_batched", "orthogonalize_grouped", "orthogonalize_static",
     "grouped_workspace_size", "plan_kernels", "soft_threshold_split",
     "status_code", "status_string",
-    "workspace_size", "gram_flops", "ns_flops", "standard_flops",
+    "workspace_size", "embedding", "embedding_backward",
+    "embedding_workspace_size", "layer_norm", "layer_norm_backward",
+    "layer_norm_workspace_size", "linear_cross_entropy",
+    "linear_cross_entropy_backward", "linear_cross_entropy_workspace_size",
+    "gram_flops", "ns_flops", "standard_flops",
     "fit_coefficients", "root_coefficients",
 ]

@@ -28,6 +28,7 @@ STATUS_AT_STATE = 1 << 9
 STATUS_AT_ITERATE = 1 << 10
 STATUS_AT_OUTPUT = 1 << 11
 STATUS_AT_SPLIT = 1 << 12
+STATUS_BAD_INDEX = 1 << 13
 STATUS_GUARD_RESTART = 1 << 16
 NS_BF16, NS_FP16, NS_FP32 = 0, 1, 2
 NS_STANDARD, NS_GRAM = 0, 1
@@ -167,6 +168,66 @@ _SIGNATURES = {
                                  ctypes.POINTER(ctypes.c_float),
                                  ctypes.c_int, ctypes.POINTER(Options),
                                  ctypes.c_void_p]),
+    "ns_layer_norm": (ctypes.c_int,
+                      [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                       ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+                       ctypes.c_void_p, ctypes.c_int, ctypes.c_float,
+                       ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "ns_layer_norm_workspace_size": (ctypes.c_size_t,
+                                     [ctypes.c_int64, ctypes.c_int64]),
+    "ns_layer_norm_backward": (ctypes.c_int,
+                               [ctypes.c_void_p, ctypes.c_int64,
+                                ctypes.c_void_p, ctypes.c_int64,
+                                ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                                ctypes.c_void_p, ctypes.c_void_p,
+                                ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                ctypes.c_int64, ctypes.c_void_p,
+                                ctypes.c_void_p, ctypes.c_void_p,
+                                ctypes.c_void_p, ctypes.c_size_t,
+                                ctypes.c_void_p]),
+    "ns_embedding": (ctypes.c_int,
+                     [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
+                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                      ctypes.c_int64, ctypes.c_int, ctypes.c_float,
+                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                      ctypes.c_void_p]),
+    "ns_embedding_workspace_size": (ctypes.c_size_t,
+                                    [ctypes.c_int64, ctypes.c_int64,
+                                     ctypes.c_int64]),
+    "ns_embedding_backward": (ctypes.c_int,
+                              [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
+                               ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                               ctypes.c_int64, ctypes.c_int, ctypes.c_float,
+                               ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                               ctypes.c_void_p, ctypes.c_void_p,
+                               ctypes.c_size_t, ctypes.c_void_p]),
+    "ns_linear_cross_entropy_workspace_size": (ctypes.c_size_t,
+                                               [ctypes.c_int64, ctypes.c_int64,
+                                                ctypes.c_int64, ctypes.c_int,
+                                                ctypes.c_int32,
+                                                ctypes.c_int32]),
+    "ns_linear_cross_entropy": (ctypes.c_int,
+                                [ctypes.c_void_p, ctypes.c_int64,
+                                 ctypes.c_void_p, ctypes.c_int64,
+                                 ctypes.c_void_p, ctypes.c_int32,
+                                 ctypes.c_int64, ctypes.c_int64,
+                                 ctypes.c_int64, ctypes.c_int, ctypes.c_int64,
+                                 ctypes.c_void_p, ctypes.c_void_p,
+                                 ctypes.c_void_p, ctypes.c_void_p,
+                                 ctypes.c_size_t, ctypes.c_void_p]),
+    "ns_linear_cross_entropy_backward": (ctypes.c_int,
+                                         [ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p, ctypes.c_int32,
+                                          ctypes.c_int64, ctypes.c_int64,
+                                          ctypes.c_int64, ctypes.c_int,
+                                          ctypes.c_int64, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_int64, ctypes.c_void_p,
+                                          ctypes.c_int64, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_size_t,
+                                          ctypes.c_void_p]),
     "ns_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ns_version": (ctypes.c_int32, []),
 }

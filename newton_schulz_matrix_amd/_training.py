@@ -1,0 +1,390 @@
+"""The two ends of a training step: embedding, layer norm, cross entropy.
+
+Argument marshalling for the calls that include/nsortho.h describes under
+"The two ends of a training step".  Like the other calls they run on the
+current stream of their tensors' device, write new tensors (or the ``out``
+given), never synchronize, and raise ValueError or TypeError for arguments
+that the library could not use.  ``workspace`` is an optional device buffer of
+the size that the matching ``*_workspace_size`` names; without it one is
+allocated by torch.  ``status`` is the device int32 status word.
+"""
+
+from __future__ import annotations
+
+from typing import Optional, Tuple, Union
+
+import torch
+
+from . import _binding as B
+from ._binding import NSError, _check, dtype_code, lib
+
+
+class _On:
+    """Makes a tensor's device the current one for the launches of a call."""
+
+    def __init__(self, device: torch.device):
+        self.guard = (torch.cuda.device(device)
+                      if device.index != torch.cuda.current_device() else None)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _device(x: torch.Tensor) -> torch.device:
+    if not x.is_cuda:
+        raise ValueError("expects a device tensor")
+    return x.device
+
+
+def _same_device(device: torch.device, **tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def _rows(x: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    """(rows, cols, row stride) of a tensor seen as a matrix of its last axis.
+
+    A 2-D tensor may have any row stride; one of another rank is contiguous.
+    """
+    if x.dim() == 0:
+        raise ValueError(f"{name} must have at least one axis")
+    cols = x.shape[-1]
+    if cols < 1:
+        raise ValueError(f"{name}'s last axis must not be empty")
+    if x.dim() == 2:
+        rows, ld = x.shape[0], x.stride(0)
+        if x.stride(1) != 1 and cols > 1:
+            raise ValueError(f"{name}'s rows must be contiguous (stride(-1) == 1)")
+        if rows > 1 and ld < cols:
+            raise ValueError(f"{name}'s rows must not overlap")
+        return rows, cols, ld if rows > 1 else cols
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (or 2-D)")
+    return x.numel() // cols, cols, cols
+
+
+def _output(out: Optional[torch.Tensor], shape, dtype: torch.dtype,
+            device: torch.device, name: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, {dtype} and device {device}")
+    return out
+
+
+def _status_ptr(status: Optional[torch.Tensor], device: torch.device) -> Optional[int]:
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or not status.is_cuda:
+        raise TypeError("status must be a device int32 tensor")
+    if status.device != device or status.numel() < 1:
+        raise ValueError(f"status must hold a word on {device}")
+    return status.data_ptr()
+
+
+def _workspace_args(need: int, device: torch.device,
+                    workspace: Optional[torch.Tensor], query: str):
+    if need == 0:
+        raise NSError(1, query)
+    return B._workspace(need, device, workspace)
+
+
+def _ids(ids: torch.Tensor, device: torch.device, name: str) -> int:
+    """1 for int64 ids, 0 for int32."""
+    if ids.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"{name} must be int64 or int32")
+    if ids.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if not ids.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return 1 if ids.dtype == torch.int64 else 0
+
+
+def _param(p: Optional[torch.Tensor], x: torch.Tensor, cols: int, name: str) -> None:
+    if p is None:
+        return
+    if p.dtype != x.dtype and p.dtype != torch.float32:
+        raise TypeError(f"{name} must have x's dtype or float32")
+    if p.device != x.device or p.numel() != cols or not p.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {cols} elements on {x.device}")
+
+
+def _per_row(t: torch.Tensor, rows: int, device: torch.device, name: str) -> None:
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32")
+    if t.device != device or t.numel() != rows or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {rows} elements on {device}")
+
+
+# ---------------------------------------------------------------------------
+# Layer norm.
+# ---------------------------------------------------------------------------
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+               stats: bool = True, out: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None):
+    """Layer norm over the last axis: returns (y, mean, rstd).
+
+    ``x``: a 2-D tensor with contiguous rows, or a contiguous one of any
+    rank.  ``weight`` and ``bias``: x's dtype or float32, both the same.
+    ``mean`` and ``rstd`` (fp32, one per row, x's leading axes) are what the
+    backward pass takes; with ``stats=False`` they are None.  ``out`` may be
+    ``x``.
+    """
+    device = _device(x)
+    rows, cols, ldx = _rows(x, "x")
+    code = dtype_code(x.dtype)
+    _param(weight, x, cols, "weight")
+    _param(bias, x, cols, "bias")
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same dtype")
+    param = weight if weight is not None else bias
+    pcode = code if param is None else dtype_code(param.dtype)
+    y = _output(out, x.shape, x.dtype, device, "out")
+    ldy = _rows(y, "out")[2]
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+        rstd = torch.empty_like(mean)
+    with _On(device):
+        _check(lib().ns_layer_norm(
+            x.data_ptr(), rows, cols, ldx, code,
+            None if weight is None else weight.data_ptr(),
+            None if bias is None else bias.data_ptr(), pcode, eps,
+            y.data_ptr(), ldy, None if mean is None else mean.data_ptr(),
+            None if rstd is None else rstd.data_ptr(),
+            _status_ptr(status, device), _stream(device)), "ns_layer_norm")
+    return y, mean, rstd
+
+
+def layer_norm_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().ns_layer_norm_workspace_size(rows, cols))
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
+                        rstd: torch.Tensor,
+                        weight: Optional[torch.Tensor] = None,
+                        params: bool = True,
+                        out: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None):
+    """Gradients of layer_norm: returns (dx, dweight, dbias).
+
+    ``mean`` and ``rstd`` as returned by layer_norm.  dweight and dbias have
+    weight's dtype (x's without a weight); with ``params=False`` they are
+    None.  ``out`` receives dx and may be ``dy``.
+    """
+    device = _device(x)
+    rows, cols, ldx = _rows(x, "x")
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must have x's shape and dtype")
+    _same_device(device, dy=dy)
+    lddy = _rows(dy, "dy")[2]
+    code = dtype_code(x.dtype)
+    _per_row(mean, rows, device, "mean")
+    _per_row(rstd, rows, device, "rstd")
+    _param(weight, x, cols, "weight")
+    pdtype = x.dtype if weight is None else weight.dtype
+    dx = _output(out, x.shape, x.dtype, device, "out")
+    lddx = _rows(dx, "out")[2]
+    dweight = dbias = keep = None
+    wptr, wbytes = None, 0
+    if params:
+        dweight = torch.empty(cols, dtype=pdtype, device=device)
+        dbias = torch.empty_like(dweight)
+        wptr, wbytes, keep = _workspace_args(
+            int(lib().ns_layer_norm_workspace_size(rows, cols)), device,
+            workspace, "ns_layer_norm_workspace_size")
+    with _On(device):
+        _check(lib().ns_layer_norm_backward(
+            dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols, code,
+            mean.data_ptr(), rstd.data_ptr(),
+            None if weight is None else weight.data_ptr(), dtype_code(pdtype),
+            dx.data_ptr(), lddx, None if dweight is None else dweight.data_ptr(),
+            None if dbias is None else dbias.data_ptr(),
+            _status_ptr(status, device), wptr, wbytes, _stream(device)),
+            "ns_layer_norm_backward")
+    return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+# Embedding.
+# ---------------------------------------------------------------------------
+
+def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
+              out: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """scale * table[ids], of shape ids.shape + (cols,).
+
+    ``ids``: contiguous int64 or int32, any shape; ``table``: [vocab, cols]
+    with contiguous rows.  An id outside the table gives a row of zeros and
+    sets STATUS_BAD_INDEX in ``status``.
+    """
+    device = _device(table)
+    if table.dim() != 2:
+        raise ValueError("table must be 2-D")
+    vocab, cols, ldt = _rows(table, "table")
+    ids64 = _ids(ids, device, "ids")
+    code = dtype_code(table.dtype)
+    y = _output(out, tuple(ids.shape) + (cols,), table.dtype, device, "out")
+    ldo = _rows(y, "out")[2]
+    with _On(device):
+        _check(lib().ns_embedding(
+            ids.data_ptr(), ids64, ids.numel(), table.data_ptr(), vocab, cols,
+            ldt, code, scale, y.data_ptr(), ldo, _status_ptr(status, device),
+            _stream(device)), "ns_embedding")
+    return y
+
+
+def embedding_workspace_size(n: int, vocab: int, cols: int) -> int:
+    return int(lib().ns_embedding_workspace_size(n, vocab, cols))
+
+
+def embedding_backward(ids: torch.Tensor, dy: torch.Tensor, vocab: int,
+                       scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                       accumulate: bool = False,
+                       status: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The table's gradient, [vocab, cols]: rows of ``dy`` summed by id.
+
+    ``dy`` has the shape ids.shape + (cols,).  ``out`` receives the gradient;
+    with ``accumulate`` it is added to what ``out`` holds (tied embeddings),
+    and rows without an id are left alone.
+    """
+    device = _device(dy)
+    ids64 = _ids(ids, device, "ids")
+    n, cols, lddy = _rows(dy, "dy")
+    if tuple(dy.shape[:-1]) != tuple(ids.shape):
+        raise ValueError("dy must have the shape of ids and one more axis")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    code = dtype_code(dy.dtype)
+    dt = _output(out, (vocab, cols), dy.dtype, device, "out")
+    ldt = _rows(dt, "out")[2]
+    wptr, wbytes, keep = _workspace_args(
+        int(lib().ns_embedding_workspace_size(n, vocab, cols)), device,
+        workspace, "ns_embedding_workspace_size")
+    with _On(device):
+        _check(lib().ns_embedding_backward(
+            ids.data_ptr(), ids64, n, dy.data_ptr(), lddy, vocab, cols, code,
+            scale, dt.data_ptr(), ldt, 1 if accumulate else 0,
+            _status_ptr(status, device), wptr, wbytes, _stream(device)),
+            "ns_embedding_backward")
+    return dt
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy of the output projection.
+# ---------------------------------------------------------------------------
+
+def _projection(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor):
+    device = _device(h)
+    if h.dim() != 2 or w.dim() != 2:
+        raise ValueError("h and w must be 2-D")
+    rows, cols, ldh = _rows(h, "h")
+    vocab, wcols, ldw = _rows(w, "w")
+    if wcols != cols or w.dtype != h.dtype:
+        raise ValueError("w must have h's dtype and number of columns")
+    if vocab < 1:
+        raise ValueError("w must have at least one row")
+    _same_device(device, w=w)
+    t64 = _ids(targets, device, "targets")
+    if targets.numel() != rows:
+        raise ValueError("targets must have one entry per row of h")
+    size = h.element_size()
+    aligned = (h.data_ptr() % 16 == 0 and w.data_ptr() % 16 == 0
+               and ldh * size % 128 == 0 and ldw * size % 128 == 0)
+    return device, rows, cols, ldh, vocab, ldw, t64, 1 if aligned else 0
+
+
+def linear_cross_entropy_workspace_size(rows: int, cols: int, vocab: int,
+                                        dtype: torch.dtype = torch.bfloat16,
+                                        aligned: bool = True,
+                                        backward: bool = False) -> int:
+    """``aligned``: h and w start on 16-byte boundaries and their row strides
+    are multiples of 128 bytes (contiguous rows of 64 16-bit or 32 fp32
+    elements are)."""
+    return int(lib().ns_linear_cross_entropy_workspace_size(
+        rows, cols, vocab, dtype_code(dtype), 1 if aligned else 0,
+        1 if backward else 0))
+
+
+def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                         ignore_index: int = -100,
+                         status: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None
+                         ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Softmax cross entropy of the logits h w^T: returns (loss, lse), fp32.
+
+    ``h``: [rows, cols] hidden states, ``w``: [vocab, cols] weights, of one
+    dtype; ``targets``: rows ids (int64 or int32).  The logits are never
+    stored.  A row whose target is ``ignore_index`` has loss 0; another
+    target outside the vocabulary gives NaN and sets STATUS_BAD_INDEX.
+    """
+    device, rows, cols, ldh, vocab, ldw, t64, aligned = _projection(h, w, targets)
+    code = dtype_code(h.dtype)
+    loss = torch.empty(rows, dtype=torch.float32, device=device)
+    lse = torch.empty_like(loss)
+    wptr, wbytes, keep = _workspace_args(
+        int(lib().ns_linear_cross_entropy_workspace_size(
+            rows, cols, vocab, code, aligned, 0)), device, workspace,
+        "ns_linear_cross_entropy_workspace_size")
+    with _On(device):
+        _check(lib().ns_linear_cross_entropy(
+            h.data_ptr(), ldh, w.data_ptr(), ldw, targets.data_ptr(), t64, rows,
+            cols, vocab, code, ignore_index, loss.data_ptr(), lse.data_ptr(),
+            _status_ptr(status, device), wptr, wbytes, _stream(device)),
+            "ns_linear_cross_entropy")
+    return loss, lse
+
+
+def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor,
+                                  targets: torch.Tensor, lse: torch.Tensor,
+                                  dloss: Union[torch.Tensor, float],
+                                  ignore_index: int = -100, need_dh: bool = True,
+                                  need_dw: bool = True,
+                                  out_dh: Optional[torch.Tensor] = None,
+                                  out_dw: Optional[torch.Tensor] = None,
+                                  status: Optional[torch.Tensor] = None,
+                                  workspace: Optional[torch.Tensor] = None):
+    """Gradients of linear_cross_entropy: returns (dh, dw).
+
+    ``lse`` as returned by linear_cross_entropy; ``dloss``: the losses'
+    gradients, fp32, one per row, or one number for all of them (1 / valid
+    rows for a mean).  ``need_dh`` / ``need_dw`` False skip a gradient and
+    return None for it.
+    """
+    device, rows, cols, ldh, vocab, ldw, t64, aligned = _projection(h, w, targets)
+    code = dtype_code(h.dtype)
+    _per_row(lse, rows, device, "lse")
+    if not isinstance(dloss, torch.Tensor):
+        dloss = torch.full((rows,), float(dloss), dtype=torch.float32, device=device)
+    _per_row(dloss, rows, device, "dloss")
+    dh = _output(out_dh, (rows, cols), h.dtype, device, "out_dh") if need_dh else None
+    dw = _output(out_dw, (vocab, cols), w.dtype, device, "out_dw") if need_dw else None
+    lddh = _rows(dh, "out_dh")[2] if need_dh else cols
+    lddw = _rows(dw, "out_dw")[2] if need_dw else cols
+    wptr, wbytes, keep = _workspace_args(
+        int(lib().ns_linear_cross_entropy_workspace_size(
+            rows, cols, vocab, code, aligned, 1)), device, workspace,
+        "ns_linear_cross_entropy_workspace_size")
+    with _On(device):
+        _check(lib().ns_linear_cross_entropy_backward(
+            h.data_ptr(), ldh, w.data_ptr(), ldw, targets.data_ptr(), t64, rows,
+            cols, vocab, code, ignore_index, lse.data_ptr(), dloss.data_ptr(),
+            None if dh is None else dh.data_ptr(), lddh,
+            None if dw is None else dw.data_ptr(), lddw,
+            _status_ptr(status, device), wptr, wbytes, _stream(device)),
+            "ns_linear_cross_entropy_backward")
+    return dh, dw

@@ -1,0 +1,602 @@
+// train.hip - C entry points of the operators at the two ends of a training
+// step, beside the Muon step of the hidden matrices: embedding lookup and
+// its gradient, layer norm forward and backward, and the output projection's
+// softmax cross entropy with its gradients.  Argument checks, workspace
+// layout and kernel choice; the kernels are in norm.hpp, embed.hpp and
+// xent.hpp.
+#include <math.h>
+
+#include <algorithm>
+
+#include "../../include/nsortho.h"
+#include "embed.hpp"
+#include "norm.hpp"
+#include "xent.hpp"
+
+namespace {
+
+using namespace nsk;
+using namespace nsr;
+
+constexpr size_t kAlignTo = 256;
+inline size_t align_up_to(size_t x) { return (x + kAlignTo - 1) / kAlignTo * kAlignTo; }
+inline int64_t round_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+inline bool known(ns_dtype d) { return d == NS_BF16 || d == NS_FP16 || d == NS_FP32; }
+inline int bytes_of(ns_dtype d) { return d == NS_FP32 ? 4 : 2; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline ns_status launched() { return hipGetLastError() == hipSuccess ? NS_OK : NS_ERR_HIP; }
+inline ns_status launched(hipError_t e) { return e == hipSuccess ? NS_OK : NS_ERR_HIP; }
+// Grids of the kernels that loop over their rows stay below this many blocks
+// (a launch may not have 2^32 threads).
+constexpr int64_t kMaxBlocks = 1 << 20;
+
+// Buffers carved out of a workspace in order.
+struct Carver {
+  char* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(int64_t count) {
+    char* p = base ? base + used : nullptr;
+    used += align_up_to((size_t)count * sizeof(T));
+    return reinterpret_cast<T*>(p);
+  }
+};
+
+bool workspace_ok(const void* ws, size_t have, size_t need) {
+  return need == 0 || (ws && have >= need && reinterpret_cast<uintptr_t>(ws) % kAlignTo == 0);
+}
+
+// Calls f(IO{}, PT{}) for a data type and a parameter type that is the same
+// or fp32.
+template <class F>
+ns_status with_types(ns_dtype io, ns_dtype pt, F&& f) {
+  if (io == NS_FP32) return f(float{}, float{});
+  if (io == NS_BF16) return pt == NS_FP32 ? f(__bf16{}, float{}) : f(__bf16{}, __bf16{});
+  return pt == NS_FP32 ? f(_Float16{}, float{}) : f(_Float16{}, _Float16{});
+}
+template <class F>
+ns_status with_type(ns_dtype io, F&& f) {
+  if (io == NS_FP32) return f(float{});
+  if (io == NS_BF16) return f(__bf16{});
+  return f(_Float16{});
+}
+
+// ---------------------------------------------------------------------------
+// Layer norm.
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxNormCols = 1 << 24;
+constexpr int kNormRegisterCols = 16384;  // the widest row that the kernels hold in registers
+// Blocks of the backward pass, each of which leaves one partial row of dw
+// and db.
+constexpr int64_t kNormParts = 512;
+
+// Calls f.template run<V, E, TPR>() for a row width: one wave per row up to
+// 1024 columns, four up to 8192 (4096 without vectors), sixteen above.  More
+// elements per thread would not leave registers for the backward's sums.
+template <typename IO, class F>
+void with_norm_form(int64_t cols, bool vec, F&& f) {
+  constexpr int V = 16 / sizeof(IO);
+  if (vec) {
+    if (cols <= 64 * 8) return f.template run<V, 8, 64>();
+    if (cols <= 64 * 16) return f.template run<V, 16, 64>();
+    if (cols <= 256 * 8) return f.template run<V, 8, 256>();
+    if (cols <= 256 * 16) return f.template run<V, 16, 256>();
+    if (cols <= 256 * 32) return f.template run<V, 32, 256>();
+    return f.template run<V, 16, 1024>();
+  }
+  if (cols <= 64 * 4) return f.template run<1, 4, 64>();
+  if (cols <= 64 * 16) return f.template run<1, 16, 64>();
+  if (cols <= 256 * 16) return f.template run<1, 16, 256>();
+  return f.template run<1, 16, 1024>();
+}
+
+template <typename IO, typename PT>
+struct NormFwdRun {
+  const NormFwdArgs& a;
+  hipStream_t st;
+  template <int V, int E, int TPR>
+  void run() const {
+    const int64_t blocks = std::min((a.rows + kNormRows<TPR> - 1) / kNormRows<TPR>, kMaxBlocks);
+    hipLaunchKernelGGL((k_norm_fwd<IO, PT, V, E, TPR>), dim3((unsigned)blocks), dim3(kNormThreads<TPR>), 0, st, a);
+  }
+};
+
+template <typename IO, typename PT>
+struct NormBwdRun {
+  const NormBwdArgs& a;
+  int64_t parts;
+  hipStream_t st;
+  template <int V, int E, int TPR>
+  void run() const {
+    hipLaunchKernelGGL((k_norm_bwd<IO, PT, V, E, TPR>), dim3((unsigned)parts), dim3(kNormThreads<TPR>), 0, st, a);
+  }
+};
+
+// Partial rows of dw and db.  The register kernels' blocks take whole groups
+// of rows (four rows of one wave each, or one).
+int64_t norm_parts(int64_t rows, int64_t cols) {
+  const int64_t groups = cols <= 1024 ? (rows + 3) / 4 : rows;
+  return std::min(groups, kNormParts);
+}
+
+bool norm_shape_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && rows < (int64_t(1) << 31) && cols >= 1 && cols <= kMaxNormCols;
+}
+
+// ---------------------------------------------------------------------------
+// Embedding.
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxEmbedRows = int64_t(1) << 28;
+constexpr int64_t kMaxEmbedCols = 1 << 24;
+constexpr int64_t kMaxEmbedIds = (int64_t(1) << 31) - 1;
+
+bool embed_shape_ok(int64_t n, int64_t vocab, int64_t cols) {
+  return n >= 0 && n <= kMaxEmbedIds && vocab >= 1 && vocab <= kMaxEmbedRows && cols >= 1 && cols <= kMaxEmbedCols;
+}
+
+// Ids per sorting block: about 512 blocks (two per compute unit), each of
+// which reads all ids, and at most the counters that fit.
+int embed_ids_per_block(int64_t vocab) {
+  int r = 64;
+  while (r < kSortMaxIds && (int64_t)r * 512 < vocab) r *= 2;
+  return r;
+}
+
+// Positions per partial sum.  A list of c positions leaves a wave about
+// 2 chunk + c / chunk rows to add up, least at chunk = sqrt(c / 2); the
+// longest list of a text is some twentieth of its positions.
+int embed_chunk(int64_t n) {
+  if (n <= 256) return 0;
+  int c = 32;
+  while ((int64_t)c * c * 40 < n) c *= 2;
+  return c;
+}
+
+struct EmbedPlan {
+  int32_t *order, *start;
+  float* partial;
+  int chunk;
+  size_t total;
+};
+
+EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t cols, void* ws) {
+  EmbedPlan p;
+  Carver c{reinterpret_cast<char*>(ws)};
+  p.chunk = embed_chunk(n);
+  p.order = c.take<int32_t>(n);
+  p.start = c.take<int32_t>(vocab + 1);
+  p.partial = c.take<float>(p.chunk ? n / p.chunk * cols : 0);
+  p.total = c.used;
+  return p;
+}
+
+template <typename IO, int V, int U>
+void embed_sum(const EmbedSumArgs& a, hipStream_t st) {
+  const unsigned slices = (unsigned)((a.cols + 64 * V * U - 1) / (64 * V * U));
+  if (a.chunk && a.n / a.chunk > 0)
+    hipLaunchKernelGGL((k_embed_chunks<IO, V, U>), dim3((unsigned)(a.n / a.chunk), slices), dim3(64), 0, st, a);
+  const int64_t per = 4 * kEmbedRowsPerWave;
+  hipLaunchKernelGGL((k_embed_rows<IO, V, U>), dim3((unsigned)((a.vocab + per - 1) / per), slices), dim3(256), 0, st, a);
+}
+
+// ---------------------------------------------------------------------------
+// Cross entropy.
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxXentRows = 1 << 23, kMaxXentVocab = 1 << 23, kMaxXentCols = 1 << 20;
+// Elements of one piece of dz (bf16 and fp16: 256 MiB in each orientation).
+constexpr int64_t kXentPieceElems = int64_t(1) << 27;
+
+struct XentPlan {
+  int64_t n = 0, d = 0, v = 0;
+  int es = 2, bk = 64;
+  bool few = false;
+  int64_t k = 0;                    // d in whole k-tiles
+  bool stage = false;               // H and W need staging copies
+  int64_t n_pad = 0, tiles_m = 0;   // rows of the first product
+  int64_t tm = 0, tn = 0;
+  int64_t tiles_n = 0;              // forward: vocabulary tiles
+  int64_t d_pad = 0, piece = 0;     // backward
+  int splits = 1;
+  // Buffers.
+  int32_t* tgt = nullptr;
+  char *Hs = nullptr, *Ws = nullptr;
+  float2* parts = nullptr;
+  float *zt = nullptr, *coef = nullptr, *lse = nullptr, *gmax = nullptr, *acc = nullptr;
+  char *dz = nullptr, *dzt = nullptr, *WT = nullptr, *HT = nullptr;
+  size_t total = 0;
+};
+
+bool xent_shape_ok(int64_t n, int64_t d, int64_t v) {
+  return n >= 0 && n <= kMaxXentRows && d >= 1 && d <= kMaxXentCols && v >= 1 && v <= kMaxXentVocab;
+}
+
+XentPlan xent_plan(int64_t n, int64_t d, int64_t v, ns_dtype dtype, bool aligned, bool backward, void* ws) {
+  XentPlan p;
+  p.n = n;
+  p.d = d;
+  p.v = v;
+  p.es = bytes_of(dtype);
+  p.bk = kRowBytes / p.es;
+  p.k = round_to(d, p.bk);
+  p.stage = p.k != d || !aligned;
+  const int64_t edge = p.es == 2 ? kXentEdge<_Float16> : kXentEdge<float>;
+  p.few = !backward && n <= kXentFewRows;
+  p.tm = !p.few ? edge : p.es == 2 ? kXentFewM<_Float16> : kXentFewM<float>;
+  p.tn = !p.few ? edge : p.es == 2 ? kXentFewN<_Float16> : kXentFewN<float>;
+  p.n_pad = round_to(n, p.tm);
+  p.tiles_m = p.n_pad / p.tm;
+  Carver c{reinterpret_cast<char*>(ws)};
+  p.tgt = c.take<int32_t>(p.n_pad);
+  if (p.stage) p.Hs = c.take<char>(n * p.k * p.es);
+  if (!backward) {
+    p.tiles_n = (v + p.tn - 1) / p.tn;
+    if (p.stage) p.Ws = c.take<char>(v * p.k * p.es);
+    p.zt = c.take<float>(p.n_pad);
+    p.parts = c.take<float2>(2 * p.tiles_n * p.n_pad);
+  } else {
+    p.d_pad = round_to(d, edge);
+    const int64_t v_pad = round_to(v, edge);
+    p.piece = std::max<int64_t>(edge, std::min(v_pad, kXentPieceElems / std::max<int64_t>(p.n_pad, 1) / edge * edge));
+    const int64_t pieces = (v_pad + p.piece - 1) / p.piece;
+    p.piece = round_to((v_pad + pieces - 1) / pieces, edge);
+    // Few tiles of dH leave compute units idle: the contraction is split.
+    const int64_t tiles = p.tiles_m * (p.d_pad / edge);
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(16, 256 / std::max<int64_t>(tiles, 1)));
+    if (p.stage) p.Ws = c.take<char>(p.piece * p.k * p.es);
+    p.coef = c.take<float>(p.n_pad);
+    p.lse = c.take<float>(p.n_pad);
+    p.gmax = c.take<float>(1);
+    p.dz = c.take<char>(p.n_pad * p.piece * p.es);
+    p.dzt = c.take<char>(p.n_pad * p.piece * p.es);
+    p.WT = c.take<char>(p.d_pad * p.piece * p.es);
+    p.HT = c.take<char>(p.d_pad * p.n_pad * p.es);
+    p.acc = c.take<float>((int64_t)p.splits * p.n_pad * p.d_pad);
+  }
+  p.total = c.used;
+  return p;
+}
+
+// The products' copies take 16-byte chunks, swizzled by bits 4 to 6 of the
+// address within a row: rows a multiple of 128 bytes apart.
+bool xent_aligned(const void* H, int64_t ldh, const void* W, int64_t ldw, ns_dtype dtype) {
+  const int64_t b = bytes_of(dtype);
+  return aligned16(H) && aligned16(W) && ldh * b % kRowBytes == 0 && ldw * b % kRowBytes == 0;
+}
+
+template <typename T>
+ns_status xent_forward(const XentPlan& p, const void* H, int64_t ldh, const void* W, int64_t ldw, XentRowArgs rows,
+                       float* loss, float* lse, int32_t* d_status, hipStream_t st) {
+  hipLaunchKernelGGL(k_xent_rows, dim3((unsigned)((p.n_pad + 255) / 256)), dim3(256), 0, st, rows);
+  XentArgs a{};
+  a.H = H;
+  a.W = W;
+  a.ldh = ldh * sizeof(T);
+  a.ldw = ldw * sizeof(T);
+  if (p.stage) {
+    hipLaunchKernelGGL((k_xent_pad<T>), dim3((unsigned)p.n), dim3(256), 0, st, (const T*)H, ldh, p.n, (int)p.d,
+                       (T*)p.Hs, (int)p.k);
+    hipLaunchKernelGGL((k_xent_pad<T>), dim3((unsigned)p.v), dim3(256), 0, st, (const T*)W, ldw, p.v, (int)p.d,
+                       (T*)p.Ws, (int)p.k);
+    a.H = p.Hs;
+    a.W = p.Ws;
+    a.ldh = a.ldw = p.k * (int64_t)sizeof(T);
+  }
+  a.row_bytes = (uint32_t)(p.k * sizeof(T));
+  a.k = (int)p.k;
+  a.n = p.n;
+  a.v = p.v;
+  a.tiles_m = (int)p.tiles_m;
+  a.tiles_n = (int)p.tiles_n;
+  a.tgt = p.tgt;
+  a.n_pad = p.n_pad;
+  a.parts = p.parts;
+  a.zt = p.zt;
+  const hipError_t e = launch_xent_fwd<T>(a, p.few, st);
+  if (e != hipSuccess) return NS_ERR_HIP;
+  const XentJoinArgs j{p.parts, (int)(2 * p.tiles_n), p.n, p.n_pad, p.zt, p.tgt, loss, lse, d_status,
+                       (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT)};
+  hipLaunchKernelGGL(k_xent_join, dim3((unsigned)(p.n_pad / 16)), dim3(1024), 0, st, j);
+  return launched();
+}
+
+template <typename T>
+ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const void* W, int64_t ldw, XentRowArgs rows,
+                        void* dH, int64_t lddh, void* dW, int64_t lddw, int32_t* d_status, hipStream_t st) {
+  constexpr int64_t edge = kXentEdge<T>;
+  hipLaunchKernelGGL(k_xent_clear, dim3(1), dim3(1), 0, st, p.gmax);
+  hipLaunchKernelGGL(k_xent_rows, dim3((unsigned)((p.n_pad + 255) / 256)), dim3(256), 0, st, rows);
+  const T* h = reinterpret_cast<const T*>(H);
+  if (p.stage) {
+    hipLaunchKernelGGL((k_xent_pad<T>), dim3((unsigned)p.n), dim3(256), 0, st, h, ldh, p.n, (int)p.d, (T*)p.Hs,
+                       (int)p.k);
+  }
+  if (dW)
+    hipLaunchKernelGGL((k_xent_transpose<T>), dim3((unsigned)(p.n_pad / 64), (unsigned)(p.d_pad / 64)), dim3(256), 0, st,
+                       h, ldh, p.n, (int)p.d, (T*)p.HT, p.n_pad);
+  if (hipGetLastError() != hipSuccess) return NS_ERR_HIP;
+  for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
+    const int64_t rows_v = std::min(p.piece, p.v - v0), width = round_to(rows_v, edge);
+    const T* w = reinterpret_cast<const T*>(W) + v0 * ldw;
+    XentArgs a{};
+    a.H = h;
+    a.W = w;
+    a.ldh = ldh * sizeof(T);
+    a.ldw = ldw * sizeof(T);
+    if (p.stage) {
+      hipLaunchKernelGGL((k_xent_pad<T>), dim3((unsigned)rows_v), dim3(256), 0, st, w, ldw, rows_v, (int)p.d, (T*)p.Ws,
+                         (int)p.k);
+      a.H = p.Hs;
+      a.W = p.Ws;
+      a.ldh = a.ldw = p.k * (int64_t)sizeof(T);
+    }
+    a.row_bytes = (uint32_t)(p.k * sizeof(T));
+    a.k = (int)p.k;
+    a.n = p.n;
+    a.v = rows_v;
+    a.tiles_m = (int)p.tiles_m;
+    a.tiles_n = (int)(width / edge);
+    a.tgt = p.tgt;
+    a.n_pad = p.n_pad;
+    a.v0 = (int)v0;
+    a.coef = p.coef;
+    a.lse = p.lse;
+    a.gmax = p.gmax;
+    a.dz = p.dz;
+    a.dzt = p.dzt;
+    a.ldz = p.piece;
+    hipError_t e = launch_xent_dz<T>(a, st);
+    if (e != hipSuccess) return NS_ERR_HIP;
+    if (dW) {
+      XentDwArgs b{};
+      b.L = p.dzt;
+      b.R = p.HT;
+      b.ldl = b.ldr = p.n_pad * (int64_t)sizeof(T);
+      b.k = (int)p.n_pad;
+      b.tiles_m = (int)(width / edge);
+      b.tiles_n = (int)(p.d_pad / edge);
+      b.out = reinterpret_cast<T*>(dW) + v0 * lddw;
+      b.ldo = lddw;
+      b.rows = rows_v;
+      b.cols = p.d;
+      b.gmax = p.gmax;
+      if ((e = launch_xent_dw<T>(b, st)) != hipSuccess) return NS_ERR_HIP;
+    }
+    if (dH) {
+      hipLaunchKernelGGL((k_xent_transpose<T>), dim3((unsigned)(width / 64), (unsigned)(p.d_pad / 64)), dim3(256), 0, st,
+                         w, ldw, rows_v, (int)p.d, (T*)p.WT, p.piece);
+      XentDhArgs b{};
+      b.L = p.dz;
+      b.R = p.WT;
+      b.ldl = b.ldr = p.piece * (int64_t)sizeof(T);
+      b.ktiles = (int)(width / (kRowBytes / sizeof(T)));
+      b.splits = p.splits;
+      b.tiles_m = (int)p.tiles_m;
+      b.tiles_n = (int)(p.d_pad / edge);
+      b.acc = p.acc;
+      b.n_pad = p.n_pad;
+      b.d_pad = p.d_pad;
+      b.first = v0 == 0;
+      if ((e = launch_xent_dh<T>(b, st)) != hipSuccess) return NS_ERR_HIP;
+    }
+  }
+  if (dH)
+    hipLaunchKernelGGL((k_xent_dh_out<T>), dim3((unsigned)p.n), dim3(256), 0, st, p.acc, p.splits, p.n_pad, p.d_pad,
+                       reinterpret_cast<T*>(dH), lddh, (int)p.d, p.gmax, d_status,
+                       (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT));
+  return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+ns_status ns_layer_norm(const void* X, int64_t rows, int64_t cols, int64_t ldx, ns_dtype dtype, const void* weight,
+                        const void* bias, ns_dtype param_dtype, float eps, void* Y, int64_t ldy, float* mean,
+                        float* rstd, int32_t* d_status, ns_stream_t stream) {
+  if (!norm_shape_ok(rows, cols) || ldx < cols || ldy < cols) return NS_ERR_INVALID_ARG;
+  if (!(eps >= 0.f && isfinite(eps))) return NS_ERR_INVALID_ARG;
+  if (!known(dtype) || !(param_dtype == dtype || param_dtype == NS_FP32)) return NS_ERR_UNSUPPORTED_DTYPE;
+  if (rows == 0) return NS_OK;
+  if (!X || !Y) return NS_ERR_INVALID_ARG;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const NormFwdArgs a{X,    Y,   weight,    bias, mean, rstd, rows, ldx, ldy, (int)cols,
+                      eps, d_status, (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT)};
+  return with_types(dtype, param_dtype, [&](auto io, auto pt) {
+    using IO = decltype(io);
+    using PT = decltype(pt);
+    constexpr int V = 16 / sizeof(IO);
+    if (cols > kNormRegisterCols) {
+      hipLaunchKernelGGL((k_norm_fwd_long<IO, PT>), dim3((unsigned)std::min(rows, kMaxBlocks)), dim3(1024), 0, st, a);
+    } else {
+      const bool vec = cols % V == 0 && ldx % V == 0 && ldy % V == 0 && aligned16(X) && aligned16(Y) &&
+                       aligned16(weight) && aligned16(bias);
+      with_norm_form<IO>(cols, vec, NormFwdRun<IO, PT>{a, st});
+    }
+    return launched();
+  });
+}
+
+size_t ns_layer_norm_workspace_size(int64_t rows, int64_t cols) {
+  if (!norm_shape_ok(rows, cols)) return 0;
+  return std::max(kAlignTo, align_up_to((size_t)norm_parts(rows, cols) * 2 * cols * sizeof(float)));
+}
+
+ns_status ns_layer_norm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, int64_t rows, int64_t cols,
+                                 ns_dtype dtype, const float* mean, const float* rstd, const void* weight,
+                                 ns_dtype param_dtype, void* dX, int64_t lddx, void* dweight, void* dbias,
+                                 int32_t* d_status, void* workspace, size_t workspace_bytes, ns_stream_t stream) {
+  if (!norm_shape_ok(rows, cols) || ldx < cols || lddy < cols || lddx < cols) return NS_ERR_INVALID_ARG;
+  if (!known(dtype) || !(param_dtype == dtype || param_dtype == NS_FP32)) return NS_ERR_UNSUPPORTED_DTYPE;
+  if (rows > 0 && (!dY || !X || !mean || !rstd || !dX)) return NS_ERR_INVALID_ARG;
+  const bool params = dweight || dbias;
+  if (rows == 0 && !params) return NS_OK;
+  if (params && !workspace_ok(workspace, workspace_bytes, ns_layer_norm_workspace_size(rows, cols)))
+    return NS_ERR_WORKSPACE;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const int64_t parts = norm_parts(rows, cols);
+  const NormBwdArgs a{dY,   X,   weight, dX,   mean,      rstd,     params ? reinterpret_cast<float*>(workspace) : nullptr,
+                      rows, lddy, ldx,    lddx, (int)cols, d_status, (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT)};
+  return with_types(dtype, param_dtype, [&](auto io, auto pt) {
+    using IO = decltype(io);
+    using PT = decltype(pt);
+    constexpr int V = 16 / sizeof(IO);
+    if (rows > 0) {
+      if (cols > kNormRegisterCols) {
+        // The parameters' pass comes first: dX may be dY.
+        if (params)
+          hipLaunchKernelGGL((k_norm_cols<IO>), dim3((unsigned)((cols + 255) / 256), (unsigned)parts), dim3(256), 0, st,
+                             a);
+        hipLaunchKernelGGL((k_norm_bwd_long<IO, PT>), dim3((unsigned)std::min(rows, kMaxBlocks)), dim3(1024), 0, st, a);
+      } else {
+        const bool vec = cols % V == 0 && ldx % V == 0 && lddy % V == 0 && lddx % V == 0 && aligned16(X) &&
+                         aligned16(dY) && aligned16(dX) && aligned16(weight);
+        with_norm_form<IO>(cols, vec, NormBwdRun<IO, PT>{a, parts, st});
+      }
+    }
+    if (params)
+      hipLaunchKernelGGL((k_norm_join<PT>), dim3((unsigned)((2 * cols + 63) / 64)), dim3(1024), 0, st,
+                         reinterpret_cast<const float*>(workspace), (int)(rows > 0 ? parts : 0), (int)cols,
+                         reinterpret_cast<PT*>(dweight), reinterpret_cast<PT*>(dbias));
+    return launched();
+  });
+}
+
+ns_status ns_embedding(const void* ids, int32_t ids64, int64_t n, const void* table, int64_t vocab, int64_t cols,
+                       int64_t ldt, ns_dtype dtype, float scale, void* out, int64_t ldo, int32_t* d_status,
+                       ns_stream_t stream) {
+  if (!embed_shape_ok(n, vocab, cols) || ldt < cols || ldo < cols || !isfinite(scale)) return NS_ERR_INVALID_ARG;
+  if (ids64 != 0 && ids64 != 1) return NS_ERR_INVALID_ARG;
+  if (!known(dtype)) return NS_ERR_UNSUPPORTED_DTYPE;
+  if (n == 0) return NS_OK;
+  if (!ids || !table || !out) return NS_ERR_INVALID_ARG;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const EmbedArgs a{ids, ids64, n,        vocab,          (int)cols, table, out, ldt, ldo,
+                    scale, d_status, (int32_t)NS_STATUS_BAD_INDEX, (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT)};
+  const dim3 grid((unsigned)std::min((n + 3) / 4, kMaxBlocks));
+  return with_type(dtype, [&](auto io) {
+    using IO = decltype(io);
+    constexpr int V = 16 / sizeof(IO);
+    if (cols % V == 0 && ldt % V == 0 && ldo % V == 0 && aligned16(table) && aligned16(out))
+      hipLaunchKernelGGL((k_embed<IO, V>), grid, dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((k_embed<IO, 1>), grid, dim3(256), 0, st, a);
+    return launched();
+  });
+}
+
+size_t ns_embedding_workspace_size(int64_t n, int64_t vocab, int64_t cols) {
+  if (!embed_shape_ok(n, vocab, cols)) return 0;
+  return embed_plan(n, vocab, cols, nullptr).total;
+}
+
+ns_status ns_embedding_backward(const void* ids, int32_t ids64, int64_t n, const void* dY, int64_t lddy, int64_t vocab,
+                                int64_t cols, ns_dtype dtype, float scale, void* dT, int64_t ldt, int32_t accumulate,
+                                int32_t* d_status, void* workspace, size_t workspace_bytes, ns_stream_t stream) {
+  if (!embed_shape_ok(n, vocab, cols) || lddy < cols || ldt < cols || !isfinite(scale)) return NS_ERR_INVALID_ARG;
+  if ((ids64 != 0 && ids64 != 1) || (accumulate != 0 && accumulate != 1)) return NS_ERR_INVALID_ARG;
+  if (!known(dtype)) return NS_ERR_UNSUPPORTED_DTYPE;
+  if (!dT || (n > 0 && (!ids || !dY))) return NS_ERR_INVALID_ARG;
+  const EmbedPlan p = embed_plan(n, vocab, cols, workspace);
+  if (!workspace_ok(workspace, workspace_bytes, p.total)) return NS_ERR_WORKSPACE;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const int per = embed_ids_per_block(vocab);
+  const SortArgs s{ids, ids64, n, vocab, per, p.order, p.start, d_status, (int32_t)NS_STATUS_BAD_INDEX};
+  hipLaunchKernelGGL(k_embed_sort, dim3((unsigned)((vocab + per - 1) / per)), dim3(kSortWaves * 64), 0, st, s);
+  const EmbedSumArgs a{dY,      dT,      n,         vocab,   lddy,  ldt,        (int)cols, ids,
+                       ids64,   p.order, p.start,   p.partial, p.chunk, scale, accumulate, d_status,
+                       (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT)};
+  return with_type(dtype, [&](auto io) {
+    using IO = decltype(io);
+    constexpr int V = 16 / sizeof(IO);
+    if (cols % V == 0 && lddy % V == 0 && ldt % V == 0 && aligned16(dY) && aligned16(dT)) {
+      if (cols <= 64 * V)
+        embed_sum<IO, V, 1>(a, st);
+      else if (cols <= 128 * V)
+        embed_sum<IO, V, 2>(a, st);
+      else
+        embed_sum<IO, V, 4>(a, st);
+    } else {
+      embed_sum<IO, 1, 4>(a, st);
+    }
+    return launched();
+  });
+}
+
+size_t ns_linear_cross_entropy_workspace_size(int64_t rows, int64_t cols, int64_t vocab, ns_dtype dtype,
+                                              int32_t aligned, int32_t backward) {
+  if (!xent_shape_ok(rows, cols, vocab) || !known(dtype)) return 0;
+  return std::max(kAlignTo, xent_plan(rows, cols, vocab, dtype, aligned != 0, backward != 0, nullptr).total);
+}
+
+ns_status ns_linear_cross_entropy(const void* H, int64_t ldh, const void* W, int64_t ldw, const void* targets,
+                                  int32_t targets64, int64_t rows, int64_t cols, int64_t vocab, ns_dtype dtype,
+                                  int64_t ignore_index, float* loss, float* lse, int32_t* d_status, void* workspace,
+                                  size_t workspace_bytes, ns_stream_t stream) {
+  if (!xent_shape_ok(rows, cols, vocab) || ldh < cols || ldw < cols) return NS_ERR_INVALID_ARG;
+  if (ldh > kMaxXentCols * 8 || ldw > kMaxXentCols * 8) return NS_ERR_INVALID_ARG;
+  if (targets64 != 0 && targets64 != 1) return NS_ERR_INVALID_ARG;
+  if (!known(dtype)) return NS_ERR_UNSUPPORTED_DTYPE;
+  if (rows == 0) return NS_OK;
+  if (!H || !W || !targets || !loss || !lse) return NS_ERR_INVALID_ARG;
+  const XentPlan p = xent_plan(rows, cols, vocab, dtype, xent_aligned(H, ldh, W, ldw, dtype), false, workspace);
+  if (!workspace_ok(workspace, workspace_bytes, p.total)) return NS_ERR_WORKSPACE;
+  XentRowArgs r{};
+  r.targets = targets;
+  r.targets64 = targets64;
+  r.ignore_index = ignore_index;
+  r.n = rows;
+  r.n_pad = p.n_pad;
+  r.vocab = vocab;
+  r.tgt = p.tgt;
+  r.d_status = d_status;
+  r.index_bit = (int32_t)NS_STATUS_BAD_INDEX;
+  return with_type(dtype, [&](auto io) {
+    return xent_forward<decltype(io)>(p, H, ldh, W, ldw, r, loss, lse, d_status, reinterpret_cast<hipStream_t>(stream));
+  });
+}
+
+ns_status ns_linear_cross_entropy_backward(const void* H, int64_t ldh, const void* W, int64_t ldw, const void* targets,
+                                           int32_t targets64, int64_t rows, int64_t cols, int64_t vocab, ns_dtype dtype,
+                                           int64_t ignore_index, const float* lse, const float* dloss, void* dH,
+                                           int64_t lddh, void* dW, int64_t lddw, int32_t* d_status, void* workspace,
+                                           size_t workspace_bytes, ns_stream_t stream) {
+  if (!xent_shape_ok(rows, cols, vocab) || ldh < cols || ldw < cols) return NS_ERR_INVALID_ARG;
+  if (ldh > kMaxXentCols * 8 || ldw > kMaxXentCols * 8) return NS_ERR_INVALID_ARG;
+  if ((dH && lddh < cols) || (dW && lddw < cols)) return NS_ERR_INVALID_ARG;
+  if (targets64 != 0 && targets64 != 1) return NS_ERR_INVALID_ARG;
+  if (!known(dtype)) return NS_ERR_UNSUPPORTED_DTYPE;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (rows == 0) {
+    if (!dW) return NS_OK;
+    return with_type(dtype, [&](auto io) {
+      using T = decltype(io);
+      hipLaunchKernelGGL((k_xent_zero<T>), dim3((unsigned)vocab), dim3(256), 0, st, reinterpret_cast<T*>(dW), lddw,
+                         (int)cols);
+      return launched();
+    });
+  }
+  if (!H || !W || !targets || !lse || !dloss) return NS_ERR_INVALID_ARG;
+  const XentPlan p = xent_plan(rows, cols, vocab, dtype, xent_aligned(H, ldh, W, ldw, dtype), true, workspace);
+  if (!workspace_ok(workspace, workspace_bytes, p.total)) return NS_ERR_WORKSPACE;
+  if (!dH && !dW) return NS_OK;
+  XentRowArgs r{};
+  r.targets = targets;
+  r.targets64 = targets64;
+  r.ignore_index = ignore_index;
+  r.n = rows;
+  r.n_pad = p.n_pad;
+  r.vocab = vocab;
+  r.tgt = p.tgt;
+  r.dloss = dloss;
+  r.lse = lse;
+  r.coef = p.coef;
+  r.lse_pad = p.lse;
+  r.gmax = p.gmax;
+  r.d_status = d_status;
+  r.index_bit = (int32_t)NS_STATUS_BAD_INDEX;
+  return with_type(dtype, [&](auto io) {
+    return xent_backward<decltype(io)>(p, H, ldh, W, ldw, r, dH, lddh, dW, lddw, d_status, st);
+  });
+}
+
+}  // extern "C"

@@ -49,6 +49,10 @@ come from the oracle itself):
 * ``muon_step`` / ``momentum_update``: the momentum recurrence against its
   geometric-series closed form for a constant gradient, and the whole step
   against ``W - lr U diag(p^T(s/||s||)) V^T`` on a designed spectrum.
+* ``layer_norm``, ``embedding``, ``linear_cross_entropy`` and their gradients:
+  each gradient against central differences of the forward function along
+  random directions; the forward functions against their defining properties
+  (normalized rows, a one-hot product, log of a sum of exponentials).
 
 No function here is "parity unpinned".
 """
@@ -58,10 +62,16 @@ from .ns import (CLASSIC_ABC, TUNED_ABC, coefficient_schedule, frobenius_stage,
 from .svd import jacobi_svd, polar_eigh, polar_jacobi, orthogonalization_mse
 from .soft_threshold import lower_median_abs, soft_threshold_split
 from .muon import momentum_update, muon_step
+from .training import (embedding, embedding_backward, layer_norm,
+                       layer_norm_backward, linear_cross_entropy,
+                       linear_cross_entropy_backward, linear_cross_entropy_dz)
 
 __all__ = [
     "CLASSIC_ABC", "TUNED_ABC", "coefficient_schedule", "frobenius_stage",
     "gram_iterate", "ns_gram", "ns_standard", "scalar_map", "jacobi_svd", "polar_eigh",
     "polar_jacobi", "orthogonalization_mse", "lower_median_abs",
     "soft_threshold_split", "momentum_update", "muon_step",
+    "embedding", "embedding_backward", "layer_norm", "layer_norm_backward",
+    "linear_cross_entropy", "linear_cross_entropy_backward",
+    "linear_cross_entropy_dz",
 ]
