@@ -19,24 +19,26 @@ from . import _binding as B
 from ._binding import NSError, _check, dtype_code, lib
 
 
-class _On:
-    """Makes a tensor's device the current one for the launches of a call."""
-
-    def __init__(self, device: torch.device):
-        self.guard = (torch.cuda.device(device)
-                      if device.index != torch.cuda.current_device() else None)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device index
+_current_device = torch._C._cuda_getDevice
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _call(name: str, device: torch.device, *args) -> None:
+    """Calls an entry point on the current stream of ``device``, which is made
+    the current device for its launches."""
+    fn = getattr(lib(), name)
+    index = device.index
+    if index == _current_device():
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _raw_stream(index))
+    if st != B.NS_OK:
+        _check(st, name)
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _device(x: torch.Tensor) -> torch.device:
@@ -56,30 +58,32 @@ def _rows(x: torch.Tensor, name: str) -> Tuple[int, int, int]:
 
     A 2-D tensor may have any row stride; one of another rank is contiguous.
     """
-    if x.dim() == 0:
+    shape = x.shape
+    if not shape:
         raise ValueError(f"{name} must have at least one axis")
-    cols = x.shape[-1]
+    cols = shape[-1]
     if cols < 1:
         raise ValueError(f"{name}'s last axis must not be empty")
-    if x.dim() == 2:
-        rows, ld = x.shape[0], x.stride(0)
-        if x.stride(1) != 1 and cols > 1:
+    if x.is_contiguous():
+        return (shape[0] if len(shape) == 2 else x.numel() // cols), cols, cols
+    if len(shape) == 2:
+        rows, (ld, step) = shape[0], x.stride()
+        if step != 1 and cols > 1:
             raise ValueError(f"{name}'s rows must be contiguous (stride(-1) == 1)")
         if rows > 1 and ld < cols:
             raise ValueError(f"{name}'s rows must not overlap")
         return rows, cols, ld if rows > 1 else cols
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (or 2-D)")
-    return x.numel() // cols, cols, cols
+    raise ValueError(f"{name} must be contiguous (or 2-D)")
 
 
 def _output(out: Optional[torch.Tensor], shape, dtype: torch.dtype,
-            device: torch.device, name: str) -> torch.Tensor:
+            device: torch.device, name: str) -> Tuple[torch.Tensor, int]:
+    """The tensor to write and its row stride."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device), shape[-1]
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
         raise ValueError(f"{name} must have shape {tuple(shape)}, {dtype} and device {device}")
-    return out
+    return out, _rows(out, name)[2]
 
 
 def _status_ptr(status: Optional[torch.Tensor], device: torch.device) -> Optional[int]:
@@ -151,20 +155,18 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         raise TypeError("weight and bias must have the same dtype")
     param = weight if weight is not None else bias
     pcode = code if param is None else dtype_code(param.dtype)
-    y = _output(out, x.shape, x.dtype, device, "out")
-    ldy = _rows(y, "out")[2]
+    y, ldy = _output(out, x.shape, x.dtype, device, "out")
     mean = rstd = None
     if stats:
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
         rstd = torch.empty_like(mean)
-    with _On(device):
-        _check(lib().ns_layer_norm(
-            x.data_ptr(), rows, cols, ldx, code,
-            None if weight is None else weight.data_ptr(),
-            None if bias is None else bias.data_ptr(), pcode, eps,
-            y.data_ptr(), ldy, None if mean is None else mean.data_ptr(),
-            None if rstd is None else rstd.data_ptr(),
-            _status_ptr(status, device), _stream(device)), "ns_layer_norm")
+    _call("ns_layer_norm", device,
+          x.data_ptr(), rows, cols, ldx, code,
+          _ptr(weight),
+          _ptr(bias), pcode, eps,
+          y.data_ptr(), ldy, _ptr(mean),
+          _ptr(rstd),
+          _status_ptr(status, device))
     return y, mean, rstd
 
 
@@ -196,8 +198,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     _per_row(rstd, rows, device, "rstd")
     _param(weight, x, cols, "weight")
     pdtype = x.dtype if weight is None else weight.dtype
-    dx = _output(out, x.shape, x.dtype, device, "out")
-    lddx = _rows(dx, "out")[2]
+    dx, lddx = _output(out, x.shape, x.dtype, device, "out")
     dweight = dbias = keep = None
     wptr, wbytes = None, 0
     if params:
@@ -206,15 +207,13 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
         wptr, wbytes, keep = _workspace_args(
             int(lib().ns_layer_norm_workspace_size(rows, cols)), device,
             workspace, "ns_layer_norm_workspace_size")
-    with _On(device):
-        _check(lib().ns_layer_norm_backward(
-            dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols, code,
-            mean.data_ptr(), rstd.data_ptr(),
-            None if weight is None else weight.data_ptr(), dtype_code(pdtype),
-            dx.data_ptr(), lddx, None if dweight is None else dweight.data_ptr(),
-            None if dbias is None else dbias.data_ptr(),
-            _status_ptr(status, device), wptr, wbytes, _stream(device)),
-            "ns_layer_norm_backward")
+    _call("ns_layer_norm_backward", device,
+          dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols, code,
+          mean.data_ptr(), rstd.data_ptr(),
+          _ptr(weight), dtype_code(pdtype),
+          dx.data_ptr(), lddx, _ptr(dweight),
+          _ptr(dbias),
+          _status_ptr(status, device), wptr, wbytes)
     return dx, dweight, dbias
 
 
@@ -237,13 +236,10 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
     vocab, cols, ldt = _rows(table, "table")
     ids64 = _ids(ids, device, "ids")
     code = dtype_code(table.dtype)
-    y = _output(out, tuple(ids.shape) + (cols,), table.dtype, device, "out")
-    ldo = _rows(y, "out")[2]
-    with _On(device):
-        _check(lib().ns_embedding(
-            ids.data_ptr(), ids64, ids.numel(), table.data_ptr(), vocab, cols,
-            ldt, code, scale, y.data_ptr(), ldo, _status_ptr(status, device),
-            _stream(device)), "ns_embedding")
+    y, ldo = _output(out, tuple(ids.shape) + (cols,), table.dtype, device, "out")
+    _call("ns_embedding", device,
+          ids.data_ptr(), ids64, ids.numel(), table.data_ptr(), vocab, cols,
+          ldt, code, scale, y.data_ptr(), ldo, _status_ptr(status, device))
     return y
 
 
@@ -270,17 +266,14 @@ def embedding_backward(ids: torch.Tensor, dy: torch.Tensor, vocab: int,
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     code = dtype_code(dy.dtype)
-    dt = _output(out, (vocab, cols), dy.dtype, device, "out")
-    ldt = _rows(dt, "out")[2]
+    dt, ldt = _output(out, (vocab, cols), dy.dtype, device, "out")
     wptr, wbytes, keep = _workspace_args(
         int(lib().ns_embedding_workspace_size(n, vocab, cols)), device,
         workspace, "ns_embedding_workspace_size")
-    with _On(device):
-        _check(lib().ns_embedding_backward(
-            ids.data_ptr(), ids64, n, dy.data_ptr(), lddy, vocab, cols, code,
-            scale, dt.data_ptr(), ldt, 1 if accumulate else 0,
-            _status_ptr(status, device), wptr, wbytes, _stream(device)),
-            "ns_embedding_backward")
+    _call("ns_embedding_backward", device,
+          ids.data_ptr(), ids64, n, dy.data_ptr(), lddy, vocab, cols, code,
+          scale, dt.data_ptr(), ldt, 1 if accumulate else 0,
+          _status_ptr(status, device), wptr, wbytes)
     return dt
 
 
@@ -340,12 +333,10 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
         int(lib().ns_linear_cross_entropy_workspace_size(
             rows, cols, vocab, code, aligned, 0)), device, workspace,
         "ns_linear_cross_entropy_workspace_size")
-    with _On(device):
-        _check(lib().ns_linear_cross_entropy(
-            h.data_ptr(), ldh, w.data_ptr(), ldw, targets.data_ptr(), t64, rows,
-            cols, vocab, code, ignore_index, loss.data_ptr(), lse.data_ptr(),
-            _status_ptr(status, device), wptr, wbytes, _stream(device)),
-            "ns_linear_cross_entropy")
+    _call("ns_linear_cross_entropy", device,
+          h.data_ptr(), ldh, w.data_ptr(), ldw, targets.data_ptr(), t64, rows,
+          cols, vocab, code, ignore_index, loss.data_ptr(), lse.data_ptr(),
+          _status_ptr(status, device), wptr, wbytes)
     return loss, lse
 
 
@@ -371,20 +362,20 @@ def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor,
     if not isinstance(dloss, torch.Tensor):
         dloss = torch.full((rows,), float(dloss), dtype=torch.float32, device=device)
     _per_row(dloss, rows, device, "dloss")
-    dh = _output(out_dh, (rows, cols), h.dtype, device, "out_dh") if need_dh else None
-    dw = _output(out_dw, (vocab, cols), w.dtype, device, "out_dw") if need_dw else None
-    lddh = _rows(dh, "out_dh")[2] if need_dh else cols
-    lddw = _rows(dw, "out_dw")[2] if need_dw else cols
+    dh = dw = None
+    lddh = lddw = cols
+    if need_dh:
+        dh, lddh = _output(out_dh, (rows, cols), h.dtype, device, "out_dh")
+    if need_dw:
+        dw, lddw = _output(out_dw, (vocab, cols), w.dtype, device, "out_dw")
     wptr, wbytes, keep = _workspace_args(
         int(lib().ns_linear_cross_entropy_workspace_size(
             rows, cols, vocab, code, aligned, 1)), device, workspace,
         "ns_linear_cross_entropy_workspace_size")
-    with _On(device):
-        _check(lib().ns_linear_cross_entropy_backward(
-            h.data_ptr(), ldh, w.data_ptr(), ldw, targets.data_ptr(), t64, rows,
-            cols, vocab, code, ignore_index, lse.data_ptr(), dloss.data_ptr(),
-            None if dh is None else dh.data_ptr(), lddh,
-            None if dw is None else dw.data_ptr(), lddw,
-            _status_ptr(status, device), wptr, wbytes, _stream(device)),
-            "ns_linear_cross_entropy_backward")
+    _call("ns_linear_cross_entropy_backward", device,
+          h.data_ptr(), ldh, w.data_ptr(), ldw, targets.data_ptr(), t64, rows,
+          cols, vocab, code, ignore_index, lse.data_ptr(), dloss.data_ptr(),
+          _ptr(dh), lddh,
+          _ptr(dw), lddw,
+          _status_ptr(status, device), wptr, wbytes)
     return dh, dw

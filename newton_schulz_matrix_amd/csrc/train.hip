@@ -7,6 +7,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/nsortho.h"
 #include "embed.hpp"
@@ -66,38 +67,62 @@ ns_status with_type(ns_dtype io, F&& f) {
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxNormCols = 1 << 24;
 constexpr int kNormRegisterCols = 16384;  // the widest row that the kernels hold in registers
+// Threads of the forward pass: as many as the chip holds at 64 registers
+// each.  Blocks walk the rows beyond that.
+constexpr int64_t kNormFwdThreads = 256 * 2048;
 // Blocks of the backward pass, each of which leaves one partial row of dw
 // and db.
 constexpr int64_t kNormParts = 512;
 
-// Calls f.template run<V, E, TPR>() for a row width: one wave per row up to
-// 1024 columns, four up to 8192 (4096 without vectors), sixteen above.  More
-// elements per thread would not leave registers for the backward's sums.
-template <typename IO, class F>
-void with_norm_form(int64_t cols, bool vec, F&& f) {
-  constexpr int V = 16 / sizeof(IO);
-  if (vec) {
-    if (cols <= 64 * 8) return f.template run<V, 8, 64>();
-    if (cols <= 64 * 16) return f.template run<V, 16, 64>();
-    if (cols <= 256 * 8) return f.template run<V, 8, 256>();
-    if (cols <= 256 * 16) return f.template run<V, 16, 256>();
-    if (cols <= 256 * 32) return f.template run<V, 32, 256>();
-    return f.template run<V, 16, 1024>();
+// Calls f.template run<NV, TPR, FORM>() for a row width: as few threads per row as
+// hold it in NV vectors each, so that a block works on many narrow rows and a
+// row's sums stay within a wave up to 256 vectors (2048 16-bit columns).
+// More vectors per thread would not leave registers for the backward's sums.
+template <typename IO, int FORM, class F>
+void norm_form(int64_t cols, F&& f) {
+  const int64_t n = (cols + kVec<IO> - 1) / kVec<IO>;
+  if (n <= 32) return f.template run<1, 32, FORM>();
+  if (n <= 64) return f.template run<2, 32, FORM>();
+  if (n <= 96) return f.template run<3, 32, FORM>();
+  if (n <= 128) return f.template run<4, 32, FORM>();
+  if (n <= 192) return f.template run<3, 64, FORM>();
+  if (n <= 256) return f.template run<4, 64, FORM>();
+  if (n <= 512) return f.template run<2, 256, FORM>();
+  if (n <= 1024) return f.template run<4, 256, FORM>();
+  if constexpr (sizeof(IO) == 4) {
+    if (n > 2048) return f.template run<4, 1024, FORM>();
   }
-  if (cols <= 64 * 4) return f.template run<1, 4, 64>();
-  if (cols <= 64 * 16) return f.template run<1, 16, 64>();
-  if (cols <= 256 * 16) return f.template run<1, 16, 256>();
-  return f.template run<1, 16, 1024>();
+  return f.template run<2, 1024, FORM>();
+}
+template <typename IO, class F>
+void with_norm_form(int64_t cols, F&& f) {
+  if (cols % kVec<IO> == 0)
+    norm_form<IO, kEven>(cols, f);
+  else
+    norm_form<IO, kRagged>(cols, f);
+}
+// Rows of less than a vector or too long for registers take the kernels that
+// go element by element.
+template <typename IO>
+bool norm_by_element(int64_t cols) {
+  return cols < kVec<IO> || cols > kNormRegisterCols;
+}
+
+template <typename IO>
+int norm_rows_per_block(int64_t cols) {
+  const int64_t n = (cols + kVec<IO> - 1) / kVec<IO>;
+  return n <= 128 ? kNormRows<32> : n <= 256 ? kNormRows<64> : 1;
 }
 
 template <typename IO, typename PT>
 struct NormFwdRun {
   const NormFwdArgs& a;
   hipStream_t st;
-  template <int V, int E, int TPR>
+  template <int NV, int TPR, int FORM>
   void run() const {
-    const int64_t blocks = std::min((a.rows + kNormRows<TPR> - 1) / kNormRows<TPR>, kMaxBlocks);
-    hipLaunchKernelGGL((k_norm_fwd<IO, PT, V, E, TPR>), dim3((unsigned)blocks), dim3(kNormThreads<TPR>), 0, st, a);
+    const int64_t groups = (a.rows + kNormRows<TPR> - 1) / kNormRows<TPR>;
+    const int64_t blocks = std::min<int64_t>(groups, kNormFwdThreads / kNormThreads<TPR>);
+    hipLaunchKernelGGL((k_norm_fwd<IO, PT, NV, TPR, FORM>), dim3((unsigned)blocks), dim3(kNormThreads<TPR>), 0, st, a);
   }
 };
 
@@ -106,18 +131,14 @@ struct NormBwdRun {
   const NormBwdArgs& a;
   int64_t parts;
   hipStream_t st;
-  template <int V, int E, int TPR>
+  template <int NV, int TPR, int FORM>
   void run() const {
-    hipLaunchKernelGGL((k_norm_bwd<IO, PT, V, E, TPR>), dim3((unsigned)parts), dim3(kNormThreads<TPR>), 0, st, a);
+    hipLaunchKernelGGL((k_norm_bwd<IO, PT, NV, TPR, FORM>), dim3((unsigned)parts), dim3(kNormThreads<TPR>), 0, st, a);
   }
 };
 
-// Partial rows of dw and db.  The register kernels' blocks take whole groups
-// of rows (four rows of one wave each, or one).
-int64_t norm_parts(int64_t rows, int64_t cols) {
-  const int64_t groups = cols <= 1024 ? (rows + 3) / 4 : rows;
-  return std::min(groups, kNormParts);
-}
+// Partial rows of dw and db: one per block of the backward pass.
+int64_t norm_parts(int64_t rows, int per_block) { return std::min((rows + per_block - 1) / per_block, kNormParts); }
 
 bool norm_shape_ok(int64_t rows, int64_t cols) {
   return rows >= 0 && rows < (int64_t(1) << 31) && cols >= 1 && cols <= kMaxNormCols;
@@ -134,49 +155,66 @@ bool embed_shape_ok(int64_t n, int64_t vocab, int64_t cols) {
   return n >= 0 && n <= kMaxEmbedIds && vocab >= 1 && vocab <= kMaxEmbedRows && cols >= 1 && cols <= kMaxEmbedCols;
 }
 
-// Ids per sorting block: about 512 blocks (two per compute unit), each of
-// which reads all ids, and at most the counters that fit.
+// Ids per sorting block: about a block per compute unit (every block reads
+// all ids, so fewer blocks read less), and at most the counters that fit.
 int embed_ids_per_block(int64_t vocab) {
   int r = 64;
-  while (r < kSortMaxIds && (int64_t)r * 512 < vocab) r *= 2;
+  while (r < kSortMaxIds && (int64_t)r * 256 < vocab) r *= 2;
   return r;
 }
 
-// Positions per partial sum.  A list of c positions leaves a wave about
-// 2 chunk + c / chunk rows to add up, least at chunk = sqrt(c / 2); the
-// longest list of a text is some twentieth of its positions.
+// Positions per chunk.  A wave adds up `chunk` rows, and the longest list,
+// some twentieth of a text's positions, joins n / (20 chunk) pieces: the two
+// are balanced at the square root.
 int embed_chunk(int64_t n) {
-  if (n <= 256) return 0;
-  int c = 32;
+  int c = 8;
   while ((int64_t)c * c * 40 < n) c *= 2;
   return c;
 }
 
 struct EmbedPlan {
-  int32_t *order, *start;
+  int32_t *order, *key, *start;
   float* partial;
-  int chunk;
+  int chunk, chunks;
+  int64_t cols_pad;
   size_t total;
 };
 
-EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t cols, void* ws) {
+// Columns that one wave covers: one, two or four vectors per lane.
+int64_t embed_slice(int64_t cols, int es) {
+  const int64_t wave = 64 * 16 / es;
+  return wave * (cols <= wave ? 1 : cols <= 2 * wave ? 2 : 4);
+}
+
+EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t cols, void* ws, int es) {
   EmbedPlan p;
   Carver c{reinterpret_cast<char*>(ws)};
   p.chunk = embed_chunk(n);
+  p.chunks = (int)((n + p.chunk - 1) / p.chunk);
   p.order = c.take<int32_t>(n);
+  p.key = c.take<int32_t>(n);
   p.start = c.take<int32_t>(vocab + 1);
-  p.partial = c.take<float>(p.chunk ? n / p.chunk * cols : 0);
+  p.cols_pad = round_to(cols, embed_slice(cols, es));
+  p.partial = c.take<float>(2 * p.chunks * p.cols_pad);
   p.total = c.used;
   return p;
 }
 
-template <typename IO, int V, int U>
+// Calls f(std::integral_constant<int, FORM>{}) for a row width.
+template <typename IO, class F>
+void with_row_form(int64_t cols, F&& f) {
+  if (cols % kVec<IO> == 0) return f(std::integral_constant<int, kEven>{});
+  if (cols > kVec<IO>) return f(std::integral_constant<int, kRagged>{});
+  return f(std::integral_constant<int, kTiny>{});
+}
+
+template <typename IO, int U, int B, int FORM>
 void embed_sum(const EmbedSumArgs& a, hipStream_t st) {
-  const unsigned slices = (unsigned)((a.cols + 64 * V * U - 1) / (64 * V * U));
-  if (a.chunk && a.n / a.chunk > 0)
-    hipLaunchKernelGGL((k_embed_chunks<IO, V, U>), dim3((unsigned)(a.n / a.chunk), slices), dim3(64), 0, st, a);
-  const int64_t per = 4 * kEmbedRowsPerWave;
-  hipLaunchKernelGGL((k_embed_rows<IO, V, U>), dim3((unsigned)((a.vocab + per - 1) / per), slices), dim3(256), 0, st, a);
+  const unsigned slices = (unsigned)(a.cols_pad / (64 * kVec<IO> * U));
+  const int64_t zeros = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
+  if (a.chunks + zeros > 0)
+    hipLaunchKernelGGL((k_embed_sum<IO, U, B, FORM>), dim3((unsigned)(a.chunks + zeros), slices), dim3(64), 0, st, a);
+  if (a.chunks > 1) hipLaunchKernelGGL((k_embed_join<IO, U, FORM>), dim3((unsigned)a.chunks, slices), dim3(64), 0, st, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -404,21 +442,17 @@ ns_status ns_layer_norm(const void* X, int64_t rows, int64_t cols, int64_t ldx, 
   return with_types(dtype, param_dtype, [&](auto io, auto pt) {
     using IO = decltype(io);
     using PT = decltype(pt);
-    constexpr int V = 16 / sizeof(IO);
-    if (cols > kNormRegisterCols) {
+    if (norm_by_element<IO>(cols))
       hipLaunchKernelGGL((k_norm_fwd_long<IO, PT>), dim3((unsigned)std::min(rows, kMaxBlocks)), dim3(1024), 0, st, a);
-    } else {
-      const bool vec = cols % V == 0 && ldx % V == 0 && ldy % V == 0 && aligned16(X) && aligned16(Y) &&
-                       aligned16(weight) && aligned16(bias);
-      with_norm_form<IO>(cols, vec, NormFwdRun<IO, PT>{a, st});
-    }
+    else
+      with_norm_form<IO>(cols, NormFwdRun<IO, PT>{a, st});
     return launched();
   });
 }
 
 size_t ns_layer_norm_workspace_size(int64_t rows, int64_t cols) {
   if (!norm_shape_ok(rows, cols)) return 0;
-  return std::max(kAlignTo, align_up_to((size_t)norm_parts(rows, cols) * 2 * cols * sizeof(float)));
+  return std::max(kAlignTo, align_up_to((size_t)norm_parts(rows, 1) * 2 * cols * sizeof(float)));
 }
 
 ns_status ns_layer_norm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, int64_t rows, int64_t cols,
@@ -433,24 +467,21 @@ ns_status ns_layer_norm_backward(const void* dY, int64_t lddy, const void* X, in
   if (params && !workspace_ok(workspace, workspace_bytes, ns_layer_norm_workspace_size(rows, cols)))
     return NS_ERR_WORKSPACE;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const int64_t parts = norm_parts(rows, cols);
   const NormBwdArgs a{dY,   X,   weight, dX,   mean,      rstd,     params ? reinterpret_cast<float*>(workspace) : nullptr,
                       rows, lddy, ldx,    lddx, (int)cols, d_status, (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT)};
   return with_types(dtype, param_dtype, [&](auto io, auto pt) {
     using IO = decltype(io);
     using PT = decltype(pt);
-    constexpr int V = 16 / sizeof(IO);
+    const int64_t parts = norm_parts(rows, norm_rows_per_block<IO>(cols));
     if (rows > 0) {
-      if (cols > kNormRegisterCols) {
+      if (norm_by_element<IO>(cols)) {
         // The parameters' pass comes first: dX may be dY.
         if (params)
           hipLaunchKernelGGL((k_norm_cols<IO>), dim3((unsigned)((cols + 255) / 256), (unsigned)parts), dim3(256), 0, st,
                              a);
         hipLaunchKernelGGL((k_norm_bwd_long<IO, PT>), dim3((unsigned)std::min(rows, kMaxBlocks)), dim3(1024), 0, st, a);
       } else {
-        const bool vec = cols % V == 0 && ldx % V == 0 && lddy % V == 0 && lddx % V == 0 && aligned16(X) &&
-                         aligned16(dY) && aligned16(dX) && aligned16(weight);
-        with_norm_form<IO>(cols, vec, NormBwdRun<IO, PT>{a, parts, st});
+        with_norm_form<IO>(cols, NormBwdRun<IO, PT>{a, parts, st});
       }
     }
     if (params)
@@ -474,19 +505,17 @@ ns_status ns_embedding(const void* ids, int32_t ids64, int64_t n, const void* ta
                     scale, d_status, (int32_t)NS_STATUS_BAD_INDEX, (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT)};
   const dim3 grid((unsigned)std::min((n + 3) / 4, kMaxBlocks));
   return with_type(dtype, [&](auto io) {
-    using IO = decltype(io);
-    constexpr int V = 16 / sizeof(IO);
-    if (cols % V == 0 && ldt % V == 0 && ldo % V == 0 && aligned16(table) && aligned16(out))
-      hipLaunchKernelGGL((k_embed<IO, V>), grid, dim3(256), 0, st, a);
-    else
-      hipLaunchKernelGGL((k_embed<IO, 1>), grid, dim3(256), 0, st, a);
+    with_row_form<decltype(io)>(cols, [&](auto form) {
+      hipLaunchKernelGGL((k_embed<decltype(io), decltype(form)::value>), grid, dim3(256), 0, st, a);
+    });
     return launched();
   });
 }
 
 size_t ns_embedding_workspace_size(int64_t n, int64_t vocab, int64_t cols) {
   if (!embed_shape_ok(n, vocab, cols)) return 0;
-  return embed_plan(n, vocab, cols, nullptr).total;
+  // The same for every type: fp32's slices are the narrowest, 16-bit ones the widest.
+  return std::max(embed_plan(n, vocab, cols, nullptr, 2).total, embed_plan(n, vocab, cols, nullptr, 4).total);
 }
 
 ns_status ns_embedding_backward(const void* ids, int32_t ids64, int64_t n, const void* dY, int64_t lddy, int64_t vocab,
@@ -496,28 +525,27 @@ ns_status ns_embedding_backward(const void* ids, int32_t ids64, int64_t n, const
   if ((ids64 != 0 && ids64 != 1) || (accumulate != 0 && accumulate != 1)) return NS_ERR_INVALID_ARG;
   if (!known(dtype)) return NS_ERR_UNSUPPORTED_DTYPE;
   if (!dT || (n > 0 && (!ids || !dY))) return NS_ERR_INVALID_ARG;
-  const EmbedPlan p = embed_plan(n, vocab, cols, workspace);
+  const EmbedPlan p = embed_plan(n, vocab, cols, workspace, bytes_of(dtype));
   if (!workspace_ok(workspace, workspace_bytes, p.total)) return NS_ERR_WORKSPACE;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const int per = embed_ids_per_block(vocab);
-  const SortArgs s{ids, ids64, n, vocab, per, p.order, p.start, d_status, (int32_t)NS_STATUS_BAD_INDEX};
+  const SortArgs s{ids, ids64, n, vocab, per, p.order, p.key, p.start, d_status, (int32_t)NS_STATUS_BAD_INDEX};
   hipLaunchKernelGGL(k_embed_sort, dim3((unsigned)((vocab + per - 1) / per)), dim3(kSortWaves * 64), 0, st, s);
-  const EmbedSumArgs a{dY,      dT,      n,         vocab,   lddy,  ldt,        (int)cols, ids,
-                       ids64,   p.order, p.start,   p.partial, p.chunk, scale, accumulate, d_status,
+  const EmbedSumArgs a{dY,      dT,        n,       vocab,    lddy,  ldt,        (int)cols, p.order, p.key,
+                       p.start, p.partial, (int)p.cols_pad, p.chunk, p.chunks, scale, accumulate, d_status,
                        (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT)};
   return with_type(dtype, [&](auto io) {
     using IO = decltype(io);
-    constexpr int V = 16 / sizeof(IO);
-    if (cols % V == 0 && lddy % V == 0 && ldt % V == 0 && aligned16(dY) && aligned16(dT)) {
-      if (cols <= 64 * V)
-        embed_sum<IO, V, 1>(a, st);
-      else if (cols <= 128 * V)
-        embed_sum<IO, V, 2>(a, st);
+    with_row_form<IO>(cols, [&](auto form) {
+      constexpr int FORM = decltype(form)::value;
+      const int64_t vectors = embed_slice(cols, sizeof(IO)) / (64 * kVec<IO>);
+      if (FORM == kTiny || vectors == 1)
+        embed_sum<IO, 1, 8, FORM>(a, st);
+      else if (vectors == 2)
+        embed_sum<IO, 2, 8, FORM == kTiny ? kEven : FORM>(a, st);
       else
-        embed_sum<IO, V, 4>(a, st);
-    } else {
-      embed_sum<IO, 1, 4>(a, st);
-    }
+        embed_sum<IO, 4, 4, FORM == kTiny ? kEven : FORM>(a, st);
+    });
     return launched();
   });
 }

@@ -19,8 +19,7 @@
 // The products run on the caller's type with fp32 accumulation; logits,
 // maxima, sums and dH's running sum are fp32.  dz is rounded to the operands'
 // type, because it is an operand itself: one rounding of half a step per
-// term, of the size of the result's own.  For fp16, whose range a
-// probability leaves, it is held as dz / max|g| * 2^15.
+// term, of the size of the result's own (see xent_scale).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -246,22 +245,25 @@ static __global__ void __launch_bounds__(1024) k_xent_join(XentJoinArgs p) {
   }
 }
 
-// fp16 holds dz as dz * 2^15 / max|g|, which puts its largest entry just
-// inside the type and keeps probabilities down to 2^-39 of it; the products'
-// results are taken back in fp32.  (Coefficients so small that 2^15 / max|g|
-// overflows give gradients that fp16 rounds to zero: the limit keeps them
-// finite on the way.)
+// 16-bit types hold dz in units of max|g|: bf16 as dz / max|g|, whose entries
+// at the targets then lie just below 1, where the type's relative step is
+// finest; fp16 as dz * 2^15 / max|g|, its largest entry just inside the type
+// and probabilities down to 2^-39 of it still held.  The products' results
+// are taken back in fp32.  (Coefficients so small that the quotient
+// overflows give gradients below 2^-100: the limit keeps them finite on the
+// way.)
+template <typename T> inline constexpr float kDzUnit = __is_same(T, _Float16) ? 0x1p15f : 1.f;
 template <typename T>
 __device__ __forceinline__ float xent_scale(const float* gmax) {
-  if constexpr (__is_same(T, _Float16)) {
+  if constexpr (sizeof(T) == 2) {
     const float g = *gmax;
-    return g > 0.f ? fminf(0x1p15f / g, 1e34f) : g;  // 0 stays 0, NaN stays NaN
+    return g > 0.f ? fminf(kDzUnit<T> / g, 1e34f) : g;  // 0 stays 0, NaN stays NaN
   }
   return 1.f;
 }
 template <typename T>
 __device__ __forceinline__ float xent_unscale(const float* gmax) {
-  if constexpr (__is_same(T, _Float16)) return *gmax * 0x1p-15f;
+  if constexpr (sizeof(T) == 2) return *gmax / kDzUnit<T>;
   return 1.f;
 }
 
