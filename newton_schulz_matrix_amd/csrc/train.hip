@@ -221,19 +221,33 @@ void embed_sum(const EmbedSumArgs& a, hipStream_t st) {
 // Cross entropy.
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxXentRows = 1 << 23, kMaxXentVocab = 1 << 23, kMaxXentCols = 1 << 20;
-// Elements of one piece of dz (bf16 and fp16: 256 MiB in each orientation).
-constexpr int64_t kXentPieceElems = int64_t(1) << 27;
+// Elements of one piece of dz at most (16-bit: 512 MiB in each orientation).
+constexpr int64_t kXentPieceElems = int64_t(1) << 28;
+// Forward with at most this many rows takes the short, wide tiles (16-bit).
+constexpr int64_t kXentFewRows = kXentFewM;
+
+// Estimated time of a product in us: rounds of tiles over the compute units,
+// each of so many us per k-tile and a fixed part, as measured on MI355X with
+// random operands.
+struct EdgeCost {
+  int edge;
+  double ktile, fixed;
+};
+constexpr EdgeCost kXentCost16[2] = {{kXentLarge<_Float16>, 0.95, 3.0}, {kXentSmall<_Float16>, 0.52, 2.0}};
+constexpr EdgeCost kXentCost32[2] = {{kXentLarge<float>, 1.85, 2.5}, {kXentSmall<float>, 0.55, 1.5}};
+double product_us(const EdgeCost& c, int64_t tiles, double ktiles) {
+  return (double)((tiles + kXentGroups - 1) / kXentGroups) * (ktiles * c.ktile + c.fixed);
+}
 
 struct XentPlan {
   int64_t n = 0, d = 0, v = 0;
   int es = 2, bk = 64;
-  bool few = false;
-  int64_t k = 0;                    // d in whole k-tiles
-  bool stage = false;               // H and W need staging copies
-  int64_t n_pad = 0, tiles_m = 0;   // rows of the first product
+  int64_t k = 0;                   // d in whole k-tiles
+  bool stage = false;              // H and W need staging copies
+  int64_t n_pad = 0, tiles_m = 0;  // rows of the first product
   int64_t tm = 0, tn = 0;
-  int64_t tiles_n = 0;              // forward: vocabulary tiles
-  int64_t d_pad = 0, piece = 0;     // backward
+  int64_t tiles_n = 0;             // forward: vocabulary tiles
+  int64_t d_pad = 0, piece = 0;    // backward
   int splits = 1;
   // Buffers.
   int32_t* tgt = nullptr;
@@ -248,6 +262,38 @@ bool xent_shape_ok(int64_t n, int64_t d, int64_t v) {
   return n >= 0 && n <= kMaxXentRows && d >= 1 && d <= kMaxXentCols && v >= 1 && v <= kMaxXentVocab;
 }
 
+// The backward pass's piece of the vocabulary (in tiles) and dH's splits for
+// one tile edge, and their estimated time.  Between the largest piece that is
+// allowed and a sixteenth of it, the one whose three products leave the
+// fewest compute units idle in their last rounds; fewer, larger pieces touch
+// dH's fp32 sums less often.
+struct BackwardChoice {
+  int64_t piece_tiles = 1;
+  int splits = 1;
+  double us = 1e300;
+};
+BackwardChoice choose_backward(const EdgeCost& c, int64_t n, int64_t d, int64_t v, int64_t k, int bk) {
+  const int64_t e = c.edge, m = std::max<int64_t>(1, (n + e - 1) / e), dt = (d + e - 1) / e, vt = (v + e - 1) / e;
+  const int64_t most = std::max<int64_t>(1, std::min(vt, kXentPieceElems / (m * e * e)));
+  const int64_t fewest = (vt + most - 1) / most;
+  BackwardChoice best;
+  for (int64_t pieces = fewest; pieces < fewest + 16 && pieces <= vt; ++pieces) {
+    const int64_t q = (vt + pieces - 1) / pieces, count = (vt + q - 1) / q, rest = vt - (count - 1) * q;
+    for (int s = 1; s <= 8; ++s) {
+      // Every split of every piece has its k-tiles (three at least).
+      if (s > 1 && rest * e / bk / s < 3) break;
+      auto one = [&](int64_t tiles) {
+        const double sums = (double)s * m * dt * e * e * 8.0 / 4.5e6;  // fp32 read and written, in us
+        return product_us(c, m * tiles, (double)k / bk) + product_us(c, tiles * dt, (double)m * e / bk) +
+               product_us(c, m * dt * s, (double)(tiles * e / bk) / s) + sums + 12.0;
+      };
+      const double us = (double)(count - 1) * one(q) + one(rest);
+      if (us < best.us) best = {q, s, us};
+    }
+  }
+  return best;
+}
+
 XentPlan xent_plan(int64_t n, int64_t d, int64_t v, ns_dtype dtype, bool aligned, bool backward, void* ws) {
   XentPlan p;
   p.n = n;
@@ -257,13 +303,29 @@ XentPlan xent_plan(int64_t n, int64_t d, int64_t v, ns_dtype dtype, bool aligned
   p.bk = kRowBytes / p.es;
   p.k = round_to(d, p.bk);
   p.stage = p.k != d || !aligned;
-  const int64_t edge = p.es == 2 ? kXentEdge<_Float16> : kXentEdge<float>;
-  p.few = !backward && n <= kXentFewRows;
-  p.tm = !p.few ? edge : p.es == 2 ? kXentFewM<_Float16> : kXentFewM<float>;
-  p.tn = !p.few ? edge : p.es == 2 ? kXentFewN<_Float16> : kXentFewN<float>;
+  const EdgeCost* costs = p.es == 2 ? kXentCost16 : kXentCost32;
+  Carver c{reinterpret_cast<char*>(ws)};
+  if (!backward) {
+    if (p.es == 2 && n <= kXentFewRows) {
+      p.tm = kXentFewM;
+      p.tn = kXentFewN;
+    } else {
+      auto us = [&](const EdgeCost& x) {
+        const int64_t e = x.edge;
+        return product_us(x, ((n + e - 1) / e) * ((v + e - 1) / e), (double)p.k / p.bk);
+      };
+      p.tm = p.tn = us(costs[0]) <= us(costs[1]) ? costs[0].edge : costs[1].edge;
+    }
+  } else {
+    const BackwardChoice large = choose_backward(costs[0], n, d, v, p.k, p.bk);
+    const BackwardChoice small = choose_backward(costs[1], n, d, v, p.k, p.bk);
+    const bool l = large.us <= small.us;
+    p.tm = p.tn = l ? costs[0].edge : costs[1].edge;
+    p.piece = (l ? large : small).piece_tiles * p.tm;
+    p.splits = (l ? large : small).splits;
+  }
   p.n_pad = round_to(n, p.tm);
   p.tiles_m = p.n_pad / p.tm;
-  Carver c{reinterpret_cast<char*>(ws)};
   p.tgt = c.take<int32_t>(p.n_pad);
   if (p.stage) p.Hs = c.take<char>(n * p.k * p.es);
   if (!backward) {
@@ -272,15 +334,8 @@ XentPlan xent_plan(int64_t n, int64_t d, int64_t v, ns_dtype dtype, bool aligned
     p.zt = c.take<float>(p.n_pad);
     p.parts = c.take<float2>(2 * p.tiles_n * p.n_pad);
   } else {
-    p.d_pad = round_to(d, edge);
-    const int64_t v_pad = round_to(v, edge);
-    p.piece = std::max<int64_t>(edge, std::min(v_pad, kXentPieceElems / std::max<int64_t>(p.n_pad, 1) / edge * edge));
-    const int64_t pieces = (v_pad + p.piece - 1) / p.piece;
-    p.piece = round_to((v_pad + pieces - 1) / pieces, edge);
-    // Few tiles of dH leave compute units idle: the contraction is split.
-    const int64_t tiles = p.tiles_m * (p.d_pad / edge);
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(16, 256 / std::max<int64_t>(tiles, 1)));
-    if (p.stage) p.Ws = c.take<char>(p.piece * p.k * p.es);
+    p.d_pad = round_to(d, p.tm);
+    if (p.stage) p.Ws = c.take<char>(std::min(p.piece, v) * p.k * p.es);
     p.coef = c.take<float>(p.n_pad);
     p.lse = c.take<float>(p.n_pad);
     p.gmax = c.take<float>(1);
@@ -329,7 +384,7 @@ ns_status xent_forward(const XentPlan& p, const void* H, int64_t ldh, const void
   a.n_pad = p.n_pad;
   a.parts = p.parts;
   a.zt = p.zt;
-  const hipError_t e = launch_xent_fwd<T>(a, p.few, st);
+  const hipError_t e = launch_xent_fwd<T>(a, (int)p.tm, st, (int)p.tn);
   if (e != hipSuccess) return NS_ERR_HIP;
   const XentJoinArgs j{p.parts, (int)(2 * p.tiles_n), p.n, p.n_pad, p.zt, p.tgt, loss, lse, d_status,
                        (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT)};
@@ -340,7 +395,7 @@ ns_status xent_forward(const XentPlan& p, const void* H, int64_t ldh, const void
 template <typename T>
 ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const void* W, int64_t ldw, XentRowArgs rows,
                         void* dH, int64_t lddh, void* dW, int64_t lddw, int32_t* d_status, hipStream_t st) {
-  constexpr int64_t edge = kXentEdge<T>;
+  const int64_t edge = p.tm;
   hipLaunchKernelGGL(k_xent_clear, dim3(1), dim3(1), 0, st, p.gmax);
   hipLaunchKernelGGL(k_xent_rows, dim3((unsigned)((p.n_pad + 255) / 256)), dim3(256), 0, st, rows);
   const T* h = reinterpret_cast<const T*>(H);
@@ -382,7 +437,7 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
     a.dz = p.dz;
     a.dzt = p.dzt;
     a.ldz = p.piece;
-    hipError_t e = launch_xent_dz<T>(a, st);
+    hipError_t e = launch_xent_dz<T>(a, (int)edge, st);
     if (e != hipSuccess) return NS_ERR_HIP;
     if (dW) {
       XentDwArgs b{};
@@ -395,9 +450,9 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
       b.out = reinterpret_cast<T*>(dW) + v0 * lddw;
       b.ldo = lddw;
       b.rows = rows_v;
-      b.cols = p.d;
+      b.cols = (int)p.d;
       b.gmax = p.gmax;
-      if ((e = launch_xent_dw<T>(b, st)) != hipSuccess) return NS_ERR_HIP;
+      if ((e = launch_xent_dw<T>(b, (int)edge, st)) != hipSuccess) return NS_ERR_HIP;
     }
     if (dH) {
       hipLaunchKernelGGL((k_xent_transpose<T>), dim3((unsigned)(width / 64), (unsigned)(p.d_pad / 64)), dim3(256), 0, st,
@@ -414,7 +469,7 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
       b.n_pad = p.n_pad;
       b.d_pad = p.d_pad;
       b.first = v0 == 0;
-      if ((e = launch_xent_dh<T>(b, st)) != hipSuccess) return NS_ERR_HIP;
+      if ((e = launch_xent_dh<T>(b, (int)edge, st)) != hipSuccess) return NS_ERR_HIP;
     }
   }
   if (dH)

@@ -26,6 +26,7 @@
 #include <stdint.h>
 
 #include "norm.hpp"
+#include "stream.hpp"
 
 namespace nsk {
 
@@ -117,7 +118,8 @@ __global__ void __launch_bounds__(256) k_xent_transpose(const T* src, int64_t ld
 }
 
 // ---------------------------------------------------------------------------
-// The products.
+// The products, each a persistent grid of at most one work-group per compute
+// unit whose tiles run as one stream (stream.hpp).
 // ---------------------------------------------------------------------------
 struct XentArgs {
   const void *H, *W;      // n x k and v x k, rows of whole k-tiles
@@ -138,70 +140,141 @@ struct XentArgs {
   int64_t ldz;
 };
 
-// One tile of logits into acc.
-template <typename T, int TM, int TN, int G>
-__device__ __forceinline__ void xent_logits(const XentArgs& p, int tm, int tn, Acc<T, TM, TN>& acc) {
+// The tiles of one work-group of a persistent grid: every gridDim.x-th of the
+// list, offset so that work-groups of one XCD run neighbours.
+struct TileRun {
+  int first, count;
+  __device__ __forceinline__ explicit TileRun(int total) {
+    first = xcd_order(blockIdx.x, gridDim.x);
+    count = first < total ? (total - first + (int)gridDim.x - 1) / (int)gridDim.x : 0;
+  }
+  __device__ __forceinline__ int at(int j) const { return first + j * (int)gridDim.x; }
+};
+
+// The logits' tiles, for the forward pass and for dz.
+template <typename T, int TM, int TN, class Epilogue>
+__device__ __forceinline__ void xent_logits(const XentArgs& p, const TileRun& run, Epilogue&& epi) {
   constexpr int BK = kRowBytes / sizeof(T);
-  const int64_t row0 = (int64_t)tm * TM, col0 = (int64_t)tn * TN;
-  const RowBound bl{(int)(p.n - row0 < TM ? p.n - row0 : TM), p.row_bytes};
-  const RowBound br{(int)(p.v - col0 < TN ? p.v - col0 : TN), p.row_bytes};
-  acc_zero(acc);
-  mainloop<T, TM, TN, 0, G>(reinterpret_cast<const char*>(p.H) + row0 * p.ldh, p.ldh,
-                            reinterpret_cast<const char*>(p.W) + col0 * p.ldw, p.ldw, 0, p.k / BK, acc, false, [] {},
-                            [](int, const char*, const FragAddr&) {}, &bl, &br);
+  stream_tiles<T, TM, TN>(
+      run.count, p.ldh, p.ldw, p.row_bytes,
+      [&](int j) {
+        int tm, tn;
+        grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+        const int64_t row0 = (int64_t)tm * TM, col0 = (int64_t)tn * TN;
+        return StreamTile{reinterpret_cast<const char*>(p.H) + row0 * p.ldh,
+                          reinterpret_cast<const char*>(p.W) + col0 * p.ldw,
+                          (int)(p.n - row0 < TM ? p.n - row0 : TM),
+                          (int)(p.v - col0 < TN ? p.v - col0 : TN),
+                          0,
+                          p.k / BK};
+      },
+      epi);
+}
+
+// Holds a value where it is until the wait before this point covers its load.
+template <typename V>
+__device__ __forceinline__ void pin(V& v) {
+  asm volatile("" : "+v"(v));
+}
+
+// Where a lane's values lie in a tile.
+template <int TM, int TN>
+struct LanePlace {
+  int lr, h, wr, wc;
+  __device__ __forceinline__ LanePlace() {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    lr = lane & 31;
+    h = lane >> 5;
+    wr = (w >> 1) * (TM / 2);
+    wc = (w & 1) * (TN / 2);
+  }
+};
+
+// -inf in the accumulators' columns from `cols` on, counted from the lane's
+// first column: logits past the vocabulary.
+template <typename T, int TM, int TN>
+__device__ __forceinline__ void mask_columns(Acc<T, TM, TN>& acc, int cols) {
+  using A = Acc<T, TM, TN>;
+#pragma unroll
+  for (int fm = 0; fm < A::FM; ++fm)
+#pragma unroll
+    for (int fn = 0; fn < A::FN; ++fn)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        acc.v[fm][fn][e] = 32 * fn + 8 * (e >> 2) + (e & 3) >= cols ? -__builtin_inff() : acc.v[fm][fn][e];
 }
 
 // Forward: each wave owns TN / 2 columns of its rows, half of them in each
 // half wave; a row's maximum and sum over them leave as one pair.
-template <typename T, int TM, int TN, int G>
-__global__ void __launch_bounds__(kThreads, G) k_xent_fwd(XentArgs p) {
+template <typename T, int TM, int TN>
+struct FwdEpilogue {
   using A = Acc<T, TM, TN>;
-  int tm, tn;
-  grouped_tile(xcd_order(blockIdx.x, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, tm, tn);
-  A acc;
-  xent_logits<T, TM, TN, G>(p, tm, tn, acc);
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int lr = lane & 31, h = lane >> 5;
-  const int wr = (w >> 1) * (TM / 2), wc = (w & 1) * (TN / 2);
-  const int64_t row0 = (int64_t)tm * TM, col0 = (int64_t)tn * TN;
-  const float inf = __builtin_inff();
-  if (col0 + TN > p.v) {
+  const XentArgs& p;
+  const TileRun& run;
+  LanePlace<TM, TN> at;
+  int cur[A::FM], next[A::FM];
+  __device__ __forceinline__ void load(int j) {
+    int tm, tn;
+    grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
 #pragma unroll
-    for (int fm = 0; fm < A::FM; ++fm)
-#pragma unroll
-      for (int fn = 0; fn < A::FN; ++fn)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (col0 + wc + 32 * fn + 8 * (e >> 2) + 4 * h + (e & 3) >= p.v) acc.v[fm][fn][e] = -inf;
-  }
-#pragma unroll
-  for (int fm = 0; fm < A::FM; ++fm) {
-    const int64_t row = row0 + wr + fm * 32 + lr;
-    const int64_t at = (int64_t)p.tgt[row] - col0 - wc - 4 * h;  // the target's column in this lane's part
-    if (__any(at >= 0 && at < TN / 2)) {
-#pragma unroll
-      for (int fn = 0; fn < A::FN; ++fn)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (at == 32 * fn + 8 * (e >> 2) + (e & 3)) p.zt[row] = acc.v[fm][fn][e];
+    for (int fm = 0; fm < A::FM; ++fm) {
+      cur[fm] = next[fm];
+      next[fm] = p.tgt[(int64_t)tm * TM + at.wr + fm * 32 + at.lr];
     }
-    float m = -inf;
-#pragma unroll
-    for (int fn = 0; fn < A::FN; ++fn)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) m = fmaxf(m, acc.v[fm][fn][e]);
-    m = fmaxf(m, __shfl_xor(m, 32, 64));
-    // A part without a finite logit (all columns past the vocabulary, or all
-    // -inf) keeps m = -inf and a sum of zeros.
-    const float ref = m == -inf ? 0.f : m;
-    float s = 0.f;
-#pragma unroll
-    for (int fn = 0; fn < A::FN; ++fn)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f((acc.v[fm][fn][e] - ref) * kLog2e);
-    s += __shfl_xor(s, 32, 64);
-    if (h == 0) p.parts[(int64_t)(2 * tn + (w & 1)) * p.n_pad + row] = float2{m, s};
   }
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int fm = 0; fm < A::FM; ++fm) pin(next[fm]);
+  }
+  __device__ __forceinline__ void store(int j, A& acc) {
+    int tm, tn;
+    grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+    const int64_t row0 = (int64_t)tm * TM;
+    const int col0 = tn * TN + at.wc + 4 * at.h;  // this lane's first column
+    const int cols = (int)p.v - col0;             // and how many from there are in the vocabulary
+    const float inf = __builtin_inff();
+    if ((int64_t)(tn + 1) * TN > p.v) mask_columns(acc, cols);
+#pragma unroll
+    for (int fm = 0; fm < A::FM; ++fm) {
+      const int64_t row = row0 + at.wr + fm * 32 + at.lr;
+      const int t = cur[fm] - col0;  // the target's column in this lane's part
+      if (__any(t >= 0 && t < TN / 2)) {
+        float z = 0.f;
+        bool mine = false;
+#pragma unroll
+        for (int fn = 0; fn < A::FN; ++fn)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const bool hit = t == 32 * fn + 8 * (e >> 2) + (e & 3);
+            z = hit ? acc.v[fm][fn][e] : z;
+            mine |= hit;
+          }
+        if (mine) p.zt[row] = z;
+      }
+      float m = -inf;
+#pragma unroll
+      for (int fn = 0; fn < A::FN; ++fn)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, acc.v[fm][fn][e]);
+      m = fmaxf(m, __shfl_xor(m, 32, 64));
+      // A part without a finite logit (all columns past the vocabulary, or
+      // all -inf) keeps m = -inf and a sum of zeros.
+      const float ref = m == -inf ? 0.f : m;
+      float s = 0.f;
+#pragma unroll
+      for (int fn = 0; fn < A::FN; ++fn)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f((acc.v[fm][fn][e] - ref) * kLog2e);
+      s += __shfl_xor(s, 32, 64);
+      if (at.h == 0) p.parts[(int64_t)(2 * tn + (at.wc ? 1 : 0)) * p.n_pad + row] = float2{m, s};
+    }
+  }
+};
+
+template <typename T, int TM, int TN>
+__global__ void __launch_bounds__(kThreads, 1) k_xent_fwd(XentArgs p) {
+  const TileRun run(p.tiles_m * p.tiles_n);
+  xent_logits<T, TM, TN>(p, run, FwdEpilogue<T, TM, TN>{p, run});
 }
 
 // Joins the parts of each row: 16 rows per block, 64 threads each.
@@ -267,124 +340,178 @@ __device__ __forceinline__ float xent_unscale(const float* gmax) {
   return 1.f;
 }
 
-// Backward, first product: dz of one tile, stored in both orientations.
-template <typename T, int TM, int TN, int G>
-__global__ void __launch_bounds__(kThreads, G) k_xent_dz(XentArgs p) {
+// Backward, first product: dz of one tile, stored in both orientations from
+// the accumulators.
+template <typename T, int TM, int TN>
+struct DzEpilogue {
   using A = Acc<T, TM, TN>;
-  using TL = TileLds<T, TM, TN, G>;
-  int tm, tn;
-  grouped_tile(xcd_order(blockIdx.x, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, tm, tn);
-  A acc;
-  xent_logits<T, TM, TN, G>(p, tm, tn, acc);
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int lr = lane & 31, h = lane >> 5;
-  const int wr = (w >> 1) * (TM / 2), wc = (w & 1) * (TN / 2);
-  const int64_t row0 = (int64_t)tm * TM, col0 = (int64_t)tn * TN;
-  const float unit = xent_scale<T>(p.gmax);
+  const XentArgs& p;
+  const TileRun& run;
+  float unit;
+  LanePlace<TM, TN> at;
+  int cur_t[A::FM], next_t[A::FM];
+  float cur_c[A::FM], next_c[A::FM], cur_l[A::FM], next_l[A::FM];
+  __device__ __forceinline__ void load(int j) {
+    int tm, tn;
+    grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
 #pragma unroll
-  for (int fm = 0; fm < A::FM; ++fm) {
-    const int il = wr + fm * 32 + lr;
-    const float c = p.coef[row0 + il] * unit, l = p.lse[row0 + il];
-    const int64_t at = (int64_t)p.tgt[row0 + il] - p.v0 - col0;
+    for (int fm = 0; fm < A::FM; ++fm) {
+      cur_t[fm] = next_t[fm];
+      cur_c[fm] = next_c[fm];
+      cur_l[fm] = next_l[fm];
+      const int64_t row = (int64_t)tm * TM + at.wr + fm * 32 + at.lr;
+      next_t[fm] = p.tgt[row];
+      next_c[fm] = p.coef[row];
+      next_l[fm] = p.lse[row];
+    }
+  }
+  __device__ __forceinline__ void settle() {
 #pragma unroll
-    for (int fn = 0; fn < A::FN; ++fn) {
+    for (int fm = 0; fm < A::FM; ++fm) {
+      pin(next_t[fm]);
+      pin(next_c[fm]);
+      pin(next_l[fm]);
+    }
+  }
+  __device__ __forceinline__ void store(int j, A& acc) {
+    int tm, tn;
+    grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+    const int64_t row0 = (int64_t)tm * TM + at.wr;
+    const int col0 = tn * TN + at.wc;
+    const int cols = (int)p.v - col0 - 4 * at.h;  // columns of the piece from this lane's first
+    T* dz = reinterpret_cast<T*>(p.dz);
+    T* dzt = reinterpret_cast<T*>(p.dzt);
+    const int q = at.lr & 3, i4 = at.lr & ~3;  // place in the quad, the quad's first row
+    if ((int64_t)(tn + 1) * TN > p.v) mask_columns(acc, cols);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int jl = wc + fn * 32 + 8 * g + 4 * h;
-        f32x4 v;
+    for (int fm = 0; fm < A::FM; ++fm) {
+      const float c = cur_c[fm] * unit, l = cur_l[fm];
+      const bool none = c == 0.f;
+      const int t = cur_t[fm] - p.v0 - col0 - 4 * at.h;
+      T* row = dz + (row0 + fm * 32 + at.lr) * p.ldz + col0;
+      T* col = dzt + (int64_t)(col0 + 4 * at.h + q) * p.n_pad + row0 + fm * 32 + i4;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float q = __builtin_amdgcn_exp2f((acc.v[fm][fn][4 * g + e] - l) * kLog2e);
-          if (at == jl + e) q -= 1.f;
-          // A row without a gradient, and the columns past the vocabulary,
-          // are exact zeros whatever their logits.
-          v[e] = c == 0.f || col0 + jl + e >= p.v ? 0.f : c * q;
+      for (int fn = 0; fn < A::FN; ++fn) {
+        f32x4 v[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = 32 * fn + 8 * g + e;
+            float x = __builtin_amdgcn_exp2f((acc.v[fm][fn][4 * g + e] - l) * kLog2e);
+            x -= t == k ? 1.f : 0.f;
+            // A row without a gradient is exact zeros whatever its logits.
+            x *= c;
+            v[g][e] = none ? 0.f : x;
+          }
+        if constexpr (sizeof(T) == 2) {
+          uint2 b[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            b[g] = pack_quad<T>(v[g]);
+            *reinterpret_cast<uint2*>(col + (int64_t)(32 * fn + 8 * g) * p.n_pad) = transpose_quad(b[g]);
+          }
+#pragma unroll
+          for (int g = 0; g < 4; g += 2)
+            *reinterpret_cast<uint4*>(row + 32 * fn + 8 * (g + at.h)) = join_quads(b[g], b[g + 1]);
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            *reinterpret_cast<f32x4*>(row + 32 * fn + 8 * g + 4 * at.h) = v[g];
+            *reinterpret_cast<f32x4*>(col + (int64_t)(32 * fn + 8 * g) * p.n_pad) = transpose_quad(v[g]);
+          }
         }
-        Quad<T>::store(reinterpret_cast<T*>(TL::at(il, jl)), v);
       }
     }
   }
-  __syncthreads();
-  constexpr int kEC = TL::kEC, kChunks = TM * TL::kCPR;
-  static_assert(kChunks % kThreads == 0, "whole chunks per thread");
-  T* dz = reinterpret_cast<T*>(p.dz);
-  T* dzt = reinterpret_cast<T*>(p.dzt);
-#pragma unroll 6
-  for (int it = 0; it < kChunks / kThreads; ++it) {
-    const int q = it * kThreads + threadIdx.x;
-    const int r = q / TL::kCPR, c = q % TL::kCPR;
-    store16<false>(dz + (row0 + r) * p.ldz + col0 + c * kEC, *reinterpret_cast<const uint4*>(TL::chunk(r, c)));
-  }
-  constexpr int kRB = TM / kEC, kBlocks = kRB * TL::kCPR;
-#pragma unroll 1
-  for (int q = threadIdx.x; q < kBlocks; q += kThreads) {
-    const int rb = q % kRB, cb = q / kRB;
-    uint4 cols[kEC];
-    TL::block_t(rb, cb, cols);
-#pragma unroll
-    for (int e = 0; e < kEC; ++e)
-      store16<false>(dzt + (col0 + cb * kEC + e) * p.n_pad + row0 + rb * kEC, cols[e]);
-  }
+};
+
+template <typename T, int TM, int TN>
+__global__ void __launch_bounds__(kThreads, 1) k_xent_dz(XentArgs p) {
+  const TileRun run(p.tiles_m * p.tiles_n);
+  xent_logits<T, TM, TN>(p, run, DzEpilogue<T, TM, TN>{p, run, xent_scale<T>(p.gmax)});
 }
 
-// dW rows of one piece: dzt (pieces rows x n_pad) times H^T (d_pad x n_pad).
+// dW rows of one piece: dzt (piece x n_pad) times H^T (d_pad x n_pad).
 struct XentDwArgs {
   const void *L, *R;
   int64_t ldl, ldr;  // bytes
   int k;
   int tiles_m, tiles_n;
   void* out;
-  int64_t ldo, rows, cols;  // valid rows and columns of out
+  int64_t ldo, rows;  // valid rows of out
+  int cols;           // and columns
   const float* gmax;
 };
 
-template <typename T, int TM, int TN, int G>
-__global__ void __launch_bounds__(kThreads, G) k_xent_dw(XentDwArgs p) {
+template <typename T, int TM, int TN>
+struct DwEpilogue {
   using A = Acc<T, TM, TN>;
-  using TL = TileLds<T, TM, TN, G>;
-  int tm, tn;
-  grouped_tile(xcd_order(blockIdx.x, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, tm, tn);
-  const int64_t row0 = (int64_t)tm * TM, col0 = (int64_t)tn * TN;
-  constexpr int BK = kRowBytes / sizeof(T);
-  A acc;
-  acc_zero(acc);
-  mainloop<T, TM, TN, 0, G>(reinterpret_cast<const char*>(p.L) + row0 * p.ldl, p.ldl,
-                            reinterpret_cast<const char*>(p.R) + col0 * p.ldr, p.ldr, 0, p.k / BK, acc, false, [] {},
-                            [](int, const char*, const FragAddr&) {});
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int lr = lane & 31, h = lane >> 5;
-  const int wr = (w >> 1) * (TM / 2), wc = (w & 1) * (TN / 2);
-  const float s = xent_unscale<T>(p.gmax);
+  const XentDwArgs& p;
+  const TileRun& run;
+  float scale;
+  LanePlace<TM, TN> at;
+  __device__ __forceinline__ void load(int) {}
+  __device__ __forceinline__ void settle() {}
+  __device__ __forceinline__ void store(int j, A& acc) {
+    int tm, tn;
+    grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+    const int64_t row0 = (int64_t)tm * TM + at.wr;
+    const int col0 = tn * TN + at.wc;
+    constexpr int V = kVec<T>;
+    T* out = reinterpret_cast<T*>(p.out);
 #pragma unroll
-  for (int fm = 0; fm < A::FM; ++fm)
+    for (int fm = 0; fm < A::FM; ++fm) {
+      const int64_t i = row0 + fm * 32 + at.lr;
+      if (i >= p.rows) continue;
+      T* row = out + i * p.ldo;
 #pragma unroll
-    for (int fn = 0; fn < A::FN; ++fn)
+      for (int fn = 0; fn < A::FN; ++fn) {
+        // 16-byte chunks of the row at any alignment; the row's last one may
+        // be partial.
+        auto put = [&](int c, const u32x4_t& q) {
+          if (c + V <= p.cols) {
+            *reinterpret_cast<typename Vec16<sizeof(T)>::type*>(row + c) = q;
+          } else {
+            const T* e = reinterpret_cast<const T*>(&q);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        f32x4 v;
+            for (int k = 0; k < V; ++k)
+              if (c + k < p.cols) row[c + k] = e[k];
+          }
+        };
+        f32x4 v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = s * acc.v[fm][fn][4 * g + e];
-        Quad<T>::store(reinterpret_cast<T*>(TL::at(wr + fm * 32 + lr, wc + fn * 32 + 8 * g + 4 * h)), v);
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[g][e] = scale * acc.v[fm][fn][4 * g + e];
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+          for (int g = 0; g < 4; g += 2) {
+            const uint4 q = join_quads(pack_quad<T>(v[g]), pack_quad<T>(v[g + 1]));
+            put(col0 + 32 * fn + 8 * (g + at.h), u32x4_t{q.x, q.y, q.z, q.w});
+          }
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) put(col0 + 32 * fn + 8 * g + 4 * at.h, __builtin_bit_cast(u32x4_t, v[g]));
+        }
       }
-  __syncthreads();
-  constexpr int kEC = TL::kEC, kChunks = TM * TL::kCPR;
-  T* out = reinterpret_cast<T*>(p.out);
-  const bool vec = p.ldo % kEC == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-#pragma unroll 6
-  for (int it = 0; it < kChunks / kThreads; ++it) {
-    const int q = it * kThreads + threadIdx.x;
-    const int r = q / TL::kCPR, c = q % TL::kCPR;
-    const int64_t i = row0 + r, j = col0 + c * kEC;
-    if (i >= p.rows || j >= p.cols) continue;
-    const uint4 val = *reinterpret_cast<const uint4*>(TL::chunk(r, c));
-    T* dst = out + i * p.ldo + j;
-    if (vec && j + kEC <= p.cols) {
-      store16<false>(dst, val);
-    } else {
-      const T* vals = reinterpret_cast<const T*>(&val);
-      for (int e = 0; e < kEC && j + e < p.cols; ++e) dst[e] = vals[e];
     }
   }
+};
+
+template <typename T, int TM, int TN>
+__global__ void __launch_bounds__(kThreads, 1) k_xent_dw(XentDwArgs p) {
+  const TileRun run(p.tiles_m * p.tiles_n);
+  constexpr int BK = kRowBytes / sizeof(T);
+  stream_tiles<T, TM, TN>(
+      run.count, p.ldl, p.ldr, (uint32_t)(p.k * sizeof(T)),
+      [&](int j) {
+        int tm, tn;
+        grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+        return StreamTile{reinterpret_cast<const char*>(p.L) + (int64_t)tm * TM * p.ldl,
+                          reinterpret_cast<const char*>(p.R) + (int64_t)tn * TN * p.ldr, TM, TN, 0, p.k / BK};
+      },
+      DwEpilogue<T, TM, TN>{p, run, xent_unscale<T>(p.gmax)});
 }
 
 // dH's running sums: acc[split] (+)= dz (n_pad x piece) W^T (d_pad x piece)
@@ -399,38 +526,53 @@ struct XentDhArgs {
   int first;         // the first piece writes, the others add
 };
 
-template <typename T, int TM, int TN, int G>
-__global__ void __launch_bounds__(kThreads, G) k_xent_dh(XentDhArgs p) {
+template <typename T, int TM, int TN>
+struct DhEpilogue {
   using A = Acc<T, TM, TN>;
+  const XentDhArgs& p;
+  const TileRun& run;
+  int per;
+  LanePlace<TM, TN> at;
+  __device__ __forceinline__ void load(int) {}
+  __device__ __forceinline__ void settle() {}
+  __device__ __forceinline__ void store(int j, A& acc) {
+    int tm, tn;
+    grouped_tile(run.at(j) % per, p.tiles_m, p.tiles_n, tm, tn);
+    float* out = p.acc + ((int64_t)(run.at(j) / per) * p.n_pad + (int64_t)tm * TM + at.wr + at.lr) * p.d_pad +
+                 tn * TN + at.wc + 4 * at.h;
+#pragma unroll
+    for (int fm = 0; fm < A::FM; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < A::FN; ++fn)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          f32x4* dst = reinterpret_cast<f32x4*>(out + (int64_t)fm * 32 * p.d_pad + fn * 32 + 8 * g);
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc.v[fm][fn][4 * g + e];
+          if (!p.first) v += *dst;
+          *dst = v;
+        }
+  }
+};
+
+template <typename T, int TM, int TN>
+__global__ void __launch_bounds__(kThreads, 1) k_xent_dh(XentDhArgs p) {
   const int per = p.tiles_m * p.tiles_n;
-  const int pos = xcd_order(blockIdx.x, per * p.splits);
-  const int split = pos / per;
-  int tm, tn;
-  grouped_tile(pos % per, p.tiles_m, p.tiles_n, tm, tn);
-  const int64_t row0 = (int64_t)tm * TM, col0 = (int64_t)tn * TN;
-  const int kt0 = (int)((int64_t)p.ktiles * split / p.splits), kt1 = (int)((int64_t)p.ktiles * (split + 1) / p.splits);
-  A acc;
-  acc_zero(acc);
-  mainloop<T, TM, TN, 0, G>(reinterpret_cast<const char*>(p.L) + row0 * p.ldl, p.ldl,
-                            reinterpret_cast<const char*>(p.R) + col0 * p.ldr, p.ldr, kt0, kt1, acc, false, [] {},
-                            [](int, const char*, const FragAddr&) {});
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int lr = lane & 31, h = lane >> 5;
-  const int wr = (w >> 1) * (TM / 2), wc = (w & 1) * (TN / 2);
-  float* out = p.acc + ((int64_t)split * p.n_pad + row0) * p.d_pad + col0;
-#pragma unroll
-  for (int fm = 0; fm < A::FM; ++fm)
-#pragma unroll
-    for (int fn = 0; fn < A::FN; ++fn)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        f32x4* dst = reinterpret_cast<f32x4*>(out + (int64_t)(wr + fm * 32 + lr) * p.d_pad + wc + fn * 32 + 8 * g + 4 * h);
-        f32x4 v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc.v[fm][fn][4 * g + e];
-        if (!p.first) v += *dst;
-        *dst = v;
-      }
+  const TileRun run(per * p.splits);
+  constexpr int BK = kRowBytes / sizeof(T);
+  stream_tiles<T, TM, TN>(
+      run.count, p.ldl, p.ldr, (uint32_t)(p.ktiles * BK * sizeof(T)),
+      [&](int j) {
+        const int split = run.at(j) / per;
+        int tm, tn;
+        grouped_tile(run.at(j) % per, p.tiles_m, p.tiles_n, tm, tn);
+        const int kt0 = (int)((int64_t)p.ktiles * split / p.splits);
+        const int kt1 = (int)((int64_t)p.ktiles * (split + 1) / p.splits);
+        return StreamTile{reinterpret_cast<const char*>(p.L) + (int64_t)tm * TM * p.ldl,
+                          reinterpret_cast<const char*>(p.R) + (int64_t)tn * TN * p.ldr, TM, TN, kt0, kt1 - kt0};
+      },
+      DhEpilogue<T, TM, TN>{p, run, per});
 }
 
 // dH = the splits' sum, unscaled and rounded.
@@ -460,46 +602,67 @@ namespace nsr {
 
 using namespace nsk;
 
-// Tile edges of the products: the edge that is fastest for the iteration's
-// large products too (products.hpp).
-template <typename T> inline constexpr int kXentEdge = sizeof(T) == 2 ? 192 : 128;
-// Forward with at most kXentFewRows rows: short, wide tiles.
-constexpr int kXentFewRows = 128;
-template <typename T> inline constexpr int kXentFewM = sizeof(T) == 2 ? 128 : 64;
-template <typename T> inline constexpr int kXentFewN = sizeof(T) == 2 ? 256 : 128;
+// Tile edges of the products: square tiles of the large or the small edge
+// (a call's choice: xent_edge in train.hip); forward with few rows, 16-bit:
+// short, wide tiles.
+template <typename T> inline constexpr int kXentLarge = sizeof(T) == 2 ? 192 : 128;
+template <typename T> inline constexpr int kXentSmall = sizeof(T) == 2 ? 128 : 64;
+constexpr int kXentFewM = 128, kXentFewN = 256;
+constexpr int kXentGroups = 256;  // one work-group per compute unit
 
-template <typename T> hipError_t launch_xent_fwd(const XentArgs& a, bool few, hipStream_t s);
-template <typename T> hipError_t launch_xent_dz(const XentArgs& a, hipStream_t s);
-template <typename T> hipError_t launch_xent_dw(const XentDwArgs& a, hipStream_t s);
-template <typename T> hipError_t launch_xent_dh(const XentDhArgs& a, hipStream_t s);
+template <typename T> hipError_t launch_xent_fwd(const XentArgs& a, int tm, hipStream_t s, int tn);
+template <typename T> hipError_t launch_xent_dz(const XentArgs& a, int edge, hipStream_t s);
+template <typename T> hipError_t launch_xent_dw(const XentDwArgs& a, int edge, hipStream_t s);
+template <typename T> hipError_t launch_xent_dh(const XentDhArgs& a, int edge, hipStream_t s);
+
+template <typename T, class Large, class Small>
+hipError_t launch_edge(int edge, Large&& large, Small&& small) {
+  if (edge == kXentLarge<T>)
+    large();
+  else
+    small();
+  return hipGetLastError();
+}
+inline dim3 xent_grid(int64_t tiles) { return dim3((unsigned)(tiles < kXentGroups ? tiles : kXentGroups)); }
 
 #define NS_XENT_LAUNCHERS(T)                                                                                        \
   template <>                                                                                                       \
-  hipError_t launch_xent_fwd<T>(const XentArgs& a, bool few, hipStream_t s) {                                       \
-    const dim3 grid((unsigned)((int64_t)a.tiles_m * a.tiles_n));                                                    \
-    if (few)                                                                                                        \
-      hipLaunchKernelGGL((k_xent_fwd<T, kXentFewM<T>, kXentFewN<T>, 1>), grid, dim3(kThreads), 0, s, a);            \
-    else                                                                                                            \
-      hipLaunchKernelGGL((k_xent_fwd<T, kXentEdge<T>, kXentEdge<T>, 1>), grid, dim3(kThreads), 0, s, a);            \
-    return hipGetLastError();                                                                                       \
+  hipError_t launch_xent_fwd<T>(const XentArgs& a, int tm, hipStream_t s, int tn) {                                 \
+    const dim3 grid = xent_grid((int64_t)a.tiles_m * a.tiles_n);                                                    \
+    if constexpr (sizeof(T) == 2) {                                                                                 \
+      if (tm != tn) {                                                                                               \
+        hipLaunchKernelGGL((k_xent_fwd<T, kXentFewM, kXentFewN>), grid, dim3(kThreads), 0, s, a);                   \
+        return hipGetLastError();                                                                                   \
+      }                                                                                                             \
+    }                                                                                                               \
+    constexpr int L = kXentLarge<T>, S = kXentSmall<T>;                                                             \
+    return launch_edge<T>(                                                                                          \
+        tm, [&] { hipLaunchKernelGGL((k_xent_fwd<T, L, L>), grid, dim3(kThreads), 0, s, a); },                      \
+        [&] { hipLaunchKernelGGL((k_xent_fwd<T, S, S>), grid, dim3(kThreads), 0, s, a); });                         \
   }                                                                                                                 \
   template <>                                                                                                       \
-  hipError_t launch_xent_dz<T>(const XentArgs& a, hipStream_t s) {                                                  \
-    hipLaunchKernelGGL((k_xent_dz<T, kXentEdge<T>, kXentEdge<T>, 1>),                                               \
-                       dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)), dim3(kThreads), 0, s, a);                  \
-    return hipGetLastError();                                                                                       \
+  hipError_t launch_xent_dz<T>(const XentArgs& a, int edge, hipStream_t s) {                                        \
+    const dim3 grid = xent_grid((int64_t)a.tiles_m * a.tiles_n);                                                    \
+    constexpr int L = kXentLarge<T>, S = kXentSmall<T>;                                                             \
+    return launch_edge<T>(                                                                                          \
+        edge, [&] { hipLaunchKernelGGL((k_xent_dz<T, L, L>), grid, dim3(kThreads), 0, s, a); },                     \
+        [&] { hipLaunchKernelGGL((k_xent_dz<T, S, S>), grid, dim3(kThreads), 0, s, a); });                          \
   }                                                                                                                 \
   template <>                                                                                                       \
-  hipError_t launch_xent_dw<T>(const XentDwArgs& a, hipStream_t s) {                                                \
-    hipLaunchKernelGGL((k_xent_dw<T, kXentEdge<T>, kXentEdge<T>, 1>),                                               \
-                       dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n)), dim3(kThreads), 0, s, a);                  \
-    return hipGetLastError();                                                                                       \
+  hipError_t launch_xent_dw<T>(const XentDwArgs& a, int edge, hipStream_t s) {                                      \
+    const dim3 grid = xent_grid((int64_t)a.tiles_m * a.tiles_n);                                                    \
+    constexpr int L = kXentLarge<T>, S = kXentSmall<T>;                                                             \
+    return launch_edge<T>(                                                                                          \
+        edge, [&] { hipLaunchKernelGGL((k_xent_dw<T, L, L>), grid, dim3(kThreads), 0, s, a); },                     \
+        [&] { hipLaunchKernelGGL((k_xent_dw<T, S, S>), grid, dim3(kThreads), 0, s, a); });                          \
   }                                                                                                                 \
   template <>                                                                                                       \
-  hipError_t launch_xent_dh<T>(const XentDhArgs& a, hipStream_t s) {                                                \
-    hipLaunchKernelGGL((k_xent_dh<T, kXentEdge<T>, kXentEdge<T>, 1>),                                               \
-                       dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n * a.splits)), dim3(kThreads), 0, s, a);       \
-    return hipGetLastError();                                                                                       \
+  hipError_t launch_xent_dh<T>(const XentDhArgs& a, int edge, hipStream_t s) {                                      \
+    const dim3 grid = xent_grid((int64_t)a.tiles_m * a.tiles_n * a.splits);                                         \
+    constexpr int L = kXentLarge<T>, S = kXentSmall<T>;                                                             \
+    return launch_edge<T>(                                                                                          \
+        edge, [&] { hipLaunchKernelGGL((k_xent_dh<T, L, L>), grid, dim3(kThreads), 0, s, a); },                     \
+        [&] { hipLaunchKernelGGL((k_xent_dh<T, S, S>), grid, dim3(kThreads), 0, s, a); });                          \
   }
 
 }  // namespace nsr

@@ -95,12 +95,14 @@ def test_workspace_sizes():
     # Layer norm: at most 512 partial rows, whatever the number of rows.
     assert nsa.layer_norm_workspace_size(1 << 20, 4096) == 512 * 2 * 4096 * 4
     # The logits are not kept: forward needs a few bytes per row and 192
-    # columns, backward stays near one piece of 2^27 elements in two
+    # columns, backward holds one piece of at most 2^28 elements in two
     # orientations plus H^T, one piece of W^T and dH in fp32.
     logits = 8192 * 128000 * 2
     assert nsa.linear_cross_entropy_workspace_size(8192, 4096, 128000) < logits / 15
-    back = nsa.linear_cross_entropy_workspace_size(8192, 4096, 128000, backward=True)
-    assert back < logits / 2
+    for n in (8192, 65536):
+        back = nsa.linear_cross_entropy_workspace_size(n, 4096, 128000, backward=True)
+        h = (n + 192) * 4224
+        assert back < 2 * 2 ** 28 * 2 + 128000 * 4224 * 2 + h * 2 + 8 * h * 4
     # Operands that are not aligned, or rows that are not whole k-tiles, are copied.
     plain = nsa.linear_cross_entropy_workspace_size(300, 1024, 5000)
     copied = nsa.linear_cross_entropy_workspace_size(300, 1024, 5000, aligned=False)
