@@ -10,6 +10,8 @@
 // in flight.  Stages, fragments and the steps themselves are products.hpp's.
 #pragma once
 
+#include <type_traits>
+
 #include "products.hpp"
 
 namespace nsk {
@@ -42,7 +44,9 @@ __device__ __forceinline__ void border_first(const DmaLoader<TM>& la, const DmaL
   mma_frags<T, FM, FN>(fs.f2, acc);
   mma_frags<T, FM, FN>(fs.f3, acc);
 }
-template <typename T, int TM, int TN>
+// STORES: a lower bound on the epilogue's stores per wave, all of them issued
+// after the border's copies.
+template <typename T, int TM, int TN, int STORES>
 __device__ __forceinline__ void border_second(const char* P, const FragAddr& fa, FragSets<TM / 64, TN / 64>& fs,
                                               f32x16 (&acc)[TM / 64][TN / 64]) {
   constexpr int FM = TM / 64, FN = TN / 64, kOffR = TM * kRowBytes;
@@ -50,16 +54,42 @@ __device__ __forceinline__ void border_second(const char* P, const FragAddr& fa,
   load_frags<FM, FN>(P, P + kOffR, fa, 3, fs.f3);
   mma_frags<T, FM, FN>(fs.f0, acc);
   mma_frags<T, FM, FN>(fs.f1, acc);
-  // The epilogue's own loads and stores are younger than the border's copies,
-  // so this wait is stricter than needed, never weaker.
-  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(TM / 32 + TN / 32));
+  // The copies of the step before must have landed.  Memory operations
+  // complete in order; younger than those copies are the border's own and the
+  // epilogue's stores, which need not be waited for.
+  constexpr int kYounger = TM / 32 + TN / 32 + STORES;
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kYounger < 63 ? kYounger : 63));
+}
+
+// pipe_step (products.hpp) for the first step after a border: the border's
+// copies, for which it waits, are older than the epilogue's stores.
+template <typename T, int TM, int TN, int STORES>
+__device__ __forceinline__ void first_step(const DmaLoader<TM>& la, const DmaLoader<TN>& lb, int kt,
+                                           char* __restrict__ D, const char* __restrict__ P, const FragAddr& fa,
+                                           FragSets<TM / 64, TN / 64>& fs, f32x16 (&acc)[TM / 64][TN / 64]) {
+  constexpr int FM = TM / 64, FN = TN / 64, kOffR = TM * kRowBytes;
+  la.issue(kt, D);
+  lb.issue(kt, D + kOffR);
+  load_frags<FM, FN>(P, P + kOffR, fa, 0, fs.f0);
+  load_frags<FM, FN>(P, P + kOffR, fa, 1, fs.f1);
+  mma_frags<T, FM, FN>(fs.f2, acc);
+  mma_frags<T, FM, FN>(fs.f3, acc);
+  load_frags<FM, FN>(P, P + kOffR, fa, 2, fs.f2);
+  load_frags<FM, FN>(P, P + kOffR, fa, 3, fs.f3);
+  mma_frags<T, FM, FN>(fs.f0, acc);
+  mma_frags<T, FM, FN>(fs.f1, acc);
+  schedule_step<T, TM, TN, 1>();
+  constexpr int kYounger = TM / 32 + TN / 32 + STORES;
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kYounger < 63 ? kYounger : 63));
+  lds_barrier();
 }
 
 // Runs tiles 0 .. count - 1 of one work-group.  tile_of(j) gives tile j
 // (uniform).  epi.load(j) puts the values loaded before into place and issues
 // the loads that tile j's epilogue needs (called once more for the last tile,
 // whose values it then puts into place), epi.settle() makes them final after
-// a wait that covers them, and epi.store(j, acc) is the epilogue.
+// a wait that covers them (they are issued before the border's copies), and
+// epi.store(j, acc) is the epilogue, with at least kStores stores per wave.
 template <typename T, int TM, int TN, class TileOf, class Epilogue>
 __device__ __forceinline__ void stream_tiles(int count, int64_t ldl, int64_t ldr, uint32_t row_bytes, TileOf&& tile_of,
                                              Epilogue&& epi) {
@@ -68,6 +98,7 @@ __device__ __forceinline__ void stream_tiles(int count, int64_t ldl, int64_t ldr
   constexpr int kDma = TM / 32 + TN / 32;
   using S = Stages<TM, TN, 1>;
   static_assert(S::kCount == 3, "the stream has three stages");
+  constexpr int kStores = std::remove_reference_t<Epilogue>::kStores;
   if (count <= 0) return;
   const int w = threadIdx.x >> 6;
   const int wr = (w >> 1) * (TM / 2), wc = (w & 1) * (TN / 2);
@@ -154,7 +185,9 @@ __device__ __forceinline__ void stream_tiles(int count, int64_t ldl, int64_t ldr
   }
   mma_frags<T, FM, FN>(fs.f0, acc.v);
   mma_frags<T, FM, FN>(fs.f1, acc.v);
-  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kDma));
+  // All three k-tiles: the first step's wait counts an epilogue's stores,
+  // and there has been none.
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
   lds_barrier();
 
   // From the current k-tile (in stage D) to the next one of the tile (in P).
@@ -163,12 +196,12 @@ __device__ __forceinline__ void stream_tiles(int count, int64_t ldl, int64_t ldr
     pipe_step<T, TM, TN, 1>(nullptr, nullptr, la, lb, kt, 0, D, P, fa, fs, acc.v, [](int, const char*, const FragAddr&) {});
   };
   for (int j = 0;; ++j) {
+    first_step<T, TM, TN, kStores>(la, lb, advance(), S::s0(), S::s1(), fa, fs, acc.v);
     for (int g = tile.groups(); g > 1; --g) {
-      step(S::s0(), S::s1());
       step(S::s1(), S::s2());
       step(S::s2(), S::s0());
+      step(S::s0(), S::s1());
     }
-    step(S::s0(), S::s1());
     step(S::s1(), S::s2());
     // The border: a step from this tile's last k-tile to the next tile's
     // first (past the end, a repeated one), in two halves around the
@@ -183,7 +216,7 @@ __device__ __forceinline__ void stream_tiles(int count, int64_t ldl, int64_t ldr
     epi.store(j, acc);
     if (!more) break;
     acc_zero(acc);
-    border_second<T, TM, TN>(S::s0(), fa, fs, acc.v);
+    border_second<T, TM, TN, kStores>(S::s0(), fa, fs, acc.v);
     epi.settle();
     lds_barrier();
   }
@@ -226,12 +259,12 @@ __device__ __forceinline__ uint2 transpose_quad(uint2 v) {
   // Lanes 0 and 1 take columns 0, 1 of all rows, lanes 2 and 3 columns 2, 3.
   const uint32_t got = quad_move<0x4E>(high ? v.x : v.y);
   const uint32_t r0 = high ? got : v.x, r1 = high ? v.y : got;  // rows (0, 1) and (2, 3) of this lane's pair
-  // Even lanes take the low columns, odd lanes the high ones.
+  // Even lanes take the low columns of their own and their neighbour's row,
+  // odd lanes the high ones (byte selects: as selects between shifts these
+  // became branches).
   const uint32_t p0 = quad_move<0xB1>(r0), p1 = quad_move<0xB1>(r1);
-  uint2 o;
-  o.x = odd ? (p0 >> 16) | (r0 & 0xffff0000u) : (r0 & 0xffffu) | (p0 << 16);
-  o.y = odd ? (p1 >> 16) | (r1 & 0xffff0000u) : (r1 & 0xffffu) | (p1 << 16);
-  return o;
+  const uint32_t sel = odd ? 0x03020706u : 0x05040100u;
+  return uint2{__builtin_amdgcn_perm(p0, r0, sel), __builtin_amdgcn_perm(p1, r1, sel)};
 }
 
 // The same for 32-bit columns.

@@ -357,6 +357,13 @@ bool xent_aligned(const void* H, int64_t ldh, const void* W, int64_t ldw, ns_dty
 }
 
 template <typename T>
+void xent_pad(const XentPlan& p, const void* src, int64_t ld, int64_t rows, char* dst, hipStream_t st) {
+  const int64_t blocks = std::min<int64_t>((rows * (p.k / kVec<T>) + 255) / 256, 8192);
+  hipLaunchKernelGGL((k_xent_pad<T>), dim3((unsigned)blocks), dim3(256), 0, st, reinterpret_cast<const T*>(src), ld,
+                     rows, (int)p.d, reinterpret_cast<T*>(dst), (int)p.k);
+}
+
+template <typename T>
 ns_status xent_forward(const XentPlan& p, const void* H, int64_t ldh, const void* W, int64_t ldw, XentRowArgs rows,
                        float* loss, float* lse, int32_t* d_status, hipStream_t st) {
   hipLaunchKernelGGL(k_xent_rows, dim3((unsigned)((p.n_pad + 255) / 256)), dim3(256), 0, st, rows);
@@ -366,10 +373,8 @@ ns_status xent_forward(const XentPlan& p, const void* H, int64_t ldh, const void
   a.ldh = ldh * sizeof(T);
   a.ldw = ldw * sizeof(T);
   if (p.stage) {
-    hipLaunchKernelGGL((k_xent_pad<T>), dim3((unsigned)p.n), dim3(256), 0, st, (const T*)H, ldh, p.n, (int)p.d,
-                       (T*)p.Hs, (int)p.k);
-    hipLaunchKernelGGL((k_xent_pad<T>), dim3((unsigned)p.v), dim3(256), 0, st, (const T*)W, ldw, p.v, (int)p.d,
-                       (T*)p.Ws, (int)p.k);
+    xent_pad<T>(p, H, ldh, p.n, p.Hs, st);
+    xent_pad<T>(p, W, ldw, p.v, p.Ws, st);
     a.H = p.Hs;
     a.W = p.Ws;
     a.ldh = a.ldw = p.k * (int64_t)sizeof(T);
@@ -399,10 +404,7 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
   hipLaunchKernelGGL(k_xent_clear, dim3(1), dim3(1), 0, st, p.gmax);
   hipLaunchKernelGGL(k_xent_rows, dim3((unsigned)((p.n_pad + 255) / 256)), dim3(256), 0, st, rows);
   const T* h = reinterpret_cast<const T*>(H);
-  if (p.stage) {
-    hipLaunchKernelGGL((k_xent_pad<T>), dim3((unsigned)p.n), dim3(256), 0, st, h, ldh, p.n, (int)p.d, (T*)p.Hs,
-                       (int)p.k);
-  }
+  if (p.stage) xent_pad<T>(p, H, ldh, p.n, p.Hs, st);
   if (dW)
     hipLaunchKernelGGL((k_xent_transpose<T>), dim3((unsigned)(p.n_pad / 64), (unsigned)(p.d_pad / 64)), dim3(256), 0, st,
                        h, ldh, p.n, (int)p.d, (T*)p.HT, p.n_pad);
@@ -416,8 +418,7 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
     a.ldh = ldh * sizeof(T);
     a.ldw = ldw * sizeof(T);
     if (p.stage) {
-      hipLaunchKernelGGL((k_xent_pad<T>), dim3((unsigned)rows_v), dim3(256), 0, st, w, ldw, rows_v, (int)p.d, (T*)p.Ws,
-                         (int)p.k);
+      xent_pad<T>(p, w, ldw, rows_v, p.Ws, st);
       a.H = p.Hs;
       a.W = p.Ws;
       a.ldh = a.ldw = p.k * (int64_t)sizeof(T);

@@ -89,32 +89,71 @@ static __global__ void __launch_bounds__(256) k_xent_rows(XentRowArgs p) {
   if (p.d_status) report_status(p.d_status, p.index_bit, t == kTargetBad);
 }
 
-// dst (rows_pad x cols_pad) = src's rows x cols corner, zeros elsewhere: the
-// staging copy of an operand whose rows are not whole k-tiles or not aligned.
+// dst (rows x cols_pad) = src's rows, zeros behind cols: the staging copy of
+// an operand whose rows are not whole k-tiles or not aligned.  cols_pad is a
+// multiple of a vector; one vector per thread and step.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_pad(const T* src, int64_t ld, int64_t rows, int cols, T* dst,
                                                   int cols_pad) {
-  const int64_t r = blockIdx.x;
-  for (int c = threadIdx.x; c < cols_pad; c += 256)
-    dst[r * cols_pad + c] = r < rows && c < cols ? src[r * ld + c] : from_f32<T>(0.f);
+  constexpr int V = kVec<T>;
+  const int per = cols_pad / V;
+  const int64_t total = rows * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per;
+    const int c = (int)(i - r * per) * V;
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (c + V <= cols) {
+      v = *reinterpret_cast<const typename Vec16<sizeof(T)>::type*>(src + r * ld + c);
+    } else {
+      T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (c + k < cols) e[k] = src[r * ld + c + k];
+    }
+    *reinterpret_cast<u32x4_t*>(dst + r * cols_pad + c) = v;
+  }
 }
 
 // dst (cols_pad x ldd) = the transpose of src's rows x cols, zeros elsewhere,
-// through 64 x 64 tiles in LDS.
+// through 64 x 64 tiles in LDS: 16-byte vectors on both sides, and in between
+// a lane writes its vector's elements down a column of the transposed tile.
+// Its rows are 64 elements and 16 bytes apart, which puts the lanes of a
+// write (same row group, neighbouring vectors) on different banks.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_transpose(const T* src, int64_t ld, int64_t rows, int cols, T* dst,
                                                         int64_t ldd) {
-  __shared__ T tile[64][64 + 4 / sizeof(T)];
+  constexpr int V = kVec<T>, C = 64 / V;  // vectors per tile row
+  constexpr int kStride = 64 + V;
+  __shared__ __attribute__((aligned(16))) T tile[64 * kStride];
   const int64_t r0 = (int64_t)blockIdx.x * 64;
-  const int c0 = blockIdx.y * 64, x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  const int c0 = blockIdx.y * 64;
+  typedef typename Vec16<sizeof(T)>::type vec_t;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int64_t r = r0 + y + 4 * k;
-    tile[y + 4 * k][x] = r < rows && c0 + x < cols ? src[r * ld + c0 + x] : from_f32<T>(0.f);
+  for (int i = 0; i < 64 * C / 256; ++i) {
+    const int q = i * 256 + threadIdx.x, r = q / C, c = q % C * V;
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (r0 + r < rows) {
+      const T* p = src + (r0 + r) * ld + c0 + c;
+      if (c0 + c + V <= cols) {
+        v = *reinterpret_cast<const vec_t*>(p);
+      } else {
+        T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (c0 + c + k < cols) e[k] = p[k];
+      }
+    }
+    const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int k = 0; k < V; ++k) tile[(c + k) * kStride + r] = e[k];
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 16; ++k) dst[(int64_t)(c0 + y + 4 * k) * ldd + r0 + x] = tile[x][y + 4 * k];
+  for (int i = 0; i < 64 * C / 256; ++i) {
+    const int q = i * 256 + threadIdx.x, c = q / C, r = q % C * V;
+    *reinterpret_cast<uint4*>(dst + (int64_t)(c0 + c) * ldd + r0 + r) =
+        *reinterpret_cast<const uint4*>(&tile[c * kStride + r]);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -177,6 +216,15 @@ __device__ __forceinline__ void pin(V& v) {
   asm volatile("" : "+v"(v));
 }
 
+// exp(z - ref).  The difference is taken first: folded into one fused
+// multiply-add in base 2 (an operation less per logit) the exponent would be
+// off by 2^-24 of ref, and a probability of 1 among logits of some thousands
+// by parts in a thousand.
+struct LogitExp {
+  float ref;
+  __device__ __forceinline__ float operator()(float z) const { return __builtin_amdgcn_exp2f((z - ref) * kLog2e); }
+};
+
 // Where a lane's values lie in a tile.
 template <int TM, int TN>
 struct LanePlace {
@@ -209,6 +257,7 @@ __device__ __forceinline__ void mask_columns(Acc<T, TM, TN>& acc, int cols) {
 template <typename T, int TM, int TN>
 struct FwdEpilogue {
   using A = Acc<T, TM, TN>;
+  static constexpr int kStores = 0;  // the few there are may be skipped by a wave
   const XentArgs& p;
   const TileRun& run;
   LanePlace<TM, TN> at;
@@ -259,12 +308,12 @@ struct FwdEpilogue {
       m = fmaxf(m, __shfl_xor(m, 32, 64));
       // A part without a finite logit (all columns past the vocabulary, or
       // all -inf) keeps m = -inf and a sum of zeros.
-      const float ref = m == -inf ? 0.f : m;
+      const LogitExp exp_of{m == -inf ? 0.f : m};
       float s = 0.f;
 #pragma unroll
       for (int fn = 0; fn < A::FN; ++fn)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f((acc.v[fm][fn][e] - ref) * kLog2e);
+        for (int e = 0; e < 16; ++e) s += exp_of(acc.v[fm][fn][e]);
       s += __shfl_xor(s, 32, 64);
       if (at.h == 0) p.parts[(int64_t)(2 * tn + (at.wc ? 1 : 0)) * p.n_pad + row] = float2{m, s};
     }
@@ -345,6 +394,9 @@ __device__ __forceinline__ float xent_unscale(const float* gmax) {
 template <typename T, int TM, int TN>
 struct DzEpilogue {
   using A = Acc<T, TM, TN>;
+  // Per 32 x 32 block, every one executed by every wave: 4 of dz^T, and 2 of
+  // 16-bit dz rows or 4 of fp32 ones.
+  static constexpr int kStores = A::FM * A::FN * (sizeof(T) == 2 ? 6 : 8);
   const XentArgs& p;
   const TileRun& run;
   float unit;
@@ -385,30 +437,40 @@ struct DzEpilogue {
     if ((int64_t)(tn + 1) * TN > p.v) mask_columns(acc, cols);
 #pragma unroll
     for (int fm = 0; fm < A::FM; ++fm) {
-      const float c = cur_c[fm] * unit, l = cur_l[fm];
-      const bool none = c == 0.f;
+      const float c = cur_c[fm] * unit;
+      // A row without a gradient is exact zeros, whatever its logits: by a
+      // mask, since a select became a branch around every conversion.
+      const uint32_t keep = c == 0.f ? 0u : ~0u;
+      const LogitExp p_of{cur_l[fm]};
       const int t = cur_t[fm] - p.v0 - col0 - 4 * at.h;
       T* row = dz + (row0 + fm * 32 + at.lr) * p.ldz + col0;
       T* col = dzt + (int64_t)(col0 + 4 * at.h + q) * p.n_pad + row0 + fm * 32 + i4;
+      // Few parts hold a target; only those spend the comparisons.
+      const bool hot = __any(t >= 0 && t < TN / 2);
 #pragma unroll
       for (int fn = 0; fn < A::FN; ++fn) {
         f32x4 v[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = 32 * fn + 8 * g + e;
-            float x = __builtin_amdgcn_exp2f((acc.v[fm][fn][4 * g + e] - l) * kLog2e);
-            x -= t == k ? 1.f : 0.f;
-            // A row without a gradient is exact zeros whatever its logits.
-            x *= c;
-            v[g][e] = none ? 0.f : x;
-          }
+          for (int e = 0; e < 4; ++e) v[g][e] = p_of(acc.v[fm][fn][4 * g + e]);
+        if (hot) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[g][e] -= t == 32 * fn + 8 * g + e ? 1.f : 0.f;
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[g][e] *= c;
         if constexpr (sizeof(T) == 2) {
           uint2 b[4];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             b[g] = pack_quad<T>(v[g]);
+            b[g].x &= keep;
+            b[g].y &= keep;
             *reinterpret_cast<uint2*>(col + (int64_t)(32 * fn + 8 * g) * p.n_pad) = transpose_quad(b[g]);
           }
 #pragma unroll
@@ -417,6 +479,8 @@ struct DzEpilogue {
         } else {
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[g][e] = __uint_as_float(__float_as_uint(v[g][e]) & keep);
             *reinterpret_cast<f32x4*>(row + 32 * fn + 8 * g + 4 * at.h) = v[g];
             *reinterpret_cast<f32x4*>(col + (int64_t)(32 * fn + 8 * g) * p.n_pad) = transpose_quad(v[g]);
           }
@@ -447,6 +511,7 @@ struct XentDwArgs {
 template <typename T, int TM, int TN>
 struct DwEpilogue {
   using A = Acc<T, TM, TN>;
+  static constexpr int kStores = 0;  // rows and columns past the result store nothing
   const XentDwArgs& p;
   const TileRun& run;
   float scale;
@@ -529,6 +594,7 @@ struct XentDhArgs {
 template <typename T, int TM, int TN>
 struct DhEpilogue {
   using A = Acc<T, TM, TN>;
+  static constexpr int kStores = A::FM * A::FN * 4;
   const XentDhArgs& p;
   const TileRun& run;
   int per;
@@ -540,6 +606,24 @@ struct DhEpilogue {
     grouped_tile(run.at(j) % per, p.tiles_m, p.tiles_n, tm, tn);
     float* out = p.acc + ((int64_t)(run.at(j) / per) * p.n_pad + (int64_t)tm * TM + at.wr + at.lr) * p.d_pad +
                  tn * TN + at.wc + 4 * at.h;
+    if (!p.first) {
+      // The loads of a block row go together.
+#pragma unroll
+      for (int fm = 0; fm < A::FM; ++fm) {
+        f32x4 old[A::FN][4];
+#pragma unroll
+        for (int fn = 0; fn < A::FN; ++fn)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            old[fn][g] = *reinterpret_cast<const f32x4*>(out + (int64_t)fm * 32 * p.d_pad + fn * 32 + 8 * g);
+#pragma unroll
+        for (int fn = 0; fn < A::FN; ++fn)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc.v[fm][fn][4 * g + e] += old[fn][g][e];
+      }
+    }
 #pragma unroll
     for (int fm = 0; fm < A::FM; ++fm)
 #pragma unroll
@@ -547,11 +631,7 @@ struct DhEpilogue {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           f32x4* dst = reinterpret_cast<f32x4*>(out + (int64_t)fm * 32 * p.d_pad + fn * 32 + 8 * g);
-          f32x4 v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc.v[fm][fn][4 * g + e];
-          if (!p.first) v += *dst;
-          *dst = v;
+          *dst = f32x4{acc.v[fm][fn][4 * g], acc.v[fm][fn][4 * g + 1], acc.v[fm][fn][4 * g + 2], acc.v[fm][fn][4 * g + 3]};
         }
   }
 };
