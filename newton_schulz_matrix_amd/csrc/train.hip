@@ -223,8 +223,13 @@ void embed_sum(const EmbedSumArgs& a, hipStream_t st) {
 constexpr int64_t kMaxXentRows = 1 << 23, kMaxXentVocab = 1 << 23, kMaxXentCols = 1 << 20;
 // Elements of one piece of dz at most (16-bit: 512 MiB in each orientation).
 constexpr int64_t kXentPieceElems = int64_t(1) << 28;
-// Forward with at most this many rows takes the short, wide tiles (16-bit).
-constexpr int64_t kXentFewRows = kXentFewM;
+// Forward: up to kXentDotRows rows go without tiles (128000 x 4096 bf16: one
+// row 202 us against 226 with tiles, eight 279 against 231), up to
+// kXentDotRowsStaged where tiles would need staging copies of the operands,
+// which cost more than the product; up to kXentFewRows take the short, wide
+// tiles (16-bit) and are joined by a block per row.
+constexpr int64_t kXentDotRows = 4, kXentDotRowsStaged = 8, kXentFewRows = kXentFewM;
+constexpr int64_t kXentDotWaves = 4096;  // sixteen per compute unit
 
 // Estimated time of a product in us: rounds of tiles over the compute units,
 // each of so many us per k-tile and a fixed part, as measured on MI355X with
@@ -247,6 +252,7 @@ struct XentPlan {
   int64_t n_pad = 0, tiles_m = 0;  // rows of the first product
   int64_t tm = 0, tn = 0;
   int64_t tiles_n = 0;             // forward: vocabulary tiles
+  int64_t groups = 0, waves = 0;   // forward without tiles
   int64_t d_pad = 0, piece = 0;    // backward
   int splits = 1;
   // Buffers.
@@ -305,6 +311,15 @@ XentPlan xent_plan(int64_t n, int64_t d, int64_t v, ns_dtype dtype, bool aligned
   p.stage = p.k != d || !aligned;
   const EdgeCost* costs = p.es == 2 ? kXentCost16 : kXentCost32;
   Carver c{reinterpret_cast<char*>(ws)};
+  if (!backward && n <= (p.stage ? kXentDotRowsStaged : kXentDotRows)) {
+    p.groups = (v + kDotRows - 1) / kDotRows;
+    const int64_t each = (p.groups + kXentDotWaves - 1) / kXentDotWaves;
+    p.waves = (p.groups + each - 1) / each;
+    p.zt = c.take<float>(n);
+    p.parts = c.take<float2>(n * p.waves);
+    p.total = c.used;
+    return p;
+  }
   if (!backward) {
     if (p.es == 2 && n <= kXentFewRows) {
       p.tm = kXentFewM;
@@ -364,8 +379,26 @@ void xent_pad(const XentPlan& p, const void* src, int64_t ld, int64_t rows, char
 }
 
 template <typename T>
-ns_status xent_forward(const XentPlan& p, const void* H, int64_t ldh, const void* W, int64_t ldw, XentRowArgs rows,
-                       float* loss, float* lse, int32_t* d_status, hipStream_t st) {
+ns_status xent_forward(const XentPlan& p, const void* H, int64_t ldh, const void* W, int64_t ldw,
+                       const XentTargets& targets, float* loss, float* lse, int32_t* d_status, hipStream_t st) {
+  XentJoinArgs j{p.parts, 0,       p.n, 0,   0,        p.zt,
+                 targets, loss, lse, d_status, (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT),
+                 (int32_t)NS_STATUS_BAD_INDEX};
+  if (p.waves) {
+    const XentDotArgs a{H, W, ldh, ldw, p.n, p.v, (int)p.d, (int)p.waves, (int)p.groups, targets, p.parts, p.zt};
+    const hipError_t e = launch_xent_dot<T>(a, st);
+    if (e != hipSuccess) return NS_ERR_HIP;
+    j.count = (int)p.waves;
+    j.part_stride = 1;
+    j.row_stride = p.waves;
+    hipLaunchKernelGGL(k_xent_join_row, dim3((unsigned)p.n), dim3(1024), 0, st, j);
+    return launched();
+  }
+  XentRowArgs rows{};
+  rows.targets = targets;
+  rows.n = p.n;
+  rows.n_pad = p.n_pad;
+  rows.tgt = p.tgt;
   hipLaunchKernelGGL(k_xent_rows, dim3((unsigned)((p.n_pad + 255) / 256)), dim3(256), 0, st, rows);
   XentArgs a{};
   a.H = H;
@@ -391,9 +424,13 @@ ns_status xent_forward(const XentPlan& p, const void* H, int64_t ldh, const void
   a.zt = p.zt;
   const hipError_t e = launch_xent_fwd<T>(a, (int)p.tm, st, (int)p.tn);
   if (e != hipSuccess) return NS_ERR_HIP;
-  const XentJoinArgs j{p.parts, (int)(2 * p.tiles_n), p.n, p.n_pad, p.zt, p.tgt, loss, lse, d_status,
-                       (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT)};
-  hipLaunchKernelGGL(k_xent_join, dim3((unsigned)(p.n_pad / 16)), dim3(1024), 0, st, j);
+  j.count = (int)(2 * p.tiles_n);
+  j.part_stride = p.n_pad;
+  j.row_stride = 1;
+  if (p.n <= kXentFewRows)
+    hipLaunchKernelGGL(k_xent_join_row, dim3((unsigned)p.n), dim3(1024), 0, st, j);
+  else
+    hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((p.n + 15) / 16)), dim3(1024), 0, st, j);
   return launched();
 }
 
@@ -624,18 +661,9 @@ ns_status ns_linear_cross_entropy(const void* H, int64_t ldh, const void* W, int
   if (!H || !W || !targets || !loss || !lse) return NS_ERR_INVALID_ARG;
   const XentPlan p = xent_plan(rows, cols, vocab, dtype, xent_aligned(H, ldh, W, ldw, dtype), false, workspace);
   if (!workspace_ok(workspace, workspace_bytes, p.total)) return NS_ERR_WORKSPACE;
-  XentRowArgs r{};
-  r.targets = targets;
-  r.targets64 = targets64;
-  r.ignore_index = ignore_index;
-  r.n = rows;
-  r.n_pad = p.n_pad;
-  r.vocab = vocab;
-  r.tgt = p.tgt;
-  r.d_status = d_status;
-  r.index_bit = (int32_t)NS_STATUS_BAD_INDEX;
+  const XentTargets t{targets, targets64, ignore_index, vocab};
   return with_type(dtype, [&](auto io) {
-    return xent_forward<decltype(io)>(p, H, ldh, W, ldw, r, loss, lse, d_status, reinterpret_cast<hipStream_t>(stream));
+    return xent_forward<decltype(io)>(p, H, ldh, W, ldw, t, loss, lse, d_status, reinterpret_cast<hipStream_t>(stream));
   });
 }
 
@@ -664,12 +692,9 @@ ns_status ns_linear_cross_entropy_backward(const void* H, int64_t ldh, const voi
   if (!workspace_ok(workspace, workspace_bytes, p.total)) return NS_ERR_WORKSPACE;
   if (!dH && !dW) return NS_OK;
   XentRowArgs r{};
-  r.targets = targets;
-  r.targets64 = targets64;
-  r.ignore_index = ignore_index;
+  r.targets = XentTargets{targets, targets64, ignore_index, vocab};
   r.n = rows;
   r.n_pad = p.n_pad;
-  r.vocab = vocab;
   r.tgt = p.tgt;
   r.dloss = dloss;
   r.lse = lse;

@@ -39,11 +39,21 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kTargetNone = -1;  // ignored (or a padding row)
 constexpr int kTargetBad = -2;   // outside the vocabulary
 
+// Row i's target: an id, kTargetNone or kTargetBad.
+struct XentTargets {
+  const void* ids;
+  int ids64;
+  int64_t ignore_index, vocab;
+  __device__ __forceinline__ int at(int64_t i) const {
+    const int64_t id = ids64 ? reinterpret_cast<const int64_t*>(ids)[i]
+                             : (int64_t) reinterpret_cast<const int32_t*>(ids)[i];
+    return id == ignore_index ? kTargetNone : id >= 0 && id < vocab ? (int)id : kTargetBad;
+  }
+};
+
 struct XentRowArgs {
-  const void* targets;
-  int targets64;
-  int64_t ignore_index;
-  int64_t n, n_pad, vocab;
+  XentTargets targets;
+  int64_t n, n_pad;
   int32_t* tgt;        // n_pad
   const float* dloss;  // n, or null (forward)
   const float* lse;    // n (backward)
@@ -63,12 +73,7 @@ __global__ void __launch_bounds__(256) k_xent_zero(T* dst, int64_t ld, int cols)
 
 static __global__ void __launch_bounds__(256) k_xent_rows(XentRowArgs p) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  int t = kTargetNone;
-  if (i < p.n) {
-    const int64_t id = p.targets64 ? reinterpret_cast<const int64_t*>(p.targets)[i]
-                                   : (int64_t) reinterpret_cast<const int32_t*>(p.targets)[i];
-    t = id == p.ignore_index ? kTargetNone : id >= 0 && id < p.vocab ? (int)id : kTargetBad;
-  }
+  const int t = i < p.n ? p.targets.at(i) : kTargetNone;
   if (i < p.n_pad) p.tgt[i] = t;
   if (p.coef) {
     const float g = t >= 0 ? p.dloss[i] : 0.f;
@@ -326,44 +331,171 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent_fwd(XentArgs p) {
   xent_logits<T, TM, TN>(p, run, FwdEpilogue<T, TM, TN>{p, run});
 }
 
-// Joins the parts of each row: 16 rows per block, 64 threads each.
+// Joins the parts of each row.
 struct XentJoinArgs {
   const float2* parts;
   int count;
-  int64_t n, n_pad;
+  int64_t n, part_stride, row_stride;  // part i of row r: parts[i part_stride + r row_stride]
   const float* zt;
-  const int32_t* tgt;
+  XentTargets targets;
   float *loss, *lse;
   int32_t* d_status;
-  int32_t status_bits;
+  int32_t status_bits, index_bit;
 };
 
+struct PartJoin {
+  float m = -__builtin_inff(), s = 0.f;
+  __device__ __forceinline__ void add(float om, float os) {
+    const float t = fmaxf(m, om);
+    if (t == -__builtin_inff()) {  // both empty: zeros, or a NaN to keep
+      s += os;
+      return;
+    }
+    s = s * __builtin_amdgcn_exp2f((m - t) * kLog2e) + os * __builtin_amdgcn_exp2f((om - t) * kLog2e);
+    m = t;
+  }
+  __device__ __forceinline__ void finish(const XentJoinArgs& p, int64_t row) const {
+    const float lse = m + kLn2 * __builtin_amdgcn_logf(s);
+    const int t = p.targets.at(row);
+    p.lse[row] = lse;
+    p.loss[row] = t >= 0 ? lse - p.zt[row] : t == kTargetBad ? __builtin_nanf("") : 0.f;
+    if (p.d_status) {
+      if (!(fabsf(lse) < __builtin_inff())) atomicOr(p.d_status, p.status_bits);
+      if (t == kTargetBad) atomicOr(p.d_status, p.index_bit);
+    }
+  }
+};
+
+// Many rows: 16 per block, 64 threads each.
 static __global__ void __launch_bounds__(1024) k_xent_join(XentJoinArgs p) {
   __shared__ float2 sh[64][17];
   const int r = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int64_t row = (int64_t)blockIdx.x * 16 + r;  // below n_pad, which is a multiple of 16
-  const float inf = __builtin_inff();
-  float m = -inf, s = 0.f;
-  auto join = [&](float2 o) {
-    const float t = fmaxf(m, o.x);
-    if (t == -inf) {  // both empty: zeros, or a NaN to keep
-      s += o.y;
-      return;
-    }
-    s = s * __builtin_amdgcn_exp2f((m - t) * kLog2e) + o.y * __builtin_amdgcn_exp2f((o.x - t) * kLog2e);
-    m = t;
-  };
+  const int64_t row = (int64_t)blockIdx.x * 16 + r;
+  PartJoin j;
+  if (row < p.n) {
 #pragma unroll 4
-  for (int i = g; i < p.count; i += 64) join(p.parts[(int64_t)i * p.n_pad + row]);
-  sh[g][r] = float2{m, s};
+    for (int i = g; i < p.count; i += 64) {
+      const float2 o = p.parts[(int64_t)i * p.part_stride + row * p.row_stride];
+      j.add(o.x, o.y);
+    }
+  }
+  sh[g][r] = float2{j.m, j.s};
   __syncthreads();
   if (g == 0 && row < p.n) {
-    for (int i = 1; i < 64; ++i) join(sh[i][r]);
-    const float lse = m + kLn2 * __builtin_amdgcn_logf(s);
-    const int t = p.tgt[row];
-    p.lse[row] = lse;
-    p.loss[row] = t >= 0 ? lse - p.zt[row] : t == kTargetBad ? __builtin_nanf("") : 0.f;
-    if (p.d_status && !(fabsf(lse) < inf)) atomicOr(p.d_status, p.status_bits);
+    for (int i = 1; i < 64; ++i) j.add(sh[i][r].x, sh[i][r].y);
+    j.finish(p, row);
+  }
+}
+
+// Few rows: a block each.
+static __global__ void __launch_bounds__(1024) k_xent_join_row(XentJoinArgs p) {
+  __shared__ float2 sh[16];
+  const int64_t row = blockIdx.x;
+  PartJoin j;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < p.count; i += 1024) {
+    const float2 o = p.parts[(int64_t)i * p.part_stride + row * p.row_stride];
+    j.add(o.x, o.y);
+  }
+  for (int off = 32; off > 0; off >>= 1) {
+    const float om = __shfl_xor(j.m, off, 64), os = __shfl_xor(j.s, off, 64);
+    j.add(om, os);
+  }
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = float2{j.m, j.s};
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 16; ++i) j.add(sh[i].x, sh[i].y);
+    j.finish(p, row);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Forward for a few rows (one token, or one per sequence): bound by reading W
+// once, so no tiles: a wave takes R rows of W at a time, whole and in
+// vectors at any alignment (no staging copies), the rows of H coming from the
+// cache, and keeps each row's running maximum and sum until its last W row.
+// One row against 128000 x 4096 bf16 takes 202 us, 5.2 TB/s, the rate of a
+// large copy; in 128-byte columns of 256 rows, as the tiles read it, W comes
+// at 4.6 TB/s.
+// ---------------------------------------------------------------------------
+constexpr int kDotRows = 8;  // R
+struct XentDotArgs {
+  const void *H, *W;
+  int64_t ldh, ldw, n, v;  // elements
+  int cols;
+  int waves, groups;       // groups of R rows, dealt to the waves in turn
+  XentTargets targets;
+  float2* parts;           // [n][waves]
+  float* zt;               // [n]
+};
+
+template <typename T, int N, int FORM>
+__global__ void __launch_bounds__(256) k_xent_dot(XentDotArgs p) {
+  constexpr int V = kVec<T>, R = kDotRows;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (wave >= p.waves) return;
+  const T* H = reinterpret_cast<const T*>(p.H);
+  const T* W = reinterpret_cast<const T*>(p.W);
+  PartJoin run[N];
+  int tgt[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) tgt[i] = i < p.n ? p.targets.at(i) : kTargetNone;
+  for (int g = wave; g < p.groups; g += p.waves) {
+    const int64_t v0 = (int64_t)g * R;
+    const T* w[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[r] = W + (v0 + r < p.v ? v0 + r : p.v - 1) * p.ldw;
+    float acc[R][N];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[r][i] = 0.f;
+    u32x4_t raw[R], next[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) raw[r] = issue16<FORM, T>(w[r], lane * V, p.cols);
+    for (int c0 = 0; c0 < p.cols; c0 += 64 * V) {
+      const int c = c0 + lane * V, cn = c0 + 64 * V < p.cols ? c + 64 * V : c;
+#pragma unroll
+      for (int r = 0; r < R; ++r) next[r] = issue16<FORM, T>(w[r], cn, p.cols);
+      float h[N][V];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const T* row = H + (i < p.n ? i : 0) * p.ldh;
+        unpack<T>(settle16<FORM, T>(issue16<FORM, T>(row, c, p.cols), row, c, p.cols), h[i]);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float x[V];
+        unpack<T>(settle16<FORM, T>(raw[r], w[r], c, p.cols), x);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int k = 0; k < V; ++k) acc[r][i] = fmaf(x[k], h[i][k], acc[r][i]);
+        raw[r] = next[r];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float m = -__builtin_inff();
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        acc[r][i] = wave_row_sum<64>(acc[r][i]);
+        if (v0 + r >= p.v) acc[r][i] = -__builtin_inff();
+        if (lane == 0 && tgt[i] == v0 + r) p.zt[i] = acc[r][i];
+        m = fmaxf(m, acc[r][i]);
+      }
+      const LogitExp exp_of{m == -__builtin_inff() ? 0.f : m};
+      float s = 0.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) s += exp_of(acc[r][i]);
+      run[i].add(m, s);
+    }
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < p.n) p.parts[(int64_t)i * p.waves + wave] = float2{run[i].m, run[i].s};
   }
 }
 
@@ -691,6 +823,7 @@ constexpr int kXentFewM = 128, kXentFewN = 256;
 constexpr int kXentGroups = 256;  // one work-group per compute unit
 
 template <typename T> hipError_t launch_xent_fwd(const XentArgs& a, int tm, hipStream_t s, int tn);
+template <typename T> hipError_t launch_xent_dot(const XentDotArgs& a, hipStream_t s);
 template <typename T> hipError_t launch_xent_dz(const XentArgs& a, int edge, hipStream_t s);
 template <typename T> hipError_t launch_xent_dw(const XentDwArgs& a, int edge, hipStream_t s);
 template <typename T> hipError_t launch_xent_dh(const XentDhArgs& a, int edge, hipStream_t s);
@@ -704,6 +837,19 @@ hipError_t launch_edge(int edge, Large&& large, Small&& small) {
   return hipGetLastError();
 }
 inline dim3 xent_grid(int64_t tiles) { return dim3((unsigned)(tiles < kXentGroups ? tiles : kXentGroups)); }
+
+template <typename T, int FORM>
+void launch_dot(const XentDotArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.waves + 3) / 4));
+  if (a.n <= 1)
+    hipLaunchKernelGGL((k_xent_dot<T, 1, FORM>), grid, dim3(256), 0, s, a);
+  else if (a.n <= 2)
+    hipLaunchKernelGGL((k_xent_dot<T, 2, FORM>), grid, dim3(256), 0, s, a);
+  else if (a.n <= 4)
+    hipLaunchKernelGGL((k_xent_dot<T, 4, FORM>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_xent_dot<T, 8, FORM>), grid, dim3(256), 0, s, a);
+}
 
 #define NS_XENT_LAUNCHERS(T)                                                                                        \
   template <>                                                                                                       \
@@ -719,6 +865,16 @@ inline dim3 xent_grid(int64_t tiles) { return dim3((unsigned)(tiles < kXentGroup
     return launch_edge<T>(                                                                                          \
         tm, [&] { hipLaunchKernelGGL((k_xent_fwd<T, L, L>), grid, dim3(kThreads), 0, s, a); },                      \
         [&] { hipLaunchKernelGGL((k_xent_fwd<T, S, S>), grid, dim3(kThreads), 0, s, a); });                         \
+  }                                                                                                                 \
+  template <>                                                                                                       \
+  hipError_t launch_xent_dot<T>(const XentDotArgs& a, hipStream_t s) {                                              \
+    if (a.cols % kVec<T> == 0)                                                                                      \
+      launch_dot<T, kEven>(a, s);                                                                                   \
+    else if (a.cols > kVec<T>)                                                                                      \
+      launch_dot<T, kRagged>(a, s);                                                                                 \
+    else                                                                                                            \
+      launch_dot<T, kTiny>(a, s);                                                                                   \
+    return hipGetLastError();                                                                                       \
   }                                                                                                                 \
   template <>                                                                                                       \
   hipError_t launch_xent_dz<T>(const XentArgs& a, int edge, hipStream_t s) {                                        \

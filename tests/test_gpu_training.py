@@ -380,7 +380,7 @@ def _check_xent(n, d, v, dtype, dev, h, w, t, dloss, ignore_index=-100, dw_rows=
     return loss, lse, dh, dw
 
 
-XENT_SHAPES = [(1, 1, 1), (1, 64, 1000), (2, 128, 191), (17, 100, 193), (64, 64, 500), (128, 256, 385), (129, 192, 700),
+XENT_SHAPES = [(1, 1, 1), (1, 64, 1000), (1, 4096, 70), (1, 7, 40000), (2, 128, 191), (3, 5, 9), (5, 1001, 77), (8, 96, 1000), (9, 100, 600), (17, 100, 193), (64, 64, 500), (128, 256, 385), (129, 192, 700),
                (200, 1000, 777), (385, 320, 1153), (700, 64, 64)]
 
 

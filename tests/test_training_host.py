@@ -194,8 +194,8 @@ def test_cross_entropy_refusals():
     assert _xent(vocab=(1 << 23) + 1) == INV and _xent(dtype=5) == DT
     assert _xent(ws=None) == WSP and _xent(ws=64) == WSP and _xent(nb=16) == WSP
     # A misaligned operand needs the copies' workspace too.
-    need = nsa.linear_cross_entropy_workspace_size(4, 64, 10, aligned=True)
-    assert _xent(H=PTR + 2, nb=need) == WSP
+    need = nsa.linear_cross_entropy_workspace_size(40, 64, 10, aligned=True)
+    assert _xent(rows=40, H=PTR + 2, nb=need) == WSP
     assert _xent(rows=0, H=None, W=None, t=None, loss=None, lse=None, ws=None, nb=0) == 0
 
 
