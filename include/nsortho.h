@@ -428,7 +428,7 @@ ns_status ns_layer_norm_backward(const void* dY, int64_t lddy, const void* X,
  *            outside [0, vocab) reads nothing: its row of out is zero and
  *            NS_STATUS_BAD_INDEX is set.
  *   table    vocab x cols, row stride ldt; out n x cols, row stride ldo.
- *   n < 2^31, 1 <= vocab <= 2^28, 1 <= cols <= 2^24; scale finite.
+ *   n <= 2^30, 1 <= vocab <= 2^28, 1 <= cols <= 2^24; scale finite.
  */
 ns_status ns_embedding(const void* ids, int32_t ids64, int64_t n,
                        const void* table, int64_t vocab, int64_t cols,
@@ -467,7 +467,8 @@ ns_status ns_embedding_backward(const void* ids, int32_t ids64, int64_t n,
  *            NS_STATUS_BAD_INDEX.
  *   loss, lse   rows floats each.  A row of logits that holds a NaN or
  *            +Inf gives NaN; -Inf logits count as probability 0.
- *   rows, vocab <= 2^23, cols <= 2^20, ldh and ldw <= 2^23.
+ *   rows, vocab <= 2^23, rows * vocab <= 2^42, cols <= 2^20, ldh and
+ *            ldw <= 2^23.
  *   workspace   ns_linear_cross_entropy_workspace_size(rows, cols, vocab,
  *            dtype, aligned, 0) bytes, 256-byte aligned; aligned is 1 when H
  *            and W start on 16-byte boundaries and their row strides are

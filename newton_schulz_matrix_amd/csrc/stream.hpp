@@ -214,6 +214,8 @@ __device__ __forceinline__ void stream_tiles(int count, int64_t ldl, int64_t ldr
     epi.load(more ? j + 1 : j);
     border_first<T, TM, TN>(la, lb, advance(), S::s2(), S::s0(), fa, fs, acc.v);
     epi.store(j, acc);
+    // The waits after this count on the stores being issued by now.
+    asm volatile("" ::: "memory");
     if (!more) break;
     acc_zero(acc);
     border_second<T, TM, TN, kStores>(S::s0(), fa, fs, acc.v);

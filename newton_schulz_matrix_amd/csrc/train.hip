@@ -149,7 +149,7 @@ bool norm_shape_ok(int64_t rows, int64_t cols) {
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxEmbedRows = int64_t(1) << 28;
 constexpr int64_t kMaxEmbedCols = 1 << 24;
-constexpr int64_t kMaxEmbedIds = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxEmbedIds = int64_t(1) << 30;
 
 bool embed_shape_ok(int64_t n, int64_t vocab, int64_t cols) {
   return n >= 0 && n <= kMaxEmbedIds && vocab >= 1 && vocab <= kMaxEmbedRows && cols >= 1 && cols <= kMaxEmbedCols;
@@ -223,12 +223,14 @@ void embed_sum(const EmbedSumArgs& a, hipStream_t st) {
 constexpr int64_t kMaxXentRows = 1 << 23, kMaxXentVocab = 1 << 23, kMaxXentCols = 1 << 20;
 // Elements of one piece of dz at most (16-bit: 512 MiB in each orientation).
 constexpr int64_t kXentPieceElems = int64_t(1) << 28;
+// Logits of one call at most: tiles are counted in 32 bits.
+constexpr int64_t kMaxXentLogits = int64_t(1) << 42;
 // Forward: up to kXentDotRows rows go without tiles (128000 x 4096 bf16: one
 // row 202 us against 226 with tiles, eight 279 against 231), up to
 // kXentDotRowsStaged where tiles would need staging copies of the operands,
 // which cost more than the product; up to kXentFewRows take the short, wide
-// tiles (16-bit) and are joined by a block per row.
-constexpr int64_t kXentDotRows = 4, kXentDotRowsStaged = 8, kXentFewRows = kXentFewM;
+// tiles (16-bit).  Up to kXentJoinRows rows are joined by a block each.
+constexpr int64_t kXentDotRows = 4, kXentDotRowsStaged = 8, kXentFewRows = kXentFewM, kXentJoinRows = 1024;
 constexpr int64_t kXentDotWaves = 4096;  // sixteen per compute unit
 
 // Estimated time of a product in us: rounds of tiles over the compute units,
@@ -265,7 +267,8 @@ struct XentPlan {
 };
 
 bool xent_shape_ok(int64_t n, int64_t d, int64_t v) {
-  return n >= 0 && n <= kMaxXentRows && d >= 1 && d <= kMaxXentCols && v >= 1 && v <= kMaxXentVocab;
+  return n >= 0 && n <= kMaxXentRows && d >= 1 && d <= kMaxXentCols && v >= 1 && v <= kMaxXentVocab &&
+         n <= kMaxXentLogits / v;
 }
 
 // The backward pass's piece of the vocabulary (in tiles) and dH's splits for
@@ -427,7 +430,7 @@ ns_status xent_forward(const XentPlan& p, const void* H, int64_t ldh, const void
   j.count = (int)(2 * p.tiles_n);
   j.part_stride = p.n_pad;
   j.row_stride = 1;
-  if (p.n <= kXentFewRows)
+  if (p.n <= kXentJoinRows)
     hipLaunchKernelGGL(k_xent_join_row, dim3((unsigned)p.n), dim3(1024), 0, st, j);
   else
     hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((p.n + 15) / 16)), dim3(1024), 0, st, j);
