@@ -428,7 +428,7 @@ ns_status ns_layer_norm_backward(const void* dY, int64_t lddy, const void* X,
  *            outside [0, vocab) reads nothing: its row of out is zero and
  *            NS_STATUS_BAD_INDEX is set.
  *   table    vocab x cols, row stride ldt; out n x cols, row stride ldo.
- *   n <= 2^30, 1 <= vocab <= 2^28, 1 <= cols <= 2^24; scale finite.
+ *   n <= 2^30, 1 <= vocab <= 2^28, 1 <= cols <= 2^23; scale finite.
  */
 ns_status ns_embedding(const void* ids, int32_t ids64, int64_t n,
                        const void* table, int64_t vocab, int64_t cols,

@@ -361,46 +361,44 @@ __global__ void __launch_bounds__(64) k_embed_sum(EmbedSumArgs p) {
 }
 
 // Chunk c's wave joins the list that leaves c if it did not enter it: the
-// leaving piece, then the entering pieces of the chunks it goes through.
-template <typename IO, int U, int FORM>
+// leaving piece, then the entering pieces of the chunks it goes through.  One
+// vector of columns per lane and sixteen pieces in flight: the longest list's
+// latency is what this kernel takes (eight waves per list, joined in LDS, cost
+// more in idle blocks than they saved).
+template <typename IO, int FORM>
 __global__ void __launch_bounds__(64) k_embed_join(EmbedSumArgs p) {
-  constexpr int V = kVec<IO>;
+  constexpr int V = kVec<IO>, B = 16;
   const int total = p.start[p.vocab];
   const int64_t s = (int64_t)blockIdx.x * p.chunk, e = s + p.chunk;
   if (e >= total) return;
   const int id = p.key[e];
   if (p.key[e - 1] != id || (s > 0 && p.key[s - 1] == id)) return;
-  const int c0 = (blockIdx.y * U * 64 + threadIdx.x) * V;
+  const int c0 = (blockIdx.y * 64 + threadIdx.x) * V;
   const int last = (p.start[id + 1] - 1) / p.chunk;
-  float acc[U][V];
-  zero_acc<U, V>(acc);
-  // Pieces last .. blockIdx.x + 1 have their entering rows at even places;
-  // this chunk's leaving row comes first.
+  float acc[1][V];
+  zero_acc<1, V>(acc);
+  // Pieces 1 .. have their entering rows at even places; piece 0 is this
+  // chunk's leaving row.
   const float* first = p.partial + ((int64_t)blockIdx.x * 2 + 1) * p.cols_pad + c0;
-  const int pieces = last - (int)blockIdx.x;
-  constexpr int B = 4;
-  for (int j = 0; j <= pieces; j += B) {
-    f32x4 raw[B][U][V / 4];
+  const int pieces = last - (int)blockIdx.x + 1;
+  for (int j = 0; j < pieces; j += B) {
+    f32x4 raw[B][V / 4];
 #pragma unroll
     for (int q = 0; q < B; ++q) {
-      const int i = j + q <= pieces ? j + q : pieces;
+      const int i = j + q < pieces ? j + q : pieces - 1;
       const float* part = i == 0 ? first : first + (2 * (int64_t)i - 1) * p.cols_pad;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int k = 0; k < V / 4; ++k) raw[q][u][k] = *reinterpret_cast<const f32x4*>(part + u * 64 * V + 4 * k);
+      for (int k = 0; k < V / 4; ++k) raw[q][k] = *reinterpret_cast<const f32x4*>(part + 4 * k);
     }
 #pragma unroll
     for (int q = 0; q < B; ++q) {
-      if (j + q <= pieces) {
+      if (j + q < pieces) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int k = 0; k < V; ++k) acc[u][k] += raw[q][u][k / 4][k % 4];
+        for (int k = 0; k < V; ++k) acc[0][k] += raw[q][k / 4][k % 4];
       }
     }
   }
-  const bool bad = embed_finish<IO, U, FORM>(p, id, c0, acc);
+  const bool bad = embed_finish<IO, 1, FORM>(p, id, c0, acc);
   if (p.d_status) report_status(p.d_status, p.status_bits, bad);
 }
 

@@ -148,7 +148,7 @@ bool norm_shape_ok(int64_t rows, int64_t cols) {
 // Embedding.
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxEmbedRows = int64_t(1) << 28;
-constexpr int64_t kMaxEmbedCols = 1 << 24;
+constexpr int64_t kMaxEmbedCols = 1 << 23;
 constexpr int64_t kMaxEmbedIds = int64_t(1) << 30;
 
 bool embed_shape_ok(int64_t n, int64_t vocab, int64_t cols) {
@@ -164,11 +164,11 @@ int embed_ids_per_block(int64_t vocab) {
 }
 
 // Positions per chunk.  A wave adds up `chunk` rows, and the longest list,
-// some twentieth of a text's positions, joins n / (20 chunk) pieces: the two
-// are balanced at the square root.
+// some twentieth of a text's positions, joins n / (20 chunk) pieces with four
+// times as many in flight: balanced at chunk = sqrt(n / 160).
 int embed_chunk(int64_t n) {
   int c = 8;
-  while ((int64_t)c * c * 40 < n) c *= 2;
+  while ((int64_t)c * c * 160 < n) c *= 2;
   return c;
 }
 
@@ -214,7 +214,8 @@ void embed_sum(const EmbedSumArgs& a, hipStream_t st) {
   const int64_t zeros = a.accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
   if (a.chunks + zeros > 0)
     hipLaunchKernelGGL((k_embed_sum<IO, U, B, FORM>), dim3((unsigned)(a.chunks + zeros), slices), dim3(64), 0, st, a);
-  if (a.chunks > 1) hipLaunchKernelGGL((k_embed_join<IO, U, FORM>), dim3((unsigned)a.chunks, slices), dim3(64), 0, st, a);
+  if (a.chunks > 1)
+    hipLaunchKernelGGL((k_embed_join<IO, FORM>), dim3((unsigned)a.chunks, slices * U), dim3(64), 0, st, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -236,12 +237,15 @@ constexpr int64_t kXentDotWaves = 4096;  // sixteen per compute unit
 // Estimated time of a product in us: rounds of tiles over the compute units,
 // each of so many us per k-tile and a fixed part, as measured on MI355X with
 // random operands.
+// (Two or three of the smallest float tiles on a compute unit, with stages of
+// 16 KB, gained 5 to 10 % where tiles filled them evenly and lost up to 30 %
+// where they did not: 300 x 1000 x 8191 took 76 and 56 us against 59.)
 struct EdgeCost {
   int edge;
   double ktile, fixed;
 };
-constexpr EdgeCost kXentCost16[2] = {{kXentLarge<_Float16>, 0.95, 3.0}, {kXentSmall<_Float16>, 0.52, 2.0}};
-constexpr EdgeCost kXentCost32[2] = {{kXentLarge<float>, 1.85, 2.5}, {kXentSmall<float>, 0.55, 1.5}};
+constexpr EdgeCost kXentCost16[2] = {{kXentLarge<_Float16>, 0.90, 3.0}, {kXentSmall<_Float16>, 0.52, 2.0}};
+constexpr EdgeCost kXentCost32[2] = {{kXentLarge<float>, 2.10, 2.5}, {kXentSmall<float>, 0.53, 1.5}};
 double product_us(const EdgeCost& c, int64_t tiles, double ktiles) {
   return (double)((tiles + kXentGroups - 1) / kXentGroups) * (ktiles * c.ktile + c.fixed);
 }
@@ -261,7 +265,8 @@ struct XentPlan {
   int32_t* tgt = nullptr;
   char *Hs = nullptr, *Ws = nullptr;
   float2* parts = nullptr;
-  float *zt = nullptr, *coef = nullptr, *lse = nullptr, *gmax = nullptr, *acc = nullptr;
+  float *zt = nullptr, *coef = nullptr, *lse = nullptr, *gmax = nullptr, *gmax_parts = nullptr,
+        *acc = nullptr;
   char *dz = nullptr, *dzt = nullptr, *WT = nullptr, *HT = nullptr;
   size_t total = 0;
 };
@@ -357,6 +362,7 @@ XentPlan xent_plan(int64_t n, int64_t d, int64_t v, ns_dtype dtype, bool aligned
     p.coef = c.take<float>(p.n_pad);
     p.lse = c.take<float>(p.n_pad);
     p.gmax = c.take<float>(1);
+    p.gmax_parts = c.take<float>((p.n_pad + 255) / 256);
     p.dz = c.take<char>(p.n_pad * p.piece * p.es);
     p.dzt = c.take<char>(p.n_pad * p.piece * p.es);
     p.WT = c.take<char>(p.d_pad * p.piece * p.es);
@@ -374,11 +380,31 @@ bool xent_aligned(const void* H, int64_t ldh, const void* W, int64_t ldw, ns_dty
   return aligned16(H) && aligned16(W) && ldh * b % kRowBytes == 0 && ldw * b % kRowBytes == 0;
 }
 
+// The copies of one operand (rows x d at src): padded when the products read
+// a staging copy, transposed into dst_t (ldt wide) unless that is null.
+XentCopyArgs xent_copy(const XentPlan& p, const void* src, int64_t ld, int64_t rows, char* padded, char* dst_t,
+                       int64_t rows_pad, int64_t ldt) {
+  XentCopyArgs a{};
+  if (!padded && !dst_t) return a;
+  a.src = src;
+  a.ld = ld;
+  a.rows = rows;
+  a.cols = (int)p.d;
+  a.padded = padded;
+  a.cols_k = (int)p.k;
+  a.transposed = dst_t;
+  a.ldt = ldt;
+  a.tiles_r = (int)((dst_t ? rows_pad : round_to(rows, 64)) / 64);
+  a.tiles_c = (int)((dst_t ? p.d_pad : round_to(p.k, 64)) / 64);
+  return a;
+}
+
 template <typename T>
-void xent_pad(const XentPlan& p, const void* src, int64_t ld, int64_t rows, char* dst, hipStream_t st) {
-  const int64_t blocks = std::min<int64_t>((rows * (p.k / kVec<T>) + 255) / 256, 8192);
-  hipLaunchKernelGGL((k_xent_pad<T>), dim3((unsigned)blocks), dim3(256), 0, st, reinterpret_cast<const T*>(src), ld,
-                     rows, (int)p.d, reinterpret_cast<T*>(dst), (int)p.k);
+ns_status xent_prep(const XentPrepArgs& a, hipStream_t st) {
+  const int64_t blocks = a.row_blocks + a.h.blocks() + a.w.blocks();
+  if (blocks == 0) return NS_OK;
+  hipLaunchKernelGGL((k_xent_prep<T>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+  return launched();
 }
 
 template <typename T>
@@ -397,24 +423,20 @@ ns_status xent_forward(const XentPlan& p, const void* H, int64_t ldh, const void
     hipLaunchKernelGGL(k_xent_join_row, dim3((unsigned)p.n), dim3(1024), 0, st, j);
     return launched();
   }
-  XentRowArgs rows{};
-  rows.targets = targets;
-  rows.n = p.n;
-  rows.n_pad = p.n_pad;
-  rows.tgt = p.tgt;
-  hipLaunchKernelGGL(k_xent_rows, dim3((unsigned)((p.n_pad + 255) / 256)), dim3(256), 0, st, rows);
+  XentPrepArgs prep{};
+  prep.rows.targets = targets;
+  prep.rows.n = p.n;
+  prep.rows.n_pad = p.n_pad;
+  prep.rows.tgt = p.tgt;
+  prep.row_blocks = (int)((p.n_pad + 255) / 256);
+  prep.h = xent_copy(p, H, ldh, p.n, p.Hs, nullptr, 0, 0);
+  prep.w = xent_copy(p, W, ldw, p.v, p.Ws, nullptr, 0, 0);
+  if (xent_prep<T>(prep, st) != NS_OK) return NS_ERR_HIP;
   XentArgs a{};
-  a.H = H;
-  a.W = W;
-  a.ldh = ldh * sizeof(T);
-  a.ldw = ldw * sizeof(T);
-  if (p.stage) {
-    xent_pad<T>(p, H, ldh, p.n, p.Hs, st);
-    xent_pad<T>(p, W, ldw, p.v, p.Ws, st);
-    a.H = p.Hs;
-    a.W = p.Ws;
-    a.ldh = a.ldw = p.k * (int64_t)sizeof(T);
-  }
+  a.H = p.stage ? p.Hs : H;
+  a.W = p.stage ? p.Ws : W;
+  a.ldh = (p.stage ? p.k : ldh) * (int64_t)sizeof(T);
+  a.ldw = (p.stage ? p.k : ldw) * (int64_t)sizeof(T);
   a.row_bytes = (uint32_t)(p.k * sizeof(T));
   a.k = (int)p.k;
   a.n = p.n;
@@ -441,28 +463,22 @@ template <typename T>
 ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const void* W, int64_t ldw, XentRowArgs rows,
                         void* dH, int64_t lddh, void* dW, int64_t lddw, int32_t* d_status, hipStream_t st) {
   const int64_t edge = p.tm;
-  hipLaunchKernelGGL(k_xent_clear, dim3(1), dim3(1), 0, st, p.gmax);
-  hipLaunchKernelGGL(k_xent_rows, dim3((unsigned)((p.n_pad + 255) / 256)), dim3(256), 0, st, rows);
-  const T* h = reinterpret_cast<const T*>(H);
-  if (p.stage) xent_pad<T>(p, H, ldh, p.n, p.Hs, st);
-  if (dW)
-    hipLaunchKernelGGL((k_xent_transpose<T>), dim3((unsigned)(p.n_pad / 64), (unsigned)(p.d_pad / 64)), dim3(256), 0, st,
-                       h, ldh, p.n, (int)p.d, (T*)p.HT, p.n_pad);
-  if (hipGetLastError() != hipSuccess) return NS_ERR_HIP;
+  XentPrepArgs prep{};
+  prep.rows = rows;
+  prep.row_blocks = (int)((p.n_pad + 255) / 256);
+  prep.h = xent_copy(p, H, ldh, p.n, p.Hs, dW ? p.HT : nullptr, p.n_pad, p.n_pad);
   for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
     const int64_t rows_v = std::min(p.piece, p.v - v0), width = round_to(rows_v, edge);
     const T* w = reinterpret_cast<const T*>(W) + v0 * ldw;
+    prep.w = xent_copy(p, w, ldw, rows_v, p.Ws, dH ? p.WT : nullptr, width, p.piece);
+    if (xent_prep<T>(prep, st) != NS_OK) return NS_ERR_HIP;
+    prep.row_blocks = 0;  // H and the rows once, W for every piece
+    prep.h = XentCopyArgs{};
     XentArgs a{};
-    a.H = h;
-    a.W = w;
-    a.ldh = ldh * sizeof(T);
-    a.ldw = ldw * sizeof(T);
-    if (p.stage) {
-      xent_pad<T>(p, w, ldw, rows_v, p.Ws, st);
-      a.H = p.Hs;
-      a.W = p.Ws;
-      a.ldh = a.ldw = p.k * (int64_t)sizeof(T);
-    }
+    a.H = p.stage ? p.Hs : H;
+    a.W = p.stage ? p.Ws : reinterpret_cast<const char*>(w);
+    a.ldh = (p.stage ? p.k : ldh) * (int64_t)sizeof(T);
+    a.ldw = (p.stage ? p.k : ldw) * (int64_t)sizeof(T);
     a.row_bytes = (uint32_t)(p.k * sizeof(T));
     a.k = (int)p.k;
     a.n = p.n;
@@ -475,6 +491,8 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
     a.coef = p.coef;
     a.lse = p.lse;
     a.gmax = p.gmax;
+    a.gmax_parts = p.gmax_parts;
+    a.gmax_count = (int)((p.n_pad + 255) / 256);
     a.dz = p.dz;
     a.dzt = p.dzt;
     a.ldz = p.piece;
@@ -496,8 +514,6 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
       if ((e = launch_xent_dw<T>(b, (int)edge, st)) != hipSuccess) return NS_ERR_HIP;
     }
     if (dH) {
-      hipLaunchKernelGGL((k_xent_transpose<T>), dim3((unsigned)(width / 64), (unsigned)(p.d_pad / 64)), dim3(256), 0, st,
-                         w, ldw, rows_v, (int)p.d, (T*)p.WT, p.piece);
       XentDhArgs b{};
       b.L = p.dz;
       b.R = p.WT;
@@ -703,7 +719,7 @@ ns_status ns_linear_cross_entropy_backward(const void* H, int64_t ldh, const voi
   r.lse = lse;
   r.coef = p.coef;
   r.lse_pad = p.lse;
-  r.gmax = p.gmax;
+  r.gmax_parts = p.gmax_parts;
   r.d_status = d_status;
   r.index_bit = (int32_t)NS_STATUS_BAD_INDEX;
   return with_type(dtype, [&](auto io) {

@@ -51,6 +51,10 @@ struct XentTargets {
   }
 };
 
+// What the products need beside the caller's own arrays, made by one kernel:
+// the rows' targets and coefficients, and, tile by tile of 64 x 64, copies of
+// H and of a piece of W: padded (an operand whose rows are not whole k-tiles
+// or not aligned) and transposed.
 struct XentRowArgs {
   XentTargets targets;
   int64_t n, n_pad;
@@ -58,24 +62,35 @@ struct XentRowArgs {
   const float* dloss;  // n, or null (forward)
   const float* lse;    // n (backward)
   float *coef, *lse_pad;  // n_pad (backward): dloss or 0, lse or 0
-  float* gmax;         // backward: max |coef| over the rows, cleared beforehand
+  float* gmax_parts;   // backward: max |coef| of each 256 rows
   int32_t* d_status;
   int32_t index_bit;
 };
 
-static __global__ void k_xent_clear(float* gmax) { *gmax = 0.f; }
+struct XentCopyArgs {
+  const void* src;        // rows x cols, row stride ld
+  int64_t ld, rows;
+  int cols;
+  void* padded;           // rows x cols_k, zeros behind cols; or null
+  int cols_k;
+  void* transposed;       // cols_pad x ldt, zeros behind rows and cols; or null
+  int64_t ldt;
+  int tiles_r, tiles_c;   // 64 x 64 tiles that cover the outputs
+  __host__ __device__ int64_t blocks() const { return (int64_t)tiles_r * tiles_c; }
+};
 
-// rows x cols zeros (dW when there is no row).
-template <typename T>
-__global__ void __launch_bounds__(256) k_xent_zero(T* dst, int64_t ld, int cols) {
-  for (int c = threadIdx.x; c < cols; c += 256) dst[(int64_t)blockIdx.x * ld + c] = from_f32<T>(0.f);
-}
+struct XentPrepArgs {
+  XentRowArgs rows;
+  int row_blocks;  // of 256 rows; then the tiles of H, then those of W
+  XentCopyArgs h, w;
+};
 
-static __global__ void __launch_bounds__(256) k_xent_rows(XentRowArgs p) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__device__ __forceinline__ void xent_rows_block(const XentRowArgs& p, int block) {
+  const int64_t i = (int64_t)block * 256 + threadIdx.x;
   const int t = i < p.n ? p.targets.at(i) : kTargetNone;
   if (i < p.n_pad) p.tgt[i] = t;
   if (p.coef) {
+    __shared__ uint32_t sh[4];
     const float g = t >= 0 ? p.dloss[i] : 0.f;
     if (i < p.n_pad) {
       p.coef[i] = g;
@@ -89,76 +104,86 @@ static __global__ void __launch_bounds__(256) k_xent_rows(XentRowArgs p) {
       const uint32_t o = __shfl_xor(m, off, 64);
       m = o > m ? o : m;
     }
-    if ((threadIdx.x & 63) == 0 && m) atomicMax(reinterpret_cast<uint32_t*>(p.gmax), m);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int k = 1; k < 4; ++k) m = sh[k] > m ? sh[k] : m;
+      p.gmax_parts[block] = __uint_as_float(m);
+    }
   }
   if (p.d_status) report_status(p.d_status, p.index_bit, t == kTargetBad);
 }
 
-// dst (rows x cols_pad) = src's rows, zeros behind cols: the staging copy of
-// an operand whose rows are not whole k-tiles or not aligned.  cols_pad is a
-// multiple of a vector; one vector per thread and step.
+// One 64 x 64 tile, read once in 16-byte vectors.  For the transpose a lane
+// writes its vector's elements down a column of the transposed tile in LDS,
+// whose rows are 64 elements and 16 bytes apart, and whole vectors leave.
 template <typename T>
-__global__ void __launch_bounds__(256) k_xent_pad(const T* src, int64_t ld, int64_t rows, int cols, T* dst,
-                                                  int cols_pad) {
-  constexpr int V = kVec<T>;
-  const int per = cols_pad / V;
-  const int64_t total = rows * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / per;
-    const int c = (int)(i - r * per) * V;
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if (c + V <= cols) {
-      v = *reinterpret_cast<const typename Vec16<sizeof(T)>::type*>(src + r * ld + c);
-    } else {
-      T* e = reinterpret_cast<T*>(&v);
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (c + k < cols) e[k] = src[r * ld + c + k];
-    }
-    *reinterpret_cast<u32x4_t*>(dst + r * cols_pad + c) = v;
-  }
-}
-
-// dst (cols_pad x ldd) = the transpose of src's rows x cols, zeros elsewhere,
-// through 64 x 64 tiles in LDS: 16-byte vectors on both sides, and in between
-// a lane writes its vector's elements down a column of the transposed tile.
-// Its rows are 64 elements and 16 bytes apart, which puts the lanes of a
-// write (same row group, neighbouring vectors) on different banks.
-template <typename T>
-__global__ void __launch_bounds__(256) k_xent_transpose(const T* src, int64_t ld, int64_t rows, int cols, T* dst,
-                                                        int64_t ldd) {
+__device__ __forceinline__ void xent_copy_tile(const XentCopyArgs& p, int tr, int tc) {
   constexpr int V = kVec<T>, C = 64 / V;  // vectors per tile row
   constexpr int kStride = 64 + V;
   __shared__ __attribute__((aligned(16))) T tile[64 * kStride];
-  const int64_t r0 = (int64_t)blockIdx.x * 64;
-  const int c0 = blockIdx.y * 64;
+  const int64_t r0 = (int64_t)tr * 64;
+  const int c0 = tc * 64;
   typedef typename Vec16<sizeof(T)>::type vec_t;
+  const T* src = reinterpret_cast<const T*>(p.src);
+  u32x4_t v[64 * C / 256];
 #pragma unroll
   for (int i = 0; i < 64 * C / 256; ++i) {
     const int q = i * 256 + threadIdx.x, r = q / C, c = q % C * V;
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if (r0 + r < rows) {
-      const T* p = src + (r0 + r) * ld + c0 + c;
-      if (c0 + c + V <= cols) {
-        v = *reinterpret_cast<const vec_t*>(p);
+    v[i] = u32x4_t{0u, 0u, 0u, 0u};
+    if (r0 + r < p.rows) {
+      const T* s = src + (r0 + r) * p.ld + c0 + c;
+      if (c0 + c + V <= p.cols) {
+        v[i] = *reinterpret_cast<const vec_t*>(s);
       } else {
-        T* e = reinterpret_cast<T*>(&v);
+        T* e = reinterpret_cast<T*>(&v[i]);
 #pragma unroll
         for (int k = 0; k < V; ++k)
-          if (c0 + c + k < cols) e[k] = p[k];
+          if (c0 + c + k < p.cols) e[k] = s[k];
       }
     }
-    const T* e = reinterpret_cast<const T*>(&v);
-#pragma unroll
-    for (int k = 0; k < V; ++k) tile[(c + k) * kStride + r] = e[k];
   }
-  __syncthreads();
+  if (p.padded) {
+    T* dst = reinterpret_cast<T*>(p.padded);
 #pragma unroll
-  for (int i = 0; i < 64 * C / 256; ++i) {
-    const int q = i * 256 + threadIdx.x, c = q / C, r = q % C * V;
-    *reinterpret_cast<uint4*>(dst + (int64_t)(c0 + c) * ldd + r0 + r) =
-        *reinterpret_cast<const uint4*>(&tile[c * kStride + r]);
+    for (int i = 0; i < 64 * C / 256; ++i) {
+      const int q = i * 256 + threadIdx.x, r = q / C, c = q % C * V;
+      if (r0 + r < p.rows && c0 + c < p.cols_k) *reinterpret_cast<u32x4_t*>(dst + (r0 + r) * p.cols_k + c0 + c) = v[i];
+    }
   }
+  if (p.transposed) {
+    T* dst = reinterpret_cast<T*>(p.transposed);
+#pragma unroll
+    for (int i = 0; i < 64 * C / 256; ++i) {
+      const int q = i * 256 + threadIdx.x, r = q / C, c = q % C * V;
+      const T* e = reinterpret_cast<const T*>(&v[i]);
+#pragma unroll
+      for (int k = 0; k < V; ++k) tile[(c + k) * kStride + r] = e[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 64 * C / 256; ++i) {
+      const int q = i * 256 + threadIdx.x, c = q / C, r = q % C * V;
+      *reinterpret_cast<uint4*>(dst + (int64_t)(c0 + c) * p.ldt + r0 + r) =
+          *reinterpret_cast<const uint4*>(&tile[c * kStride + r]);
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_xent_prep(XentPrepArgs p) {
+  int64_t b = blockIdx.x;
+  if (b < p.row_blocks) return xent_rows_block(p.rows, (int)b);
+  b -= p.row_blocks;
+  const XentCopyArgs& c = b < p.h.blocks() ? p.h : p.w;
+  if (b >= p.h.blocks()) b -= p.h.blocks();
+  xent_copy_tile<T>(c, (int)(b / c.tiles_c), (int)(b % c.tiles_c));
+}
+
+// rows x cols zeros (dW when there is no row).
+template <typename T>
+__global__ void __launch_bounds__(256) k_xent_zero(T* dst, int64_t ld, int cols) {
+  for (int c = threadIdx.x; c < cols; c += 256) dst[(int64_t)blockIdx.x * ld + c] = from_f32<T>(0.f);
 }
 
 // ---------------------------------------------------------------------------
@@ -179,7 +204,9 @@ struct XentArgs {
   float* zt;              // [n_pad]: the target's logit
   // backward: W, tgt and v are those of one piece of the vocabulary
   int v0;                 // its first id
-  const float *coef, *lse, *gmax;
+  const float *coef, *lse, *gmax_parts;
+  float* gmax;            // their maximum, for the kernels that follow
+  int gmax_count;
   void *dz, *dzt;         // n_pad x ldz and ldz x n_pad
   int64_t ldz;
 };
@@ -508,9 +535,20 @@ __global__ void __launch_bounds__(256) k_xent_dot(XentDotArgs p) {
 // way.)
 template <typename T> inline constexpr float kDzUnit = __is_same(T, _Float16) ? 0x1p15f : 1.f;
 template <typename T>
-__device__ __forceinline__ float xent_scale(const float* gmax) {
+__device__ __forceinline__ float xent_scale(const XentArgs& p) {
   if constexpr (sizeof(T) == 2) {
-    const float g = *gmax;
+    uint32_t m = 0;
+    for (int i = threadIdx.x & 63; i < p.gmax_count; i += 64) {
+      const uint32_t o = __float_as_uint(p.gmax_parts[i]);
+      m = o > m ? o : m;
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+      const uint32_t o = __shfl_xor(m, off, 64);
+      m = o > m ? o : m;
+    }
+    const float g = __uint_as_float(m);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.gmax = g;
     return g > 0.f ? fminf(kDzUnit<T> / g, 1e34f) : g;  // 0 stays 0, NaN stays NaN
   }
   return 1.f;
@@ -625,7 +663,7 @@ struct DzEpilogue {
 template <typename T, int TM, int TN>
 __global__ void __launch_bounds__(kThreads, 1) k_xent_dz(XentArgs p) {
   const TileRun run(p.tiles_m * p.tiles_n);
-  xent_logits<T, TM, TN>(p, run, DzEpilogue<T, TM, TN>{p, run, xent_scale<T>(p.gmax)});
+  xent_logits<T, TM, TN>(p, run, DzEpilogue<T, TM, TN>{p, run, xent_scale<T>(p)});
 }
 
 // dW rows of one piece: dzt (piece x n_pad) times H^T (d_pad x n_pad).
@@ -828,14 +866,6 @@ template <typename T> hipError_t launch_xent_dz(const XentArgs& a, int edge, hip
 template <typename T> hipError_t launch_xent_dw(const XentDwArgs& a, int edge, hipStream_t s);
 template <typename T> hipError_t launch_xent_dh(const XentDhArgs& a, int edge, hipStream_t s);
 
-template <typename T, class Large, class Small>
-hipError_t launch_edge(int edge, Large&& large, Small&& small) {
-  if (edge == kXentLarge<T>)
-    large();
-  else
-    small();
-  return hipGetLastError();
-}
 inline dim3 xent_grid(int64_t tiles) { return dim3((unsigned)(tiles < kXentGroups ? tiles : kXentGroups)); }
 
 template <typename T, int FORM>
@@ -851,54 +881,59 @@ void launch_dot(const XentDotArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_xent_dot<T, 8, FORM>), grid, dim3(256), 0, s, a);
 }
 
-#define NS_XENT_LAUNCHERS(T)                                                                                        \
-  template <>                                                                                                       \
-  hipError_t launch_xent_fwd<T>(const XentArgs& a, int tm, hipStream_t s, int tn) {                                 \
-    const dim3 grid = xent_grid((int64_t)a.tiles_m * a.tiles_n);                                                    \
-    if constexpr (sizeof(T) == 2) {                                                                                 \
-      if (tm != tn) {                                                                                               \
-        hipLaunchKernelGGL((k_xent_fwd<T, kXentFewM, kXentFewN>), grid, dim3(kThreads), 0, s, a);                   \
-        return hipGetLastError();                                                                                   \
-      }                                                                                                             \
-    }                                                                                                               \
-    constexpr int L = kXentLarge<T>, S = kXentSmall<T>;                                                             \
-    return launch_edge<T>(                                                                                          \
-        tm, [&] { hipLaunchKernelGGL((k_xent_fwd<T, L, L>), grid, dim3(kThreads), 0, s, a); },                      \
-        [&] { hipLaunchKernelGGL((k_xent_fwd<T, S, S>), grid, dim3(kThreads), 0, s, a); });                         \
-  }                                                                                                                 \
-  template <>                                                                                                       \
-  hipError_t launch_xent_dot<T>(const XentDotArgs& a, hipStream_t s) {                                              \
-    if (a.cols % kVec<T> == 0)                                                                                      \
-      launch_dot<T, kEven>(a, s);                                                                                   \
-    else if (a.cols > kVec<T>)                                                                                      \
-      launch_dot<T, kRagged>(a, s);                                                                                 \
-    else                                                                                                            \
-      launch_dot<T, kTiny>(a, s);                                                                                   \
-    return hipGetLastError();                                                                                       \
-  }                                                                                                                 \
-  template <>                                                                                                       \
-  hipError_t launch_xent_dz<T>(const XentArgs& a, int edge, hipStream_t s) {                                        \
-    const dim3 grid = xent_grid((int64_t)a.tiles_m * a.tiles_n);                                                    \
-    constexpr int L = kXentLarge<T>, S = kXentSmall<T>;                                                             \
-    return launch_edge<T>(                                                                                          \
-        edge, [&] { hipLaunchKernelGGL((k_xent_dz<T, L, L>), grid, dim3(kThreads), 0, s, a); },                     \
-        [&] { hipLaunchKernelGGL((k_xent_dz<T, S, S>), grid, dim3(kThreads), 0, s, a); });                          \
-  }                                                                                                                 \
-  template <>                                                                                                       \
-  hipError_t launch_xent_dw<T>(const XentDwArgs& a, int edge, hipStream_t s) {                                      \
-    const dim3 grid = xent_grid((int64_t)a.tiles_m * a.tiles_n);                                                    \
-    constexpr int L = kXentLarge<T>, S = kXentSmall<T>;                                                             \
-    return launch_edge<T>(                                                                                          \
-        edge, [&] { hipLaunchKernelGGL((k_xent_dw<T, L, L>), grid, dim3(kThreads), 0, s, a); },                     \
-        [&] { hipLaunchKernelGGL((k_xent_dw<T, S, S>), grid, dim3(kThreads), 0, s, a); });                          \
-  }                                                                                                                 \
-  template <>                                                                                                       \
-  hipError_t launch_xent_dh<T>(const XentDhArgs& a, int edge, hipStream_t s) {                                      \
-    const dim3 grid = xent_grid((int64_t)a.tiles_m * a.tiles_n * a.splits);                                         \
-    constexpr int L = kXentLarge<T>, S = kXentSmall<T>;                                                             \
-    return launch_edge<T>(                                                                                          \
-        edge, [&] { hipLaunchKernelGGL((k_xent_dh<T, L, L>), grid, dim3(kThreads), 0, s, a); },                     \
-        [&] { hipLaunchKernelGGL((k_xent_dh<T, S, S>), grid, dim3(kThreads), 0, s, a); });                          \
+#define NS_XENT_LAUNCH(K, TM, TN, TILES) \
+  hipLaunchKernelGGL((K<T, TM, TN>), xent_grid(TILES), dim3(kThreads), 0, s, a)
+#define NS_XENT_EDGE(K, TILES)                              \
+  if (edge == kXentLarge<T>)                                \
+    NS_XENT_LAUNCH(K, kXentLarge<T>, kXentLarge<T>, TILES); \
+  else                                                      \
+    NS_XENT_LAUNCH(K, kXentSmall<T>, kXentSmall<T>, TILES); \
+  return hipGetLastError()
+
+template <typename T>
+hipError_t xent_fwd_of(const XentArgs& a, int edge, hipStream_t s, int tn) {
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  if constexpr (sizeof(T) == 2) {
+    if (edge != tn) {
+      NS_XENT_LAUNCH(k_xent_fwd, kXentFewM, kXentFewN, tiles);
+      return hipGetLastError();
+    }
   }
+  NS_XENT_EDGE(k_xent_fwd, tiles);
+}
+template <typename T>
+hipError_t xent_dot_of(const XentDotArgs& a, hipStream_t s) {
+  if (a.cols % kVec<T> == 0)
+    launch_dot<T, kEven>(a, s);
+  else if (a.cols > kVec<T>)
+    launch_dot<T, kRagged>(a, s);
+  else
+    launch_dot<T, kTiny>(a, s);
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t xent_dz_of(const XentArgs& a, int edge, hipStream_t s) {
+  NS_XENT_EDGE(k_xent_dz, (int64_t)a.tiles_m * a.tiles_n);
+}
+template <typename T>
+hipError_t xent_dw_of(const XentDwArgs& a, int edge, hipStream_t s) {
+  NS_XENT_EDGE(k_xent_dw, (int64_t)a.tiles_m * a.tiles_n);
+}
+template <typename T>
+hipError_t xent_dh_of(const XentDhArgs& a, int edge, hipStream_t s) {
+  NS_XENT_EDGE(k_xent_dh, (int64_t)a.tiles_m * a.tiles_n * a.splits);
+}
+
+#define NS_XENT_LAUNCHERS(T)                                                                                     \
+  template <>                                                                                                    \
+  hipError_t launch_xent_fwd<T>(const XentArgs& a, int tm, hipStream_t s, int tn) { return xent_fwd_of<T>(a, tm, s, tn); } \
+  template <>                                                                                                    \
+  hipError_t launch_xent_dot<T>(const XentDotArgs& a, hipStream_t s) { return xent_dot_of<T>(a, s); }            \
+  template <>                                                                                                    \
+  hipError_t launch_xent_dz<T>(const XentArgs& a, int edge, hipStream_t s) { return xent_dz_of<T>(a, edge, s); } \
+  template <>                                                                                                    \
+  hipError_t launch_xent_dw<T>(const XentDwArgs& a, int edge, hipStream_t s) { return xent_dw_of<T>(a, edge, s); } \
+  template <>                                                                                                    \
+  hipError_t launch_xent_dh<T>(const XentDhArgs& a, int edge, hipStream_t s) { return xent_dh_of<T>(a, edge, s); }
 
 }  // namespace nsr

@@ -159,6 +159,7 @@ def _embed(ids=PTR, ids64=1, n=4, T=PTR, vocab=10, cols=8, ldt=8, dtype=B.NS_BF1
 def test_embedding_refusals():
     assert _embed(ids=None) == INV and _embed(T=None) == INV and _embed(out=None) == INV
     assert _embed(ids64=2) == INV and _embed(n=-1) == INV and _embed(vocab=0) == INV and _embed(cols=0) == INV
+    assert _embed(cols=(1 << 23) + 1, ldt=1 << 24, ldo=1 << 24) == INV
     assert _embed(vocab=(1 << 28) + 1) == INV and _embed(n=(1 << 30) + 1) == INV
     assert _embed(ldt=7) == INV and _embed(ldo=7) == INV
     assert _embed(scale=float("nan")) == INV and _embed(scale=float("inf")) == INV
