@@ -249,6 +249,29 @@ constexpr EdgeCost kXentCost32[2] = {{kXentLarge<float>, 2.10, 2.5}, {kXentSmall
 double product_us(const EdgeCost& c, int64_t tiles, double ktiles) {
   return (double)((tiles + kXentGroups - 1) / kXentGroups) * (ktiles * c.ktile + c.fixed);
 }
+const EdgeCost* edge_costs(int es) { return es == 2 ? kXentCost16 : kXentCost32; }
+
+// The gradients' two products in one launch: dW's tiles go round the
+// work-groups, so that some have one more than the others; those others take
+// part in `extra` rounds of dH's tiles before all do.  The number of rounds
+// that ends first.
+struct GradRounds {
+  int extra = 0;
+  double us = 1e300;
+};
+GradRounds grad_rounds(const EdgeCost& c, int64_t dw_tiles, double dw_ktiles, int64_t dh_tiles, double dh_ktiles) {
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(kXentGroups, dw_tiles + dh_tiles));
+  const int64_t busy = dw_tiles % grid, idle = grid - busy;
+  const double one_w = dw_ktiles * c.ktile + c.fixed, one_h = dh_ktiles * c.ktile + c.fixed;
+  const double before = (double)(dw_tiles / grid) * one_w;
+  GradRounds best;
+  for (int64_t e = 0; e == 0 || (busy && e <= one_w / one_h + 1 && (e - 1) * idle < dh_tiles); ++e) {
+    const int64_t left = std::max<int64_t>(0, dh_tiles - e * idle), r = (left + grid - 1) / grid;
+    const double us = before + std::max(busy ? one_w + r * one_h : 0, (e + r) * one_h);
+    if (us < best.us) best = {(int)e, us};
+  }
+  return best;
+}
 
 struct XentPlan {
   int64_t n = 0, d = 0, v = 0;
@@ -278,8 +301,7 @@ bool xent_shape_ok(int64_t n, int64_t d, int64_t v) {
 
 // The backward pass's piece of the vocabulary (in tiles) and dH's splits for
 // one tile edge, and their estimated time.  Between the largest piece that is
-// allowed and a sixteenth of it, the one whose three products leave the
-// fewest compute units idle in their last rounds; fewer, larger pieces touch
+// allowed and a sixteenth of it, the one whose products leave the fewest compute units idle in their last rounds; fewer, larger pieces touch
 // dH's fp32 sums less often.
 struct BackwardChoice {
   int64_t piece_tiles = 1;
@@ -298,8 +320,8 @@ BackwardChoice choose_backward(const EdgeCost& c, int64_t n, int64_t d, int64_t 
       if (s > 1 && rest * e / bk / s < 3) break;
       auto one = [&](int64_t tiles) {
         const double sums = (double)s * m * dt * e * e * 8.0 / 4.5e6;  // fp32 read and written, in us
-        return product_us(c, m * tiles, (double)k / bk) + product_us(c, tiles * dt, (double)m * e / bk) +
-               product_us(c, m * dt * s, (double)(tiles * e / bk) / s) + sums + 12.0;
+        return product_us(c, m * tiles, (double)k / bk) +
+               grad_rounds(c, tiles * dt, (double)m * e / bk, m * dt * s, (double)(tiles * e / bk) / s).us + sums + 12.0;
       };
       const double us = (double)(count - 1) * one(q) + one(rest);
       if (us < best.us) best = {q, s, us};
@@ -317,7 +339,7 @@ XentPlan xent_plan(int64_t n, int64_t d, int64_t v, ns_dtype dtype, bool aligned
   p.bk = kRowBytes / p.es;
   p.k = round_to(d, p.bk);
   p.stage = p.k != d || !aligned;
-  const EdgeCost* costs = p.es == 2 ? kXentCost16 : kXentCost32;
+  const EdgeCost* costs = edge_costs(p.es);
   Carver c{reinterpret_cast<char*>(ws)};
   if (!backward && n <= (p.stage ? kXentDotRowsStaged : kXentDotRows)) {
     p.groups = (v + kDotRows - 1) / kDotRows;
@@ -498,8 +520,9 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
     a.ldz = p.piece;
     hipError_t e = launch_xent_dz<T>(a, (int)edge, st);
     if (e != hipSuccess) return NS_ERR_HIP;
+    XentDwArgs b{};
+    b.gmax = p.gmax;
     if (dW) {
-      XentDwArgs b{};
       b.L = p.dzt;
       b.R = p.HT;
       b.ldl = b.ldr = p.n_pad * (int64_t)sizeof(T);
@@ -510,24 +533,26 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
       b.ldo = lddw;
       b.rows = rows_v;
       b.cols = (int)p.d;
-      b.gmax = p.gmax;
-      if ((e = launch_xent_dw<T>(b, (int)edge, st)) != hipSuccess) return NS_ERR_HIP;
     }
+    XentDhArgs h{};
     if (dH) {
-      XentDhArgs b{};
-      b.L = p.dz;
-      b.R = p.WT;
-      b.ldl = b.ldr = p.piece * (int64_t)sizeof(T);
-      b.ktiles = (int)(width / (kRowBytes / sizeof(T)));
-      b.splits = p.splits;
-      b.tiles_m = (int)p.tiles_m;
-      b.tiles_n = (int)(p.d_pad / edge);
-      b.acc = p.acc;
-      b.n_pad = p.n_pad;
-      b.d_pad = p.d_pad;
-      b.first = v0 == 0;
-      if ((e = launch_xent_dh<T>(b, (int)edge, st)) != hipSuccess) return NS_ERR_HIP;
+      h.L = p.dz;
+      h.R = p.WT;
+      h.ldl = h.ldr = p.piece * (int64_t)sizeof(T);
+      h.ktiles = (int)(width / p.bk);
+      h.splits = p.splits;
+      h.tiles_m = (int)p.tiles_m;
+      h.tiles_n = (int)(p.d_pad / edge);
+      h.acc = p.acc;
+      h.n_pad = p.n_pad;
+      h.d_pad = p.d_pad;
+      h.first = v0 == 0;
+      const EdgeCost* costs = edge_costs(p.es);
+      h.extra = grad_rounds(costs[edge == costs[0].edge ? 0 : 1], (int64_t)b.tiles_m * b.tiles_n, (double)b.k / p.bk,
+                            (int64_t)h.tiles_m * h.tiles_n * h.splits, (double)h.ktiles / h.splits)
+                    .extra;
     }
+    if ((dW || dH) && (e = launch_xent_grads<T>(b, h, (int)edge, st)) != hipSuccess) return NS_ERR_HIP;
   }
   if (dH)
     hipLaunchKernelGGL((k_xent_dh_out<T>), dim3((unsigned)p.n), dim3(256), 0, st, p.acc, p.splits, p.n_pad, p.d_pad,

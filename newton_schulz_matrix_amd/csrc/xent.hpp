@@ -666,7 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent_dz(XentArgs p) {
   xent_logits<T, TM, TN>(p, run, DzEpilogue<T, TM, TN>{p, run, xent_scale<T>(p)});
 }
 
-// dW rows of one piece: dzt (piece x n_pad) times H^T (d_pad x n_pad).
+// The gradients' products of one piece, in one launch: neither fills the
+// compute units by itself (16384 x 768 against a piece of 10176: 212 tiles of
+// 256 k-tiles for dW and 344 of 159 for dH, 301 and 250 us as two launches),
+// so the work-groups with fewer tiles of dW take more of dH's.
+//
+// dW rows of the piece: dzt (piece x n_pad) times H^T (d_pad x n_pad).
 struct XentDwArgs {
   const void *L, *R;
   int64_t ldl, ldr;  // bytes
@@ -734,21 +739,6 @@ struct DwEpilogue {
   }
 };
 
-template <typename T, int TM, int TN>
-__global__ void __launch_bounds__(kThreads, 1) k_xent_dw(XentDwArgs p) {
-  const TileRun run(p.tiles_m * p.tiles_n);
-  constexpr int BK = kRowBytes / sizeof(T);
-  stream_tiles<T, TM, TN>(
-      run.count, p.ldl, p.ldr, (uint32_t)(p.k * sizeof(T)),
-      [&](int j) {
-        int tm, tn;
-        grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
-        return StreamTile{reinterpret_cast<const char*>(p.L) + (int64_t)tm * TM * p.ldl,
-                          reinterpret_cast<const char*>(p.R) + (int64_t)tn * TN * p.ldr, TM, TN, 0, p.k / BK};
-      },
-      DwEpilogue<T, TM, TN>{p, run, xent_unscale<T>(p.gmax)});
-}
-
 // dH's running sums: acc[split] (+)= dz (n_pad x piece) W^T (d_pad x piece)
 // over the split's share of the piece's k-tiles.
 struct XentDhArgs {
@@ -759,6 +749,29 @@ struct XentDhArgs {
   float* acc;        // [splits][n_pad][d_pad]
   int64_t n_pad, d_pad;
   int first;         // the first piece writes, the others add
+  int extra;         // rounds that only the work-groups with fewer tiles of dW take part in
+};
+// dH's tiles of one work-group: `extra` rounds among the work-groups past the
+// ones with a last tile of dW, then rounds among all.
+struct DhRun {
+  int first, step, rounds, base, count;
+  __device__ __forceinline__ DhRun(int dw_tiles, int total, int extra) {
+    const int w = xcd_order(blockIdx.x, gridDim.x), grid = (int)gridDim.x;
+    const int busy = dw_tiles % grid;
+    step = grid - busy;
+    first = w - busy;
+    const int shared = extra * step;
+    rounds = 0;
+    if (first >= 0 && first < total) {
+      rounds = (total - first + step - 1) / step;
+      rounds = rounds < extra ? rounds : extra;
+    }
+    base = shared + w;
+    count = rounds + (base < total ? (total - base + grid - 1) / grid : 0);
+  }
+  __device__ __forceinline__ int at(int j) const {
+    return j < rounds ? first + j * step : base + (j - rounds) * (int)gridDim.x;
+  }
 };
 
 template <typename T, int TM, int TN>
@@ -766,7 +779,7 @@ struct DhEpilogue {
   using A = Acc<T, TM, TN>;
   static constexpr int kStores = A::FM * A::FN * 4;
   const XentDhArgs& p;
-  const TileRun& run;
+  const DhRun& run;
   int per;
   LanePlace<TM, TN> at;
   __device__ __forceinline__ void load(int) {}
@@ -806,23 +819,39 @@ struct DhEpilogue {
   }
 };
 
+// dw.tiles_m or dh.tiles_m is 0 where that gradient is not wanted.
 template <typename T, int TM, int TN>
-__global__ void __launch_bounds__(kThreads, 1) k_xent_dh(XentDhArgs p) {
-  const int per = p.tiles_m * p.tiles_n;
-  const TileRun run(per * p.splits);
+__global__ void __launch_bounds__(kThreads, 1) k_xent_grads(XentDwArgs dw, XentDhArgs dh) {
   constexpr int BK = kRowBytes / sizeof(T);
+  const int dw_tiles = dw.tiles_m * dw.tiles_n;
+  {
+    const TileRun run(dw_tiles);
+    stream_tiles<T, TM, TN>(
+        run.count, dw.ldl, dw.ldr, (uint32_t)(dw.k * sizeof(T)),
+        [&](int j) {
+          int tm, tn;
+          grouped_tile(run.at(j), dw.tiles_m, dw.tiles_n, tm, tn);
+          return StreamTile{reinterpret_cast<const char*>(dw.L) + (int64_t)tm * TM * dw.ldl,
+                            reinterpret_cast<const char*>(dw.R) + (int64_t)tn * TN * dw.ldr, TM, TN, 0, dw.k / BK};
+        },
+        DwEpilogue<T, TM, TN>{dw, run, xent_unscale<T>(dw.gmax)});
+  }
+  // All reads of the stages are over before they are filled again.
+  lds_barrier();
+  const int per = dh.tiles_m * dh.tiles_n;
+  const DhRun run(dw_tiles, per * dh.splits, dh.extra);
   stream_tiles<T, TM, TN>(
-      run.count, p.ldl, p.ldr, (uint32_t)(p.ktiles * BK * sizeof(T)),
+      run.count, dh.ldl, dh.ldr, (uint32_t)(dh.ktiles * BK * sizeof(T)),
       [&](int j) {
-        const int split = run.at(j) / per;
+        const int i = run.at(j), split = i / per;
         int tm, tn;
-        grouped_tile(run.at(j) % per, p.tiles_m, p.tiles_n, tm, tn);
-        const int kt0 = (int)((int64_t)p.ktiles * split / p.splits);
-        const int kt1 = (int)((int64_t)p.ktiles * (split + 1) / p.splits);
-        return StreamTile{reinterpret_cast<const char*>(p.L) + (int64_t)tm * TM * p.ldl,
-                          reinterpret_cast<const char*>(p.R) + (int64_t)tn * TN * p.ldr, TM, TN, kt0, kt1 - kt0};
+        grouped_tile(i % per, dh.tiles_m, dh.tiles_n, tm, tn);
+        const int kt0 = (int)((int64_t)dh.ktiles * split / dh.splits);
+        const int kt1 = (int)((int64_t)dh.ktiles * (split + 1) / dh.splits);
+        return StreamTile{reinterpret_cast<const char*>(dh.L) + (int64_t)tm * TM * dh.ldl,
+                          reinterpret_cast<const char*>(dh.R) + (int64_t)tn * TN * dh.ldr, TM, TN, kt0, kt1 - kt0};
       },
-      DhEpilogue<T, TM, TN>{p, run, per});
+      DhEpilogue<T, TM, TN>{dh, run, per});
 }
 
 // dH = the splits' sum, unscaled and rounded.
@@ -863,8 +892,7 @@ constexpr int kXentGroups = 256;  // one work-group per compute unit
 template <typename T> hipError_t launch_xent_fwd(const XentArgs& a, int tm, hipStream_t s, int tn);
 template <typename T> hipError_t launch_xent_dot(const XentDotArgs& a, hipStream_t s);
 template <typename T> hipError_t launch_xent_dz(const XentArgs& a, int edge, hipStream_t s);
-template <typename T> hipError_t launch_xent_dw(const XentDwArgs& a, int edge, hipStream_t s);
-template <typename T> hipError_t launch_xent_dh(const XentDhArgs& a, int edge, hipStream_t s);
+template <typename T> hipError_t launch_xent_grads(const XentDwArgs& a, const XentDhArgs& b, int edge, hipStream_t s);
 
 inline dim3 xent_grid(int64_t tiles) { return dim3((unsigned)(tiles < kXentGroups ? tiles : kXentGroups)); }
 
@@ -881,13 +909,13 @@ void launch_dot(const XentDotArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_xent_dot<T, 8, FORM>), grid, dim3(256), 0, s, a);
 }
 
-#define NS_XENT_LAUNCH(K, TM, TN, TILES) \
-  hipLaunchKernelGGL((K<T, TM, TN>), xent_grid(TILES), dim3(kThreads), 0, s, a)
-#define NS_XENT_EDGE(K, TILES)                              \
-  if (edge == kXentLarge<T>)                                \
-    NS_XENT_LAUNCH(K, kXentLarge<T>, kXentLarge<T>, TILES); \
-  else                                                      \
-    NS_XENT_LAUNCH(K, kXentSmall<T>, kXentSmall<T>, TILES); \
+#define NS_XENT_LAUNCH(K, TM, TN, TILES, ...) \
+  hipLaunchKernelGGL((K<T, TM, TN>), xent_grid(TILES), dim3(kThreads), 0, s, __VA_ARGS__)
+#define NS_XENT_EDGE(K, TILES, ...)                                      \
+  if (edge == kXentLarge<T>)                                             \
+    NS_XENT_LAUNCH(K, kXentLarge<T>, kXentLarge<T>, TILES, __VA_ARGS__); \
+  else                                                                   \
+    NS_XENT_LAUNCH(K, kXentSmall<T>, kXentSmall<T>, TILES, __VA_ARGS__); \
   return hipGetLastError()
 
 template <typename T>
@@ -895,11 +923,11 @@ hipError_t xent_fwd_of(const XentArgs& a, int edge, hipStream_t s, int tn) {
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   if constexpr (sizeof(T) == 2) {
     if (edge != tn) {
-      NS_XENT_LAUNCH(k_xent_fwd, kXentFewM, kXentFewN, tiles);
+      NS_XENT_LAUNCH(k_xent_fwd, kXentFewM, kXentFewN, tiles, a);
       return hipGetLastError();
     }
   }
-  NS_XENT_EDGE(k_xent_fwd, tiles);
+  NS_XENT_EDGE(k_xent_fwd, tiles, a);
 }
 template <typename T>
 hipError_t xent_dot_of(const XentDotArgs& a, hipStream_t s) {
@@ -913,27 +941,30 @@ hipError_t xent_dot_of(const XentDotArgs& a, hipStream_t s) {
 }
 template <typename T>
 hipError_t xent_dz_of(const XentArgs& a, int edge, hipStream_t s) {
-  NS_XENT_EDGE(k_xent_dz, (int64_t)a.tiles_m * a.tiles_n);
+  NS_XENT_EDGE(k_xent_dz, (int64_t)a.tiles_m * a.tiles_n, a);
 }
 template <typename T>
-hipError_t xent_dw_of(const XentDwArgs& a, int edge, hipStream_t s) {
-  NS_XENT_EDGE(k_xent_dw, (int64_t)a.tiles_m * a.tiles_n);
-}
-template <typename T>
-hipError_t xent_dh_of(const XentDhArgs& a, int edge, hipStream_t s) {
-  NS_XENT_EDGE(k_xent_dh, (int64_t)a.tiles_m * a.tiles_n * a.splits);
+hipError_t xent_grads_of(const XentDwArgs& a, const XentDhArgs& b, int edge, hipStream_t s) {
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n + (int64_t)b.tiles_m * b.tiles_n * b.splits;
+  NS_XENT_EDGE(k_xent_grads, tiles, a, b);
 }
 
-#define NS_XENT_LAUNCHERS(T)                                                                                     \
-  template <>                                                                                                    \
-  hipError_t launch_xent_fwd<T>(const XentArgs& a, int tm, hipStream_t s, int tn) { return xent_fwd_of<T>(a, tm, s, tn); } \
-  template <>                                                                                                    \
-  hipError_t launch_xent_dot<T>(const XentDotArgs& a, hipStream_t s) { return xent_dot_of<T>(a, s); }            \
-  template <>                                                                                                    \
-  hipError_t launch_xent_dz<T>(const XentArgs& a, int edge, hipStream_t s) { return xent_dz_of<T>(a, edge, s); } \
-  template <>                                                                                                    \
-  hipError_t launch_xent_dw<T>(const XentDwArgs& a, int edge, hipStream_t s) { return xent_dw_of<T>(a, edge, s); } \
-  template <>                                                                                                    \
-  hipError_t launch_xent_dh<T>(const XentDhArgs& a, int edge, hipStream_t s) { return xent_dh_of<T>(a, edge, s); }
+#define NS_XENT_LAUNCHERS(T)                                                                    \
+  template <>                                                                                   \
+  hipError_t launch_xent_fwd<T>(const XentArgs& a, int tm, hipStream_t s, int tn) {             \
+    return xent_fwd_of<T>(a, tm, s, tn);                                                        \
+  }                                                                                             \
+  template <>                                                                                   \
+  hipError_t launch_xent_dot<T>(const XentDotArgs& a, hipStream_t s) {                          \
+    return xent_dot_of<T>(a, s);                                                                \
+  }                                                                                             \
+  template <>                                                                                   \
+  hipError_t launch_xent_dz<T>(const XentArgs& a, int edge, hipStream_t s) {                    \
+    return xent_dz_of<T>(a, edge, s);                                                           \
+  }                                                                                             \
+  template <>                                                                                   \
+  hipError_t launch_xent_grads<T>(const XentDwArgs& a, const XentDhArgs& b, int edge, hipStream_t s) { \
+    return xent_grads_of<T>(a, b, edge, s);                                                     \
+  }
 
 }  // namespace nsr
