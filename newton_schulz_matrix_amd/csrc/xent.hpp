@@ -560,7 +560,10 @@ __device__ __forceinline__ float xent_unscale(const float* gmax) {
 }
 
 // Backward, first product: dz of one tile, stored in both orientations from
-// the accumulators.
+// the accumulators, at once: kept in registers and stored a block per step
+// while the next tile's products run, the copies behind them waited for the
+// stores (they complete in order) and a piece of 16384 x 768 x 12672 took 633
+// us instead of 498.
 template <typename T, int TM, int TN>
 struct DzEpilogue {
   using A = Acc<T, TM, TN>;
