@@ -443,6 +443,7 @@ ns_status ns_embedding(const void* ids, int32_t ids64, int64_t n,
  *            holds the output projection's gradient); rows without an id
  *            are not touched.
  *   Ids outside [0, vocab) contribute nothing and set NS_STATUS_BAD_INDEX.
+ *   n * vocab <= 2^46.
  *   workspace   ns_embedding_workspace_size(n, vocab, cols) bytes, 256-byte
  *            aligned.
  */
@@ -496,7 +497,8 @@ ns_status ns_linear_cross_entropy(const void* H, int64_t ldh, const void* W,
  *   dH       rows x cols, row stride lddh; dW vocab x cols, row stride lddw;
  *            dtype.  Either may be NULL.
  * Rows whose target is ignored or out of range, and rows with dloss 0,
- * contribute exact zeros.  dz is rounded to dtype (fp16: scaled by
+ * contribute exact zeros to dW, whatever their row of H holds, and their
+ * rows of dH are zeros.  dz is rounded to dtype (fp16: scaled by
  * 2^15 / max|dloss| first, so dloss may span about 2^24 between rows); both
  * products accumulate in fp32.
  *   workspace   ns_linear_cross_entropy_workspace_size(..., aligned, 1)

@@ -150,9 +150,16 @@ bool norm_shape_ok(int64_t rows, int64_t cols) {
 constexpr int64_t kMaxEmbedRows = int64_t(1) << 28;
 constexpr int64_t kMaxEmbedCols = 1 << 23;
 constexpr int64_t kMaxEmbedIds = int64_t(1) << 30;
+// The gradient's sort reads all ids once per 512 table rows: at most about
+// 2^40 bytes from L2, a fraction of a second.
+constexpr int64_t kMaxEmbedSort = int64_t(1) << 46;
 
 bool embed_shape_ok(int64_t n, int64_t vocab, int64_t cols) {
   return n >= 0 && n <= kMaxEmbedIds && vocab >= 1 && vocab <= kMaxEmbedRows && cols >= 1 && cols <= kMaxEmbedCols;
+}
+
+bool embed_grad_shape_ok(int64_t n, int64_t vocab, int64_t cols) {
+  return embed_shape_ok(n, vocab, cols) && n <= kMaxEmbedSort / vocab;
 }
 
 // Ids per sorting block: about a block per compute unit (every block reads
@@ -489,6 +496,7 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
   prep.rows = rows;
   prep.row_blocks = (int)((p.n_pad + 255) / 256);
   prep.h = xent_copy(p, H, ldh, p.n, p.Hs, dW ? p.HT : nullptr, p.n_pad, p.n_pad);
+  prep.h.masked = 1;
   for (int64_t v0 = 0; v0 < p.v; v0 += p.piece) {
     const int64_t rows_v = std::min(p.piece, p.v - v0), width = round_to(rows_v, edge);
     const T* w = reinterpret_cast<const T*>(W) + v0 * ldw;
@@ -556,7 +564,7 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
   }
   if (dH)
     hipLaunchKernelGGL((k_xent_dh_out<T>), dim3((unsigned)p.n), dim3(256), 0, st, p.acc, p.splits, p.n_pad, p.d_pad,
-                       reinterpret_cast<T*>(dH), lddh, (int)p.d, p.gmax, d_status,
+                       reinterpret_cast<T*>(dH), lddh, (int)p.d, p.coef, p.gmax, d_status,
                        (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT));
   return launched();
 }
@@ -650,7 +658,7 @@ ns_status ns_embedding(const void* ids, int32_t ids64, int64_t n, const void* ta
 }
 
 size_t ns_embedding_workspace_size(int64_t n, int64_t vocab, int64_t cols) {
-  if (!embed_shape_ok(n, vocab, cols)) return 0;
+  if (!embed_grad_shape_ok(n, vocab, cols)) return 0;
   // The same for every type: fp32's slices are the narrowest, 16-bit ones the widest.
   return std::max(embed_plan(n, vocab, cols, nullptr, 2).total, embed_plan(n, vocab, cols, nullptr, 4).total);
 }
@@ -658,7 +666,7 @@ size_t ns_embedding_workspace_size(int64_t n, int64_t vocab, int64_t cols) {
 ns_status ns_embedding_backward(const void* ids, int32_t ids64, int64_t n, const void* dY, int64_t lddy, int64_t vocab,
                                 int64_t cols, ns_dtype dtype, float scale, void* dT, int64_t ldt, int32_t accumulate,
                                 int32_t* d_status, void* workspace, size_t workspace_bytes, ns_stream_t stream) {
-  if (!embed_shape_ok(n, vocab, cols) || lddy < cols || ldt < cols || !isfinite(scale)) return NS_ERR_INVALID_ARG;
+  if (!embed_grad_shape_ok(n, vocab, cols) || lddy < cols || ldt < cols || !isfinite(scale)) return NS_ERR_INVALID_ARG;
   if ((ids64 != 0 && ids64 != 1) || (accumulate != 0 && accumulate != 1)) return NS_ERR_INVALID_ARG;
   if (!known(dtype)) return NS_ERR_UNSUPPORTED_DTYPE;
   if (!dT || (n > 0 && (!ids || !dY))) return NS_ERR_INVALID_ARG;

@@ -62,7 +62,7 @@ struct XentRowArgs {
   const float* dloss;  // n, or null (forward)
   const float* lse;    // n (backward)
   float *coef, *lse_pad;  // n_pad (backward): dloss or 0, lse or 0
-  float* gmax_parts;   // backward: max |coef| of each 256 rows
+  float* gmax_parts;   // backward: max |coef| of each 256 rows, finite ones
   int32_t* d_status;
   int32_t index_bit;
 };
@@ -74,6 +74,7 @@ struct XentCopyArgs {
   void* padded;           // rows x cols_k, zeros behind cols; or null
   int cols_k;
   void* transposed;       // cols_pad x ldt, zeros behind rows and cols; or null
+  int masked;             // transposed: zeros for the rows without a coefficient
   int64_t ldt;
   int tiles_r, tiles_c;   // 64 x 64 tiles that cover the outputs
   __host__ __device__ int64_t blocks() const { return (int64_t)tiles_r * tiles_c; }
@@ -96,9 +97,11 @@ __device__ __forceinline__ void xent_rows_block(const XentRowArgs& p, int block)
       p.coef[i] = g;
       p.lse_pad[i] = i < p.n ? p.lse[i] : 0.f;
     }
-    // The maximum of non-negative floats is that of their bit patterns; a
-    // NaN's is above all of them and stays.
+    // The maximum of non-negative floats is that of their bit patterns.  An
+    // infinite or NaN coefficient goes into its own row's gradient, not into
+    // the unit that all rows are held in.
     uint32_t m = __float_as_uint(fabsf(g));
+    if (m >= 0x7f800000u) m = 0;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
       const uint32_t o = __shfl_xor(m, off, 64);
@@ -117,8 +120,12 @@ __device__ __forceinline__ void xent_rows_block(const XentRowArgs& p, int block)
 // One 64 x 64 tile, read once in 16-byte vectors.  For the transpose a lane
 // writes its vector's elements down a column of the transposed tile in LDS,
 // whose rows are 64 elements and 16 bytes apart, and whole vectors leave.
+//
+// dW = dz^T H multiplies the zeros of a row without a gradient with that row
+// of H, which may hold anything (padding positions): the transposed H has
+// zeros there.
 template <typename T>
-__device__ __forceinline__ void xent_copy_tile(const XentCopyArgs& p, int tr, int tc) {
+__device__ __forceinline__ void xent_copy_tile(const XentCopyArgs& p, const XentRowArgs& rows, int tr, int tc) {
   constexpr int V = kVec<T>, C = 64 / V;  // vectors per tile row
   constexpr int kStride = 64 + V;
   __shared__ __attribute__((aligned(16))) T tile[64 * kStride];
@@ -153,6 +160,13 @@ __device__ __forceinline__ void xent_copy_tile(const XentCopyArgs& p, int tr, in
   }
   if (p.transposed) {
     T* dst = reinterpret_cast<T*>(p.transposed);
+    if (p.masked) {
+#pragma unroll
+      for (int i = 0; i < 64 * C / 256; ++i) {
+        const int64_t row = r0 + (i * 256 + threadIdx.x) / C;
+        if (row < p.rows && !(rows.targets.at(row) >= 0 && rows.dloss[row] != 0.f)) v[i] = u32x4_t{0u, 0u, 0u, 0u};
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 64 * C / 256; ++i) {
       const int q = i * 256 + threadIdx.x, r = q / C, c = q % C * V;
@@ -177,7 +191,7 @@ __global__ void __launch_bounds__(256) k_xent_prep(XentPrepArgs p) {
   b -= p.row_blocks;
   const XentCopyArgs& c = b < p.h.blocks() ? p.h : p.w;
   if (b >= p.h.blocks()) b -= p.h.blocks();
-  xent_copy_tile<T>(c, (int)(b / c.tiles_c), (int)(b % c.tiles_c));
+  xent_copy_tile<T>(c, p.rows, (int)(b / c.tiles_c), (int)(b % c.tiles_c));
 }
 
 // rows x cols zeros (dW when there is no row).
@@ -549,7 +563,7 @@ __device__ __forceinline__ float xent_scale(const XentArgs& p) {
     }
     const float g = __uint_as_float(m);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.gmax = g;
-    return g > 0.f ? fminf(kDzUnit<T> / g, 1e34f) : g;  // 0 stays 0, NaN stays NaN
+    return g > 0.f ? fminf(kDzUnit<T> / g, 1e34f) : 0.f;
   }
   return 1.f;
 }
@@ -857,18 +871,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent_grads(XentDwArgs dw, XentD
       DhEpilogue<T, TM, TN>{dh, run, per});
 }
 
-// dH = the splits' sum, unscaled and rounded.
+// dH = the splits' sum, unscaled and rounded; rows without a gradient are
+// zeros, whatever W holds.
 template <typename T>
 __global__ void __launch_bounds__(256) k_xent_dh_out(const float* acc, int splits, int64_t n_pad, int64_t d_pad,
-                                                     T* out, int64_t ldo, int cols, const float* gmax,
-                                                     int32_t* d_status, int32_t status_bits) {
+                                                     T* out, int64_t ldo, int cols, const float* coef,
+                                                     const float* gmax, int32_t* d_status, int32_t status_bits) {
   const int64_t r = blockIdx.x;
   const float s = xent_unscale<T>(gmax);
+  const bool none = coef[r] == 0.f;
   bool bad = false;
   for (int c = threadIdx.x; c < cols; c += 256) {
     float v = 0.f;
     for (int k = 0; k < splits; ++k) v += acc[((int64_t)k * n_pad + r) * d_pad + c];
-    v *= s;
+    v = none ? 0.f : v * s;
     bad |= !(fabsf(v) < kRoundsToInf<T>);
     out[r * ldo + c] = from_f32<T>(v);
   }

@@ -538,6 +538,37 @@ def test_linear_cross_entropy_nonfinite_and_extreme_logits(dtype):
     assert torch.count_nonzero(dh) == 0 and torch.count_nonzero(dw) == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_linear_cross_entropy_backward_keeps_nonfinite_rows_out(dtype):
+    # Rows without a gradient may hold anything in h; a coefficient that is
+    # not finite reaches its own row of dh only (and dw).
+    dev = _dev()
+    n, d, v = 300, 72, 400
+    h, w, t, dloss = _xent_inputs(n, d, v, dtype, dev, seed=16, ignored=0.0)
+    lse = nsa.linear_cross_entropy(h, w, t)[1]
+    t[3], t[150], t[299] = -100, v + 7, -100
+    dloss[77] = 0
+    rows = [3, 77, 150, 299]
+    dh0, dw0 = nsa.linear_cross_entropy_backward(h, w, t, lse, dloss)
+    hn, ln = h.clone(), lse.clone()
+    hn[3], hn[77], hn[150], hn[299, 5] = float("nan"), float("inf"), -float("inf"), float("nan")
+    ln[rows] = float("nan")
+    st = _word(dev)
+    dh, dw = nsa.linear_cross_entropy_backward(hn, w, t, ln, dloss, status=st)
+    assert torch.equal(dh, dh0) and torch.equal(dw, dw0) and torch.count_nonzero(dh[rows]) == 0
+    assert int(st.item()) == B.STATUS_BAD_INDEX
+    for value in (float("inf"), float("nan")):
+        bad = dloss.clone()
+        bad[20] = value
+        zero = dloss.clone()
+        zero[20] = 0
+        dh, dw = nsa.linear_cross_entropy_backward(h, w, t, lse, bad)
+        base = nsa.linear_cross_entropy_backward(h, w, t, lse, zero)[0]
+        others = torch.arange(n, device=dev) != 20
+        assert torch.equal(dh[others], base[others]) and not torch.isfinite(dh[20]).all()
+        assert not torch.isfinite(dw).all()
+
+
 def test_linear_cross_entropy_tiny_and_uneven_coefficients_fp16():
     # fp16 holds dz in units of the largest coefficient: a batch of small
     # ones, and rows whose coefficients differ by a factor of 1000.

@@ -84,6 +84,9 @@ def test_workspace_sizes():
     assert nsa.embedding_workspace_size(8, 0, 8) == 0
     assert nsa.embedding_workspace_size((1 << 30) + 1, 8, 8) == 0
     assert nsa.embedding_workspace_size(1 << 30, 8, 8) > 0
+    # The sort reads all ids once per 512 table rows.
+    assert nsa.embedding_workspace_size(1 << 30, 1 << 16, 8) > 0
+    assert nsa.embedding_workspace_size(1 << 30, (1 << 16) + 1, 8) == 0
     assert nsa.linear_cross_entropy_workspace_size(1 << 22, 8, 1 << 21) == 0
     assert nsa.linear_cross_entropy_workspace_size(8, 8, 0) == 0
     assert nsa.linear_cross_entropy_workspace_size((1 << 23) + 1, 8, 8) == 0
