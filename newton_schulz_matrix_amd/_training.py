@@ -81,6 +81,20 @@ def _output(out: Optional[torch.Tensor], shape, dtype: torch.dtype,
     """The tensor to write and its row stride."""
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device), shape[-1]
+    return _given(out, shape, dtype, device, name)
+
+
+def _output_like(out: Optional[torch.Tensor], x: torch.Tensor, cols: int,
+                 device: torch.device, name: str) -> Tuple[torch.Tensor, int]:
+    """The same for a result of x's shape and dtype (empty_like is a third
+    cheaper than empty, which counts in calls of 12 us)."""
+    if out is None and x.is_contiguous():
+        return torch.empty_like(x), cols
+    return _output(out, x.shape, x.dtype, device, name)
+
+
+def _given(out: torch.Tensor, shape, dtype: torch.dtype,
+           device: torch.device, name: str) -> Tuple[torch.Tensor, int]:
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
         raise ValueError(f"{name} must have shape {tuple(shape)}, {dtype} and device {device}")
     return out, _rows(out, name)[2]
@@ -155,10 +169,11 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         raise TypeError("weight and bias must have the same dtype")
     param = weight if weight is not None else bias
     pcode = code if param is None else dtype_code(param.dtype)
-    y, ldy = _output(out, x.shape, x.dtype, device, "out")
+    y, ldy = _output_like(out, x, cols, device, "out")
     mean = rstd = None
     if stats:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+        mean = torch.empty((rows,) if x.dim() == 2 else x.shape[:-1],
+                           dtype=torch.float32, device=device)
         rstd = torch.empty_like(mean)
     _call("ns_layer_norm", device,
           x.data_ptr(), rows, cols, ldx, code,
@@ -198,7 +213,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     _per_row(rstd, rows, device, "rstd")
     _param(weight, x, cols, "weight")
     pdtype = x.dtype if weight is None else weight.dtype
-    dx, lddx = _output(out, x.shape, x.dtype, device, "out")
+    dx, lddx = _output_like(out, x, cols, device, "out")
     dweight = dbias = keep = None
     wptr, wbytes = None, 0
     if params:
@@ -365,9 +380,9 @@ def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor,
     dh = dw = None
     lddh = lddw = cols
     if need_dh:
-        dh, lddh = _output(out_dh, (rows, cols), h.dtype, device, "out_dh")
+        dh, lddh = _output_like(out_dh, h, cols, device, "out_dh")
     if need_dw:
-        dw, lddw = _output(out_dw, (vocab, cols), w.dtype, device, "out_dw")
+        dw, lddw = _output_like(out_dw, w, cols, device, "out_dw")
     wptr, wbytes, keep = _workspace_args(
         int(lib().ns_linear_cross_entropy_workspace_size(
             rows, cols, vocab, code, aligned, 1)), device, workspace,
