@@ -253,8 +253,10 @@ struct EdgeCost {
 };
 constexpr EdgeCost kXentCost16[2] = {{kXentLarge<_Float16>, 0.90, 3.0}, {kXentSmall<_Float16>, 0.52, 2.0}};
 constexpr EdgeCost kXentCost32[2] = {{kXentLarge<float>, 2.10, 2.5}, {kXentSmall<float>, 0.53, 1.5}};
+// k-tiles go in groups of three (stream.hpp).
+double tile_us(const EdgeCost& c, double ktiles) { return ceil(ktiles / 3) * 3 * c.ktile + c.fixed; }
 double product_us(const EdgeCost& c, int64_t tiles, double ktiles) {
-  return (double)((tiles + kXentGroups - 1) / kXentGroups) * (ktiles * c.ktile + c.fixed);
+  return (double)((tiles + kXentGroups - 1) / kXentGroups) * tile_us(c, ktiles);
 }
 const EdgeCost* edge_costs(int es) { return es == 2 ? kXentCost16 : kXentCost32; }
 
@@ -269,7 +271,7 @@ struct GradRounds {
 GradRounds grad_rounds(const EdgeCost& c, int64_t dw_tiles, double dw_ktiles, int64_t dh_tiles, double dh_ktiles) {
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(kXentGroups, dw_tiles + dh_tiles));
   const int64_t busy = dw_tiles % grid, idle = grid - busy;
-  const double one_w = dw_ktiles * c.ktile + c.fixed, one_h = dh_ktiles * c.ktile + c.fixed;
+  const double one_w = tile_us(c, dw_ktiles), one_h = tile_us(c, dh_ktiles);
   const double before = (double)(dw_tiles / grid) * one_w;
   GradRounds best;
   for (int64_t e = 0; e == 0 || (busy && e <= one_w / one_h + 1 && (e - 1) * idle < dh_tiles); ++e) {
@@ -315,6 +317,9 @@ struct BackwardChoice {
   int splits = 1;
   double us = 1e300;
 };
+// dH's splits to choose from: few rows leave most compute units without a
+// tile of dH (35 x 434 x 84115: 4 tiles of 1315 k-tiles, 140 us with 8 splits).
+constexpr int kXentSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 12, 16, 24, 32, 48, 64};
 BackwardChoice choose_backward(const EdgeCost& c, int64_t n, int64_t d, int64_t v, int64_t k, int bk) {
   const int64_t e = c.edge, m = std::max<int64_t>(1, (n + e - 1) / e), dt = (d + e - 1) / e, vt = (v + e - 1) / e;
   const int64_t most = std::max<int64_t>(1, std::min(vt, kXentPieceElems / (m * e * e)));
@@ -322,7 +327,7 @@ BackwardChoice choose_backward(const EdgeCost& c, int64_t n, int64_t d, int64_t 
   BackwardChoice best;
   for (int64_t pieces = fewest; pieces < fewest + 16 && pieces <= vt; ++pieces) {
     const int64_t q = (vt + pieces - 1) / pieces, count = (vt + q - 1) / q, rest = vt - (count - 1) * q;
-    for (int s = 1; s <= 8; ++s) {
+    for (int s : kXentSplits) {
       // Every split of every piece has its k-tiles (three at least).
       if (s > 1 && rest * e / bk / s < 3) break;
       auto one = [&](int64_t tiles) {
@@ -562,8 +567,9 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
     }
     if ((dW || dH) && (e = launch_xent_grads<T>(b, h, (int)edge, st)) != hipSuccess) return NS_ERR_HIP;
   }
+  constexpr int64_t kOutCols = 64 * kVec<T>;
   if (dH)
-    hipLaunchKernelGGL((k_xent_dh_out<T>), dim3((unsigned)p.n), dim3(256), 0, st, p.acc, p.splits, p.n_pad, p.d_pad,
+    hipLaunchKernelGGL((k_xent_dh_out<T>), dim3((unsigned)p.n, (unsigned)((p.d + kOutCols - 1) / kOutCols)), dim3(64), 0, st, p.acc, p.splits, p.n_pad, p.d_pad,
                        reinterpret_cast<T*>(dH), lddh, (int)p.d, p.coef, p.gmax, d_status,
                        (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT));
   return launched();

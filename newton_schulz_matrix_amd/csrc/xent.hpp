@@ -877,21 +877,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_xent_grads(XentDwArgs dw, XentD
 }
 
 // dH = the splits' sum, unscaled and rounded; rows without a gradient are
-// zeros, whatever W holds.
+// zeros, whatever W holds.  A thread per 16 bytes of the row: few rows come
+// with many splits, whose loads go eight at a time.
 template <typename T>
-__global__ void __launch_bounds__(256) k_xent_dh_out(const float* acc, int splits, int64_t n_pad, int64_t d_pad,
-                                                     T* out, int64_t ldo, int cols, const float* coef,
-                                                     const float* gmax, int32_t* d_status, int32_t status_bits) {
+__global__ void __launch_bounds__(64) k_xent_dh_out(const float* acc, int splits, int64_t n_pad, int64_t d_pad, T* out,
+                                                    int64_t ldo, int cols, const float* coef, const float* gmax,
+                                                    int32_t* d_status, int32_t status_bits) {
+  constexpr int V = kVec<T>;
   const int64_t r = blockIdx.x;
-  const float s = xent_unscale<T>(gmax);
-  const bool none = coef[r] == 0.f;
+  const int c = (blockIdx.y * 64 + threadIdx.x) * V;
   bool bad = false;
-  for (int c = threadIdx.x; c < cols; c += 256) {
-    float v = 0.f;
-    for (int k = 0; k < splits; ++k) v += acc[((int64_t)k * n_pad + r) * d_pad + c];
-    v = none ? 0.f : v * s;
-    bad |= !(fabsf(v) < kRoundsToInf<T>);
-    out[r * ldo + c] = from_f32<T>(v);
+  if (c < cols) {
+    f32x4 v[V / 4];
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q) v[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const float* a = acc + r * d_pad + c;
+    auto sum = [&](int k0, auto batch) {
+      constexpr int B = decltype(batch)::value;
+      f32x4 add[B][V / 4];
+#pragma unroll
+      for (int k = 0; k < B; ++k)
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) add[k][q] = reinterpret_cast<const f32x4*>(a + (k0 + k) * n_pad * d_pad)[q];
+#pragma unroll
+      for (int k = 0; k < B; ++k)
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[q][e] += add[k][q][e];
+    };
+    int k = 0;
+    for (; k + 8 <= splits; k += 8) sum(k, std::integral_constant<int, 8>{});
+    for (; k + 2 <= splits; k += 2) sum(k, std::integral_constant<int, 2>{});
+    if (k < splits) sum(k, std::integral_constant<int, 1>{});
+    const bool none = coef[r] == 0.f;
+    const float s = xent_unscale<T>(gmax);
+    T* row = out + r * ldo + c;
+    u32x4_t packed;
+    T* t = reinterpret_cast<T*>(&packed);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float x = none ? 0.f : v[k / 4][k % 4] * s;
+      bad |= c + k < cols && !(fabsf(x) < kRoundsToInf<T>);
+      t[k] = from_f32<T>(x);
+    }
+    if (c + V <= cols) {
+      *reinterpret_cast<typename Vec16<sizeof(T)>::type*>(row) = packed;
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (c + k < cols) row[k] = t[k];
+    }
   }
   if (d_status) report_status(d_status, status_bits, bad);
 }
