@@ -381,7 +381,9 @@ def _check_xent(n, d, v, dtype, dev, h, w, t, dloss, ignore_index=-100, dw_rows=
 
 
 XENT_SHAPES = [(1, 1, 1), (1, 64, 1000), (1, 4096, 70), (1, 7, 40000), (2, 128, 191), (3, 5, 9), (5, 1001, 77), (8, 96, 1000), (9, 100, 600), (17, 100, 193), (64, 64, 500), (128, 256, 385), (129, 192, 700),
-               (200, 1000, 777), (385, 320, 1153), (700, 64, 64)]
+               (200, 1000, 777), (385, 320, 1153), (700, 64, 64),
+               # Few rows: dH in many splits of the vocabulary.
+               (35, 130, 20011), (1, 72, 30000)]
 
 
 @pytest.mark.parametrize("n,d,v", XENT_SHAPES)
@@ -425,7 +427,7 @@ def test_linear_cross_entropy_strides_alignment_and_int32(dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_linear_cross_entropy_several_pieces(dtype):
-    # 2^27 elements of dz per piece: 20 000 rows take the vocabulary in
+    # 2^28 elements of dz per piece: 20 000 rows take the vocabulary in
     # several.  The oracle looks at rows of every part of the result.
     dev = _dev()
     n, d, v = 20_000, 64, 15_000
