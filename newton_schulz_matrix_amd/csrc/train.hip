@@ -275,6 +275,7 @@ GradRounds grad_rounds(const EdgeCost& c, int64_t dw_tiles, double dw_ktiles, in
   const double before = (double)(dw_tiles / grid) * one_w;
   GradRounds best;
   for (int64_t e = 0; e == 0 || (busy && e <= one_w / one_h + 1 && (e - 1) * idle < dh_tiles); ++e) {
+    if (before + e * one_h >= best.us) break;
     const int64_t left = std::max<int64_t>(0, dh_tiles - e * idle), r = (left + grid - 1) / grid;
     const double us = before + std::max(busy ? one_w + r * one_h : 0, (e + r) * one_h);
     if (us < best.us) best = {(int)e, us};
@@ -327,15 +328,17 @@ BackwardChoice choose_backward(const EdgeCost& c, int64_t n, int64_t d, int64_t 
   BackwardChoice best;
   for (int64_t pieces = fewest; pieces < fewest + 16 && pieces <= vt; ++pieces) {
     const int64_t q = (vt + pieces - 1) / pieces, count = (vt + q - 1) / q, rest = vt - (count - 1) * q;
+    auto logits = [&](int64_t tiles) { return product_us(c, m * tiles, (double)k / bk) + 12.0; };
+    const double base = (double)(count - 1) * logits(q) + logits(rest);
     for (int s : kXentSplits) {
       // Every split of every piece has its k-tiles (three at least).
       if (s > 1 && rest * e / bk / s < 3) break;
-      auto one = [&](int64_t tiles) {
-        const double sums = (double)s * m * dt * e * e * 8.0 / 4.5e6;  // fp32 read and written, in us
-        return product_us(c, m * tiles, (double)k / bk) +
-               grad_rounds(c, tiles * dt, (double)m * e / bk, m * dt * s, (double)(tiles * e / bk) / s).us + sums + 12.0;
+      const double sums = (double)s * m * dt * e * e * 8.0 / 4.5e6;  // fp32 read and written, in us
+      if (base + (double)count * sums >= best.us) break;
+      auto grads = [&](int64_t tiles) {
+        return grad_rounds(c, tiles * dt, (double)m * e / bk, m * dt * s, (double)(tiles * e / bk) / s).us + sums;
       };
-      const double us = (double)(count - 1) * one(q) + one(rest);
+      const double us = base + (double)(count - 1) * grads(q) + grads(rest);
       if (us < best.us) best = {q, s, us};
     }
   }

@@ -942,7 +942,7 @@ namespace nsr {
 using namespace nsk;
 
 // Tile edges of the products: square tiles of the large or the small edge
-// (a call's choice: xent_edge in train.hip); forward with few rows, 16-bit:
+// (choose_backward and xent_plan in train.hip choose); forward with few rows, 16-bit:
 // short, wide tiles.
 template <typename T> inline constexpr int kXentLarge = sizeof(T) == 2 ? 192 : 128;
 template <typename T> inline constexpr int kXentSmall = sizeof(T) == 2 ? 128 : 64;
