@@ -549,10 +549,11 @@ __global__ void __launch_bounds__(256) k_xent_dot(XentDotArgs p) {
 // at the targets then lie just below 1, where the type's relative step is
 // finest; fp16 as dz * 2^15 / max|g|, its largest entry just inside the type
 // and probabilities down to 2^-39 of it still held.  The products' results
-// are taken back in fp32.  (Coefficients so small that the quotient
-// overflows give gradients below 2^-100: the limit keeps them finite on the
-// way.)
+// are taken back in fp32.  The scale ends at a power of two, so that the
+// smallest coefficients do not make it infinite; results are taken back by
+// what was applied.
 template <typename T> inline constexpr float kDzUnit = __is_same(T, _Float16) ? 0x1p15f : 1.f;
+constexpr float kDzScaleMax = 0x1p113f;
 template <typename T>
 __device__ __forceinline__ float xent_scale(const XentArgs& p) {
   if constexpr (sizeof(T) == 2) {
@@ -568,13 +569,16 @@ __device__ __forceinline__ float xent_scale(const XentArgs& p) {
     }
     const float g = __uint_as_float(m);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.gmax = g;
-    return g > 0.f ? fminf(kDzUnit<T> / g, 1e34f) : 0.f;
+    return g > 0.f ? fminf(kDzUnit<T> / g, kDzScaleMax) : 0.f;
   }
   return 1.f;
 }
 template <typename T>
 __device__ __forceinline__ float xent_unscale(const float* gmax) {
-  if constexpr (sizeof(T) == 2) return *gmax / kDzUnit<T>;
+  if constexpr (sizeof(T) == 2) {
+    const float g = *gmax;
+    return g > 0.f && kDzUnit<T> / g > kDzScaleMax ? 1.f / kDzScaleMax : g / kDzUnit<T>;
+  }
   return 1.f;
 }
 
