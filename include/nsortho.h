@@ -498,9 +498,9 @@ ns_status ns_linear_cross_entropy(const void* H, int64_t ldh, const void* W,
  *            dtype.  Either may be NULL.
  * Rows whose target is ignored or out of range, and rows with dloss 0,
  * contribute exact zeros to dW, whatever their row of H holds, and their
- * rows of dH are zeros.  dz is rounded to dtype (fp16: scaled by
- * 2^15 / max|dloss| first, so dloss may span about 2^24 between rows); both
- * products accumulate in fp32.
+ * rows of dH are zeros.  dz is rounded to dtype, in units of the largest
+ * finite |dloss| (fp16: 2^-15 of it, so dloss may span about 2^24 between
+ * rows; bf16: 2^24 times it); both products accumulate in fp32.
  *   workspace   ns_linear_cross_entropy_workspace_size(..., aligned, 1)
  *            bytes.
  */

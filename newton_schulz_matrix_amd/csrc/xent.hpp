@@ -545,15 +545,19 @@ __global__ void __launch_bounds__(256) k_xent_dot(XentDotArgs p) {
   }
 }
 
-// 16-bit types hold dz in units of max|g|: bf16 as dz / max|g|, whose entries
-// at the targets then lie just below 1, where the type's relative step is
-// finest; fp16 as dz * 2^15 / max|g|, its largest entry just inside the type
-// and probabilities down to 2^-39 of it still held.  The products' results
-// are taken back in fp32.  The scale ends at a power of two, so that the
-// smallest coefficients do not make it infinite; results are taken back by
+// 16-bit types hold dz in units of max|g|, so that the entries at the targets
+// lie just below a power of two, where the type's relative step is finest.
+// fp16: dz * 2^15 / max|g|, its largest entry just inside the type and
+// probabilities down to 2^-39 of it still held; its operands end at 2^16, far
+// from where the fp32 sums do.  bf16, whose operands reach as far as the sums:
+// dz * 2^-24 / max|g|, so that 2^23 rows of the largest numbers still add up
+// within fp32, with probabilities down to 2^-102 among its normal numbers.
+// The products' results are taken back in fp32.  The scale stays between two
+// powers of two, so that neither it nor its inverse is infinite or loses
+// digits for the smallest and largest coefficients; results are taken back by
 // what was applied.
-template <typename T> inline constexpr float kDzUnit = __is_same(T, _Float16) ? 0x1p15f : 1.f;
-constexpr float kDzScaleMax = 0x1p113f;
+template <typename T> inline constexpr float kDzUnit = __is_same(T, _Float16) ? 0x1p15f : 0x1p-24f;
+constexpr float kDzScaleMin = 0x1p-126f, kDzScaleMax = 0x1p113f;
 template <typename T>
 __device__ __forceinline__ float xent_scale(const XentArgs& p) {
   if constexpr (sizeof(T) == 2) {
@@ -569,15 +573,15 @@ __device__ __forceinline__ float xent_scale(const XentArgs& p) {
     }
     const float g = __uint_as_float(m);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.gmax = g;
-    return g > 0.f ? fminf(kDzUnit<T> / g, kDzScaleMax) : 0.f;
+    return g > 0.f ? fminf(fmaxf(kDzUnit<T> / g, kDzScaleMin), kDzScaleMax) : 0.f;
   }
   return 1.f;
 }
 template <typename T>
 __device__ __forceinline__ float xent_unscale(const float* gmax) {
   if constexpr (sizeof(T) == 2) {
-    const float g = *gmax;
-    return g > 0.f && kDzUnit<T> / g > kDzScaleMax ? 1.f / kDzScaleMax : g / kDzUnit<T>;
+    const float g = *gmax, scale = g > 0.f ? kDzUnit<T> / g : 1.f;
+    return scale < kDzScaleMin ? 1.f / kDzScaleMin : scale > kDzScaleMax ? 1.f / kDzScaleMax : g / kDzUnit<T>;
   }
   return 1.f;
 }
