@@ -538,6 +538,8 @@ ns_status xent_backward(const XentPlan& p, const void* H, int64_t ldh, const voi
     if (e != hipSuccess) return NS_ERR_HIP;
     XentDwArgs b{};
     b.gmax = p.gmax;
+    b.d_status = d_status;
+    b.status_bits = (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT);
     if (dW) {
       b.L = p.dzt;
       b.R = p.HT;
