@@ -515,7 +515,8 @@ __global__ void __launch_bounds__(256) k_norm_cols(NormBwdArgs p) {
 // dw and db from `parts` partial rows: 16 groups of threads take every 16th
 // partial of 64 columns each, and join in a fixed order.
 template <typename PT>
-__global__ void __launch_bounds__(1024) k_norm_join(const float* partial, int parts, int cols, PT* dw, PT* db) {
+__global__ void __launch_bounds__(1024) k_norm_join(const float* partial, int parts, int cols, PT* dw, PT* db,
+                                                    int32_t* d_status, int32_t status_bits) {
   __shared__ float sh[16][64];
   const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane, width = 2 * (int64_t)cols;
@@ -530,11 +531,9 @@ __global__ void __launch_bounds__(1024) k_norm_join(const float* partial, int pa
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s += sh[i][lane];
-    if (c < cols) {
-      if (dw) dw[c] = from_f32<PT>(s);
-    } else {
-      if (db) db[c - cols] = from_f32<PT>(s);
-    }
+    PT* out = c < cols ? dw : db;
+    if (out) out[c < cols ? c : c - cols] = from_f32<PT>(s);
+    if (d_status) report_status(d_status, status_bits, out && !(fabsf(s) < kRoundsToInf<PT>));
   }
 }
 

@@ -643,7 +643,7 @@ ns_status ns_layer_norm_backward(const void* dY, int64_t lddy, const void* X, in
     if (params)
       hipLaunchKernelGGL((k_norm_join<PT>), dim3((unsigned)((2 * cols + 63) / 64)), dim3(1024), 0, st,
                          reinterpret_cast<const float*>(workspace), (int)(rows > 0 ? parts : 0), (int)cols,
-                         reinterpret_cast<PT*>(dweight), reinterpret_cast<PT*>(dbias));
+                         reinterpret_cast<PT*>(dweight), reinterpret_cast<PT*>(dbias), d_status, a.status_bits);
     return launched();
   });
 }

@@ -54,3 +54,40 @@ def test_cross_entropy_reports_an_overflowing_weight_gradient(n, d, v, dtype, ne
         assert torch.isfinite(dw[:v - 1]).all() and torch.count_nonzero(dw[:, :d - 1]) == 0
         assert not need_dh or torch.count_nonzero(dh) == 0
         assert int(st.item()) == (BAD if overflows else 0)
+
+
+# ---------------------------------------------------------------------------
+# Layer norm: the parameters' gradients.
+# ---------------------------------------------------------------------------
+
+# Rows that share a wave, rows of a block, rows in registers of 1024 threads,
+# rows that are taken element by element, and less than a vector.
+@pytest.mark.parametrize("rows,cols", [(10000, 768), (10000, 97), (6000, 4096), (4000, 9000), (2000, 20001), (10000, 4)])
+@pytest.mark.parametrize("which", ["dbias", "dweight"])
+def test_layer_norm_reports_overflowing_parameter_gradients(rows, cols, which):
+    # Every other row of x is turned round, so that one of the two sums
+    # cancels and the other grows to 80000 times a number of about 1: past
+    # fp16, well inside the dx that the same call writes, and inside fp32.
+    dev = _dev()
+    print(f"norm sums {rows}x{cols} {which}", flush=True)
+    g = torch.Generator().manual_seed(cols)
+    sign = (1 - 2 * (torch.arange(rows) % 2)).float()[:, None].to(dev)
+    base = torch.where(torch.arange(cols) % 2 == 0, 1.0, -1.0) * (1 + 0.25 * torch.rand(cols, generator=g))
+    base = (base - base.mean()).half().to(dev)
+    x = base * sign.half()
+    size = 80000.0 / rows
+    dy = torch.full((rows, cols), size, device=dev).half() if which == "dbias" else (size * sign).half().expand(rows, cols).contiguous()
+    for pdtype, overflows in ((torch.float16, True), (torch.float32, False)):
+        w = torch.ones(cols, dtype=pdtype, device=dev)
+        _, mean, rstd = nsa.layer_norm(x, w)
+        st = _word(dev)
+        dx, dw, db = nsa.layer_norm_backward(dy, x, mean, rstd, w, status=st)
+        assert torch.isfinite(dx).all()
+        grown, cancelled = (db, dw) if which == "dbias" else (dw, db)
+        assert torch.isfinite(cancelled).all() and torch.isinf(grown).any() == overflows
+        assert not torch.isnan(grown).any()
+        assert int(st.item()) == (BAD if overflows else 0)
+        # Without the parameters' gradients there is nothing to report.
+        st.zero_()
+        nsa.layer_norm_backward(dy, x, mean, rstd, w, params=False, status=st)
+        assert int(st.item()) == 0
