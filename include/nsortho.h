@@ -465,7 +465,8 @@ ns_status ns_embedding_backward(const void* ids, int32_t ids64, int64_t n,
  *   targets  rows ids, int64 (targets64 == 1) or int32.  A row whose target
  *            is ignore_index has loss 0 (its lse is still computed); any
  *            other target outside [0, vocab) gives loss NaN and sets
- *            NS_STATUS_BAD_INDEX.
+ *            NS_STATUS_BAD_INDEX (alone: that NaN is not counted as a
+ *            non-finite result).
  *   loss, lse   rows floats each.  A row of logits that holds a NaN or
  *            +Inf gives NaN; -Inf logits count as probability 0.
  *   rows, vocab <= 2^23, rows * vocab <= 2^42, cols <= 2^20, ldh and

@@ -403,10 +403,13 @@ struct PartJoin {
   __device__ __forceinline__ void finish(const XentJoinArgs& p, int64_t row) const {
     const float lse = m + kLn2 * __builtin_amdgcn_logf(s);
     const int t = p.targets.at(row);
+    const float loss = t >= 0 ? lse - p.zt[row] : 0.f;
     p.lse[row] = lse;
-    p.loss[row] = t >= 0 ? lse - p.zt[row] : t == kTargetBad ? __builtin_nanf("") : 0.f;
+    p.loss[row] = t == kTargetBad ? __builtin_nanf("") : loss;
     if (p.d_status) {
-      if (!(fabsf(lse) < __builtin_inff())) atomicOr(p.d_status, p.status_bits);
+      // A target's logit of -inf makes the loss infinite and leaves lse finite.
+      const float inf = __builtin_inff();
+      if (!(fabsf(lse) < inf && fabsf(loss) < inf)) atomicOr(p.d_status, p.status_bits);
       if (t == kTargetBad) atomicOr(p.d_status, p.index_bit);
     }
   }

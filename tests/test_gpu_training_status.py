@@ -91,3 +91,38 @@ def test_layer_norm_reports_overflowing_parameter_gradients(rows, cols, which):
         st.zero_()
         nsa.layer_norm_backward(dy, x, mean, rstd, w, params=False, status=st)
         assert int(st.item()) == 0
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy: the loss.
+# ---------------------------------------------------------------------------
+
+# One row by whole rows of W; tiles with a block's join per row; short, wide
+# tiles; many rows' join.
+@pytest.mark.parametrize("n,d,v", [(1, 64, 100), (6, 100, 300), (40, 64, 300), (500, 72, 400), (1500, 64, 300)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_cross_entropy_reports_an_infinite_loss(n, d, v, dtype):
+    # A weight row of -inf against positive hidden states: that logit is
+    # -inf, lse finite, and the loss +inf for the row whose target it is.
+    dev = _dev()
+    print(f"infinite loss n={n} d={d} v={v} {dtype}", flush=True)
+    g = torch.Generator().manual_seed(n)
+    h = (0.1 + torch.rand(n, d, generator=g)).to(DTYPES[dtype]).to(dev)
+    w = (torch.randn(v, d, generator=g) / d).to(DTYPES[dtype]).to(dev)
+    w[5] = -float("inf")
+    t = torch.full((n,), 9, dtype=torch.int64, device=dev)
+    st = _word(dev)
+    loss, lse = nsa.linear_cross_entropy(h, w, t, status=st)
+    assert torch.isfinite(loss).all() and torch.isfinite(lse).all() and int(st.item()) == 0
+    t[n - 1] = 5
+    loss, lse = nsa.linear_cross_entropy(h, w, t, status=st)
+    assert torch.isfinite(lse).all() and torch.isfinite(loss[:n - 1]).all()
+    assert float(loss[n - 1]) == float("inf") and int(st.item()) == BAD
+    # An ignored row's loss is 0 whatever its logits, a bad target's NaN is
+    # reported by its own bit alone.
+    st.zero_()
+    loss, lse = nsa.linear_cross_entropy(h, w, t, ignore_index=5, status=st)
+    assert float(loss[n - 1]) == 0 and int(st.item()) == 0
+    t[n - 1] = v
+    loss, lse = nsa.linear_cross_entropy(h, w, t, status=st)
+    assert torch.isnan(loss[n - 1]) and int(st.item()) == B.STATUS_BAD_INDEX
