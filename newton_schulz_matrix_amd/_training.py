@@ -19,8 +19,16 @@ from . import _binding as B
 from ._binding import NSError, _check, dtype_code, lib
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device index
-_current_device = torch._C._cuda_getDevice
+def _stream_of(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The current stream's handle by device index, and the current device: the
+# functions behind torch's public ones where this torch has them (1.2 us less
+# in a call of 10 us).  A torch built for no GPU has not, and its tensors
+# never get as far as a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name: str, device: torch.device, *args) -> None:
