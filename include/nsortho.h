@@ -391,6 +391,8 @@ ns_status ns_muon_step(void* W, const void* G, float* M, int64_t batch,
  *                  may be NULL (ones, zeros).
  *   mean, rstd     rows floats each, for the backward pass; either may be
  *                  NULL.
+ *   A row whose variance is infinite in fp32 (deviations past 2^64 / sqrt(cols))
+ *   has rstd 0 and is reported like a non-finite result.
  *   Y may be X (with ldy == ldx).
  */
 ns_status ns_layer_norm(const void* X, int64_t rows, int64_t cols, int64_t ldx,

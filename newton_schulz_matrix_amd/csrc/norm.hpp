@@ -273,7 +273,9 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) k_norm_fwd(NormFwdArgs p) {
         q = in(c, k) ? fmaf(f[i][k], f[i][k], q) : q;
       }
     }
-    const float rstd = 1.f / sqrtf(row_sum<TPR>(q, sh) / n + p.eps);
+    // Squares past fp32 make rstd 0, and y finite but not the formula's: reported.
+    const float var = row_sum<TPR>(q, sh) / n, rstd = 1.f / sqrtf(var + p.eps);
+    bad |= !(var < __builtin_inff());
     if constexpr (!kHold) fetch_params();
     IO* y = reinterpret_cast<IO*>(p.Y) + row * p.ldy;
 #pragma unroll
@@ -315,7 +317,8 @@ __global__ void __launch_bounds__(1024) k_norm_fwd_long(NormFwdArgs p) {
       const float d = to_f32<IO>(x[c]) - mean;
       q = fmaf(d, d, q);
     }
-    const float rstd = 1.f / sqrtf(row_sum<1024>(q, sh) / n + p.eps);
+    const float var = row_sum<1024>(q, sh) / n, rstd = 1.f / sqrtf(var + p.eps);
+    bad |= !(var < __builtin_inff());
     for (int c = threadIdx.x; c < p.cols; c += 1024) {
       float v = (to_f32<IO>(x[c]) - mean) * rstd;
       if (W) v *= to_f32<PT>(W[c]);

@@ -126,3 +126,26 @@ def test_cross_entropy_reports_an_infinite_loss(n, d, v, dtype):
     t[n - 1] = v
     loss, lse = nsa.linear_cross_entropy(h, w, t, status=st)
     assert torch.isnan(loss[n - 1]) and int(st.item()) == B.STATUS_BAD_INDEX
+
+
+# ---------------------------------------------------------------------------
+# Layer norm: a variance that fp32 does not hold.
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,cols", [(3, 64), (5, 768), (4, 1001), (3, 4096), (2, 9000), (2, 20001), (2, 3)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_layer_norm_reports_an_infinite_variance(rows, cols, dtype):
+    # Deviations past 2^64 have infinite squares in fp32: rstd comes out as 0
+    # and y as 0 (or the bias), finite and wrong, which the word says.
+    dev = _dev()
+    print(f"infinite variance {rows}x{cols} {dtype}", flush=True)
+    x = torch.where(torch.arange(cols, device=dev) % 2 == 0, 1.0, -1.0).expand(rows, cols).contiguous()
+    st = _word(dev)
+    for size, reported in ((2.0 ** 55, False), (2.0 ** 66, True)):
+        scaled = x.clone()
+        scaled[rows - 1] *= size
+        y, mean, rstd = nsa.layer_norm(scaled.to(DTYPES[dtype]), status=st)
+        assert torch.isfinite(y).all() and torch.isfinite(rstd).all()
+        assert (float(rstd[rows - 1]) == 0) == reported
+        assert int(st.item()) == (BAD if reported else 0)
+        st.zero_()
