@@ -150,18 +150,6 @@ template <> __device__ __forceinline__ void mma_chunk<float>(const uint4& a, con
 // loop) and the k-tile's byte offset as the scalar offset, so a copy costs
 // no vector address arithmetic.  The offsets stay below 2^32: a wave covers
 // at most 64 rows of at most 2^25 bytes (the plan's limit on a row).
-//
-// An operand that is the caller's own matrix ends inside its last tile; its
-// loader is given the valid rows and their bytes (RowBound) and the resource
-// then ends with the last valid row, so that nothing past it is read: a lane
-// offset in an invalid row lies past the end whether or not the hardware
-// counts the scalar offset in its check, one in a valid row never does.
-// What lands in LDS for the invalid rows reaches only their own outputs.
-struct RowBound {
-  int rows;            // valid rows of the tile, >= 1
-  uint32_t row_bytes;  // bytes of one row that may be read, <= its stride
-};
-
 template <int ROWS>
 struct DmaLoader {
   static_assert(ROWS % 32 == 0, "each wave fills whole groups of 8 rows");
@@ -181,20 +169,13 @@ struct DmaLoader {
     // the offset is a multiple of 256 bytes).
     return (lane_off + (uint32_t)i * ld8) ^ (uint32_t)((q & 7) << 4);
   }
-  // g: operand tile base (its first row), ld_bytes: row stride, bound: null
-  // when every row of the tile may be read.
-  __device__ __forceinline__ void init(const char* g, int64_t ld_bytes, const RowBound* bound = nullptr) {
+  // g: operand tile base (its first row), ld_bytes: row stride.
+  __device__ __forceinline__ void init(const char* g, int64_t ld_bytes) {
     const int lane = threadIdx.x & 63;
     wave_row0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kRowsPerWave;
-    int records = -1;
-    if (bound) {
-      const int left = bound->rows - wave_row0;
-      records = left <= 0 ? 0 : (int)((uint32_t)((left < kRowsPerWave ? left : kRowsPerWave) - 1) * (uint32_t)ld_bytes +
-                                      bound->row_bytes);
-    }
-    // Word 3 of the resource: the raw (untyped) buffer format; without a
-    // bound no limit below 2^32 bytes.
-    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(g) + (int64_t)wave_row0 * ld_bytes, (short)0, records,
+    // Word 3 of the resource: the raw (untyped) buffer format; no bounds
+    // limit below 2^32 bytes.
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(g) + (int64_t)wave_row0 * ld_bytes, (short)0, -1,
                                              0x00020000);
     lane_off = (uint32_t)((lane >> 3) * ld_bytes) + (uint32_t)((((lane & 7) ^ (lane >> 3))) << 4);
     ld8 = (uint32_t)(8 * ld_bytes);
@@ -443,8 +424,7 @@ __device__ __forceinline__ void pipe_step(const char* Lg, const char* Rg, const 
 template <typename T, int TM, int TN, int kExtraLoads, int G, class AfterCopies, class Capture>
 __device__ __forceinline__ void mainloop(const char* Lg, int64_t ldl_bytes, const char* Rg, int64_t ldr_bytes,
                                          int kt0, int kt1, Acc<T, TM, TN>& acc, bool extra_loads,
-                                         AfterCopies&& after_copies, Capture&& capture,
-                                         const RowBound* bound_l = nullptr, const RowBound* bound_r = nullptr) {
+                                         AfterCopies&& after_copies, Capture&& capture) {
   constexpr int FM = TM / 64, FN = TN / 64;
   constexpr int kOffR = TM * kRowBytes;
   constexpr int kDma = TM / 32 + TN / 32;  // copy instructions per k-tile per wave
@@ -464,8 +444,8 @@ __device__ __forceinline__ void mainloop(const char* Lg, int64_t ldl_bytes, cons
   fa.init(wr, wc);
   DmaLoader<TM> la;
   DmaLoader<TN> lb;
-  la.init(Lg, ldl_bytes, bound_l);
-  lb.init(Rg, ldr_bytes, bound_r);
+  la.init(Lg, ldl_bytes);
+  lb.init(Rg, ldr_bytes);
 
   // Prologue: k-tiles kt0, kt0+1 (and kt0+2 with three stages), clamped,
   // into stages 0, 1 (and 2), then the MFMAs of substeps 0 and 1 of kt0.

@@ -104,6 +104,13 @@ __device__ __forceinline__ void stream_tiles(int count, int64_t ldl, int64_t ldr
   const int wr = (w >> 1) * (TM / 2), wc = (w & 1) * (TN / 2);
 
   // Copy side: the tile being copied (c) and the one after it (n).
+  //
+  // An operand that is the caller's own matrix ends inside its last tile, so a
+  // wave's resource ends with its last valid row (rec_l, rec_r bytes) and
+  // nothing past it is read: a lane offset in an invalid row lies past the end
+  // whether or not the hardware counts the scalar offset in its check, one in
+  // a valid row never does.  What lands in LDS for the invalid rows reaches
+  // only their own outputs.
   DmaLoader<TM> la;
   DmaLoader<TN> lb;
   struct Side {
