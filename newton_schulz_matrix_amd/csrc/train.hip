@@ -26,7 +26,6 @@ inline bool known(ns_dtype d) { return d == NS_BF16 || d == NS_FP16 || d == NS_F
 inline int bytes_of(ns_dtype d) { return d == NS_FP32 ? 4 : 2; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 inline ns_status launched() { return hipGetLastError() == hipSuccess ? NS_OK : NS_ERR_HIP; }
-inline ns_status launched(hipError_t e) { return e == hipSuccess ? NS_OK : NS_ERR_HIP; }
 // Grids of the kernels that loop over their rows stay below this many blocks
 // (a launch may not have 2^32 threads).
 constexpr int64_t kMaxBlocks = 1 << 20;
