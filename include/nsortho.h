@@ -550,6 +550,21 @@ int64_t ns_plan_kernels_grouped(int64_t n, int64_t m, int64_t count,
                                 ns_dtype dtype, ns_mode mode, int32_t steps,
                                 const ns_options* opt, char* buf, size_t len);
 
+/*
+ * The same for ns_linear_cross_entropy (backward == 0) or its gradients
+ * (backward == 1), with the arguments of
+ * ns_linear_cross_entropy_workspace_size.  Entries, in launch order, op the
+ * operands' type: prep<op> (targets, copies), fwd<op,rows x columns of a
+ * tile>, join or joinrow (a block per 16 rows or per row); for a few rows
+ * dot<op,rows,form> instead of prep and fwd (form: even, ragged or tiny rows
+ * against 16-byte vectors); dz<op,edge>, grads<op,edge> and dhout<op>, after
+ * them pieces=P, the pieces that the vocabulary is taken in, and splits=S,
+ * dH's splits of a piece; zero<op> (gradients without rows).
+ */
+int64_t ns_plan_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab,
+                                     ns_dtype dtype, int32_t aligned,
+                                     int32_t backward, char* buf, size_t len);
+
 /* Static description of a status code. */
 const char* ns_status_string(ns_status s);
 

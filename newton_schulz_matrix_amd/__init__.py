@@ -23,7 +23,8 @@ from ._training import (embedding, embedding_backward,
                         embedding_workspace_size, layer_norm,
                         layer_norm_backward, layer_norm_workspace_size,
                         linear_cross_entropy, linear_cross_entropy_backward,
-                        linear_cross_entropy_workspace_size)
+                        linear_cross_entropy_workspace_size,
+                        plan_linear_cross_entropy)
 from .coeffs import fit_coefficients, root_coefficients
 
 __all__ = [
@@ -36,6 +37,7 @@ __all__ = [
     "embedding_workspace_size", "layer_norm", "layer_norm_backward",
     "layer_norm_workspace_size", "linear_cross_entropy",
     "linear_cross_entropy_backward", "linear_cross_entropy_workspace_size",
+    "plan_linear_cross_entropy",
     "gram_flops", "ns_flops", "standard_flops",
     "fit_coefficients", "root_coefficients",
 ]

@@ -207,6 +207,11 @@ _SIGNATURES = {
                                                 ctypes.c_int64, ctypes.c_int,
                                                 ctypes.c_int32,
                                                 ctypes.c_int32]),
+    "ns_plan_linear_cross_entropy": (ctypes.c_int64,
+                                     [ctypes.c_int64, ctypes.c_int64,
+                                      ctypes.c_int64, ctypes.c_int,
+                                      ctypes.c_int32, ctypes.c_int32,
+                                      ctypes.c_char_p, ctypes.c_size_t]),
     "ns_linear_cross_entropy": (ctypes.c_int,
                                 [ctypes.c_void_p, ctypes.c_int64,
                                  ctypes.c_void_p, ctypes.c_int64,

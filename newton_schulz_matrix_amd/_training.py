@@ -11,7 +11,8 @@ allocated by torch.  ``status`` is the device int32 status word.
 
 from __future__ import annotations
 
-from typing import Optional, Tuple, Union
+import ctypes
+from typing import List, Optional, Tuple, Union
 
 import torch
 
@@ -334,6 +335,22 @@ def linear_cross_entropy_workspace_size(rows: int, cols: int, vocab: int,
     return int(lib().ns_linear_cross_entropy_workspace_size(
         rows, cols, vocab, dtype_code(dtype), 1 if aligned else 0,
         1 if backward else 0))
+
+
+def plan_linear_cross_entropy(rows: int, cols: int, vocab: int,
+                              dtype: torch.dtype = torch.bfloat16,
+                              aligned: bool = True,
+                              backward: bool = False) -> List[str]:
+    """The kernel builds one call would launch, and for the gradients the
+    pieces of the vocabulary and dH's splits (host only, no device)."""
+    args = (rows, cols, vocab, dtype_code(dtype), 1 if aligned else 0,
+            1 if backward else 0)
+    need = int(lib().ns_plan_linear_cross_entropy(*args, None, 0))
+    if need < 0:
+        raise NSError(1, "ns_plan_linear_cross_entropy")
+    buf = ctypes.create_string_buffer(need)
+    lib().ns_plan_linear_cross_entropy(*args, buf, need)
+    return buf.value.decode().split()
 
 
 def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,

@@ -5,6 +5,7 @@
 // layout and kernel choice; the kernels are in norm.hpp, embed.hpp and
 // xent.hpp.
 #include <math.h>
+#include <stdio.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -409,6 +410,22 @@ XentPlan xent_plan(int64_t n, int64_t d, int64_t v, ns_dtype dtype, bool aligned
   return p;
 }
 
+// A call's launches as text (see ns_plan_linear_cross_entropy); the length
+// that it needs without the NUL.
+int describe_xent(const XentPlan& p, ns_dtype dtype, bool backward, char* buf, size_t len) {
+  const char* op = dtype == NS_FP32 ? "f32" : dtype == NS_FP16 ? "f16" : "bf16";
+  const char* join = p.waves || p.n <= kXentJoinRows ? "joinrow" : "join";
+  if (p.n == 0) return backward ? snprintf(buf, len, "zero<%s>", op) : snprintf(buf, len, "%s", "");
+  if (p.waves) {
+    const int64_t v = 16 / p.es;
+    const char* form = p.d % v == 0 ? "even" : p.d > v ? "ragged" : "tiny";
+    return snprintf(buf, len, "dot<%s,%d,%s> %s", op, xent_dot_rows(p.n), form, join);
+  }
+  if (!backward) return snprintf(buf, len, "prep<%s> fwd<%s,%dx%d> %s", op, op, (int)p.tm, (int)p.tn, join);
+  return snprintf(buf, len, "prep<%s> dz<%s,%d> grads<%s,%d> dhout<%s> pieces=%d splits=%d", op, op, (int)p.tm, op,
+                  (int)p.tm, op, (int)((p.v + p.piece - 1) / p.piece), p.splits);
+}
+
 // The products' copies take 16-byte chunks, swizzled by bits 4 to 6 of the
 // address within a row: rows a multiple of 128 bytes apart.
 bool xent_aligned(const void* H, int64_t ldh, const void* W, int64_t ldw, ns_dtype dtype) {
@@ -709,6 +726,13 @@ size_t ns_linear_cross_entropy_workspace_size(int64_t rows, int64_t cols, int64_
                                               int32_t aligned, int32_t backward) {
   if (!xent_shape_ok(rows, cols, vocab) || !known(dtype)) return 0;
   return std::max(kAlignTo, xent_plan(rows, cols, vocab, dtype, aligned != 0, backward != 0, nullptr).total);
+}
+
+int64_t ns_plan_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab, ns_dtype dtype, int32_t aligned,
+                                     int32_t backward, char* buf, size_t len) {
+  if (!xent_shape_ok(rows, cols, vocab) || !known(dtype)) return -1;
+  const XentPlan p = xent_plan(rows, cols, vocab, dtype, aligned != 0, backward != 0, nullptr);
+  return describe_xent(p, dtype, backward != 0, buf, buf ? len : 0) + 1;
 }
 
 ns_status ns_linear_cross_entropy(const void* H, int64_t ldh, const void* W, int64_t ldw, const void* targets,

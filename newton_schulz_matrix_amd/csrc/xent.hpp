@@ -993,17 +993,18 @@ template <typename T> hipError_t launch_xent_grads(const XentDwArgs& a, const Xe
 
 inline dim3 xent_grid(int64_t tiles) { return dim3((unsigned)(tiles < kXentGroups ? tiles : kXentGroups)); }
 
+// Rows of H that a build of k_xent_dot takes, for n of them.
+inline int xent_dot_rows(int64_t n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8; }
+
 template <typename T, int FORM>
 void launch_dot(const XentDotArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.waves + 3) / 4));
-  if (a.n <= 1)
-    hipLaunchKernelGGL((k_xent_dot<T, 1, FORM>), grid, dim3(256), 0, s, a);
-  else if (a.n <= 2)
-    hipLaunchKernelGGL((k_xent_dot<T, 2, FORM>), grid, dim3(256), 0, s, a);
-  else if (a.n <= 4)
-    hipLaunchKernelGGL((k_xent_dot<T, 4, FORM>), grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_xent_dot<T, 8, FORM>), grid, dim3(256), 0, s, a);
+  switch (xent_dot_rows(a.n)) {
+    case 1: hipLaunchKernelGGL((k_xent_dot<T, 1, FORM>), grid, dim3(256), 0, s, a); break;
+    case 2: hipLaunchKernelGGL((k_xent_dot<T, 2, FORM>), grid, dim3(256), 0, s, a); break;
+    case 4: hipLaunchKernelGGL((k_xent_dot<T, 4, FORM>), grid, dim3(256), 0, s, a); break;
+    default: hipLaunchKernelGGL((k_xent_dot<T, 8, FORM>), grid, dim3(256), 0, s, a);
+  }
 }
 
 #define NS_XENT_LAUNCH(K, TM, TN, TILES, ...) \
