@@ -44,6 +44,14 @@ __device__ __forceinline__ void border_first(const DmaLoader<TM>& la, const DmaL
   mma_frags<T, FM, FN>(fs.f2, acc);
   mma_frags<T, FM, FN>(fs.f3, acc);
 }
+// Waits until all but the `YOUNGER` latest memory operations (and the LDS
+// reads) are done.  More than the counter holds are cut to 62: 63, its
+// maximum, would not wait at all.
+template <int YOUNGER>
+__device__ __forceinline__ void wait_for_older() {
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(YOUNGER < 62 ? YOUNGER : 62));
+}
+
 // STORES: a lower bound on the epilogue's stores per wave, all of them issued
 // after the border's copies.
 template <typename T, int TM, int TN, int STORES>
@@ -57,8 +65,7 @@ __device__ __forceinline__ void border_second(const char* P, const FragAddr& fa,
   // The copies of the step before must have landed.  Memory operations
   // complete in order; younger than those copies are the border's own and the
   // epilogue's stores, which need not be waited for.
-  constexpr int kYounger = TM / 32 + TN / 32 + STORES;
-  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kYounger < 63 ? kYounger : 63));
+  wait_for_older<TM / 32 + TN / 32 + STORES>();
 }
 
 // pipe_step (products.hpp) for the first step after a border: the border's
@@ -79,8 +86,7 @@ __device__ __forceinline__ void first_step(const DmaLoader<TM>& la, const DmaLoa
   mma_frags<T, FM, FN>(fs.f0, acc);
   mma_frags<T, FM, FN>(fs.f1, acc);
   schedule_step<T, TM, TN, 1>();
-  constexpr int kYounger = TM / 32 + TN / 32 + STORES;
-  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kYounger < 63 ? kYounger : 63));
+  wait_for_older<TM / 32 + TN / 32 + STORES>();
   lds_barrier();
 }
 
