@@ -6,7 +6,9 @@ current stream of their tensors' device, write new tensors (or the ``out``
 given), never synchronize, and raise ValueError or TypeError for arguments
 that the library could not use.  ``workspace`` is an optional device buffer of
 the size that the matching ``*_workspace_size`` names; without it one is
-allocated by torch.  ``status`` is the device int32 status word.
+allocated by torch.  ``status`` is the device int32 status word.  No call
+builds an autograd graph: tensors that require a gradient are taken for their
+values, results never require one, and the backward calls are made by hand.
 """
 
 from __future__ import annotations
@@ -361,7 +363,7 @@ def linear_cross_entropy(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
     """Softmax cross entropy of the logits h w^T: returns (loss, lse), fp32.
 
     ``h``: [rows, cols] hidden states, ``w``: [vocab, cols] weights, of one
-    dtype; ``targets``: rows ids (int64 or int32).  The logits are never
+    dtype; ``targets``: rows ids (int64 or int32).  The logits are not
     stored.  A row whose target is ``ignore_index`` has loss 0; another
     target outside the vocabulary gives NaN and sets STATUS_BAD_INDEX.
     """
@@ -394,7 +396,9 @@ def linear_cross_entropy_backward(h: torch.Tensor, w: torch.Tensor,
     ``lse`` as returned by linear_cross_entropy; ``dloss``: the losses'
     gradients, fp32, one per row, or one number for all of them (1 / valid
     rows for a mean).  ``need_dh`` / ``need_dw`` False skip a gradient and
-    return None for it.
+    return None for it.  The workspace holds a piece of the logits' gradients
+    twice and transposed copies of h and of that piece of w, about a copy of w
+    however few the rows.
     """
     device, rows, cols, ldh, vocab, ldw, t64, aligned = _projection(h, w, targets)
     code = dtype_code(h.dtype)

@@ -236,8 +236,9 @@ constexpr int64_t kMaxXentLogits = int64_t(1) << 42;
 // Forward: up to kXentDotRows rows go without tiles (128000 x 4096 bf16: one
 // row 202 us against 226 with tiles, eight 279 against 231), up to
 // kXentDotRowsStaged where tiles would need staging copies of the operands,
-// which cost more than the product; up to kXentFewRows take the short, wide
-// tiles (16-bit).  Up to kXentJoinRows rows are joined by a block each.
+// which cost more than the product; both were measured there only and serve
+// every type and size.  Up to kXentFewRows take the short, wide tiles
+// (16-bit).  Up to kXentJoinRows rows are joined by a block each.
 constexpr int64_t kXentDotRows = 4, kXentDotRowsStaged = 8, kXentFewRows = kXentFewM, kXentJoinRows = 1024;
 constexpr int64_t kXentDotWaves = 4096;  // sixteen per compute unit
 

@@ -12,7 +12,8 @@
 // Backward goes over the vocabulary in pieces: a piece's logits are made
 // again, turned into dz in the product's epilogue, and used at once for
 // dW's rows of that piece and for dH, which adds up over the pieces in fp32.
-// One piece of dz (in both orientations) is all that is stored.
+// One piece of dz (in both orientations) and transposed copies of that piece
+// of W and of H are what is stored.
 //
 // Both are bound by the matrix cores (2 n v d forward, 4 n v d and the
 // logits again backward) unless n is small, where reading W bounds them.
@@ -23,8 +24,8 @@
 //
 // Measured (MI355X, bf16): 8192 x 4096 x 128000 forward 6.9 ms, 1250 TFLOP/s,
 // at a clock that power holds near 1.9 GHz; backward 4 pieces of 2.0 ms for
-// dz and 3.3 ms for the gradients.  16384 x 768 x 50257: 1.1 ms and 4 x (0.50
-// + 0.62) ms; products that short do not hide the writing of dz.
+// dz and 3.4 ms for the gradients.  16384 x 768 x 50257: 1.1 ms and 4 x (0.50
+// + 0.63) ms; products that short do not hide the writing of dz.
 #pragma once
 
 #include <hip/hip_runtime.h>
