@@ -9,10 +9,11 @@
 // once, backward reads x and dy and writes dx once.  A row therefore lives in
 // registers from its one read to its one write: TPR threads hold NV vectors
 // of 16 bytes each.  (The backward builds of 1024 threads, for rows past 8192
-// columns, have more than their 128 registers to hold and spill.)  The variance is the sum of squared deviations from the
-// finished mean, taken over the registers, so it does not lose its digits
-// when the mean is large against the spread.  All statistics and sums are
-// fp32; y, dx, dw and db are rounded once when stored.
+// columns, have more than their 128 registers to hold and spill.)  The
+// variance is the sum of squared deviations from the finished mean, taken
+// over the registers, so it does not lose its digits when the mean is large
+// against the spread.  All statistics and sums are fp32; y, dx, dw and db are
+// rounded once when stored.
 //
 // Measured (MI355X, bf16): forward 16384 x 768 13 us (3.9 TB/s, a launch's
 // ramp included), 8192 x 4096 24 us (5.6 TB/s), one row of 4096 2.6 us;
