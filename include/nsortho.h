@@ -515,6 +515,74 @@ ns_status ns_linear_cross_entropy_backward(
     void* workspace, size_t workspace_bytes, ns_stream_t stream);
 
 /*
+ * The rest of a block's training step
+ * -----------------------------------
+ * The optimizer of the parameters that the Muon step leaves out, and a
+ * transformer block's feed-forward half, whose matrices the Muon step
+ * updates: the gated feed-forward products and the norms before and after a
+ * block with its gate and residual, each forward and backward.  What is
+ * common to the training step's calls above holds here too.
+ *
+ * One AdamW step over `count` tensors (weight decay beside the update, as
+ * the NanoGPT recipe has it: Muon / NanoGPT article, "Engineering
+ * reproduction checklist", betas 0.9 and 0.95, weight decay 0.1).  With
+ * g = grad_scale * grad and t the step:
+ *
+ *     m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+ *     p <- p - lr weight_decay p
+ *            - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ *
+ *   tensors  host array, read before the call returns.  Each entry: numel
+ *            contiguous elements of param and grad (their types may differ),
+ *            moments, its own lr and weight decay (finite), reserved 0;
+ *            numel <= 2^40, 0 is allowed.
+ *     exp_avg, exp_avg_sq   m and v in fp32 (scales NULL), or e4m3 codes of
+ *            one byte each (scales given): with k = i / 256 the block of
+ *            element i and B = ceil(numel / 256),
+ *               m_i = code * scales[k] / 448,
+ *               sqrt(v_i) = code * scales[B + k] / 448,
+ *            scales[k] and scales[B + k] the largest |m_i| and sqrt(v_i) of
+ *            the block (2^-100 at least).  Zeros are a valid start.  The
+ *            step uses the moments before they are rounded to codes; a
+ *            positive root below the smallest code takes that code.
+ *     copy   NULL, or numel elements of copy_dtype that receive the new p
+ *            too (a 16-bit copy of an fp32 master).
+ *   step     t >= 1.  d_step: optional device int32 that holds t instead
+ *            (>= 1; for captured steps), read when the kernels run.
+ *   d_grad_scale, d_lr_scale   optional device floats: a factor of all
+ *            gradients (a clipping coefficient, a loss scale's inverse) and
+ *            one of all learning rates (a schedule).
+ *   0 <= beta1, beta2 < 1; eps >= 0 and finite.
+ * All arithmetic is fp32; p is rounded once to its type (an update below
+ * half a step of a 16-bit p is lost: keep such parameters in fp32).  Tensors
+ * must not overlap each other.  Non-finite new values of p, copy and fp32
+ * moments are reported; with 8-bit moments a NaN stays in its element and an
+ * infinite moment makes its whole block NaN.
+ * Any number of tensors takes ceil(count / 48) launches.
+ */
+typedef struct ns_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* scales;
+  void* copy;
+  int64_t numel;
+  float lr;
+  float weight_decay;
+  ns_dtype param_dtype;
+  ns_dtype grad_dtype;
+  ns_dtype copy_dtype;
+  int32_t reserved;
+} ns_adamw_tensor;
+
+ns_status ns_adamw_step(const ns_adamw_tensor* tensors, int64_t count,
+                        double beta1, double beta2, float eps, int64_t step,
+                        const int32_t* d_step, const float* d_grad_scale,
+                        const float* d_lr_scale, int32_t* d_status,
+                        ns_stream_t stream);
+
+/*
  * The kernel builds one call would launch, for inspection (host only;
  * touches no device).  Arguments as for ns_workspace_size, plus the step
  * count.  Writes a NUL-terminated, space-separated list of the distinct

@@ -25,6 +25,7 @@ from ._training import (embedding, embedding_backward,
                         linear_cross_entropy, linear_cross_entropy_backward,
                         linear_cross_entropy_workspace_size,
                         plan_linear_cross_entropy)
+from ._block import adamw_states, adamw_step
 from .coeffs import fit_coefficients, root_coefficients
 
 __all__ = [
@@ -37,7 +38,7 @@ __all__ = [
     "embedding_workspace_size", "layer_norm", "layer_norm_backward",
     "layer_norm_workspace_size", "linear_cross_entropy",
     "linear_cross_entropy_backward", "linear_cross_entropy_workspace_size",
-    "plan_linear_cross_entropy",
+    "plan_linear_cross_entropy", "adamw_states", "adamw_step",
     "gram_flops", "ns_flops", "standard_flops",
     "fit_coefficients", "root_coefficients",
 ]

@@ -233,6 +233,11 @@ _SIGNATURES = {
                                           ctypes.c_int64, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_size_t,
                                           ctypes.c_void_p]),
+    "ns_adamw_step": (ctypes.c_int,
+                      [ctypes.c_void_p, ctypes.c_int64, ctypes.c_double,
+                       ctypes.c_double, ctypes.c_float, ctypes.c_int64,
+                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                       ctypes.c_void_p, ctypes.c_void_p]),
     "ns_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "ns_version": (ctypes.c_int32, []),
 }

@@ -1,0 +1,291 @@
+// adamw.hpp - one AdamW step over many tensors.
+//
+//   g = s g0,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   p = p - lr wd p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+//
+// Bound by memory: every element of p, g, m and v is read once and p, m and v
+// are written once, 22 bytes an element with 16-bit p and g and fp32 moments,
+// 10 with 8-bit moments.
+//
+// The tensors come as a table in the kernel's arguments (no copy to the
+// device, no workspace), so a launch takes up to kAdamwItems of them, cut into
+// chunks that the blocks take in turn.
+//
+// 8-bit moments: blocks of 256 elements, each with the largest magnitude `top`
+// of its block in fp32 and e4m3 codes for x * (448 / top).  The second moment
+// is held by its root: v = g^2 spans twice the exponents of m, its root the
+// same, and an error of the root is what the update sees.  A positive root
+// below the smallest code (2^-9 of 448, 2^-17.8 of the block's largest) takes
+// that code: as 0 it would make the next update of that element as large as
+// its gradient's share of the second moment allows.  The step itself uses the
+// moments before they are rounded.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "norm.hpp"
+
+namespace nsk {
+
+constexpr int kAdamwItems = 48;                   // tensors of one launch: 3.6 KB of arguments
+constexpr int kAdamwThreads = 256, kAdamwEach = 8;  // elements of a thread: one 16-byte vector of a 16-bit type
+constexpr int kAdamwChunk = kAdamwThreads * kAdamwEach;
+constexpr int kStateBlock = 256;                  // elements that share a scale: 32 lanes of 8
+constexpr float kCodeTop = 448.f;                 // the largest e4m3 number
+constexpr float kCodeLeast = 0x1p-9f;             // and the smallest positive one
+constexpr float kScaleLeast = 0x1p-100f;          // keeps 448 / top finite
+
+struct AdamwItem {
+  void* p;
+  const void* g;
+  void *m, *v;
+  float* scales;  // [2][blocks of 256]: 8-bit moments; null: fp32 ones
+  void* copy;     // p rounded to another type, or null
+  int64_t n;
+  float lr, decay;
+  int32_t types;  // ns_dtype of p, g and copy in bits 0, 4 and 8
+  int32_t first;  // its first chunk
+};
+
+struct AdamwArgs {
+  AdamwItem item[kAdamwItems];
+  int count, chunks;
+  float b1, a1, b2, a2;  // a = 1 - b
+  float eps, c1, c2;     // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t); from d_step where that is given
+  double log_b1, log_b2;
+  const int32_t* d_step;
+  const float *d_grad_scale, *d_lr_scale;
+  int32_t* d_status;
+  int32_t status_bits;
+};
+
+// Eight consecutive elements of a type known at run time, as raw vectors and
+// as floats; `left`: how many of them there are.  The type is the same for a
+// whole block, so its branches cost no divergence.
+struct Eight {
+  u32x4_t q[2];
+};
+template <typename T>
+__device__ __forceinline__ void load_eight(const T* s, int64_t left, Eight& r) {
+  constexpr int N = 8 / kVec<T>;
+  if (left >= 8) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      r.q[i] = *reinterpret_cast<const typename Vec16<sizeof(T)>::type*>(s + i * kVec<T>);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      r.q[i] = u32x4_t{0u, 0u, 0u, 0u};
+      T* e = reinterpret_cast<T*>(&r.q[i]);
+#pragma unroll
+      for (int k = 0; k < kVec<T>; ++k)
+        if (i * kVec<T> + k < left) e[k] = s[i * kVec<T> + k];
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void floats_of(const Eight& r, float (&f)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = to_f32<T>(reinterpret_cast<const T*>(&r.q[k / kVec<T>])[k % kVec<T>]);
+}
+template <typename T>
+__device__ __forceinline__ bool store_eight(T* d, int64_t left, const float (&f)[8]) {
+  constexpr int N = 8 / kVec<T>;
+  Eight r;
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    reinterpret_cast<T*>(&r.q[k / kVec<T>])[k % kVec<T>] = from_f32<T>(f[k]);
+    bad |= k < left && !(fabsf(f[k]) < kRoundsToInf<T>);
+  }
+  if (left >= 8) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      *reinterpret_cast<typename Vec16<sizeof(T)>::type*>(d + i * kVec<T>) = r.q[i];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < left) d[k] = reinterpret_cast<const T*>(&r.q[k / kVec<T>])[k % kVec<T>];
+  }
+  return bad;
+}
+
+// Calls f(T{}) for an ns_dtype.
+template <class F>
+__device__ __forceinline__ void of_type(int type, F&& f) {
+  if (type == NS_FP32)
+    f(float{});
+  else if (type == NS_BF16)
+    f(__bf16{});
+  else
+    f(_Float16{});
+}
+
+// Eight e4m3 codes.
+struct Codes {
+  uint32_t w[2];
+};
+__device__ __forceinline__ Codes load_codes(const uint8_t* s, int64_t left) {
+  typedef uint32_t u32x2_b __attribute__((ext_vector_type(2), aligned(1)));
+  Codes c{{0u, 0u}};
+  if (left >= 8) {
+    const u32x2_b q = *reinterpret_cast<const u32x2_b*>(s);
+    c.w[0] = q[0];
+    c.w[1] = q[1];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < left) c.w[k / 4] |= (uint32_t)s[k] << (8 * (k % 4));
+  }
+  return c;
+}
+__device__ __forceinline__ void store_codes(uint8_t* d, int64_t left, const Codes& c) {
+  typedef uint32_t u32x2_b __attribute__((ext_vector_type(2), aligned(1)));
+  if (left >= 8) {
+    *reinterpret_cast<u32x2_b*>(d) = u32x2_b{c.w[0], c.w[1]};
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < left) d[k] = (uint8_t)(c.w[k / 4] >> (8 * (k % 4)));
+  }
+}
+__device__ __forceinline__ void decode(const Codes& c, float unit, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.w[i], false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.w[i], true);
+    f[4 * i] = lo[0] * unit;
+    f[4 * i + 1] = lo[1] * unit;
+    f[4 * i + 2] = hi[0] * unit;
+    f[4 * i + 3] = hi[1] * unit;
+  }
+}
+// Codes of f * inv; ROOT: positive numbers take the smallest code at least.
+template <bool ROOT>
+__device__ __forceinline__ Codes encode(const float (&f)[8], float inv) {
+  float q[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    q[k] = f[k] * inv;
+    if (ROOT) q[k] = f[k] > 0.f && q[k] < kCodeLeast ? kCodeLeast : q[k];
+  }
+  Codes c;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
+    c.w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], w, true);
+  }
+  return c;
+}
+
+// Largest of 32 lanes' values (>= 0, NaN passed over), in every one of them.
+template <int CTRL>
+__device__ __forceinline__ float max_dpp(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false);
+  return fmaxf(v, __builtin_bit_cast(float, o));
+}
+__device__ __forceinline__ float half_wave_max(float v) {
+  v = max_dpp<0xB1>(v);
+  v = max_dpp<0x4E>(v);
+  v = max_dpp<0x141>(v);
+  v = max_dpp<0x140>(v);
+  const uint32_t u = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
+static __global__ void __launch_bounds__(kAdamwThreads) k_adamw(AdamwArgs a) {
+  float c1 = a.c1, c2 = a.c2;
+  if (a.d_step) {
+    const double t = (double)*a.d_step;
+    c1 = (float)(-1.0 / expm1(t * a.log_b1));
+    c2 = (float)(1.0 / sqrt(-expm1(t * a.log_b2)));
+  }
+  const float gs = a.d_grad_scale ? *a.d_grad_scale : 1.f, lrs = a.d_lr_scale ? *a.d_lr_scale : 1.f;
+  // The first chunk's tensor: the last one that begins at or before it.
+  int i = 0;
+  for (int step = 32; step > 0; step >>= 1)
+    if (i + step < a.count && a.item[i + step].first <= (int)blockIdx.x) i += step;
+  bool bad = false;
+  for (int chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    while (i + 1 < a.count && a.item[i + 1].first <= chunk) ++i;
+    const AdamwItem& it = a.item[i];
+    const int64_t e = (int64_t)(chunk - it.first) * kAdamwChunk + threadIdx.x * kAdamwEach;
+    const int64_t left = it.n - e;
+    const int pt = it.types & 15, gt = it.types >> 4 & 15, ct = it.types >> 8 & 15;
+    const bool coded = it.scales != nullptr;
+    Eight rp{}, rg{}, rm{}, rv{};
+    Codes cm{}, cv{};
+    float um = 0.f, uv = 0.f;
+    const int64_t block = e / kStateBlock, blocks = (it.n + kStateBlock - 1) / kStateBlock;
+    if (left > 0) {
+      of_type(gt, [&](auto t) { load_eight(reinterpret_cast<const decltype(t)*>(it.g) + e, left, rg); });
+      of_type(pt, [&](auto t) { load_eight(reinterpret_cast<const decltype(t)*>(it.p) + e, left, rp); });
+      if (coded) {
+        cm = load_codes(reinterpret_cast<const uint8_t*>(it.m) + e, left);
+        cv = load_codes(reinterpret_cast<const uint8_t*>(it.v) + e, left);
+        um = it.scales[block] * (1.f / kCodeTop);
+        uv = it.scales[blocks + block] * (1.f / kCodeTop);
+      } else {
+        load_eight(reinterpret_cast<const float*>(it.m) + e, left, rm);
+        load_eight(reinterpret_cast<const float*>(it.v) + e, left, rv);
+      }
+    }
+    float p[8], g[8], m[8], v[8], root[8];
+    of_type(pt, [&](auto t) { floats_of<decltype(t)>(rp, p); });
+    of_type(gt, [&](auto t) { floats_of<decltype(t)>(rg, g); });
+    if (coded) {
+      decode(cm, um, m);
+      decode(cv, uv, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= v[k];
+    } else {
+      floats_of<float>(rm, m);
+      floats_of<float>(rv, v);
+    }
+    const float lr = it.lr * lrs, keep = lr * it.decay;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      g[k] *= gs;
+      m[k] = a.b1 * m[k] + a.a1 * g[k];
+      v[k] = a.b2 * v[k] + a.a2 * g[k] * g[k];
+      root[k] = sqrtf(v[k]);
+      p[k] = p[k] - keep * p[k] - lr * (c1 * m[k] / (root[k] * c2 + a.eps));
+    }
+    if (coded) {
+      // All 32 lanes of a block take part, those past the tensor's end with zeros.
+      float tm = 0.f, tv = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        tm = fmaxf(tm, fabsf(m[k]));
+        tv = fmaxf(tv, root[k]);
+        // An infinite second moment leaves p finite.
+        bad |= !(fabsf(m[k]) < __builtin_inff() && root[k] < __builtin_inff());
+      }
+      tm = fmaxf(half_wave_max(tm), kScaleLeast);
+      tv = fmaxf(half_wave_max(tv), kScaleLeast);
+      cm = encode<false>(m, kCodeTop / tm);
+      cv = encode<true>(root, kCodeTop / tv);
+      if (left > 0) {
+        store_codes(reinterpret_cast<uint8_t*>(it.m) + e, left, cm);
+        store_codes(reinterpret_cast<uint8_t*>(it.v) + e, left, cv);
+        if ((threadIdx.x & 31) == 0) {
+          it.scales[block] = tm;
+          it.scales[blocks + block] = tv;
+        }
+      }
+    } else if (left > 0) {
+      bad |= store_eight(reinterpret_cast<float*>(it.m) + e, left, m);
+      bad |= store_eight(reinterpret_cast<float*>(it.v) + e, left, v);
+    }
+    if (left > 0) {
+      of_type(pt, [&](auto t) { bad |= store_eight(reinterpret_cast<decltype(t)*>(it.p) + e, left, p); });
+      if (it.copy)
+        of_type(ct, [&](auto t) { bad |= store_eight(reinterpret_cast<decltype(t)*>(it.copy) + e, left, p); });
+    }
+  }
+  if (a.d_status) report_status(a.d_status, a.status_bits, bad);
+}
+
+}  // namespace nsk

@@ -53,6 +53,8 @@ come from the oracle itself):
   each gradient against central differences of the forward function along
   random directions; the forward functions against their defining properties
   (normalized rows, a one-hot product, log of a sum of exponentials).
+* ``adamw``: a constant gradient's first step (lr along its sign) and the
+  closed form of the moments.
 
 No function here is "parity unpinned".
 """
@@ -65,6 +67,7 @@ from .muon import momentum_update, muon_step
 from .training import (embedding, embedding_backward, layer_norm,
                        layer_norm_backward, linear_cross_entropy,
                        linear_cross_entropy_backward, linear_cross_entropy_dz)
+from .block import adamw, state_tops
 
 __all__ = [
     "CLASSIC_ABC", "TUNED_ABC", "coefficient_schedule", "frobenius_stage",
@@ -73,5 +76,5 @@ __all__ = [
     "soft_threshold_split", "momentum_update", "muon_step",
     "embedding", "embedding_backward", "layer_norm", "layer_norm_backward",
     "linear_cross_entropy", "linear_cross_entropy_backward",
-    "linear_cross_entropy_dz",
+    "linear_cross_entropy_dz", "adamw", "state_tops",
 ]
