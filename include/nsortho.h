@@ -583,6 +583,71 @@ ns_status ns_adamw_step(const ns_adamw_tensor* tensors, int64_t count,
                         ns_stream_t stream);
 
 /*
+ * The norms before and after a block with its gate and the scaled residual.
+ * With x the residual stream, z the block's output and n = cols:
+ *     rb_i = 1 / sqrt(sum_j z_ij^2 / n + eps)    (norm_branch; else 1)
+ *     s_ij = scale x_ij + gate_ij (z_ij rb_i branch_weight_j)
+ *     rs_i = 1 / sqrt(sum_j s_ij^2 / n + eps)
+ *     y_ij = s_ij rs_i weight_j
+ * s is the new residual stream and y the next block's input (formed from s
+ * before s is rounded).
+ *   X, Z     rows x cols with row strides ldx and ldz.  Z may be NULL: there
+ *            is then only y, the norm of x, and gate, branch_weight and S
+ *            have to be NULL and scale 1.
+ *   gate     groups x cols, contiguous, or NULL (ones): `groups` divides
+ *            rows, and rows / groups consecutive rows share a row of it (1: a
+ *            layer scale; one per sequence; rows: one per token).
+ *   branch_weight, weight   cols elements, or NULL (ones).  Gate and weights
+ *            have param_dtype (dtype or NS_FP32).
+ *   S, Y     rows x cols, row strides lds and ldy; Y may be NULL (no second
+ *            norm).  S may be X and Y may be Z, with equal strides.
+ *   branch_rstd, rstd   rows floats each, for the backward pass; either may
+ *            be NULL.
+ *   rows < 2^31, 1 <= cols <= 2^24; eps >= 0 and finite; scale finite.
+ *   A row whose mean square is infinite in fp32 has rstd 0 and is reported
+ *   like a non-finite result.
+ */
+ns_status ns_residual_norm(const void* X, int64_t ldx, const void* Z,
+                           int64_t ldz, int64_t rows, int64_t cols,
+                           ns_dtype dtype, const void* gate, int64_t groups,
+                           const void* branch_weight, const void* weight,
+                           ns_dtype param_dtype, float scale,
+                           int32_t norm_branch, float eps, void* S,
+                           int64_t lds, void* Y, int64_t ldy,
+                           float* branch_rstd, float* rstd, int32_t* d_status,
+                           ns_stream_t stream);
+
+/*
+ * Its gradients, from dS and dY, the gradients of s and y.  With
+ * shat = s rs, bhat = z rb and u = weight dY:
+ *     G = dS + rs (u - shat mean_j(u shat)),          dX = scale G
+ *     a = branch_weight gate G
+ *     dZ = rb (a - bhat mean_j(a bhat))   (rb given; else dZ = a)
+ *     dgate = sum of G bhat branch_weight over the rows that share it
+ *     dbranch_weight_j = sum_i gate G bhat,   dweight_j = sum_i dY shat
+ *   dS, dY   either may be NULL (zeros), not both.  S and rstd are read with
+ *            dY only.
+ *   Z, branch_rstd   as given to and written by ns_residual_norm;
+ *            branch_rstd NULL if the block's output was not normed.
+ *   dX may be NULL; dgate, dbranch_weight and dweight (param_dtype) too.
+ *   dX may be dS and dZ may be dY, with equal strides.  With no rows the
+ *   parameters' gradients are zeros.
+ *   workspace   ns_residual_norm_workspace_size(rows, cols) bytes, 256-byte
+ *            aligned.
+ */
+size_t ns_residual_norm_workspace_size(int64_t rows, int64_t cols);
+
+ns_status ns_residual_norm_backward(
+    const void* dS, int64_t ldds, const void* dY, int64_t lddy, const void* S,
+    int64_t lds, const void* Z, int64_t ldz, int64_t rows, int64_t cols,
+    ns_dtype dtype, const float* branch_rstd, const float* rstd,
+    const void* gate, int64_t groups, const void* branch_weight,
+    const void* weight, ns_dtype param_dtype, float scale, void* dX,
+    int64_t lddx, void* dZ, int64_t lddz, void* dgate, void* dbranch_weight,
+    void* dweight, int32_t* d_status, void* workspace, size_t workspace_bytes,
+    ns_stream_t stream);
+
+/*
  * The kernel builds one call would launch, for inspection (host only;
  * touches no device).  Arguments as for ns_workspace_size, plus the step
  * count.  Writes a NUL-terminated, space-separated list of the distinct

@@ -25,7 +25,8 @@ from ._training import (embedding, embedding_backward,
                         linear_cross_entropy, linear_cross_entropy_backward,
                         linear_cross_entropy_workspace_size,
                         plan_linear_cross_entropy)
-from ._block import adamw_states, adamw_step
+from ._block import (adamw_states, adamw_step, residual_norm,
+                     residual_norm_backward, residual_norm_workspace_size)
 from .coeffs import fit_coefficients, root_coefficients
 
 __all__ = [
@@ -39,6 +40,7 @@ __all__ = [
     "layer_norm_workspace_size", "linear_cross_entropy",
     "linear_cross_entropy_backward", "linear_cross_entropy_workspace_size",
     "plan_linear_cross_entropy", "adamw_states", "adamw_step",
+    "residual_norm", "residual_norm_backward", "residual_norm_workspace_size",
     "gram_flops", "ns_flops", "standard_flops",
     "fit_coefficients", "root_coefficients",
 ]

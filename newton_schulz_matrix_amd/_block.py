@@ -16,7 +16,9 @@ from typing import List, Optional, Sequence, Tuple, Union
 import torch
 
 from . import _binding as B
-from ._training import _call, _device, _status_ptr
+from ._binding import dtype_code, lib
+from ._training import (_call, _device, _output, _output_like, _param, _per_row, _ptr,
+                        _rows, _same_device, _status_ptr, _workspace_args)
 
 # ---------------------------------------------------------------------------
 # AdamW.
@@ -155,3 +157,163 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
           _scalar(grad_scale, torch.float32, device, "grad_scale"),
           _scalar(lr_scale, torch.float32, device, "lr_scale"),
           _status_ptr(status, device))
+
+
+# ---------------------------------------------------------------------------
+# Norms before and after a block.
+# ---------------------------------------------------------------------------
+
+def _like(t: torch.Tensor, x: torch.Tensor, device: torch.device, name: str) -> int:
+    """The row stride of a tensor of x's shape and dtype."""
+    if t.shape != x.shape or t.dtype != x.dtype:
+        raise ValueError(f"{name} must have the shape and dtype of the other tensors")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return _rows(t, name)[2]
+
+
+def _gate_groups(gate: Optional[torch.Tensor], x: torch.Tensor, rows: int, cols: int) -> int:
+    if gate is None:
+        return 0
+    if gate.dtype != x.dtype and gate.dtype != torch.float32:
+        raise TypeError("gate must have the data's dtype or float32")
+    if gate.device != x.device or not gate.is_contiguous() or gate.dim() < 1 or gate.shape[-1] != cols:
+        raise ValueError(f"gate must be a contiguous tensor on {x.device} whose last axis has {cols} elements")
+    groups = gate.numel() // cols
+    if groups < 1 or (rows and (groups > rows or rows % groups)):
+        raise ValueError("gate must have rows that divide the data's")
+    return groups
+
+
+def _param_dtype(x: torch.Tensor, **params: Optional[torch.Tensor]) -> torch.dtype:
+    """The one type of the gate and the weights (x's without any)."""
+    types = {p.dtype for p in params.values() if p is not None}
+    if len(types) > 1:
+        raise TypeError(f"{', '.join(params)} must have the same dtype")
+    return types.pop() if types else x.dtype
+
+
+def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                  branch_weight: Optional[torch.Tensor] = None,
+                  weight: Optional[torch.Tensor] = None, norm_branch: bool = True,
+                  norm_out: bool = True, eps: float = 1e-6, stats: bool = True,
+                  out: Optional[torch.Tensor] = None,
+                  out_norm: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None):
+    """scale * residual + gate * rms_norm(branch), and its RMS norm.
+
+    Returns (stream, normed, branch_rstd, rstd): the new residual stream, the
+    next block's input, and what the backward pass takes (fp32, one per row;
+    None with ``stats=False`` or without that norm).  ``residual`` and
+    ``branch`` (the block's output): one shape and dtype, 2-D with contiguous
+    rows or contiguous of any rank.  ``gate``: contiguous, last axis as the
+    data's; each of its rows is shared by as many consecutive rows of the
+    data (one row: a layer scale; one per sequence; one per token).
+    ``branch_weight`` and ``weight`` scale the two norms.  Gate and weights
+    have the data's dtype or float32, all the same.  ``norm_branch=False``
+    takes the branch as it is (times branch_weight), ``norm_out=False`` gives
+    no normed.  Without ``branch`` only normed is computed, the norm of
+    ``residual`` itself, which is returned as the stream.  ``out`` (the
+    stream) may be ``residual`` and ``out_norm`` may be ``branch``.
+    """
+    device = _device(residual)
+    rows, cols, ldx = _rows(residual, "residual")
+    code = dtype_code(residual.dtype)
+    if branch is None:
+        if gate is not None or branch_weight is not None or out is not None or scale != 1.0:
+            raise ValueError("gate, branch_weight, out and scale go with a branch")
+        if not norm_out:
+            raise ValueError("nothing to compute")
+    ldz = _like(branch, residual, device, "branch") if branch is not None else 0
+    groups = _gate_groups(gate, residual, rows, cols)
+    _param(branch_weight, residual, cols, "branch_weight")
+    _param(weight, residual, cols, "weight")
+    pcode = dtype_code(_param_dtype(residual, gate=gate, branch_weight=branch_weight, weight=weight))
+    stream, normed, lds, ldy = residual, None, 0, 0
+    if branch is not None:
+        stream, lds = _output_like(out, residual, cols, device, "out")
+    if norm_out:
+        normed, ldy = _output_like(out_norm, residual, cols, device, "out_norm")
+    lead = (rows,) if residual.dim() == 2 else residual.shape[:-1]
+    rb = rs = None
+    if stats and branch is not None and norm_branch:
+        rb = torch.empty(lead, dtype=torch.float32, device=device)
+    if stats and norm_out:
+        rs = torch.empty(lead, dtype=torch.float32, device=device)
+    _call("ns_residual_norm", device,
+          residual.data_ptr(), ldx, _ptr(branch), ldz, rows, cols, code, _ptr(gate), groups,
+          _ptr(branch_weight), _ptr(weight), pcode, scale, 1 if norm_branch else 0, eps,
+          stream.data_ptr() if branch is not None else None, lds, _ptr(normed), ldy, _ptr(rb), _ptr(rs),
+          _status_ptr(status, device))
+    return stream, normed, rb, rs
+
+
+def residual_norm_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().ns_residual_norm_workspace_size(rows, cols))
+
+
+def residual_norm_backward(dstream: Optional[torch.Tensor], dnormed: Optional[torch.Tensor],
+                           stream: torch.Tensor, branch: Optional[torch.Tensor] = None,
+                           branch_rstd: Optional[torch.Tensor] = None,
+                           rstd: Optional[torch.Tensor] = None,
+                           gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                           branch_weight: Optional[torch.Tensor] = None,
+                           weight: Optional[torch.Tensor] = None, params: bool = True,
+                           out: Optional[torch.Tensor] = None,
+                           out_branch: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None):
+    """Gradients of residual_norm: returns (dresidual, dbranch, dgate, dbranch_weight, dweight).
+
+    ``dstream`` and ``dnormed``: the gradients of stream and normed, either
+    None for zeros.  ``stream``, ``branch_rstd`` and ``rstd`` as returned by
+    residual_norm (branch_rstd None if the branch was not normed, rstd None
+    without dnormed), the other arguments as given to it.  dgate and the
+    weights' gradients have their parameter's shape and dtype; they are None
+    without that parameter or with ``params=False``.  ``out`` receives
+    dresidual and may be ``dstream``; ``out_branch`` receives dbranch and may
+    be ``dnormed``.
+    """
+    device = _device(stream)
+    rows, cols, lds = _rows(stream, "stream")
+    code = dtype_code(stream.dtype)
+    if dstream is None and dnormed is None:
+        raise ValueError("dstream or dnormed must be given")
+    ldds = _like(dstream, stream, device, "dstream") if dstream is not None else 0
+    lddy = _like(dnormed, stream, device, "dnormed") if dnormed is not None else 0
+    if dnormed is not None:
+        if rstd is None:
+            raise ValueError("dnormed needs rstd")
+        _per_row(rstd, rows, device, "rstd")
+    elif weight is not None:
+        raise ValueError("weight goes with dnormed")
+    if branch is None:
+        if gate is not None or branch_weight is not None or branch_rstd is not None or scale != 1.0:
+            raise ValueError("gate, branch_weight, branch_rstd and scale go with a branch")
+        if out_branch is not None:
+            raise ValueError("out_branch goes with a branch")
+    ldz = _like(branch, stream, device, "branch") if branch is not None else 0
+    if branch_rstd is not None:
+        _per_row(branch_rstd, rows, device, "branch_rstd")
+    groups = _gate_groups(gate, stream, rows, cols)
+    _param(branch_weight, stream, cols, "branch_weight")
+    _param(weight, stream, cols, "weight")
+    pcode = dtype_code(_param_dtype(stream, gate=gate, branch_weight=branch_weight, weight=weight))
+    dres, lddx = _output_like(out, stream, cols, device, "out")
+    dbranch, lddz = (_output_like(out_branch, stream, cols, device, "out_branch") if branch is not None
+                     else (None, 0))
+
+    def grad_of(p):
+        return torch.empty_like(p, requires_grad=False) if params and p is not None else None
+
+    dgate, dwb, dw = grad_of(gate), grad_of(branch_weight), grad_of(weight)
+    wptr, wbytes, keep = _workspace_args(
+        int(lib().ns_residual_norm_workspace_size(rows, cols)), device, workspace,
+        "ns_residual_norm_workspace_size")
+    _call("ns_residual_norm_backward", device,
+          _ptr(dstream), ldds, _ptr(dnormed), lddy, stream.data_ptr(), lds, _ptr(branch), ldz, rows, cols, code,
+          _ptr(branch_rstd), _ptr(rstd), _ptr(gate), groups, _ptr(branch_weight), _ptr(weight), pcode, scale,
+          dres.data_ptr(), lddx, _ptr(dbranch), lddz, _ptr(dgate), _ptr(dwb), _ptr(dw),
+          _status_ptr(status, device), wptr, wbytes)
+    return dres, dbranch, dgate, dwb, dw

@@ -1,0 +1,257 @@
+// resnorm.hip - C entry points of the residual norms (resnorm.hpp): argument
+// checks, workspace layout and kernel choice.
+#include <math.h>
+
+#include <algorithm>
+
+#include "host.hpp"
+#include "resnorm.hpp"
+
+namespace {
+
+using namespace nsk;
+
+constexpr int64_t kMaxResNormCols = 1 << 24;
+constexpr int kResNormRegisterCols = 8192;  // the widest row that the kernels hold in registers
+constexpr int64_t kResNormFwdThreads = 256 * 2048;
+// Blocks of the backward pass, each of which leaves partial rows of dw, dwb
+// and the gate's gradient.
+constexpr int64_t kResNormParts = 512;
+
+// Calls f.template run<NV, TPR, FORM>() for a row width: at most two vectors
+// of 16-bit data per thread, or a few narrow ones three, which leave
+// registers for the backward's three column sums.
+template <typename IO, int FORM, class F>
+void resnorm_form(int64_t cols, F&& f) {
+  const int64_t n = (cols + kVec<IO> - 1) / kVec<IO>;
+  if (n <= 32) return f.template run<1, 32, FORM>();
+  if (n <= 64) return f.template run<2, 32, FORM>();
+  if (n <= 96) return f.template run<3, 32, FORM>();
+  if (n <= 128) return f.template run<2, 64, FORM>();
+  if (n <= 192) return f.template run<3, 64, FORM>();
+  if constexpr (sizeof(IO) == 2) {
+    if (n <= 256) return f.template run<2, 128, FORM>();
+    if (n <= 512) return f.template run<2, 256, FORM>();
+    return f.template run<2, 512, FORM>();
+  } else {
+    if (n <= 256) return f.template run<4, 64, FORM>();
+    if (n <= 512) return f.template run<2, 256, FORM>();
+    if (n <= 1024) return f.template run<4, 256, FORM>();
+    return f.template run<4, 512, FORM>();
+  }
+}
+template <typename IO, class F>
+void with_resnorm_form(int64_t cols, F&& f) {
+  if (cols % kVec<IO> == 0)
+    resnorm_form<IO, kEven>(cols, f);
+  else
+    resnorm_form<IO, kRagged>(cols, f);
+}
+template <typename IO>
+bool resnorm_by_element(int64_t cols) {
+  return cols < kVec<IO> || cols > kResNormRegisterCols;
+}
+template <typename IO>
+int resnorm_rows_per_block(int64_t cols) {
+  if (resnorm_by_element<IO>(cols)) return 1;
+  const int64_t n = (cols + kVec<IO> - 1) / kVec<IO>;
+  return n <= 96 ? kNormRows<32> : n <= (sizeof(IO) == 2 ? 192 : 256) ? kNormRows<64> : 1;
+}
+
+template <typename IO, typename PT>
+struct ResNormFwdRun {
+  const ResNormFwdArgs& a;
+  hipStream_t st;
+  template <int NV, int TPR, int FORM>
+  void run() const {
+    const int64_t groups = (a.rows + kNormRows<TPR> - 1) / kNormRows<TPR>;
+    const int64_t blocks = std::min<int64_t>(groups, kResNormFwdThreads / kNormThreads<TPR>);
+    hipLaunchKernelGGL((k_resnorm_fwd<IO, PT, NV, TPR, FORM>), dim3((unsigned)blocks), dim3(kNormThreads<TPR>), 0, st,
+                       a);
+  }
+};
+
+template <typename IO, typename PT>
+struct ResNormBwdRun {
+  const ResNormBwdArgs& a;
+  int64_t blocks;
+  hipStream_t st;
+  template <int NV, int TPR, int FORM>
+  void run() const {
+    hipLaunchKernelGGL((k_resnorm_bwd<IO, PT, NV, TPR, FORM>), dim3((unsigned)blocks), dim3(kNormThreads<TPR>), 0, st,
+                       a);
+  }
+};
+
+bool resnorm_shape_ok(int64_t rows, int64_t cols, int64_t groups) {
+  if (!(rows >= 0 && rows < (int64_t(1) << 31) && cols >= 1 && cols <= kMaxResNormCols)) return false;
+  // Without rows the gate's gradient is zeros, by a block for each 64 columns.
+  if (rows == 0) return groups >= 0 && groups < (int64_t(1) << 30) / ((cols + 63) / 64) - 2;
+  return groups == 0 || (groups > 0 && groups <= rows && rows % groups == 0);
+}
+
+// How the backward pass cuts the rows (ResNormBwdArgs), for `groups` rows of
+// the gate that are summed over.
+struct ResNormCut {
+  int64_t groups, group_rows, blocks;
+  int split;
+};
+ResNormCut resnorm_cut(int64_t rows, int64_t groups, int per_block) {
+  ResNormCut c;
+  c.groups = groups;
+  c.group_rows = rows / groups;
+  const int64_t most = (c.group_rows + per_block - 1) / per_block;  // no segment without rows
+  c.split = (int)std::max<int64_t>(1, std::min(kResNormParts / groups, most));
+  c.blocks = std::min(groups * c.split, kResNormParts);
+  return c;
+}
+
+}  // namespace
+
+extern "C" {
+
+ns_status ns_residual_norm(const void* X, int64_t ldx, const void* Z, int64_t ldz, int64_t rows, int64_t cols,
+                           ns_dtype dtype, const void* gate, int64_t groups, const void* branch_weight,
+                           const void* weight, ns_dtype param_dtype, float scale, int32_t norm_branch, float eps,
+                           void* S, int64_t lds, void* Y, int64_t ldy, float* branch_rstd, float* rstd,
+                           int32_t* d_status, ns_stream_t stream) {
+  if (!resnorm_shape_ok(rows, cols, gate ? groups : 0) || (gate && groups == 0)) return NS_ERR_INVALID_ARG;
+  if (ldx < cols || (Z && (ldz < cols || lds < cols)) || (Y && ldy < cols)) return NS_ERR_INVALID_ARG;
+  if (!(eps >= 0.f && isfinite(eps)) || !isfinite(scale) || (norm_branch != 0 && norm_branch != 1))
+    return NS_ERR_INVALID_ARG;
+  if (!known(dtype) || !(param_dtype == dtype || param_dtype == NS_FP32)) return NS_ERR_UNSUPPORTED_DTYPE;
+  if (rows == 0) return NS_OK;
+  // Without a block's output there is only the second norm.
+  if (!Z && (gate || branch_weight || S || scale != 1.f || !Y)) return NS_ERR_INVALID_ARG;
+  if (!X || (Z && !S)) return NS_ERR_INVALID_ARG;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  ResNormFwdArgs a{};
+  a.X = X;
+  a.Z = Z;
+  a.gate = gate;
+  a.wb = branch_weight;
+  a.w = weight;
+  a.S = S;
+  a.Y = Y;
+  a.rb = branch_rstd;
+  a.rs = rstd;
+  a.rows = rows;
+  a.ldx = ldx;
+  a.ldz = ldz;
+  a.lds = lds;
+  a.ldy = ldy;
+  a.gate_rows = gate ? (uint32_t)(rows / groups) : 1u;
+  a.cols = (int)cols;
+  a.scale = scale;
+  a.eps = eps;
+  a.norm_branch = norm_branch;
+  a.d_status = d_status;
+  a.status_bits = (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT);
+  return with_types(dtype, param_dtype, [&](auto io, auto pt) {
+    using IO = decltype(io);
+    using PT = decltype(pt);
+    if (resnorm_by_element<IO>(cols))
+      hipLaunchKernelGGL((k_resnorm_fwd_long<IO, PT>), dim3((unsigned)std::min(rows, kMaxBlocks)), dim3(1024), 0, st, a);
+    else
+      with_resnorm_form<IO>(cols, ResNormFwdRun<IO, PT>{a, st});
+    return launched();
+  });
+}
+
+size_t ns_residual_norm_workspace_size(int64_t rows, int64_t cols) {
+  if (!resnorm_shape_ok(rows, cols, 0)) return 0;
+  const size_t parts = align_up_to((size_t)std::min(rows, kResNormParts) * 3 * cols * sizeof(float));
+  return std::max(kAlignTo, parts + align_up_to((size_t)rows * sizeof(float)));
+}
+
+ns_status ns_residual_norm_backward(const void* dS, int64_t ldds, const void* dY, int64_t lddy, const void* S,
+                                    int64_t lds, const void* Z, int64_t ldz, int64_t rows, int64_t cols,
+                                    ns_dtype dtype, const float* branch_rstd, const float* rstd, const void* gate,
+                                    int64_t groups, const void* branch_weight, const void* weight,
+                                    ns_dtype param_dtype, float scale, void* dX, int64_t lddx, void* dZ, int64_t lddz,
+                                    void* dgate, void* dbranch_weight, void* dweight, int32_t* d_status,
+                                    void* workspace, size_t workspace_bytes, ns_stream_t stream) {
+  const bool gated = gate || dgate;
+  if (!resnorm_shape_ok(rows, cols, gated ? groups : 0) || (gated && groups == 0)) return NS_ERR_INVALID_ARG;
+  if ((dS && ldds < cols) || (dY && (lddy < cols || lds < cols)) || (Z && (ldz < cols || lddz < cols)) ||
+      (dX && lddx < cols) || !isfinite(scale))
+    return NS_ERR_INVALID_ARG;
+  if (!known(dtype) || !(param_dtype == dtype || param_dtype == NS_FP32)) return NS_ERR_UNSUPPORTED_DTYPE;
+  if (rows > 0) {
+    if ((!dS && !dY) || (dY && (!S || !rstd)) || (Z && !dZ)) return NS_ERR_INVALID_ARG;
+    // Without a block's output there is nothing that these would be gradients of.
+    if (!Z && (dZ || gated || branch_weight || dbranch_weight || scale != 1.f || !dX)) return NS_ERR_INVALID_ARG;
+    if (!dY && (weight || dweight)) return NS_ERR_INVALID_ARG;
+  } else if (!dgate && !dbranch_weight && !dweight) {
+    return NS_OK;
+  }
+  if (!workspace_ok(workspace, workspace_bytes, ns_residual_norm_workspace_size(rows, cols))) return NS_ERR_WORKSPACE;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  ResNormBwdArgs a{};
+  a.dS = dS;
+  a.dY = dY;
+  a.S = S;
+  a.Z = Z;
+  a.rb = branch_rstd;
+  a.rs = rstd;
+  a.gate = gate;
+  a.wb = branch_weight;
+  a.w = weight;
+  a.dX = dX;
+  a.dZ = dZ;
+  a.rows = rows;
+  a.ldds = ldds;
+  a.lddy = lddy;
+  a.lds = lds;
+  a.ldz = ldz;
+  a.lddx = lddx;
+  a.lddz = lddz;
+  a.gate_rows = gate && rows > 0 ? (uint32_t)(rows / groups) : 1u;
+  a.cols = (int)cols;
+  a.scale = scale;
+  a.want_w = dweight != nullptr;
+  a.want_wb = dbranch_weight != nullptr;
+  a.d_status = d_status;
+  a.status_bits = (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT);
+  // A gate of its own for each row has its gradient written with the row.
+  const bool own_rows = dgate && rows > 0 && groups == rows && rows > 1;
+  a.dgate_rows = own_rows ? dgate : nullptr;
+  a.want_gate = dgate && !own_rows;
+  Carver carve{reinterpret_cast<char*>(workspace)};
+  a.partial = carve.take<float>(std::min(rows, kResNormParts) * 3 * cols);
+  a.c_row = carve.take<float>(rows);
+  return with_types(dtype, param_dtype, [&](auto io, auto pt) {
+    using IO = decltype(io);
+    using PT = decltype(pt);
+    ResNormCut cut{1, 0, 0, 1};
+    if (rows > 0) {
+      cut = resnorm_cut(rows, a.want_gate ? groups : 1, resnorm_rows_per_block<IO>(cols));
+      a.groups = cut.groups;
+      a.group_rows = cut.group_rows;
+      a.split = cut.split;
+      a.dgate = a.want_gate ? dgate : nullptr;
+      if (resnorm_by_element<IO>(cols)) {
+        const dim3 grid((unsigned)std::min(rows, kMaxBlocks));
+        if (dY) hipLaunchKernelGGL((k_resnorm_rows_long<IO, PT>), grid, dim3(1024), 0, st, a);
+        if (a.want_w || a.want_wb || a.want_gate)
+          hipLaunchKernelGGL((k_resnorm_cols_long<IO, PT>), dim3((unsigned)((cols + 255) / 256), (unsigned)cut.blocks),
+                             dim3(256), 0, st, a);
+        if (dX || dZ) hipLaunchKernelGGL((k_resnorm_bwd_long<IO, PT>), grid, dim3(1024), 0, st, a);
+      } else {
+        with_resnorm_form<IO>(cols, ResNormBwdRun<IO, PT>{a, cut.blocks, st});
+      }
+    }
+    // Without rows the gradients are zeros; a gate then has no rows either
+    // unless the caller says so.
+    const bool join_gate = a.want_gate && (rows == 0 || cut.split > 1);
+    if (dweight || dbranch_weight || join_gate) {
+      const ResNormJoinArgs j{a.partial, (int)cut.blocks, rows > 0 ? cut.split : 0, (int)cols, dweight, dbranch_weight,
+                              join_gate ? dgate : nullptr, d_status, a.status_bits};
+      const int64_t outputs = 2 + (join_gate ? groups : 0);
+      hipLaunchKernelGGL((k_resnorm_join<PT>), dim3((unsigned)((cols + 63) / 64 * outputs)), dim3(1024), 0, st, j);
+    }
+    return launched();
+  });
+}
+
+}  // extern "C"

@@ -55,6 +55,8 @@ come from the oracle itself):
   (normalized rows, a one-hot product, log of a sum of exponentials).
 * ``adamw``: a constant gradient's first step (lr along its sign) and the
   closed form of the moments.
+* ``residual_norm`` and its gradients: unit mean squares; the gradients
+  against central differences along random directions.
 
 No function here is "parity unpinned".
 """
@@ -67,7 +69,7 @@ from .muon import momentum_update, muon_step
 from .training import (embedding, embedding_backward, layer_norm,
                        layer_norm_backward, linear_cross_entropy,
                        linear_cross_entropy_backward, linear_cross_entropy_dz)
-from .block import adamw, state_tops
+from .block import adamw, residual_norm, residual_norm_backward, state_tops
 
 __all__ = [
     "CLASSIC_ABC", "TUNED_ABC", "coefficient_schedule", "frobenius_stage",
@@ -77,4 +79,5 @@ __all__ = [
     "embedding", "embedding_backward", "layer_norm", "layer_norm_backward",
     "linear_cross_entropy", "linear_cross_entropy_backward",
     "linear_cross_entropy_dz", "adamw", "state_tops",
+    "residual_norm", "residual_norm_backward",
 ]

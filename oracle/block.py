@@ -30,3 +30,57 @@ def state_tops(x, block=256, least=2.0 ** -100):
     x = np.abs(_f64(x).reshape(-1))
     padded = np.pad(x, (0, -x.size % block)).reshape(-1, block)
     return np.maximum(padded.max(1), least)
+
+
+def _gate_of_rows(gate, rows, cols):
+    """The gate's row of every data row (ones without a gate)."""
+    if gate is None:
+        return np.ones((rows, cols))
+    gate = _f64(gate).reshape(-1, cols)
+    return np.repeat(gate, rows // gate.shape[0], 0)
+
+
+def residual_norm(x, z, gate=None, scale=1.0, branch_weight=None, weight=None, norm_branch=True, eps=1e-6):
+    """(s, y, rb, rs) for 2-D x and z (z None: the norm of x alone)."""
+    x = _f64(x)
+    rows, cols = x.shape
+    w = np.ones(cols) if weight is None else _f64(weight)
+    wb = np.ones(cols) if branch_weight is None else _f64(branch_weight)
+    rb = np.ones(rows)
+    s = x
+    if z is not None:
+        z = _f64(z)
+        if norm_branch:
+            rb = 1.0 / np.sqrt(np.mean(z * z, 1) + eps)
+        s = scale * x + _gate_of_rows(gate, rows, cols) * (z * rb[:, None] * wb)
+    rs = 1.0 / np.sqrt(np.mean(s * s, 1) + eps)
+    return s, s * rs[:, None] * w, rb, rs
+
+
+def residual_norm_backward(ds, dy, s, z, rb=None, rs=None, gate=None, scale=1.0, branch_weight=None, weight=None):
+    """A dict of the gradients and of the G they come from, given the statistics.
+
+    rb None: the branch was not normed.  dgate has one row per row of the data;
+    the caller sums over those that share a row of the gate.
+    """
+    some = ds if ds is not None else dy
+    rows, cols = some.shape
+    w = np.ones(cols) if weight is None else _f64(weight)
+    wb = np.ones(cols) if branch_weight is None else _f64(branch_weight)
+    g = np.zeros((rows, cols)) if ds is None else _f64(ds)
+    out = {}
+    if dy is not None:
+        rs = _f64(rs)[:, None]
+        shat, u = _f64(s) * rs, _f64(dy) * w
+        g = g + rs * (u - shat * np.mean(u * shat, 1, keepdims=True))
+        out["dw"] = (_f64(dy) * shat).sum(0)
+    out.update(g=g, dx=scale * g)
+    if z is not None:
+        r = np.ones((rows, 1)) if rb is None else _f64(rb)[:, None]
+        bhat = _f64(z) * r
+        q = _gate_of_rows(gate, rows, cols) * g
+        a = wb * q
+        out["dz"] = a if rb is None else r * (a - bhat * np.mean(a * bhat, 1, keepdims=True))
+        out["dgate"] = g * bhat * wb
+        out["dwb"] = (q * bhat).sum(0)
+    return out

@@ -83,3 +83,90 @@ def test_adamw_states_and_host_tensors():
     assert all(t.dtype == torch.float8_e4m3fn for t in m + v)
     with pytest.raises(ValueError, match="device tensor"):
         nsa.adamw_step(p, p, m, v, lr=1e-3, step=1, scales=scales)
+
+
+# ---------------------------------------------------------------------------
+# Norms before and after a block.
+# ---------------------------------------------------------------------------
+
+def _slope(f, x, direction, step=1e-5):
+    return (f(x + step * direction) - f(x - step * direction)) / (2 * step)
+
+
+@pytest.mark.parametrize("norm_branch", [True, False])
+@pytest.mark.parametrize("groups", [None, 1, 3, 6])
+def test_oracle_residual_norm_gradients_against_differences(norm_branch, groups):
+    rng = np.random.default_rng(5)
+    x, z = rng.normal(size=(6, 9)), rng.normal(size=(6, 9))
+    gate = None if groups is None else rng.normal(size=(groups, 9))
+    wb, w = rng.normal(size=9), rng.normal(size=9)
+    ds, dy = rng.normal(size=(6, 9)), rng.normal(size=(6, 9))
+    s, y, rb, rs = oracle.residual_norm(x, z, eps=0.0)
+    assert np.allclose((y * y).mean(1), 1) and np.allclose(((z * rb[:, None]) ** 2).mean(1), 1)
+
+    def value(x=x, z=z, gate=gate, wb=wb, w=w):
+        s, y, _, _ = oracle.residual_norm(x, z, gate, 0.7, wb, w, norm_branch)
+        return (ds * s).sum() + (dy * y).sum()
+
+    s, y, rb, rs = oracle.residual_norm(x, z, gate, 0.7, wb, w, norm_branch)
+    o = oracle.residual_norm_backward(ds, dy, s, z, rb if norm_branch else None, rs, gate, 0.7, wb, w)
+    for name, at, grad in (("x", x, o["dx"]), ("z", z, o["dz"]), ("wb", wb, o["dwb"]), ("w", w, o["dw"])):
+        d = rng.normal(size=at.shape)
+        assert _slope(lambda v: value(**{name: v}), at, d) == pytest.approx((grad * d).sum(), rel=1e-6), name
+    if groups is not None:
+        d = rng.normal(size=gate.shape)
+        dgate = o["dgate"].reshape(groups, -1, 9).sum(1)
+        assert _slope(lambda v: value(gate=v), gate, d) == pytest.approx((dgate * d).sum(), rel=1e-6)
+
+
+def test_oracle_residual_norm_without_a_branch():
+    rng = np.random.default_rng(6)
+    x, w, dy = rng.normal(size=(4, 5)), rng.normal(size=5), rng.normal(size=(4, 5))
+    s, y, _, rs = oracle.residual_norm(x, None, weight=w)
+    o = oracle.residual_norm_backward(None, dy, s, None, None, rs, weight=w)
+    d = rng.normal(size=x.shape)
+    slope = _slope(lambda v: (dy * oracle.residual_norm(v, None, weight=w)[1]).sum(), x, d)
+    assert slope == pytest.approx((o["dx"] * d).sum(), rel=1e-6)
+
+
+def _norm(X=PTR, ldx=8, Z=PTR, ldz=8, rows=4, cols=8, dtype=B.NS_BF16, gate=PTR, groups=2, wb=PTR, w=PTR, pt=B.NS_FP32,
+          scale=1.0, nb=1, eps=1e-6, S=PTR, lds=8, Y=PTR, ldy=8):
+    return B.lib().ns_residual_norm(X, ldx, Z, ldz, rows, cols, dtype, gate, groups, wb, w, pt, scale, nb, eps, S, lds,
+                                    Y, ldy, None, None, None, None)
+
+
+@built
+def test_residual_norm_refusals():
+    for kw in (dict(X=None), dict(S=None), dict(ldx=7), dict(ldz=7), dict(lds=7), dict(ldy=7), dict(rows=-1),
+               dict(rows=1 << 31, groups=1), dict(cols=0), dict(cols=(1 << 24) + 1, ldx=1 << 25, ldz=1 << 25, lds=1 << 25, ldy=1 << 25),
+               dict(groups=0), dict(groups=3), dict(groups=8), dict(groups=-1), dict(scale=float("nan")), dict(nb=2),
+               dict(eps=-1.0), dict(eps=float("inf")), dict(Z=None), dict(Z=None, gate=None, wb=None),
+               dict(Z=None, gate=None, wb=None, S=None, scale=0.5), dict(Z=None, gate=None, wb=None, S=None, Y=None)):
+        assert _norm(**kw) == INV, kw
+    assert _norm(dtype=5) == DT and _norm(pt=B.NS_FP16) == DT
+    assert _norm(rows=0, X=None, Z=PTR, S=None, Y=None) == 0
+
+
+def _norm_back(dS=PTR, ldds=8, dY=PTR, lddy=8, S=PTR, lds=8, Z=PTR, ldz=8, rows=4, cols=8, dtype=B.NS_BF16, rb=PTR,
+               rs=PTR, gate=PTR, groups=2, wb=PTR, w=PTR, pt=B.NS_FP32, scale=1.0, dX=PTR, lddx=8, dZ=PTR, lddz=8,
+               dg=PTR, dwb=PTR, dw=PTR, ws=256, n=1 << 30):
+    return B.lib().ns_residual_norm_backward(dS, ldds, dY, lddy, S, lds, Z, ldz, rows, cols, dtype, rb, rs, gate, groups,
+                                             wb, w, pt, scale, dX, lddx, dZ, lddz, dg, dwb, dw, None, ws, n, None)
+
+
+@built
+def test_residual_norm_backward_refusals():
+    for kw in (dict(dS=None, dY=None), dict(S=None), dict(rs=None), dict(dZ=None), dict(dY=None), dict(dY=None, w=None),
+               dict(ldds=7), dict(lddy=7), dict(lds=7), dict(ldz=7), dict(lddx=7), dict(lddz=7), dict(groups=0),
+               dict(groups=3), dict(gate=None, groups=0), dict(rows=-1), dict(cols=0), dict(scale=float("inf")),
+               dict(Z=None), dict(Z=None, gate=None, dg=None, wb=None, dwb=None),
+               dict(Z=None, gate=None, dg=None, wb=None, dwb=None, dZ=None, scale=0.5),
+               dict(Z=None, gate=None, dg=None, wb=None, dwb=None, dZ=None, dX=None),
+               dict(rows=0, groups=1 << 40)):
+        assert _norm_back(**kw) == INV, kw
+    assert _norm_back(dtype=5) == DT and _norm_back(pt=B.NS_FP16) == DT
+    assert _norm_back(ws=None) == WSP and _norm_back(ws=100) == WSP and _norm_back(n=100) == WSP
+    assert nsa.residual_norm_workspace_size(0, 8) >= 256 and nsa.residual_norm_workspace_size(-1, 8) == 0
+    assert nsa.residual_norm_workspace_size(4, 0) == 0
+    # No rows and nothing wanted.
+    assert _norm_back(rows=0, dg=None, dwb=None, dw=None) == 0
