@@ -648,6 +648,65 @@ ns_status ns_residual_norm_backward(
     ns_stream_t stream);
 
 /*
+ * A gated feed-forward block.  With x a row of X and act the activation:
+ *     a = x Wg^T,   b = x Wu^T,   h = act(a) b,   y = h Wd^T
+ *   X, Y     rows x cols, row strides ldx and ldy.
+ *   Wg, Wu   inner x cols; Wd cols x inner (a linear layer's layout), row
+ *            strides ldwg, ldwu and ldwd.
+ *   activation   silu a / (1 + exp(-a)); gelu a (1 + erf(a / sqrt 2)) / 2;
+ *            gelu_tanh a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2; relu.
+ *   gate, up   rows x inner, row stride ldg, receive a and b for the
+ *            backward pass; both NULL without one.
+ *   rows <= 2^22, cols and inner <= 2^20, rows * inner <= 2^40, row strides
+ *            <= 2^23.
+ *   workspace   ns_gated_mlp_workspace_size(rows, cols, inner, dtype,
+ *            aligned, 0) bytes, 256-byte aligned; aligned is 1 when X, Wg, Wu
+ *            and Wd start on 16-byte boundaries, their row strides are
+ *            multiples of 128 bytes and ldwg == ldwu, else 0 (the operands
+ *            are then copied, as they are when cols or inner is not a
+ *            multiple of 64, or 32 in fp32).
+ * The products accumulate in fp32; h is formed in fp32 and rounded to dtype,
+ * being an operand itself, and so are a and b where they are stored.
+ */
+typedef enum { NS_SILU = 0, NS_GELU = 1, NS_GELU_TANH = 2, NS_RELU = 3 } ns_activation;
+
+size_t ns_gated_mlp_workspace_size(int64_t rows, int64_t cols, int64_t inner,
+                                   ns_dtype dtype, int32_t aligned,
+                                   int32_t backward);
+
+ns_status ns_gated_mlp(const void* X, int64_t ldx, const void* Wg,
+                       int64_t ldwg, const void* Wu, int64_t ldwu,
+                       const void* Wd, int64_t ldwd, int64_t rows,
+                       int64_t cols, int64_t inner, ns_dtype dtype,
+                       ns_activation activation, void* Y, int64_t ldy,
+                       void* gate, void* up, int64_t ldg, int32_t* d_status,
+                       void* workspace, size_t workspace_bytes,
+                       ns_stream_t stream);
+
+/*
+ * Its gradients:
+ *     dh = dY Wd,   da = dh b act'(a),   db = dh act(a)
+ *     dX = da Wg + db Wu,  dWg = da^T X,  dWu = db^T X,  dWd = dY^T h
+ *   gate, up   a and b as written by ns_gated_mlp; h is made of them again.
+ *   dX, dWg, dWu, dWd   any may be NULL.
+ *   workspace   ns_gated_mlp_workspace_size(rows, cols, inner, dtype,
+ *            aligned, 1) bytes; aligned is 1 when dY starts on a 16-byte
+ *            boundary and its row stride is a multiple of 128 bytes.
+ * da, db and h are rounded to dtype, being operands; all products accumulate
+ * in fp32.  No row is left out: a row of dY that is zero adds nothing to the
+ * weights' gradients as long as its rows of X, gate and up are finite.
+ * With no rows the weights' gradients are zeros.
+ */
+ns_status ns_gated_mlp_backward(
+    const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* Wg,
+    int64_t ldwg, const void* Wu, int64_t ldwu, const void* Wd, int64_t ldwd,
+    const void* gate, const void* up, int64_t ldg, int64_t rows, int64_t cols,
+    int64_t inner, ns_dtype dtype, ns_activation activation, void* dX,
+    int64_t lddx, void* dWg, int64_t lddwg, void* dWu, int64_t lddwu,
+    void* dWd, int64_t lddwd, int32_t* d_status, void* workspace,
+    size_t workspace_bytes, ns_stream_t stream);
+
+/*
  * The kernel builds one call would launch, for inspection (host only;
  * touches no device).  Arguments as for ns_workspace_size, plus the step
  * count.  Writes a NUL-terminated, space-separated list of the distinct
@@ -697,6 +756,19 @@ int64_t ns_plan_kernels_grouped(int64_t n, int64_t m, int64_t count,
 int64_t ns_plan_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab,
                                      ns_dtype dtype, int32_t aligned,
                                      int32_t backward, char* buf, size_t len);
+
+/*
+ * The same for ns_gated_mlp (backward == 0) or its gradients (backward == 1,
+ * all of them), with the arguments of ns_gated_mlp_workspace_size.  Entries,
+ * in launch order: prep<op> (copies, where there are any); up<op,rows x
+ * columns of a tile of h> and products<op,edge> forward, dz<op,edge> and
+ * products<op,edge> backward, join<op> and splits=S where y or dX is summed
+ * from S parts; for a few rows dotup<op,rows,form> and
+ * dotdown<op,rows,form>; zero<op> (gradients without rows).
+ */
+int64_t ns_plan_gated_mlp(int64_t rows, int64_t cols, int64_t inner,
+                          ns_dtype dtype, int32_t aligned, int32_t backward,
+                          char* buf, size_t len);
 
 /* Static description of a status code. */
 const char* ns_status_string(ns_status s);

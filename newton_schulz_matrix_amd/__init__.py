@@ -25,7 +25,8 @@ from ._training import (embedding, embedding_backward,
                         linear_cross_entropy, linear_cross_entropy_backward,
                         linear_cross_entropy_workspace_size,
                         plan_linear_cross_entropy)
-from ._block import (adamw_states, adamw_step, residual_norm,
+from ._block import (adamw_states, adamw_step, gated_mlp, gated_mlp_backward,
+                     gated_mlp_workspace_size, plan_gated_mlp, residual_norm,
                      residual_norm_backward, residual_norm_workspace_size)
 from .coeffs import fit_coefficients, root_coefficients
 
@@ -40,6 +41,7 @@ __all__ = [
     "layer_norm_workspace_size", "linear_cross_entropy",
     "linear_cross_entropy_backward", "linear_cross_entropy_workspace_size",
     "plan_linear_cross_entropy", "adamw_states", "adamw_step",
+    "gated_mlp", "gated_mlp_backward", "gated_mlp_workspace_size", "plan_gated_mlp",
     "residual_norm", "residual_norm_backward", "residual_norm_workspace_size",
     "gram_flops", "ns_flops", "standard_flops",
     "fit_coefficients", "root_coefficients",

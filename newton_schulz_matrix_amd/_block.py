@@ -16,7 +16,7 @@ from typing import List, Optional, Sequence, Tuple, Union
 import torch
 
 from . import _binding as B
-from ._binding import dtype_code, lib
+from ._binding import NSError, dtype_code, lib
 from ._training import (_call, _device, _output, _output_like, _param, _per_row, _ptr,
                         _rows, _same_device, _status_ptr, _workspace_args)
 
@@ -317,3 +317,129 @@ def residual_norm_backward(dstream: Optional[torch.Tensor], dnormed: Optional[to
           dres.data_ptr(), lddx, _ptr(dbranch), lddz, _ptr(dgate), _ptr(dwb), _ptr(dw),
           _status_ptr(status, device), wptr, wbytes)
     return dres, dbranch, dgate, dwb, dw
+
+
+# ---------------------------------------------------------------------------
+# The gated feed-forward block.
+# ---------------------------------------------------------------------------
+_ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+
+
+def _activation(name: str) -> int:
+    try:
+        return _ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}") from None
+
+
+def _weights(x: torch.Tensor, cols: int, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor):
+    """(inner, their row strides) of a block's matrices."""
+    device = x.device
+    if w_gate.dim() != 2 or w_up.dim() != 2 or w_down.dim() != 2:
+        raise ValueError("w_gate, w_up and w_down must be 2-D")
+    inner, _, ldg = _rows(w_gate, "w_gate")
+    if inner < 1 or w_gate.shape[1] != cols or w_up.shape != w_gate.shape or tuple(w_down.shape) != (cols, inner):
+        raise ValueError("w_gate and w_up must be [inner, cols] and w_down [cols, inner]")
+    if not (w_gate.dtype == w_up.dtype == w_down.dtype == x.dtype):
+        raise ValueError("the weights must have x's dtype")
+    _same_device(device, w_gate=w_gate, w_up=w_up, w_down=w_down)
+    return inner, ldg, _rows(w_up, "w_up")[2], _rows(w_down, "w_down")[2]
+
+
+def _aligned(*operands) -> bool:
+    """Whether (tensor, row stride) pairs start on 16 bytes and step by whole 128."""
+    return all(t.data_ptr() % 16 == 0 and ld * t.element_size() % 128 == 0 for t, ld in operands)
+
+
+def gated_mlp_workspace_size(rows: int, cols: int, inner: int, dtype: torch.dtype = torch.bfloat16,
+                             aligned: bool = True, backward: bool = False) -> int:
+    """``aligned``: x and the weights (backward: dy) start on 16-byte
+    boundaries, their row strides are multiples of 128 bytes and w_gate's and
+    w_up's are the same."""
+    return int(lib().ns_gated_mlp_workspace_size(rows, cols, inner, dtype_code(dtype), 1 if aligned else 0,
+                                                 1 if backward else 0))
+
+
+def plan_gated_mlp(rows: int, cols: int, inner: int, dtype: torch.dtype = torch.bfloat16, aligned: bool = True,
+                   backward: bool = False) -> List[str]:
+    """The kernel builds one call would launch (host only, no device)."""
+    args = (rows, cols, inner, dtype_code(dtype), 1 if aligned else 0, 1 if backward else 0)
+    need = int(lib().ns_plan_gated_mlp(*args, None, 0))
+    if need < 0:
+        raise NSError(1, "ns_plan_gated_mlp")
+    buf = ctypes.create_string_buffer(need)
+    lib().ns_plan_gated_mlp(*args, buf, need)
+    return buf.value.decode().split()
+
+
+def gated_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+              activation: str = "silu", save: bool = True, out: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """A gated feed-forward block, (act(x w_gate^T) * (x w_up^T)) w_down^T: returns (y, gate, up).
+
+    ``x``: [..., cols], 2-D with contiguous rows or contiguous of any rank;
+    ``w_gate`` and ``w_up``: [inner, cols], ``w_down``: [cols, inner], all of
+    x's dtype.  ``activation``: "silu", "gelu", "gelu_tanh" or "relu".
+    ``gate`` and ``up``, [..., inner], are the two projections that the
+    backward pass takes; with ``save=False`` they are None.
+    """
+    device = _device(x)
+    rows, cols, ldx = _rows(x, "x")
+    code, act = dtype_code(x.dtype), _activation(activation)
+    inner, ldg, ldu, ldd = _weights(x, cols, w_gate, w_up, w_down)
+    y, ldy = _output_like(out, x, cols, device, "out")
+    gate = up = None
+    if save:
+        gate = torch.empty(tuple(x.shape[:-1]) + (inner,), dtype=x.dtype, device=device)
+        up = torch.empty_like(gate)
+    aligned = ldg == ldu and _aligned((x, ldx), (w_gate, ldg), (w_up, ldu), (w_down, ldd))
+    wptr, wbytes, keep = _workspace_args(
+        int(lib().ns_gated_mlp_workspace_size(rows, cols, inner, code, 1 if aligned else 0, 0)), device, workspace,
+        "ns_gated_mlp_workspace_size")
+    _call("ns_gated_mlp", device,
+          x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd, rows, cols, inner,
+          code, act, y.data_ptr(), ldy, _ptr(gate), _ptr(up), inner, _status_ptr(status, device), wptr, wbytes)
+    return y, gate, up
+
+
+def gated_mlp_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                       w_down: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, activation: str = "silu",
+                       need_dx: bool = True, need_dw: bool = True, out_dx: Optional[torch.Tensor] = None,
+                       out_dw_gate: Optional[torch.Tensor] = None, out_dw_up: Optional[torch.Tensor] = None,
+                       out_dw_down: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None):
+    """Gradients of gated_mlp: returns (dx, dw_gate, dw_up, dw_down).
+
+    ``gate`` and ``up`` as returned by gated_mlp.  ``need_dx`` / ``need_dw``
+    False skip dx or the weights' gradients and return None for them.  The
+    workspace holds the gradients of gate and up twice, h, and transposed
+    copies of x, dy and the weights.
+    """
+    device = _device(x)
+    rows, cols, ldx = _rows(x, "x")
+    code, act = dtype_code(x.dtype), _activation(activation)
+    inner, ldg, ldu, ldd = _weights(x, cols, w_gate, w_up, w_down)
+    lddy = _like(dy, x, device, "dy")
+    shape = tuple(x.shape[:-1]) + (inner,)
+    for name, t in (("gate", gate), ("up", up)):
+        if tuple(t.shape) != shape or t.dtype != x.dtype or t.device != device:
+            raise ValueError(f"{name} must have shape {shape}, {x.dtype} and device {device}")
+    lds = _rows(gate, "gate")[2]
+    if _rows(up, "up")[2] != lds:
+        raise ValueError("gate and up must have the same row stride")
+    dx = dwg = dwu = dwd = None
+    lddx, lddg, lddu, lddd = cols, cols, cols, inner
+    if need_dx:
+        dx, lddx = _output_like(out_dx, x, cols, device, "out_dx")
+    if need_dw:
+        dwg, lddg = _output(out_dw_gate, w_gate.shape, x.dtype, device, "out_dw_gate")
+        dwu, lddu = _output(out_dw_up, w_up.shape, x.dtype, device, "out_dw_up")
+        dwd, lddd = _output(out_dw_down, w_down.shape, x.dtype, device, "out_dw_down")
+    wptr, wbytes, keep = _workspace_args(
+        int(lib().ns_gated_mlp_workspace_size(rows, cols, inner, code, 1 if _aligned((dy, lddy)) else 0, 1)), device,
+        workspace, "ns_gated_mlp_workspace_size")
+    _call("ns_gated_mlp_backward", device,
+          dy.data_ptr(), lddy, x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd,
+          gate.data_ptr(), up.data_ptr(), lds, rows, cols, inner, code, act, _ptr(dx), lddx, _ptr(dwg), lddg,
+          _ptr(dwu), lddu, _ptr(dwd), lddd, _status_ptr(status, device), wptr, wbytes)
+    return dx, dwg, dwu, dwd

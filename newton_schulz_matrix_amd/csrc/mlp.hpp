@@ -1,0 +1,816 @@
+// mlp.hpp - a gated feed-forward block, forward and backward.
+//
+//   a = x Wg^T,  b = x Wu^T,  h = act(a) b,  y = h Wd^T
+//   dh = dy Wd,  da = dh b act'(a),  db = dh act(a)
+//   dx = da Wg + db Wu,  dWg = da^T x,  dWu = db^T x,  dWd = dy^T h
+//   (x, y: n x d;  a, b, h: n x f;  Wg, Wu: f x d;  Wd: d x f)
+//
+// Bound by the matrix cores (6 n d f forward, 12 n d f backward) unless n is
+// small, where reading the weights bounds them.  The products run on the
+// caller's type with fp32 accumulation, as streams of tiles (stream.hpp):
+//
+//   forward   one product for both projections: a tile's right-hand rows are
+//             half rows of Wg and half the same rows of Wu, so each wave
+//             holds a and b of the same columns and its epilogue makes h of
+//             them.  Then y.
+//   backward  dh, whose epilogue makes da, db and h again from the a and b
+//             that forward left, and writes them as the last products read
+//             them: da and db in rows for dx, all three transposed for the
+//             weights' gradients.  Then those and dx in one launch.
+//
+// h, da and db are rounded to the operands' type, because they are operands
+// themselves: half a step per term of the sums, of the size of the result's
+// own rounding.  a and b are rounded where forward leaves them for backward;
+// forward's own h is made before that.
+//
+// A few rows go without tiles: a wave reads whole rows of the weights.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "xent.hpp"
+
+namespace nsk {
+
+enum MlpAct { kSilu = 0, kGelu = 1, kGeluTanh = 2, kRelu = 3 };
+
+// Value and slope of an activation.
+template <int ACT>
+struct Act {
+  float value, slope;
+  __device__ __forceinline__ explicit Act(float a) {
+    if constexpr (ACT == kSilu) {
+      const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * a));
+      value = a * s;
+      slope = s * fmaf(a, 1.f - s, 1.f);
+    } else if constexpr (ACT == kGelu) {
+      const float phi = fmaf(0.5f, erff(a * 0.70710678118654752f), 0.5f);
+      value = a * phi;
+      slope = fmaf(a * 0.39894228040143268f, __builtin_amdgcn_exp2f(-0.5f * kLog2e * a * a), phi);
+    } else if constexpr (ACT == kGeluTanh) {
+      // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u)), u = c (a + k a^3).
+      constexpr float c = 0.79788456080286536f, k = 0.044715f;
+      const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-2.f * kLog2e * c * a * fmaf(k * a, a, 1.f)));
+      value = a * s;
+      slope = s * fmaf(2.f * a * (1.f - s), c * fmaf(3.f * k * a, a, 1.f), 1.f);
+    } else {
+      value = a < 0.f ? 0.f : a;  // a NaN stays one
+      slope = a > 0.f ? 1.f : 0.f;
+    }
+  }
+};
+
+// Calls f(std::integral_constant<int, ACT>{}) for an activation known at run
+// time (the same for a whole launch).
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  switch (act) {
+    case kSilu: f(std::integral_constant<int, kSilu>{}); break;
+    case kGelu: f(std::integral_constant<int, kGelu>{}); break;
+    case kGeluTanh: f(std::integral_constant<int, kGeluTanh>{}); break;
+    default: f(std::integral_constant<int, kRelu>{});
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Copies of operands, padded or transposed, all in one launch (xent.hpp's
+// 64 x 64 tiles).
+// ---------------------------------------------------------------------------
+constexpr int kMlpCopies = 5;
+struct MlpPrepArgs {
+  XentCopyArgs copy[kMlpCopies];
+};
+template <typename T>
+__global__ void __launch_bounds__(256) k_mlp_prep(MlpPrepArgs p) {
+  int64_t b = blockIdx.x;
+#pragma unroll
+  for (int i = 0; i < kMlpCopies; ++i) {
+    const int64_t blocks = p.copy[i].blocks();
+    if (b >= 0 && b < blocks)
+      xent_copy_tile<T>(p.copy[i], XentRowArgs{}, (int)(b / p.copy[i].tiles_c), (int)(b % p.copy[i].tiles_c));
+    b -= blocks;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Results stored from the accumulators.
+// ---------------------------------------------------------------------------
+
+// A lane's 16-byte chunk at column c of a caller's row, at any alignment; the
+// row's last one may be partial.  Returns nonfinite_bits of what was stored.
+template <typename T>
+__device__ __forceinline__ uint32_t put_chunk(T* row, int c, int cols, const u32x4_t& q) {
+  constexpr int V = kVec<T>;
+  uint32_t found = 0;
+  if (c + V <= cols) {
+    *reinterpret_cast<typename Vec16<sizeof(T)>::type*>(row + c) = q;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) found |= nonfinite_bits<T>(q[k]);
+  } else {
+    // Columns past the result may hold anything.
+    const T* e = reinterpret_cast<const T*>(&q);
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (c + k < cols) {
+        row[c + k] = e[k];
+        found |= nonfinite_bits<T>(one_bits(e[k]));
+      }
+  }
+  return found;
+}
+
+// A 32 x 32 block of a caller's matrix: lane (lr, h) gives row `row` (its
+// lr), columns c0 + 8 g + 4 h + e in v[g][e].
+template <typename T>
+__device__ __forceinline__ uint32_t put_block(T* row, int c0, int cols, int h, const f32x4 (&v)[4]) {
+  uint32_t found = 0;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      const uint4 q = join_quads(pack_quad<T>(v[g]), pack_quad<T>(v[g + 1]));
+      found |= put_chunk<T>(row, c0 + 8 * (g + h), cols, u32x4_t{q.x, q.y, q.z, q.w});
+    }
+  } else {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) found |= put_chunk<T>(row, c0 + 8 * g + 4 * h, cols, __builtin_bit_cast(u32x4_t, v[g]));
+  }
+  return found;
+}
+
+// The same into a buffer of the workspace, whose rows are whole vectors.
+template <typename T>
+__device__ __forceinline__ void put_padded(T* row, int h, const f32x4 (&v)[4]) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int g = 0; g < 4; g += 2)
+      *reinterpret_cast<uint4*>(row + 8 * (g + h)) = join_quads(pack_quad<T>(v[g]), pack_quad<T>(v[g + 1]));
+  } else {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) *reinterpret_cast<f32x4*>(row + 8 * g + 4 * h) = v[g];
+  }
+}
+// And transposed: col points at this lane's column of the quad (4 h + its
+// place q) and the quad's first row.
+template <typename T>
+__device__ __forceinline__ void put_transposed(T* col, int64_t ld, const f32x4 (&v)[4]) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(col + (int64_t)(8 * g) * ld) = transpose_quad(pack_quad<T>(v[g]));
+    else
+      *reinterpret_cast<f32x4*>(col + (int64_t)(8 * g) * ld) = transpose_quad(v[g]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Forward: both projections and the activation.
+// ---------------------------------------------------------------------------
+struct MlpUpArgs {
+  const void *X, *G, *U;   // n x k, f x k, f x k, rows of whole k-tiles
+  int64_t ldx, ldw;        // row strides in bytes
+  int ktiles;
+  int64_t n, f;
+  int tiles_m, tiles_n;    // tiles of TM rows and TN / 2 columns
+  void* h;                 // tiles_m TM x ldh
+  int64_t ldh;
+  void *gate, *up;         // n x f, row stride lds, or null
+  int64_t lds;
+  int act;
+  int32_t* d_status;
+  int32_t status_bits;
+};
+
+template <typename T, int TM, int TN>
+struct UpEpilogue {
+  using A = Acc<T, TM, TN>;
+  static constexpr int FH = A::FN / 2;  // 32-column blocks of a, then as many of b
+  static constexpr int kStores = A::FM * FH * (sizeof(T) == 2 ? 2 : 4);
+  const MlpUpArgs& p;
+  const TileRun& run;
+  LanePlace<TM, TN> at;
+  __device__ __forceinline__ void load(int) {}
+  __device__ __forceinline__ void settle() {}
+  __device__ __forceinline__ void store(int j, A& acc) {
+    int tm, tn;
+    grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+    const int64_t row0 = (int64_t)tm * TM + at.wr + at.lr;
+    const int64_t col0 = (int64_t)tn * (TN / 2) + at.wc / 2;
+    const int cols = (int)(p.f - col0);  // of this wave's, those that exist
+    if (cols < TN / 4) {
+      // Columns past f are zeros whatever x holds: they are summed over next.
+#pragma unroll
+      for (int fm = 0; fm < A::FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < A::FN; ++fn)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int c = 32 * (fn % FH) + 8 * (e >> 2) + 4 * at.h + (e & 3);
+            acc.v[fm][fn][e] = c < cols ? acc.v[fm][fn][e] : 0.f;
+          }
+    }
+    if (p.gate) {
+      uint32_t found = 0;
+#pragma unroll
+      for (int fm = 0; fm < A::FM; ++fm) {
+        const int64_t row = row0 + fm * 32;
+        if (row >= p.n) continue;
+        T* gate = reinterpret_cast<T*>(p.gate) + row * p.lds + col0;
+        T* up = reinterpret_cast<T*>(p.up) + row * p.lds + col0;
+#pragma unroll
+        for (int fn = 0; fn < FH; ++fn) {
+          f32x4 a[4], b[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[g][e] = acc.v[fm][fn][4 * g + e];
+              b[g][e] = acc.v[fm][fn + FH][4 * g + e];
+            }
+          found |= put_block<T>(gate, 32 * fn, cols, at.h, a);
+          found |= put_block<T>(up, 32 * fn, cols, at.h, b);
+        }
+      }
+      if (p.d_status) report_status(p.d_status, p.status_bits, found & kNonfiniteMask<T>);
+    }
+    with_act(p.act, [&](auto act) {
+#pragma unroll
+      for (int fm = 0; fm < A::FM; ++fm) {
+        T* row = reinterpret_cast<T*>(p.h) + (row0 + fm * 32) * p.ldh + col0;
+#pragma unroll
+        for (int fn = 0; fn < FH; ++fn) {
+          f32x4 v[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[g][e] = Act<decltype(act)::value>(acc.v[fm][fn][4 * g + e]).value * acc.v[fm][fn + FH][4 * g + e];
+          put_padded<T>(row + 32 * fn, at.h, v);
+        }
+      }
+    });
+  }
+};
+
+template <typename T, int TM, int TN>
+__global__ void __launch_bounds__(kThreads, 1) k_mlp_up(MlpUpArgs p) {
+  const TileRun run(p.tiles_m * p.tiles_n);
+  // Wave w copies TN / 4 right-hand rows of a tile: even waves rows of Wg,
+  // odd ones rows of Wu, for the columns of the waves w / 2 and w / 2 + 2.
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const char* W = reinterpret_cast<const char*>(w & 1 ? p.U : p.G);
+  stream_tiles<T, TM, TN>(
+      run.count, p.ldx, p.ldw, (uint32_t)(p.ktiles * kRowBytes),
+      [&](int j) {
+        int tm, tn;
+        grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+        const int64_t row0 = (int64_t)tm * TM, col0 = (int64_t)tn * (TN / 2) + (w >> 1) * (TN / 4);
+        const int64_t left = p.f - col0;
+        // The stream adds the wave's own offset to R and takes it off rows_r.
+        const int own = w * (TN / 4);
+        return StreamTile{reinterpret_cast<const char*>(p.X) + row0 * p.ldx, W + (col0 - own) * p.ldw,
+                          (int)(p.n - row0 < TM ? p.n - row0 : TM), own + (int)(left < TN / 4 ? left : TN / 4), 0,
+                          p.ktiles};
+      },
+      UpEpilogue<T, TM, TN>{p, run});
+}
+
+// ---------------------------------------------------------------------------
+// Backward: dh and what follows from it.
+// ---------------------------------------------------------------------------
+struct MlpDzArgs {
+  const void *dY, *WT;     // n x k and f_pad x k (Wd transposed)
+  int64_t ldy, ldw;        // bytes
+  int ktiles;
+  int64_t n, f;
+  int tiles_m, tiles_n;
+  const void *gate, *up;   // n x f, row stride lds
+  int64_t lds;
+  void* dz;                // n_pad x 2 f_pad: da, db
+  void* dzt;               // 2 f_pad x n_pad
+  void* ht;                // f_pad x n_pad
+  int64_t n_pad, f_pad;
+  int act;
+};
+
+// Four columns of a caller's row as floats.
+template <typename T>
+__device__ __forceinline__ f32x4 load_quad(const T* s) {
+  if constexpr (sizeof(T) == 2) {
+    typedef uint32_t u32x2_a __attribute__((ext_vector_type(2), aligned(2)));
+    typedef T h4 __attribute__((ext_vector_type(4)));
+    const u32x2_a q = *reinterpret_cast<const u32x2_a*>(s);
+    const h4 v = __builtin_bit_cast(h4, uint2{q[0], q[1]});
+    return f32x4{to_f32<T>(v[0]), to_f32<T>(v[1]), to_f32<T>(v[2]), to_f32<T>(v[3])};
+  } else {
+    typedef float f32x4_a __attribute__((ext_vector_type(4), aligned(4)));
+    const f32x4_a q = *reinterpret_cast<const f32x4_a*>(s);
+    return f32x4{q[0], q[1], q[2], q[3]};
+  }
+}
+
+template <typename T, int TM, int TN>
+struct MlpDzEpilogue {
+  using A = Acc<T, TM, TN>;
+  // Per 32 x 32 block, every one executed by every wave: 12 transposed ones,
+  // and in rows 4 of 16 bits or 8 of fp32.
+  static constexpr int kStores = A::FM * A::FN * (sizeof(T) == 2 ? 16 : 20);
+  const MlpDzArgs& p;
+  const TileRun& run;
+  LanePlace<TM, TN> at;
+  __device__ __forceinline__ void load(int) {}
+  __device__ __forceinline__ void settle() {}
+  __device__ __forceinline__ void store(int j, A& acc) {
+    int tm, tn;
+    grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+    const int64_t row0 = (int64_t)tm * TM + at.wr, col0 = (int64_t)tn * TN + at.wc;
+    // Rows and columns of this wave's part that exist.
+    const int rows = (int)(p.n - row0 < TM / 2 ? p.n - row0 : TM / 2), cols = (int)(p.f - col0 < TN / 2 ? p.f - col0 : TN / 2);
+    const bool whole = rows == TM / 2 && cols == TN / 2;
+    const int q = at.lr & 3, i4 = at.lr & ~3;  // place in the quad, the quad's first row
+    with_act(p.act, [&](auto act) {
+#pragma unroll
+      for (int fm = 0; fm < A::FM; ++fm) {
+        const int r = fm * 32 + at.lr;
+        const int64_t in = (row0 + r) * p.lds + col0 + 4 * at.h;
+        const T *gate = reinterpret_cast<const T*>(p.gate) + in, *up = reinterpret_cast<const T*>(p.up) + in;
+        T* dz = reinterpret_cast<T*>(p.dz) + (row0 + r) * 2 * p.f_pad + col0;
+        const int64_t t = (col0 + 4 * at.h + q) * p.n_pad + row0 + fm * 32 + i4;
+        T *dzt = reinterpret_cast<T*>(p.dzt) + t, *ht = reinterpret_cast<T*>(p.ht) + t;
+#pragma unroll
+        for (int fn = 0; fn < A::FN; ++fn) {
+          f32x4 a[4], b[4];
+          if (whole) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              a[g] = load_quad<T>(gate + 32 * fn + 8 * g);
+              b[g] = load_quad<T>(up + 32 * fn + 8 * g);
+            }
+          } else {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const bool ok = r < rows && 32 * fn + 8 * g + 4 * at.h + e < cols;
+                a[g][e] = ok ? to_f32<T>(gate[32 * fn + 8 * g + e]) : 0.f;
+                b[g][e] = ok ? to_f32<T>(up[32 * fn + 8 * g + e]) : 0.f;
+                // Outside they are operands of sums over rows or columns:
+                // zeros whatever dy holds.
+                acc.v[fm][fn][4 * g + e] = ok ? acc.v[fm][fn][4 * g + e] : 0.f;
+              }
+          }
+          f32x4 da[4], db[4], h[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const Act<decltype(act)::value> s(a[g][e]);
+              const float dh = acc.v[fm][fn][4 * g + e];
+              da[g][e] = dh * b[g][e] * s.slope;
+              db[g][e] = dh * s.value;
+              h[g][e] = s.value * b[g][e];
+            }
+          put_padded<T>(dz + 32 * fn, at.h, da);
+          put_padded<T>(dz + p.f_pad + 32 * fn, at.h, db);
+          put_transposed<T>(dzt + (int64_t)(32 * fn) * p.n_pad, p.n_pad, da);
+          put_transposed<T>(dzt + (p.f_pad + 32 * fn) * p.n_pad, p.n_pad, db);
+          put_transposed<T>(ht + (int64_t)(32 * fn) * p.n_pad, p.n_pad, h);
+        }
+      }
+    });
+  }
+};
+
+template <typename T, int TM, int TN>
+__global__ void __launch_bounds__(kThreads, 1) k_mlp_dz(MlpDzArgs p) {
+  const TileRun run(p.tiles_m * p.tiles_n);
+  stream_tiles<T, TM, TN>(
+      run.count, p.ldy, p.ldw, (uint32_t)(p.ktiles * kRowBytes),
+      [&](int j) {
+        int tm, tn;
+        grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+        const int64_t row0 = (int64_t)tm * TM;
+        return StreamTile{reinterpret_cast<const char*>(p.dY) + row0 * p.ldy,
+                          reinterpret_cast<const char*>(p.WT) + (int64_t)tn * TN * p.ldw,
+                          (int)(p.n - row0 < TM ? p.n - row0 : TM), TN, 0, p.ktiles};
+      },
+      MlpDzEpilogue<T, TM, TN>{p, run});
+}
+
+// ---------------------------------------------------------------------------
+// Products whose result is the caller's, each L R^T: up to kMlpProducts of one
+// shape of operand rows (the weights' gradients), then one more (dx, or y
+// alone), whose contraction may be split.
+// ---------------------------------------------------------------------------
+struct MlpProduct {
+  const void *L, *R;
+  int tiles_m, tiles_n;
+  int64_t rows_l, rows_r;  // rows of L and R that may be read
+  void* out;
+  int64_t ldo, rows;       // row stride, valid rows
+  int cols;                // and columns
+};
+constexpr int kMlpProducts = 3;
+struct MlpGradArgs {
+  MlpProduct w[kMlpProducts];
+  int w_tiles[kMlpProducts];  // tiles up to and with product i
+  int64_t w_ld;               // row stride of their operands, bytes
+  int w_ktiles;
+  MlpProduct x;
+  int64_t x_ldl, x_ldr;
+  int x_ktiles, splits;
+  float* parts;               // splits > 1: [splits][x.tiles_m TM][x.tiles_n TN]
+  int extra;                  // DhRun's
+  int32_t* d_status;
+  int32_t status_bits;
+};
+
+template <typename T, int TM, int TN>
+__device__ __forceinline__ void product_store(const MlpProduct& o, int tm, int tn, const LanePlace<TM, TN>& at,
+                                              const Acc<T, TM, TN>& acc, int32_t* d_status, int32_t bits) {
+  using A = Acc<T, TM, TN>;
+  const int64_t row0 = (int64_t)tm * TM + at.wr + at.lr;
+  const int col0 = tn * TN + at.wc;
+  uint32_t found = 0;
+#pragma unroll
+  for (int fm = 0; fm < A::FM; ++fm) {
+    const int64_t row = row0 + fm * 32;
+    if (row >= o.rows) continue;
+    T* out = reinterpret_cast<T*>(o.out) + row * o.ldo;
+#pragma unroll
+    for (int fn = 0; fn < A::FN; ++fn) {
+      f32x4 v[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[g][e] = acc.v[fm][fn][4 * g + e];
+      found |= put_block<T>(out, col0 + 32 * fn, o.cols, at.h, v);
+    }
+  }
+  if (d_status) report_status(d_status, bits, found & kNonfiniteMask<T>);
+}
+
+template <typename T, int TM, int TN>
+__device__ __forceinline__ StreamTile product_tile(const MlpProduct& o, int64_t ldl, int64_t ldr, int tm, int tn, int kt0,
+                                                   int kts) {
+  const int64_t l = o.rows_l - (int64_t)tm * TM, r = o.rows_r - (int64_t)tn * TN;
+  return StreamTile{reinterpret_cast<const char*>(o.L) + (int64_t)tm * TM * ldl,
+                    reinterpret_cast<const char*>(o.R) + (int64_t)tn * TN * ldr,
+                    (int)(l < TM ? l : TM), (int)(r < TN ? r : TN), kt0, kts};
+}
+
+// Which of the weights' gradients tile i of their list is, and where in it.
+struct WeightTile {
+  int which, tm, tn;
+  __device__ __forceinline__ WeightTile(const MlpGradArgs& p, int i) {
+    which = i < p.w_tiles[0] ? 0 : i < p.w_tiles[1] ? 1 : 2;
+    const int first = which == 0 ? 0 : which == 1 ? p.w_tiles[0] : p.w_tiles[1];
+    const int m = which == 0 ? p.w[0].tiles_m : which == 1 ? p.w[1].tiles_m : p.w[2].tiles_m;
+    const int n = which == 0 ? p.w[0].tiles_n : which == 1 ? p.w[1].tiles_n : p.w[2].tiles_n;
+    grouped_tile(i - first, m, n, tm, tn);
+  }
+};
+
+template <typename T, int TM, int TN>
+struct WeightEpilogue {
+  static constexpr int kStores = 0;  // rows and columns past the result store nothing
+  const MlpGradArgs& p;
+  const TileRun& run;
+  LanePlace<TM, TN> at;
+  __device__ __forceinline__ void load(int) {}
+  __device__ __forceinline__ void settle() {}
+  __device__ __forceinline__ void store(int j, Acc<T, TM, TN>& acc) {
+    const WeightTile t(p, run.at(j));
+    product_store<T, TM, TN>(p.w[t.which], t.tm, t.tn, at, acc, p.d_status, p.status_bits);
+  }
+};
+
+template <typename T, int TM, int TN>
+struct SplitEpilogue {
+  using A = Acc<T, TM, TN>;
+  static constexpr int kStores = 0;
+  const MlpGradArgs& p;
+  const DhRun& run;
+  LanePlace<TM, TN> at;
+  __device__ __forceinline__ void load(int) {}
+  __device__ __forceinline__ void settle() {}
+  __device__ __forceinline__ void store(int j, A& acc) {
+    const int per = p.x.tiles_m * p.x.tiles_n, i = run.at(j);
+    int tm, tn;
+    grouped_tile(i % per, p.x.tiles_m, p.x.tiles_n, tm, tn);
+    if (p.splits == 1) return product_store<T, TM, TN>(p.x, tm, tn, at, acc, p.d_status, p.status_bits);
+    const int64_t ld = (int64_t)p.x.tiles_n * TN;
+    float* out = p.parts + ((int64_t)(i / per) * p.x.tiles_m * TM + (int64_t)tm * TM + at.wr + at.lr) * ld + tn * TN +
+                 at.wc + 4 * at.h;
+#pragma unroll
+    for (int fm = 0; fm < A::FM; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < A::FN; ++fn)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<f32x4*>(out + (int64_t)fm * 32 * ld + fn * 32 + 8 * g) =
+              f32x4{acc.v[fm][fn][4 * g], acc.v[fm][fn][4 * g + 1], acc.v[fm][fn][4 * g + 2], acc.v[fm][fn][4 * g + 3]};
+  }
+};
+
+template <typename T, int TM, int TN>
+__global__ void __launch_bounds__(kThreads, 1) k_mlp_products(MlpGradArgs p) {
+  const int w_tiles = p.w_tiles[kMlpProducts - 1];
+  if (w_tiles > 0) {
+    const TileRun run(w_tiles);
+    stream_tiles<T, TM, TN>(
+        run.count, p.w_ld, p.w_ld, (uint32_t)(p.w_ktiles * kRowBytes),
+        [&](int j) {
+          const WeightTile t(p, run.at(j));
+          return product_tile<T, TM, TN>(p.w[t.which], p.w_ld, p.w_ld, t.tm, t.tn, 0, p.w_ktiles);
+        },
+        WeightEpilogue<T, TM, TN>{p, run});
+    // All reads of the stages are over before they are filled again.
+    lds_barrier();
+  }
+  const int per = p.x.tiles_m * p.x.tiles_n;
+  const DhRun run(w_tiles, per * p.splits, p.extra);
+  stream_tiles<T, TM, TN>(
+      run.count, p.x_ldl, p.x_ldr, (uint32_t)(p.x_ktiles * kRowBytes),
+      [&](int j) {
+        const int i = run.at(j), split = i / per;
+        int tm, tn;
+        grouped_tile(i % per, p.x.tiles_m, p.x.tiles_n, tm, tn);
+        const int kt0 = (int)((int64_t)p.x_ktiles * split / p.splits);
+        const int kt1 = (int)((int64_t)p.x_ktiles * (split + 1) / p.splits);
+        return product_tile<T, TM, TN>(p.x, p.x_ldl, p.x_ldr, tm, tn, kt0, kt1 - kt0);
+      },
+      SplitEpilogue<T, TM, TN>{p, run});
+}
+
+// The splits' sum, rounded: a thread per 16 bytes of a row.
+template <typename T>
+__global__ void __launch_bounds__(64) k_mlp_join(const float* parts, int splits, int64_t rows_pad, int64_t cols_pad,
+                                                 T* out, int64_t ldo, int cols, int32_t* d_status, int32_t status_bits) {
+  constexpr int V = kVec<T>;
+  const int64_t r = blockIdx.x;
+  const int c = (blockIdx.y * 64 + threadIdx.x) * V;
+  uint32_t found = 0;
+  if (c < cols) {
+    f32x4 v[V / 4];
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q) v[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const float* a = parts + r * cols_pad + c;
+    auto sum = [&](int k0, auto batch) {
+      constexpr int B = decltype(batch)::value;
+      f32x4 add[B][V / 4];
+#pragma unroll
+      for (int k = 0; k < B; ++k)
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) add[k][q] = reinterpret_cast<const f32x4*>(a + (k0 + k) * rows_pad * cols_pad)[q];
+#pragma unroll
+      for (int k = 0; k < B; ++k)
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[q][e] += add[k][q][e];
+    };
+    int k = 0;
+    for (; k + 8 <= splits; k += 8) sum(k, std::integral_constant<int, 8>{});
+    for (; k + 2 <= splits; k += 2) sum(k, std::integral_constant<int, 2>{});
+    if (k < splits) sum(k, std::integral_constant<int, 1>{});
+    u32x4_t packed;
+    T* t = reinterpret_cast<T*>(&packed);
+#pragma unroll
+    for (int k2 = 0; k2 < V; ++k2) t[k2] = from_f32<T>(v[k2 / 4][k2 % 4]);
+    found = put_chunk<T>(out + r * ldo, c, cols, packed);
+  }
+  if (d_status) report_status(d_status, status_bits, found & kNonfiniteMask<T>);
+}
+
+// ---------------------------------------------------------------------------
+// Forward for a few rows: a wave reads whole rows of the weights, in vectors
+// at any alignment, the rows of x or h coming from the cache.
+// ---------------------------------------------------------------------------
+constexpr int kMlpDotRows = 8;  // rows of weights that a wave has in flight
+struct MlpDotUpArgs {
+  const void *X, *G, *U;
+  int64_t ldx, ldg, ldu, n, f;  // elements
+  int d;
+  void* h;                      // n x ldh
+  int64_t ldh;
+  void *gate, *up;              // n x f, row stride lds, or null
+  int64_t lds;
+  int act;
+  int32_t* d_status;
+  int32_t status_bits;
+};
+
+// acc[r][i] = the wave's share of w[r] . x[i] over columns c0, c0 + step, ...
+template <typename T, int R, int N, int FORM>
+__device__ __forceinline__ void dot_rows(const T* const (&w)[R], const T* x, int64_t ldx, int n, int cols, int first,
+                                         int step, float (&acc)[R][N]) {
+  constexpr int V = kVec<T>;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[r][i] = 0.f;
+  u32x4_t raw[R], next[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) raw[r] = issue16<FORM, T>(w[r], first + lane * V, cols);
+  for (int c0 = first; c0 < cols; c0 += step) {
+    const int c = c0 + lane * V, cn = c0 + step < cols ? c + step : c;
+#pragma unroll
+    for (int r = 0; r < R; ++r) next[r] = issue16<FORM, T>(w[r], cn, cols);
+    float h[N][V];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const T* row = x + (i < n ? i : 0) * ldx;
+      unpack<T>(settle16<FORM, T>(issue16<FORM, T>(row, c, cols), row, c, cols), h[i]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float v[V];
+      unpack<T>(settle16<FORM, T>(raw[r], w[r], c, cols), v);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[r][i] = fmaf(v[k], h[i][k], acc[r][i]);
+      raw[r] = next[r];
+    }
+  }
+}
+
+// A wave per kMlpDotRows / 2 columns of h.
+template <typename T, int N, int FORM>
+__global__ void __launch_bounds__(256) k_mlp_dot_up(MlpDotUpArgs p) {
+  constexpr int V = kVec<T>, C = kMlpDotRows / 2;
+  const int lane = threadIdx.x & 63;
+  const int64_t c0 = ((int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * C;
+  if (c0 >= p.f) return;
+  const T* w[kMlpDotRows];
+#pragma unroll
+  for (int r = 0; r < C; ++r) {
+    const int64_t row = c0 + r < p.f ? c0 + r : p.f - 1;
+    w[r] = reinterpret_cast<const T*>(p.G) + row * p.ldg;
+    w[C + r] = reinterpret_cast<const T*>(p.U) + row * p.ldu;
+  }
+  float acc[kMlpDotRows][N];
+  dot_rows<T, kMlpDotRows, N, FORM>(w, reinterpret_cast<const T*>(p.X), p.ldx, (int)p.n, p.d, 0, 64 * V, acc);
+  // Lane r N + i keeps column c0 + r of row i.
+  float a = 0.f, b = 0.f;
+#pragma unroll
+  for (int r = 0; r < C; ++r)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float s = wave_row_sum<64>(acc[r][i]), u = wave_row_sum<64>(acc[C + r][i]);
+      a = lane == r * N + i ? s : a;
+      b = lane == r * N + i ? u : b;
+    }
+  const int row = lane % N;
+  const int64_t c = c0 + lane / N;
+  bool bad = false;
+  if (lane < C * N && row < p.n && c < p.f) {
+    float h = 0.f;
+    with_act(p.act, [&](auto act) { h = Act<decltype(act)::value>(a).value * b; });
+    reinterpret_cast<T*>(p.h)[row * p.ldh + c] = from_f32<T>(h);
+    if (p.gate) {
+      reinterpret_cast<T*>(p.gate)[row * p.lds + c] = from_f32<T>(a);
+      reinterpret_cast<T*>(p.up)[row * p.lds + c] = from_f32<T>(b);
+      bad = !(fabsf(a) < kRoundsToInf<T> && fabsf(b) < kRoundsToInf<T>);
+    }
+  }
+  if (p.d_status) report_status(p.d_status, p.status_bits, bad);
+}
+
+struct MlpDotDownArgs {
+  const void *h, *W;
+  int64_t ldh, ldw, n, d;  // elements
+  int f;
+  void* y;
+  int64_t ldy;
+  int32_t* d_status;
+  int32_t status_bits;
+};
+
+// A block per kMlpDotRows columns of y: there are few of them and their rows
+// are long, so the block's four waves share the columns of f.
+template <typename T, int N, int FORM>
+__global__ void __launch_bounds__(256) k_mlp_dot_down(MlpDotDownArgs p) {
+  constexpr int V = kVec<T>, R = kMlpDotRows;
+  __shared__ float sh[4][R * N];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t c0 = (int64_t)blockIdx.x * R;
+  const T* w[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) w[r] = reinterpret_cast<const T*>(p.W) + (c0 + r < p.d ? c0 + r : p.d - 1) * p.ldw;
+  float acc[R][N];
+  dot_rows<T, R, N, FORM>(w, reinterpret_cast<const T*>(p.h), p.ldh, (int)p.n, p.f, wave * 64 * V, 4 * 64 * V, acc);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float s = wave_row_sum<64>(acc[r][i]);
+      if (lane == 0) sh[wave][r * N + i] = s;
+    }
+  __syncthreads();
+  const int t = threadIdx.x, row = t % N;
+  const int64_t c = c0 + t / N;
+  bool bad = false;
+  if (t < R * N && row < p.n && c < p.d) {
+    const float y = (sh[0][t] + sh[1][t]) + (sh[2][t] + sh[3][t]);
+    reinterpret_cast<T*>(p.y)[row * p.ldy + c] = from_f32<T>(y);
+    bad = !(fabsf(y) < kRoundsToInf<T>);
+  }
+  if (p.d_status) report_status(p.d_status, p.status_bits, bad);
+}
+
+}  // namespace nsk
+
+// ---------------------------------------------------------------------------
+// Launchers, instantiated per operand type in kern_mlp_*.hip.
+// ---------------------------------------------------------------------------
+namespace nsr {
+
+using namespace nsk;
+
+// Tiles of the projections' product, whose right-hand rows are two columns
+// each: rows of the larger and the smaller one, right-hand rows of both.  The
+// other products have xent.hpp's square tiles.
+template <typename T> inline constexpr int kUpLargeM = 128;
+template <typename T> inline constexpr int kUpLargeN = sizeof(T) == 2 ? 256 : 128;
+template <typename T> inline constexpr int kUpSmallM = sizeof(T) == 2 ? 128 : 64;
+template <typename T> inline constexpr int kUpSmallN = 128;
+
+template <typename T> hipError_t launch_mlp_up(const MlpUpArgs& a, bool large, hipStream_t s);
+template <typename T> hipError_t launch_mlp_dz(const MlpDzArgs& a, int edge, hipStream_t s);
+template <typename T> hipError_t launch_mlp_products(const MlpGradArgs& a, int edge, hipStream_t s);
+template <typename T> hipError_t launch_mlp_dot_up(const MlpDotUpArgs& a, hipStream_t s);
+template <typename T> hipError_t launch_mlp_dot_down(const MlpDotDownArgs& a, hipStream_t s);
+
+template <typename T>
+hipError_t mlp_up_of(const MlpUpArgs& a, bool large, hipStream_t s) {
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  if (large)
+    NS_XENT_LAUNCH(k_mlp_up, kUpLargeM<T>, kUpLargeN<T>, tiles, a);
+  else
+    NS_XENT_LAUNCH(k_mlp_up, kUpSmallM<T>, kUpSmallN<T>, tiles, a);
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t mlp_dz_of(const MlpDzArgs& a, int edge, hipStream_t s) {
+  NS_XENT_EDGE(k_mlp_dz, (int64_t)a.tiles_m * a.tiles_n, a);
+}
+template <typename T>
+hipError_t mlp_products_of(const MlpGradArgs& a, int edge, hipStream_t s) {
+  const int64_t tiles = a.w_tiles[kMlpProducts - 1] + (int64_t)a.x.tiles_m * a.x.tiles_n * a.splits;
+  NS_XENT_EDGE(k_mlp_products, tiles, a);
+}
+#define NS_MLP_DOT(K, N, FORM) hipLaunchKernelGGL((K<T, N, FORM>), grid, dim3(256), 0, s, a)
+#define NS_MLP_DOTS(K, COLS)                                                      \
+  auto run = [&](auto form) {                                                     \
+    constexpr int FORM = decltype(form)::value;                                   \
+    switch (xent_dot_rows(a.n)) {                                                 \
+      case 1: NS_MLP_DOT(K, 1, FORM); break;                                      \
+      case 2: NS_MLP_DOT(K, 2, FORM); break;                                      \
+      case 4: NS_MLP_DOT(K, 4, FORM); break;                                      \
+      default: NS_MLP_DOT(K, 8, FORM);                                            \
+    }                                                                             \
+  };                                                                              \
+  if ((COLS) % kVec<T> == 0)                                                      \
+    run(std::integral_constant<int, kEven>{});                                    \
+  else if ((COLS) > kVec<T>)                                                      \
+    run(std::integral_constant<int, kRagged>{});                                  \
+  else                                                                            \
+    run(std::integral_constant<int, kTiny>{});                                    \
+  return hipGetLastError()
+template <typename T>
+hipError_t mlp_dot_up_of(const MlpDotUpArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.f + 2 * kMlpDotRows - 1) / (2 * kMlpDotRows)));
+  NS_MLP_DOTS(k_mlp_dot_up, a.d);
+}
+template <typename T>
+hipError_t mlp_dot_down_of(const MlpDotDownArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.d + kMlpDotRows - 1) / kMlpDotRows));
+  NS_MLP_DOTS(k_mlp_dot_down, a.f);
+}
+
+#define NS_MLP_LAUNCHERS(T)                                                        \
+  template <>                                                                      \
+  hipError_t launch_mlp_up<T>(const MlpUpArgs& a, bool large, hipStream_t s) {     \
+    return mlp_up_of<T>(a, large, s);                                              \
+  }                                                                                \
+  template <>                                                                      \
+  hipError_t launch_mlp_dz<T>(const MlpDzArgs& a, int edge, hipStream_t s) {       \
+    return mlp_dz_of<T>(a, edge, s);                                               \
+  }                                                                                \
+  template <>                                                                      \
+  hipError_t launch_mlp_products<T>(const MlpGradArgs& a, int edge, hipStream_t s) { \
+    return mlp_products_of<T>(a, edge, s);                                         \
+  }                                                                                \
+  template <>                                                                      \
+  hipError_t launch_mlp_dot_up<T>(const MlpDotUpArgs& a, hipStream_t s) {          \
+    return mlp_dot_up_of<T>(a, s);                                                 \
+  }                                                                                \
+  template <>                                                                      \
+  hipError_t launch_mlp_dot_down<T>(const MlpDotDownArgs& a, hipStream_t s) {      \
+    return mlp_dot_down_of<T>(a, s);                                               \
+  }
+
+}  // namespace nsr

@@ -57,6 +57,8 @@ come from the oracle itself):
   closed form of the moments.
 * ``residual_norm`` and its gradients: unit mean squares; the gradients
   against central differences along random directions.
+* ``gated_mlp`` and its gradients, the same way; ``activation``: values at
+  known points, slopes against differences.
 
 No function here is "parity unpinned".
 """
@@ -69,7 +71,8 @@ from .muon import momentum_update, muon_step
 from .training import (embedding, embedding_backward, layer_norm,
                        layer_norm_backward, linear_cross_entropy,
                        linear_cross_entropy_backward, linear_cross_entropy_dz)
-from .block import adamw, residual_norm, residual_norm_backward, state_tops
+from .block import (activation, adamw, gated_mlp, gated_mlp_backward,
+                    residual_norm, residual_norm_backward, state_tops)
 
 __all__ = [
     "CLASSIC_ABC", "TUNED_ABC", "coefficient_schedule", "frobenius_stage",
@@ -79,5 +82,6 @@ __all__ = [
     "embedding", "embedding_backward", "layer_norm", "layer_norm_backward",
     "linear_cross_entropy", "linear_cross_entropy_backward",
     "linear_cross_entropy_dz", "adamw", "state_tops",
+    "activation", "gated_mlp", "gated_mlp_backward",
     "residual_norm", "residual_norm_backward",
 ]

@@ -84,3 +84,42 @@ def residual_norm_backward(ds, dy, s, z, rb=None, rs=None, gate=None, scale=1.0,
         out["dgate"] = g * bhat * wb
         out["dwb"] = (q * bhat).sum(0)
     return out
+
+
+_C, _K = np.sqrt(2.0 / np.pi), 0.044715
+
+
+def activation(a, name):
+    """(value, slope) of an activation."""
+    from math import erf
+
+    a = _f64(a)
+    if name == "relu":
+        return np.maximum(a, 0.0), (a > 0) * 1.0
+    if name == "gelu":
+        phi = 0.5 * (1.0 + np.vectorize(erf, otypes=[float])(a / np.sqrt(2.0)))
+        return a * phi, phi + a * np.exp(-0.5 * a * a) / np.sqrt(2.0 * np.pi)
+    if name == "gelu_tanh":
+        t = np.tanh(_C * (a + _K * a ** 3))
+        return 0.5 * a * (1 + t), 0.5 * (1 + t) + 0.5 * a * (1 - t * t) * _C * (1 + 3 * _K * a * a)
+    with np.errstate(over="ignore"):
+        s = 1.0 / (1.0 + np.exp(-a))
+    return a * s, s * (1.0 + a * (1.0 - s))
+
+
+def gated_mlp(x, w_gate, w_up, w_down, act="silu"):
+    """(y, a, b, h) of a gated feed-forward block."""
+    x = _f64(x)
+    a, b = x @ _f64(w_gate).T, x @ _f64(w_up).T
+    h = activation(a, act)[0] * b
+    return h @ _f64(w_down).T, a, b, h
+
+
+def gated_mlp_backward(dy, x, w_gate, w_up, w_down, a, b, act="silu"):
+    """A dict of the gradients (dx, dwg, dwu, dwd) and of what they are made of (dh, da, db, h), given a and b."""
+    dy, x, a, b = _f64(dy), _f64(x), _f64(a), _f64(b)
+    value, slope = activation(a, act)
+    dh = dy @ _f64(w_down)
+    da, db, h = dh * b * slope, dh * value, value * b
+    return {"dx": da @ _f64(w_gate) + db @ _f64(w_up), "dwg": da.T @ x, "dwu": db.T @ x, "dwd": dy.T @ h,
+            "dh": dh, "da": da, "db": db, "h": h}

@@ -170,3 +170,109 @@ def test_residual_norm_backward_refusals():
     assert nsa.residual_norm_workspace_size(4, 0) == 0
     # No rows and nothing wanted.
     assert _norm_back(rows=0, dg=None, dwb=None, dw=None) == 0
+
+
+# ---------------------------------------------------------------------------
+# The gated feed-forward block.
+# ---------------------------------------------------------------------------
+ACTS = ["silu", "gelu", "gelu_tanh", "relu"]
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_oracle_activations(act):
+    a = np.array([-30.0, -4.0, -1.0, -0.3, 0.2, 1.0, 3.0, 30.0])
+    value, slope = oracle.activation(a, act)
+    e = 1e-6
+    assert np.allclose(slope, (oracle.activation(a + e, act)[0] - oracle.activation(a - e, act)[0]) / (2 * e), atol=1e-8)
+    at_one = {"silu": 1 / (1 + np.exp(-1.0)), "gelu": 0.841344746, "gelu_tanh": 0.841191991, "relu": 1.0}[act]
+    assert value[5] == pytest.approx(at_one, rel=1e-8) and value[7] == pytest.approx(30.0) and abs(value[0]) < 1e-10
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_oracle_gated_mlp_gradients_against_differences(act):
+    rng = np.random.default_rng(8)
+    at = {"x": rng.normal(size=(4, 5)), "w_gate": rng.normal(size=(7, 5)), "w_up": rng.normal(size=(7, 5)),
+          "w_down": rng.normal(size=(5, 7))}
+    dy = rng.normal(size=(4, 5))
+    _, a, b, h = oracle.gated_mlp(**at, act=act)
+    o = oracle.gated_mlp_backward(dy, **at, a=a, b=b, act=act)
+    assert np.allclose(o["h"], h)
+    for name, grad in (("x", "dx"), ("w_gate", "dwg"), ("w_up", "dwu"), ("w_down", "dwd")):
+        d = rng.normal(size=at[name].shape)
+        slope = _slope(lambda v: (dy * oracle.gated_mlp(**dict(at, **{name: v}), act=act)[0]).sum(), at[name], d, 1e-6)
+        assert slope == pytest.approx((o[grad] * d).sum(), rel=1e-5), name
+
+
+def _mlp(X=PTR, ldx=64, G=PTR, ldg=64, U=PTR, ldu=64, D=PTR, ldd=128, rows=40, cols=64, inner=128, dtype=B.NS_BF16, act=0,
+         Y=PTR, ldy=64, gate=PTR, up=PTR, lds=128, ws=256, nb=1 << 40):
+    return B.lib().ns_gated_mlp(X, ldx, G, ldg, U, ldu, D, ldd, rows, cols, inner, dtype, act, Y, ldy, gate, up, lds, None,
+                                ws, nb, None)
+
+
+def _mlp_back(dY=PTR, lddy=64, X=PTR, ldx=64, G=PTR, ldg=64, U=PTR, ldu=64, D=PTR, ldd=128, gate=PTR, up=PTR, lds=128,
+              rows=40, cols=64, inner=128, dtype=B.NS_BF16, act=0, dX=PTR, lddx=64, dG=PTR, lddg=64, dU=PTR, lddu=64,
+              dD=PTR, lddd=128, ws=256, nb=1 << 40):
+    return B.lib().ns_gated_mlp_backward(dY, lddy, X, ldx, G, ldg, U, ldu, D, ldd, gate, up, lds, rows, cols, inner, dtype,
+                                         act, dX, lddx, dG, lddg, dU, lddu, dD, lddd, None, ws, nb, None)
+
+
+@built
+def test_gated_mlp_refusals():
+    for call, pointers, strides in (
+            (_mlp, ("X", "G", "U", "D", "Y", "gate", "up"), ("ldx", "ldg", "ldu", "ldd", "ldy", "lds")),
+            (_mlp_back, ("dY", "X", "G", "U", "D", "gate", "up"),
+             ("lddy", "ldx", "ldg", "ldu", "ldd", "lds", "lddx", "lddg", "lddu", "lddd"))):
+        for name in pointers:
+            assert call(**{name: None}) == INV, name
+        for name in strides:
+            assert call(**{name: 63}) == INV and call(**{name: (1 << 23) + 1}) == INV, name
+        for kw in (dict(rows=-1), dict(rows=(1 << 22) + 1), dict(cols=0), dict(inner=0), dict(cols=(1 << 20) + 1),
+                   dict(inner=(1 << 20) + 1), dict(act=4), dict(act=-1), dict(rows=1 << 22, inner=1 << 19)):
+            assert call(**kw) == INV, kw
+        assert call(dtype=3) == DT
+        assert call(ws=None) == WSP and call(ws=100) == WSP and call(nb=16) == WSP
+    assert _mlp(rows=0, X=None, Y=None, ws=None, nb=0) == 0
+    assert _mlp_back(rows=0, dG=None, dU=None, dD=None, ws=None, nb=0) == 0
+    # Nothing wanted, nothing enqueued.
+    assert _mlp_back(dX=None, dG=None, dU=None, dD=None) == 0
+    # A misaligned operand needs the copies' workspace too.
+    need = nsa.gated_mlp_workspace_size(40, 64, 128)
+    assert nsa.gated_mlp_workspace_size(40, 64, 128, aligned=False) > need
+    assert _mlp(X=PTR + 2, nb=need) == WSP and _mlp(ldg=128, ldu=192, nb=need) == WSP
+    need = nsa.gated_mlp_workspace_size(40, 64, 128, backward=True)
+    assert _mlp_back(dY=PTR + 2, nb=need) == WSP
+    assert nsa.gated_mlp_workspace_size(-1, 64, 128) == 0 and nsa.gated_mlp_workspace_size(4, 0, 128) == 0
+    assert nsa.plan_gated_mlp(0, 64, 128) == [] and nsa.plan_gated_mlp(0, 64, 128, backward=True) == ["zero<bf16>"]
+    with pytest.raises(nsa.NSError):
+        nsa.plan_gated_mlp(4, 64, 0)
+
+
+@built
+def test_the_cases_reach_every_build_of_the_gated_mlp():
+    import itertools
+
+    from block_cases import MLP_RUNS
+    types = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+    def builds(n, d, f, t, aligned, backward):
+        return {e + (" back" if backward else "") for e in nsa.plan_gated_mlp(n, d, f, types[t], aligned, backward)
+                if "=" not in e}
+
+    every, covered = set(), set()
+    for n, d, f, t, aligned, backward in itertools.product(
+            [1, 2, 3, 4, 5, 8, 9, 48, 129, 300, 513, 1003, 3000, 8192, 20000], [1, 5, 64, 77, 768, 1000, 4096],
+            [1, 3, 64, 203, 1407, 2048, 14336], types, (True, False), (True, False)):
+        every |= builds(n, d, f, t, aligned, backward)
+    for n, d, f, t in MLP_RUNS:
+        for backward in (False, True):
+            covered |= builds(n, d, f, t, True, backward)
+    assert every - covered == set()
+
+
+@built
+def test_block_calls_refuse_host_tensors():
+    x, w = torch.zeros(4, 8), torch.zeros(8, 8)
+    for call in (lambda: nsa.gated_mlp(x, w, w, w), lambda: nsa.gated_mlp_backward(x, x, w, w, w, x, x),
+                 lambda: nsa.residual_norm(x, x), lambda: nsa.residual_norm_backward(x, None, x)):
+        with pytest.raises(ValueError, match="device tensor"):
+            call()

@@ -1,0 +1,42 @@
+"""The waits of the gated feed-forward block's products, read from the
+assembly that the compiler makes of them (host only; see
+test_training_waits.py)."""
+
+import re
+import subprocess
+
+import pytest
+
+from newton_schulz_matrix_amd import build as nsbuild
+from test_training_waits import HIPCC, _steps
+
+# And the vector stores that their waits count on at a tile's border, per
+# 32 x 32 block of a wave: of h 2 in 16 bits and 4 in fp32 (for half the
+# blocks, beside twice as many of a and b, which are not counted on), of da,
+# db and h 16 and 20.
+KERNELS = [("k_mlp_up<__bf16, 128, 256>(MlpUpArgs)", 4 * (2 + 4)), ("k_mlp_up<float, 64, 128>(MlpUpArgs)", 4 + 8),
+           ("k_mlp_dz<_Float16, 192, 192>(MlpDzArgs)", 9 * 16), ("k_mlp_dz<float, 64, 64>(MlpDzArgs)", 20),
+           ("k_mlp_products<__bf16, 192, 192>(MlpGradArgs)", 0)]
+
+
+@pytest.mark.skipif(HIPCC is None, reason="hipcc not found")
+@pytest.mark.parametrize("kernel,stores", KERNELS)
+def test_every_barrier_behind_copies_has_a_wait_that_waits(kernel, stores, tmp_path):
+    src = tmp_path / "one.hip"
+    src.write_text(f'#include "mlp.hpp"\nnamespace nsk {{ template __global__ void {kernel}; }}\n')
+    got = subprocess.run([HIPCC, *nsbuild.HIP_FLAGS, "-I", nsbuild.CSRC, "-I", nsbuild.INCLUDE, "-S", "--cuda-device-only",
+                          str(src), "-o", "-"], capture_output=True, text=True, timeout=600)
+    assert got.returncode == 0, got.stderr[-2000:]
+    # None of the stores is merged with another or left out.
+    assert len(re.findall(r"^\s*global_store_dwordx[24]\b", got.stdout, re.M)) >= stores
+    steps = _steps(got.stdout)
+    assert sum(k == "barrier" for k, _ in steps) >= 7 and sum(k == "copy" for k, _ in steps) >= 36
+    waited, seen = True, 0
+    for kind, count in steps:
+        if kind == "copy":
+            waited = False
+        elif kind == "wait":
+            waited |= count is not None and count < 63
+        else:
+            assert waited, f"barrier {seen} follows copies without a wait"
+            seen += 1
