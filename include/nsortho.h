@@ -539,12 +539,13 @@ ns_status ns_linear_cross_entropy_backward(
  *     exp_avg, exp_avg_sq   m and v in fp32 (scales NULL), or e4m3 codes of
  *            one byte each (scales given): with k = i / 256 the block of
  *            element i and B = ceil(numel / 256),
- *               m_i = code * scales[k] / 448,
- *               sqrt(v_i) = code * scales[B + k] / 448,
+ *               m_i = code (scales[k] (1 / 448)),
+ *               sqrt(v_i) = code (scales[B + k] (1 / 448)),
  *            scales[k] and scales[B + k] the largest |m_i| and sqrt(v_i) of
- *            the block (2^-100 at least).  Zeros are a valid start.  The
- *            step uses the moments before they are rounded to codes; a
- *            positive root below the smallest code takes that code.
+ *            the block (2^-100 at least); a code is x ((1 / scale) 448)
+ *            rounded to nearest even, a positive root's at least the
+ *            smallest one.  Zeros are a valid start.  The step uses the
+ *            moments before they are rounded to codes.
  *     copy   NULL, or numel elements of copy_dtype that receive the new p
  *            too (a 16-bit copy of an fp32 master).
  *   step     t >= 1.  d_step: optional device int32 that holds t instead
@@ -553,7 +554,9 @@ ns_status ns_linear_cross_entropy_backward(
  *            gradients (a clipping coefficient, a loss scale's inverse) and
  *            one of all learning rates (a schedule).
  *   0 <= beta1, beta2 < 1; eps >= 0 and finite.
- * All arithmetic is fp32; p is rounded once to its type (an update below
+ * All arithmetic is fp32, that of the moments in the order written, each
+ * operation rounded (so codes do not depend on who computes them); p is
+ * rounded once to its type (an update below
  * half a step of a 16-bit p is lost: keep such parameters in fp32).  Tensors
  * must not overlap each other.  Non-finite new values of p, copy and fp32
  * moments are reported; with 8-bit moments a NaN stays in its element and an
@@ -656,7 +659,8 @@ ns_status ns_residual_norm_backward(
  *   activation   silu a / (1 + exp(-a)); gelu a (1 + erf(a / sqrt 2)) / 2;
  *            gelu_tanh a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2; relu.
  *   gate, up   rows x inner, row stride ldg, receive a and b for the
- *            backward pass; both NULL without one.
+ *            backward pass, in save_dtype: NS_FP32, or dtype, which takes
+ *            half the memory and rounds them; both NULL without one.
  *   rows <= 2^22, cols and inner <= 2^20, rows * inner <= 2^40, row strides
  *            <= 2^23.
  *   workspace   ns_gated_mlp_workspace_size(rows, cols, inner, dtype,
@@ -666,7 +670,7 @@ ns_status ns_residual_norm_backward(
  *            are then copied, as they are when cols or inner is not a
  *            multiple of 64, or 32 in fp32).
  * The products accumulate in fp32; h is formed in fp32 and rounded to dtype,
- * being an operand itself, and so are a and b where they are stored.
+ * being an operand itself.
  */
 typedef enum { NS_SILU = 0, NS_GELU = 1, NS_GELU_TANH = 2, NS_RELU = 3 } ns_activation;
 
@@ -679,15 +683,16 @@ ns_status ns_gated_mlp(const void* X, int64_t ldx, const void* Wg,
                        const void* Wd, int64_t ldwd, int64_t rows,
                        int64_t cols, int64_t inner, ns_dtype dtype,
                        ns_activation activation, void* Y, int64_t ldy,
-                       void* gate, void* up, int64_t ldg, int32_t* d_status,
-                       void* workspace, size_t workspace_bytes,
-                       ns_stream_t stream);
+                       void* gate, void* up, int64_t ldg, ns_dtype save_dtype,
+                       int32_t* d_status, void* workspace,
+                       size_t workspace_bytes, ns_stream_t stream);
 
 /*
  * Its gradients:
  *     dh = dY Wd,   da = dh b act'(a),   db = dh act(a)
  *     dX = da Wg + db Wu,  dWg = da^T X,  dWu = db^T X,  dWd = dY^T h
- *   gate, up   a and b as written by ns_gated_mlp; h is made of them again.
+ *   gate, up   a and b as written by ns_gated_mlp, in save_dtype; h is made
+ *            of them again.
  *   dX, dWg, dWu, dWd   any may be NULL.
  *   workspace   ns_gated_mlp_workspace_size(rows, cols, inner, dtype,
  *            aligned, 1) bytes; aligned is 1 when dY starts on a 16-byte
@@ -700,8 +705,8 @@ ns_status ns_gated_mlp(const void* X, int64_t ldx, const void* Wg,
 ns_status ns_gated_mlp_backward(
     const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* Wg,
     int64_t ldwg, const void* Wu, int64_t ldwu, const void* Wd, int64_t ldwd,
-    const void* gate, const void* up, int64_t ldg, int64_t rows, int64_t cols,
-    int64_t inner, ns_dtype dtype, ns_activation activation, void* dX,
+    const void* gate, const void* up, int64_t ldg, ns_dtype save_dtype,
+    int64_t rows, int64_t cols, int64_t inner, ns_dtype dtype, ns_activation activation, void* dX,
     int64_t lddx, void* dWg, int64_t lddwg, void* dWu, int64_t lddwu,
     void* dWd, int64_t lddwd, int32_t* d_status, void* workspace,
     size_t workspace_bytes, ns_stream_t stream);

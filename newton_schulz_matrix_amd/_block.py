@@ -373,7 +373,8 @@ def plan_gated_mlp(rows: int, cols: int, inner: int, dtype: torch.dtype = torch.
 
 
 def gated_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
-              activation: str = "silu", save: bool = True, out: Optional[torch.Tensor] = None,
+              activation: str = "silu", save: Union[bool, torch.dtype] = True,
+              out: Optional[torch.Tensor] = None,
               status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """A gated feed-forward block, (act(x w_gate^T) * (x w_up^T)) w_down^T: returns (y, gate, up).
 
@@ -381,7 +382,9 @@ def gated_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     ``w_gate`` and ``w_up``: [inner, cols], ``w_down``: [cols, inner], all of
     x's dtype.  ``activation``: "silu", "gelu", "gelu_tanh" or "relu".
     ``gate`` and ``up``, [..., inner], are the two projections that the
-    backward pass takes; with ``save=False`` they are None.
+    backward pass takes, in float32; ``save`` may name x's dtype instead,
+    which halves their memory and doubles the gradients' rounding error.
+    With ``save=False`` they are None.
     """
     device = _device(x)
     rows, cols, ldx = _rows(x, "x")
@@ -389,8 +392,11 @@ def gated_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     inner, ldg, ldu, ldd = _weights(x, cols, w_gate, w_up, w_down)
     y, ldy = _output_like(out, x, cols, device, "out")
     gate = up = None
+    stype = save if isinstance(save, torch.dtype) else torch.float32
+    if stype not in (torch.float32, x.dtype):
+        raise TypeError("save must be True, False, torch.float32 or x's dtype")
     if save:
-        gate = torch.empty(tuple(x.shape[:-1]) + (inner,), dtype=x.dtype, device=device)
+        gate = torch.empty(tuple(x.shape[:-1]) + (inner,), dtype=stype, device=device)
         up = torch.empty_like(gate)
     aligned = ldg == ldu and _aligned((x, ldx), (w_gate, ldg), (w_up, ldu), (w_down, ldd))
     wptr, wbytes, keep = _workspace_args(
@@ -398,7 +404,8 @@ def gated_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
         "ns_gated_mlp_workspace_size")
     _call("ns_gated_mlp", device,
           x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd, rows, cols, inner,
-          code, act, y.data_ptr(), ldy, _ptr(gate), _ptr(up), inner, _status_ptr(status, device), wptr, wbytes)
+          code, act, y.data_ptr(), ldy, _ptr(gate), _ptr(up), inner, dtype_code(stype), _status_ptr(status, device),
+          wptr, wbytes)
     return y, gate, up
 
 
@@ -422,8 +429,10 @@ def gated_mlp_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     lddy = _like(dy, x, device, "dy")
     shape = tuple(x.shape[:-1]) + (inner,)
     for name, t in (("gate", gate), ("up", up)):
-        if tuple(t.shape) != shape or t.dtype != x.dtype or t.device != device:
-            raise ValueError(f"{name} must have shape {shape}, {x.dtype} and device {device}")
+        if tuple(t.shape) != shape or t.dtype != gate.dtype or t.device != device:
+            raise ValueError(f"{name} must have shape {shape}, gate's dtype and device {device}")
+    if gate.dtype not in (torch.float32, x.dtype):
+        raise TypeError("gate and up must be float32 or have x's dtype")
     lds = _rows(gate, "gate")[2]
     if _rows(up, "up")[2] != lds:
         raise ValueError("gate and up must have the same row stride")
@@ -440,6 +449,6 @@ def gated_mlp_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
         workspace, "ns_gated_mlp_workspace_size")
     _call("ns_gated_mlp_backward", device,
           dy.data_ptr(), lddy, x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd,
-          gate.data_ptr(), up.data_ptr(), lds, rows, cols, inner, code, act, _ptr(dx), lddx, _ptr(dwg), lddg,
+          gate.data_ptr(), up.data_ptr(), lds, dtype_code(gate.dtype), rows, cols, inner, code, act, _ptr(dx), lddx, _ptr(dwg), lddg,
           _ptr(dwu), lddu, _ptr(dwd), lddd, _status_ptr(status, device), wptr, wbytes)
     return dx, dwg, dwu, dwd

@@ -12,7 +12,7 @@
 // chunks that the blocks take in turn.
 //
 // 8-bit moments: blocks of 256 elements, each with the largest magnitude `top`
-// of its block in fp32 and e4m3 codes for x * (448 / top).  The second moment
+// of its block in fp32 and e4m3 codes for x * (1 / top * 448).  The second moment
 // is held by its root: v = g^2 spans twice the exponents of m, its root the
 // same, and an error of the root is what the update sees.  A positive root
 // below the smallest code (2^-9 of 448, 2^-17.8 of the block's largest) takes
@@ -195,6 +195,15 @@ __device__ __forceinline__ float half_wave_max(float v) {
   return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
 
+// The moments' update, each operation rounded on its own (no fused
+// multiply-adds): a code is then what its formula in fp32 gives, whoever
+// computes it.
+__device__ __forceinline__ void next_moments(float b1, float a1, float b2, float a2, float g, float& m, float& v) {
+#pragma clang fp contract(off)
+  m = b1 * m + a1 * g;
+  v = b2 * v + a2 * g * g;
+}
+
 static __global__ void __launch_bounds__(kAdamwThreads) k_adamw(AdamwArgs a) {
   float c1 = a.c1, c2 = a.c2;
   if (a.d_step) {
@@ -248,8 +257,7 @@ static __global__ void __launch_bounds__(kAdamwThreads) k_adamw(AdamwArgs a) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       g[k] *= gs;
-      m[k] = a.b1 * m[k] + a.a1 * g[k];
-      v[k] = a.b2 * v[k] + a.a2 * g[k] * g[k];
+      next_moments(a.b1, a.a1, a.b2, a.a2, g[k], m[k], v[k]);
       root[k] = sqrtf(v[k]);
       p[k] = p[k] - keep * p[k] - lr * (c1 * m[k] / (root[k] * c2 + a.eps));
     }
@@ -265,8 +273,8 @@ static __global__ void __launch_bounds__(kAdamwThreads) k_adamw(AdamwArgs a) {
       }
       tm = fmaxf(half_wave_max(tm), kScaleLeast);
       tv = fmaxf(half_wave_max(tv), kScaleLeast);
-      cm = encode<false>(m, kCodeTop / tm);
-      cv = encode<true>(root, kCodeTop / tv);
+      cm = encode<false>(m, 1.f / tm * kCodeTop);
+      cv = encode<true>(root, 1.f / tv * kCodeTop);
       if (left > 0) {
         store_codes(reinterpret_cast<uint8_t*>(it.m) + e, left, cm);
         store_codes(reinterpret_cast<uint8_t*>(it.v) + e, left, cv);

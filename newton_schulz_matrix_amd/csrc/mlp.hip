@@ -225,12 +225,12 @@ struct MlpIn {
 
 template <typename T>
 ns_status mlp_forward(const MlpPlan& p, const MlpIn& in, int act, void* Y, int64_t ldy, void* gate, void* up, int64_t lds,
-                      int32_t* d_status, hipStream_t st) {
+                      bool save32, int32_t* d_status, hipStream_t st) {
   const int32_t bits = (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT);
   constexpr int64_t es = sizeof(T);
   if (p.dot) {
     const MlpDotUpArgs a{in.X, in.G, in.U, in.ldx, in.ldg, in.ldu, p.n,      p.f, (int)p.d, p.h,
-                         p.h_ld, gate, up,   lds,    act,    d_status, bits};
+                         p.h_ld, gate, up, lds,    save32, act,    d_status, bits};
     if (launch_mlp_dot_up<T>(a, st) != hipSuccess) return NS_ERR_HIP;
     const MlpDotDownArgs b{p.h, in.D, p.h_ld, in.ldd, p.n, p.d, (int)p.f, Y, ldy, d_status, bits};
     return launch_mlp_dot_down<T>(b, st) == hipSuccess ? NS_OK : NS_ERR_HIP;
@@ -258,6 +258,7 @@ ns_status mlp_forward(const MlpPlan& p, const MlpIn& in, int act, void* Y, int64
   a.gate = gate;
   a.up = up;
   a.lds = lds;
+  a.save32 = save32;
   a.act = act;
   a.d_status = d_status;
   a.status_bits = bits;
@@ -283,7 +284,7 @@ struct MlpOut {
 
 template <typename T>
 ns_status mlp_backward(const MlpPlan& p, const MlpIn& in, const void* dY, int64_t lddy, const void* gate, const void* up,
-                       int64_t lds, int act, const MlpOut& out, int32_t* d_status, hipStream_t st) {
+                       int64_t lds, bool save32, int act, const MlpOut& out, int32_t* d_status, hipStream_t st) {
   const int32_t bits = (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT);
   constexpr int64_t es = sizeof(T);
   const bool dw = out.dG || out.dU || out.dD;
@@ -311,6 +312,7 @@ ns_status mlp_backward(const MlpPlan& p, const MlpIn& in, const void* dY, int64_
   a.gate = gate;
   a.up = up;
   a.lds = lds;
+  a.save32 = save32;
   a.dz = p.dz;
   a.dzt = p.dzt;
   a.ht = p.ht;
@@ -371,13 +373,13 @@ int64_t ns_plan_gated_mlp(int64_t rows, int64_t cols, int64_t inner, ns_dtype dt
 ns_status ns_gated_mlp(const void* X, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu, int64_t ldwu,
                        const void* Wd, int64_t ldwd, int64_t rows, int64_t cols, int64_t inner, ns_dtype dtype,
                        ns_activation activation, void* Y, int64_t ldy, void* gate, void* up, int64_t ldg,
-                       int32_t* d_status, void* workspace, size_t workspace_bytes, ns_stream_t stream) {
+                       ns_dtype save_dtype, int32_t* d_status, void* workspace, size_t workspace_bytes, ns_stream_t stream) {
   if (!mlp_shape_ok(rows, cols, inner)) return NS_ERR_INVALID_ARG;
   if (!stride_ok(ldx, cols) || !stride_ok(ldwg, cols) || !stride_ok(ldwu, cols) || !stride_ok(ldwd, inner) ||
       !stride_ok(ldy, cols) || ((gate || up) && !stride_ok(ldg, inner)))
     return NS_ERR_INVALID_ARG;
   if (activation < NS_SILU || activation > NS_RELU) return NS_ERR_INVALID_ARG;
-  if (!known(dtype)) return NS_ERR_UNSUPPORTED_DTYPE;
+  if (!known(dtype) || !(save_dtype == dtype || save_dtype == NS_FP32)) return NS_ERR_UNSUPPORTED_DTYPE;
   if (rows == 0) return NS_OK;
   if (!X || !Wg || !Wu || !Wd || !Y || !gate != !up) return NS_ERR_INVALID_ARG;
   const bool aligned = operand_aligned(X, ldx, dtype) && operand_aligned(Wg, ldwg, dtype) &&
@@ -386,14 +388,14 @@ ns_status ns_gated_mlp(const void* X, int64_t ldx, const void* Wg, int64_t ldwg,
   if (!workspace_ok(workspace, workspace_bytes, p.total)) return NS_ERR_WORKSPACE;
   const MlpIn in{X, Wg, Wu, Wd, ldx, ldwg, ldwu, ldwd};
   return with_type(dtype, [&](auto io) {
-    return mlp_forward<decltype(io)>(p, in, (int)activation, Y, ldy, gate, up, ldg, d_status,
-                                     reinterpret_cast<hipStream_t>(stream));
+    return mlp_forward<decltype(io)>(p, in, (int)activation, Y, ldy, gate, up, ldg,
+                                     save_dtype == NS_FP32, d_status, reinterpret_cast<hipStream_t>(stream));
   });
 }
 
 ns_status ns_gated_mlp_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* Wg, int64_t ldwg,
                                 const void* Wu, int64_t ldwu, const void* Wd, int64_t ldwd, const void* gate,
-                                const void* up, int64_t ldg, int64_t rows, int64_t cols, int64_t inner, ns_dtype dtype,
+                                const void* up, int64_t ldg, ns_dtype save_dtype, int64_t rows, int64_t cols, int64_t inner, ns_dtype dtype,
                                 ns_activation activation, void* dX, int64_t lddx, void* dWg, int64_t lddwg, void* dWu,
                                 int64_t lddwu, void* dWd, int64_t lddwd, int32_t* d_status, void* workspace,
                                 size_t workspace_bytes, ns_stream_t stream) {
@@ -403,7 +405,7 @@ ns_status ns_gated_mlp_backward(const void* dY, int64_t lddy, const void* X, int
       (dWg && !stride_ok(lddwg, cols)) || (dWu && !stride_ok(lddwu, cols)) || (dWd && !stride_ok(lddwd, inner)))
     return NS_ERR_INVALID_ARG;
   if (activation < NS_SILU || activation > NS_RELU) return NS_ERR_INVALID_ARG;
-  if (!known(dtype)) return NS_ERR_UNSUPPORTED_DTYPE;
+  if (!known(dtype) || !(save_dtype == dtype || save_dtype == NS_FP32)) return NS_ERR_UNSUPPORTED_DTYPE;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (rows == 0) {
     return with_type(dtype, [&](auto io) {
@@ -426,7 +428,8 @@ ns_status ns_gated_mlp_backward(const void* dY, int64_t lddy, const void* X, int
   const MlpIn in{X, Wg, Wu, Wd, ldx, ldwg, ldwu, ldwd};
   const MlpOut out{dX, dWg, dWu, dWd, lddx, lddwg, lddwu, lddwd};
   return with_type(dtype, [&](auto io) {
-    return mlp_backward<decltype(io)>(p, in, dY, lddy, gate, up, ldg, (int)activation, out, d_status, st);
+    return mlp_backward<decltype(io)>(p, in, dY, lddy, gate, up, ldg, save_dtype == NS_FP32, (int)activation, out,
+                                      d_status, st);
   });
 }
 

@@ -204,15 +204,15 @@ def test_oracle_gated_mlp_gradients_against_differences(act):
 
 
 def _mlp(X=PTR, ldx=64, G=PTR, ldg=64, U=PTR, ldu=64, D=PTR, ldd=128, rows=40, cols=64, inner=128, dtype=B.NS_BF16, act=0,
-         Y=PTR, ldy=64, gate=PTR, up=PTR, lds=128, ws=256, nb=1 << 40):
-    return B.lib().ns_gated_mlp(X, ldx, G, ldg, U, ldu, D, ldd, rows, cols, inner, dtype, act, Y, ldy, gate, up, lds, None,
-                                ws, nb, None)
+         Y=PTR, ldy=64, gate=PTR, up=PTR, lds=128, save=B.NS_FP32, ws=256, nb=1 << 40):
+    return B.lib().ns_gated_mlp(X, ldx, G, ldg, U, ldu, D, ldd, rows, cols, inner, dtype, act, Y, ldy, gate, up, lds, save,
+                                None, ws, nb, None)
 
 
 def _mlp_back(dY=PTR, lddy=64, X=PTR, ldx=64, G=PTR, ldg=64, U=PTR, ldu=64, D=PTR, ldd=128, gate=PTR, up=PTR, lds=128,
               rows=40, cols=64, inner=128, dtype=B.NS_BF16, act=0, dX=PTR, lddx=64, dG=PTR, lddg=64, dU=PTR, lddu=64,
-              dD=PTR, lddd=128, ws=256, nb=1 << 40):
-    return B.lib().ns_gated_mlp_backward(dY, lddy, X, ldx, G, ldg, U, ldu, D, ldd, gate, up, lds, rows, cols, inner, dtype,
+              dD=PTR, lddd=128, save=B.NS_FP32, ws=256, nb=1 << 40):
+    return B.lib().ns_gated_mlp_backward(dY, lddy, X, ldx, G, ldg, U, ldu, D, ldd, gate, up, lds, save, rows, cols, inner, dtype,
                                          act, dX, lddx, dG, lddg, dU, lddu, dD, lddd, None, ws, nb, None)
 
 
@@ -229,7 +229,7 @@ def test_gated_mlp_refusals():
         for kw in (dict(rows=-1), dict(rows=(1 << 22) + 1), dict(cols=0), dict(inner=0), dict(cols=(1 << 20) + 1),
                    dict(inner=(1 << 20) + 1), dict(act=4), dict(act=-1), dict(rows=1 << 22, inner=1 << 19)):
             assert call(**kw) == INV, kw
-        assert call(dtype=3) == DT
+        assert call(dtype=3) == DT and call(save=B.NS_FP16) == DT
         assert call(ws=None) == WSP and call(ws=100) == WSP and call(nb=16) == WSP
     assert _mlp(rows=0, X=None, Y=None, ws=None, nb=0) == 0
     assert _mlp_back(rows=0, dG=None, dU=None, dD=None, ws=None, nb=0) == 0

@@ -57,8 +57,9 @@ def _inputs(n, d, f, dtype, dev, seed=0):
                 wd=make(d, f, scale=f ** -0.5), dy=make(n, d))
 
 
-def _forward_bounds(x, wg, wu, wd, a, b, act, dtype, y):
+def _forward_bounds(x, wg, wu, wd, a, b, act, dtype, y, save):
     u, tiny, d, f = HALF_STEP[dtype], TINY[dtype], x.shape[1], wg.shape[0]
+    us, ts = HALF_STEP[save], TINY[save]
     ax = np.abs(x)
     ea, eb = (d + 1) * U32 * (ax @ np.abs(wg).T), (d + 1) * U32 * (ax @ np.abs(wu).T)
     value = np.abs(oracle.activation(a, act)[0])
@@ -67,7 +68,7 @@ def _forward_bounds(x, wg, wu, wd, a, b, act, dtype, y):
     h = value * np.abs(b)
     operand = eh + u * (h + eh) + tiny
     ey = operand @ np.abs(wd).T + (f + 1) * U32 * ((h + operand) @ np.abs(wd).T)
-    return u * np.abs(a) + (1 + u) * ea + tiny, u * np.abs(b) + (1 + u) * eb + tiny, u * np.abs(y) + (1 + u) * ey + tiny
+    return us * np.abs(a) + (1 + us) * ea + ts, us * np.abs(b) + (1 + us) * eb + ts, u * np.abs(y) + (1 + u) * ey + tiny
 
 
 def _backward_bounds(o, dy, x, wg, wu, wd, a, b, act, dtype):
@@ -94,9 +95,9 @@ def _backward_bounds(o, dy, x, wg, wu, wd, a, b, act, dtype):
             "dwd": final(o["dwd"], np.abs(dy).T @ eh + (n + 1) * U32 * (np.abs(dy).T @ h))}
 
 
-def _check(n, d, f, dtype, act="silu", strided=0, seed=0, fused=False):
+def _check(n, d, f, dtype, act="silu", strided=0, seed=0, fused=False, save="fp32"):
     dev = _dev()
-    print(f"gated mlp {n}x{d}x{f} {dtype} {act} strided {strided}", flush=True)
+    print(f"gated mlp {n}x{d}x{f} {dtype} {act} strided {strided} save {save}", flush=True)
     t = _inputs(n, d, f, dtype, dev, seed)
     if strided:
         for name, v in t.items():
@@ -109,9 +110,11 @@ def _check(n, d, f, dtype, act="silu", strided=0, seed=0, fused=False):
     m = {k: _np(v) for k, v in t.items()}
     st = torch.zeros(1, dtype=torch.int32, device=dev)
     w = (t["wg"], t["wu"], t["wd"])
-    y, gate, up = nsa.gated_mlp(t["x"], *w, activation=act, status=st, out=_poisoned((n, d), DTYPES[dtype], dev))
+    y, gate, up = nsa.gated_mlp(t["x"], *w, activation=act, status=st, out=_poisoned((n, d), DTYPES[dtype], dev),
+                                save=True if save == "fp32" else DTYPES[save])
+    assert gate.dtype == up.dtype == DTYPES[save]
     y64, a64, b64, _ = oracle.gated_mlp(m["x"], m["wg"], m["wu"], m["wd"], act)
-    ba, bb, by = _forward_bounds(m["x"], m["wg"], m["wu"], m["wd"], a64, b64, act, dtype, y64)
+    ba, bb, by = _forward_bounds(m["x"], m["wg"], m["wu"], m["wd"], a64, b64, act, dtype, y64, save)
     _close(gate, a64, ba, "gate")
     _close(up, b64, bb, "up")
     _close(y, y64, by, "y")
@@ -138,6 +141,12 @@ def _check(n, d, f, dtype, act="silu", strided=0, seed=0, fused=False):
 @pytest.mark.parametrize("n,d,f,dtype", MLP_RUNS)
 def test_matches_the_oracle(n, d, f, dtype):
     _check(n, d, f, dtype, seed=n + d + f)
+
+
+@pytest.mark.parametrize("n,d,f", [(1, 72, 40), (4, 77, 203), (130, 128, 256), (150, 100, 333), (1003, 520, 1407)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_projections_saved_in_the_datas_type(n, d, f, dtype):
+    _check(n, d, f, dtype, seed=11, save=dtype)
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -249,12 +258,13 @@ def test_a_gate_that_overflows_is_reported():
         wg[:, 0], wu[:, 1] = 2.0 ** 8, 2.0 ** -10
         wd = torch.full((64, 64), 2.0 ** -6, dtype=torch.float16, device=dev)
         st.zero_()
-        y, gate, up = nsa.gated_mlp(x, wg, wu, wd, status=st)
+        y, gate, up = nsa.gated_mlp(x, wg, wu, wd, status=st, save=torch.float16)
         assert torch.isfinite(y).all() and torch.isinf(gate).all()
         assert int(st.item()) == B.NS_ERR_NONFINITE | B.STATUS_AT_OUTPUT
         st.zero_()
-        nsa.gated_mlp(x, wg, wu, wd, status=st, save=False)
-        assert int(st.item()) == 0
+        for save in (False, True):
+            nsa.gated_mlp(x, wg, wu, wd, status=st, save=save)
+            assert int(st.item()) == 0
 
 
 def test_equal_calls_give_equal_bits():
@@ -325,11 +335,16 @@ def test_python_refusals():
                      ((x, wg, wu, wd), dict(workspace=torch.zeros(4096)))):
         with pytest.raises(ValueError):
             nsa.gated_mlp(*args, **kw)
+    for bad in (torch.float16, torch.float64):
+        with pytest.raises(TypeError):
+            nsa.gated_mlp(x, wg, wu, wd, save=bad)
+    with pytest.raises(TypeError):
+        nsa.gated_mlp_backward(dy, x, wg, wu, wd, gate.half(), up.half())
     with pytest.raises(TypeError):
         nsa.gated_mlp(*(v.double() for v in (x, wg, wu, wd)))
     for args, kw in (((dy[:5], x, wg, wu, wd, gate, up), {}), ((dy.float(), x, wg, wu, wd, gate, up), {}),
-                     ((dy, x, wg, wu, wd, gate[:5], up), {}), ((dy, x, wg, wu, wd, gate, up.float()), {}),
-                     ((dy, x, wg, wu, wd, gate, torch.zeros(6, 20, dtype=torch.bfloat16, device=dev)[:, :16]), {}),
+                     ((dy, x, wg, wu, wd, gate[:5], up), {}), ((dy, x, wg, wu, wd, gate, up.half()), {}),
+                     ((dy, x, wg, wu, wd, gate, torch.zeros(6, 20, device=dev)[:, :16]), {}),
                      ((dy, x, wg, wu, wd, gate, up), dict(out_dw_down=torch.zeros(8, 15, dtype=torch.bfloat16, device=dev)))):
         with pytest.raises(ValueError):
             nsa.gated_mlp_backward(*args, **kw)
