@@ -15,59 +15,71 @@ constexpr int64_t kMaxResNormCols = 1 << 24;
 constexpr int kResNormRegisterCols = 8192;  // the widest row that the kernels hold in registers
 constexpr int64_t kResNormFwdThreads = 256 * 2048;
 // Blocks of the backward pass, each of which leaves partial rows of dw, dwb
-// and the gate's gradient.
+// and the gate's gradient: two per compute unit (16384 x 768: one 56 us, two
+// 43, four 52, for the partial rows), or the one that fits.
 constexpr int64_t kResNormParts = 512;
 
-// Calls f.template run<NV, TPR, FORM>() for a row width: at most two vectors
-// of 16-bit data per thread, or a few narrow ones three, which leave
-// registers for the backward's three column sums.
-template <typename IO, int FORM, class F>
-void resnorm_form(int64_t cols, F&& f) {
+// Calls f.template run<NV, TPR>() for a row width: rows of up to 128 vectors
+// share a block, whose waves hold one or two each; wider ones have a block of
+// their own with one vector per thread, or two where that was faster: fp32
+// data, whose vectors are half as many values, and 16-bit data with 16-bit
+// parameters (8192 x 4096 99 us against 104; with fp32 parameters, whose reads
+// from LDS wait longer, 133 against 105).
+template <typename IO, typename PT, class F>
+auto resnorm_form(int64_t cols, F&& f) {
   const int64_t n = (cols + kVec<IO> - 1) / kVec<IO>;
-  if (n <= 32) return f.template run<1, 32, FORM>();
-  if (n <= 64) return f.template run<2, 32, FORM>();
-  if (n <= 96) return f.template run<3, 32, FORM>();
-  if (n <= 128) return f.template run<2, 64, FORM>();
-  if (n <= 192) return f.template run<3, 64, FORM>();
-  if constexpr (sizeof(IO) == 2) {
-    if (n <= 256) return f.template run<2, 128, FORM>();
-    if (n <= 512) return f.template run<2, 256, FORM>();
-    return f.template run<2, 512, FORM>();
+  if (n <= 32) return f.template run<1, 32>();
+  if (n <= 64) return f.template run<2, 32>();
+  if (n <= 96) return f.template run<3, 32>();
+  if (n <= 128) return f.template run<2, 64>();
+  if (n <= 256) return f.template run<1, 256>();
+  if constexpr (sizeof(IO) == 4) {
+    if (n <= 512) return f.template run<2, 256>();
+    if (n <= 1024) return f.template run<2, 512>();
+    return f.template run<2, 1024>();
   } else {
-    if (n <= 256) return f.template run<4, 64, FORM>();
-    if (n <= 512) return f.template run<2, 256, FORM>();
-    if (n <= 1024) return f.template run<4, 256, FORM>();
-    return f.template run<4, 512, FORM>();
+    if constexpr (sizeof(PT) == 2) {
+      if (n <= 512) return f.template run<2, 256>();
+    } else {
+      if (n <= 512) return f.template run<1, 512>();
+    }
+    return f.template run<1, 1024>();
   }
-}
-template <typename IO, class F>
-void with_resnorm_form(int64_t cols, F&& f) {
-  if (cols % kVec<IO> == 0)
-    resnorm_form<IO, kEven>(cols, f);
-  else
-    resnorm_form<IO, kRagged>(cols, f);
 }
 template <typename IO>
 bool resnorm_by_element(int64_t cols) {
   return cols < kVec<IO> || cols > kResNormRegisterCols;
 }
-template <typename IO>
-int resnorm_rows_per_block(int64_t cols) {
-  if (resnorm_by_element<IO>(cols)) return 1;
-  const int64_t n = (cols + kVec<IO> - 1) / kVec<IO>;
-  return n <= 96 ? kNormRows<32> : n <= (sizeof(IO) == 2 ? 192 : 256) ? kNormRows<64> : 1;
+
+// Rows that a block works on at a time, and the blocks of the backward pass.
+struct ResNormBlocks {
+  int rows;
+  int64_t parts;
+};
+struct ResNormBlocksOf {
+  template <int NV, int TPR>
+  ResNormBlocks run() const {
+    return {kNormRows<TPR>, TPR == 1024 ? kResNormParts / 2 : kResNormParts};
+  }
+};
+template <typename IO, typename PT>
+ResNormBlocks resnorm_blocks(int64_t cols) {
+  if (resnorm_by_element<IO>(cols)) return {1, kResNormParts};
+  return resnorm_form<IO, PT>(cols, ResNormBlocksOf{});
 }
 
 template <typename IO, typename PT>
 struct ResNormFwdRun {
   const ResNormFwdArgs& a;
   hipStream_t st;
-  template <int NV, int TPR, int FORM>
+  template <int NV, int TPR>
   void run() const {
     const int64_t groups = (a.rows + kNormRows<TPR> - 1) / kNormRows<TPR>;
-    const int64_t blocks = std::min<int64_t>(groups, kResNormFwdThreads / kNormThreads<TPR>);
-    hipLaunchKernelGGL((k_resnorm_fwd<IO, PT, NV, TPR, FORM>), dim3((unsigned)blocks), dim3(kNormThreads<TPR>), 0, st,
-                       a);
+    const dim3 blocks((unsigned)std::min<int64_t>(groups, kResNormFwdThreads / kNormThreads<TPR>)), threads(kNormThreads<TPR>);
+    if (a.cols % kVec<IO> == 0)
+      hipLaunchKernelGGL((k_resnorm_fwd<IO, PT, NV, TPR, kEven>), blocks, threads, 0, st, a);
+    else
+      hipLaunchKernelGGL((k_resnorm_fwd<IO, PT, NV, TPR, kRagged>), blocks, threads, 0, st, a);
   }
 };
 
@@ -76,17 +88,20 @@ struct ResNormBwdRun {
   const ResNormBwdArgs& a;
   int64_t blocks;
   hipStream_t st;
-  template <int NV, int TPR, int FORM>
+  template <int NV, int TPR>
   void run() const {
-    hipLaunchKernelGGL((k_resnorm_bwd<IO, PT, NV, TPR, FORM>), dim3((unsigned)blocks), dim3(kNormThreads<TPR>), 0, st,
-                       a);
+    const dim3 grid((unsigned)blocks), threads(kNormThreads<TPR>);
+    if (a.cols % kVec<IO> == 0)
+      hipLaunchKernelGGL((k_resnorm_bwd<IO, PT, NV, TPR, kEven>), grid, threads, 0, st, a);
+    else
+      hipLaunchKernelGGL((k_resnorm_bwd<IO, PT, NV, TPR, kRagged>), grid, threads, 0, st, a);
   }
 };
 
 bool resnorm_shape_ok(int64_t rows, int64_t cols, int64_t groups) {
   if (!(rows >= 0 && rows < (int64_t(1) << 31) && cols >= 1 && cols <= kMaxResNormCols)) return false;
-  // Without rows the gate's gradient is zeros, by a block for each 64 columns.
-  if (rows == 0) return groups >= 0 && groups < (int64_t(1) << 30) / ((cols + 63) / 64) - 2;
+  // Without rows the gate's gradient is zeros, by a block for each 32 columns.
+  if (rows == 0) return groups >= 0 && groups < (int64_t(1) << 30) / ((cols + 31) / 32) - 2;
   return groups == 0 || (groups > 0 && groups <= rows && rows % groups == 0);
 }
 
@@ -96,13 +111,13 @@ struct ResNormCut {
   int64_t groups, group_rows, blocks;
   int split;
 };
-ResNormCut resnorm_cut(int64_t rows, int64_t groups, int per_block) {
+ResNormCut resnorm_cut(int64_t rows, int64_t groups, const ResNormBlocks& b) {
   ResNormCut c;
   c.groups = groups;
   c.group_rows = rows / groups;
-  const int64_t most = (c.group_rows + per_block - 1) / per_block;  // no segment without rows
-  c.split = (int)std::max<int64_t>(1, std::min(kResNormParts / groups, most));
-  c.blocks = std::min(groups * c.split, kResNormParts);
+  const int64_t most = (c.group_rows + b.rows - 1) / b.rows;  // no segment without rows
+  c.split = (int)std::max<int64_t>(1, std::min(b.parts / groups, most));
+  c.blocks = std::min(groups * c.split, b.parts);
   return c;
 }
 
@@ -153,14 +168,14 @@ ns_status ns_residual_norm(const void* X, int64_t ldx, const void* Z, int64_t ld
     if (resnorm_by_element<IO>(cols))
       hipLaunchKernelGGL((k_resnorm_fwd_long<IO, PT>), dim3((unsigned)std::min(rows, kMaxBlocks)), dim3(1024), 0, st, a);
     else
-      with_resnorm_form<IO>(cols, ResNormFwdRun<IO, PT>{a, st});
+      resnorm_form<IO, PT>(cols, ResNormFwdRun<IO, PT>{a, st});
     return launched();
   });
 }
 
 size_t ns_residual_norm_workspace_size(int64_t rows, int64_t cols) {
   if (!resnorm_shape_ok(rows, cols, 0)) return 0;
-  const size_t parts = align_up_to((size_t)std::min(rows, kResNormParts) * 3 * cols * sizeof(float));
+  const size_t parts = align_up_to((size_t)std::min(rows, kResNormParts) * 3 * partial_stride(cols) * sizeof(float));
   return std::max(kAlignTo, parts + align_up_to((size_t)rows * sizeof(float)));
 }
 
@@ -217,15 +232,16 @@ ns_status ns_residual_norm_backward(const void* dS, int64_t ldds, const void* dY
   const bool own_rows = dgate && rows > 0 && groups == rows && rows > 1;
   a.dgate_rows = own_rows ? dgate : nullptr;
   a.want_gate = dgate && !own_rows;
+  a.e_gated = gate && groups > 1 && !a.want_gate;
   Carver carve{reinterpret_cast<char*>(workspace)};
-  a.partial = carve.take<float>(std::min(rows, kResNormParts) * 3 * cols);
+  a.partial = carve.take<float>(std::min(rows, kResNormParts) * 3 * partial_stride(cols));
   a.c_row = carve.take<float>(rows);
   return with_types(dtype, param_dtype, [&](auto io, auto pt) {
     using IO = decltype(io);
     using PT = decltype(pt);
     ResNormCut cut{1, 0, 0, 1};
     if (rows > 0) {
-      cut = resnorm_cut(rows, a.want_gate ? groups : 1, resnorm_rows_per_block<IO>(cols));
+      cut = resnorm_cut(rows, a.want_gate ? groups : 1, resnorm_blocks<IO, PT>(cols));
       a.groups = cut.groups;
       a.group_rows = cut.group_rows;
       a.split = cut.split;
@@ -238,7 +254,7 @@ ns_status ns_residual_norm_backward(const void* dS, int64_t ldds, const void* dY
                              dim3(256), 0, st, a);
         if (dX || dZ) hipLaunchKernelGGL((k_resnorm_bwd_long<IO, PT>), grid, dim3(1024), 0, st, a);
       } else {
-        with_resnorm_form<IO>(cols, ResNormBwdRun<IO, PT>{a, cut.blocks, st});
+        resnorm_form<IO, PT>(cols, ResNormBwdRun<IO, PT>{a, cut.blocks, st});
       }
     }
     // Without rows the gradients are zeros; a gate then has no rows either
@@ -248,7 +264,7 @@ ns_status ns_residual_norm_backward(const void* dS, int64_t ldds, const void* dY
       const ResNormJoinArgs j{a.partial, (int)cut.blocks, rows > 0 ? cut.split : 0, (int)cols, dweight, dbranch_weight,
                               join_gate ? dgate : nullptr, d_status, a.status_bits};
       const int64_t outputs = 2 + (join_gate ? groups : 0);
-      hipLaunchKernelGGL((k_resnorm_join<PT>), dim3((unsigned)((cols + 63) / 64 * outputs)), dim3(1024), 0, st, j);
+      hipLaunchKernelGGL((k_resnorm_join<PT>), dim3((unsigned)((cols + 31) / 32 * outputs)), dim3(1024), 0, st, j);
     }
     return launched();
   });

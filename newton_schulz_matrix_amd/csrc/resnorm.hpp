@@ -22,7 +22,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "norm.hpp"
+#include "xent.hpp"
 
 namespace nsk {
 
@@ -40,60 +40,146 @@ struct ResNormFwdArgs {
   int32_t status_bits;
 };
 
-// V parameters (1 where there are none) as floats.
-template <int FORM, typename PT, int V>
-__device__ __forceinline__ void param_values(const PT* p, int c, int cols, float (&f)[V]) {
-  if (p) {
-    Params<FORM, PT, V> q;
-    q.issue(p, c, cols);
-    q.settle(p, c, cols);
+// Gate and weights wait in LDS: read from the cache where a row needs them,
+// behind the sums that come before, their latency was a third of a row's time
+// (16384 x 768 27 us forward, 19.5 without parameters).  ones where there are
+// none, so that the rows' loop has no branch for them.
+//
+// A thread's V parameters of vector i are V / PV chunks of 16 bytes, chunk j
+// of all threads side by side: with a thread's own chunks side by side (fp32
+// parameters of 16-bit data) neighbours would meet in the banks.
+template <typename PT, int NV, int TPR, int V>
+struct alignas(16) ParamRow {
+  static constexpr int PV = kVec<PT>, C = V / PV;
+  u32x4_t v[NV * C * TPR];
+  // Threads `first`, + `count`, ... of the block fill it.
+  __device__ __forceinline__ void fill(const PT* src, int cols, int first, int count) {
+    for (int q = first; q < NV * C * TPR; q += count) {
+      const int t = q % TPR, j = q / TPR % C, i = q / (TPR * C);
+      const int c = (i * TPR + t) * V + j * PV;
+      u32x4_t x;
+      PT* e = reinterpret_cast<PT*>(&x);
+      if (src && c + PV <= cols) {
+        x = *reinterpret_cast<const typename Vec16<sizeof(PT)>::type*>(src + c);
+      } else {
 #pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = q.get(k);
-  } else {
+        for (int k = 0; k < PV; ++k) e[k] = src ? (c + k < cols ? src[c + k] : from_f32<PT>(0.f)) : from_f32<PT>(1.f);
+      }
+      v[q] = x;
+    }
+  }
+  // The parameters of thread t's vector i.
+  __device__ __forceinline__ void get(int i, int t, float (&f)[V]) const {
 #pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = 1.f;
+    for (int j = 0; j < C; ++j) {
+      const u32x4_t q = v[(i * C + j) * TPR + t];
+#pragma unroll
+      for (int k = 0; k < PV; ++k) f[j * PV + k] = to_f32<PT>(reinterpret_cast<const PT*>(&q)[k]);
+    }
+  }
+};
+
+// Rounds and stores a vector like store16v; adds nonfinite_bits of it to
+// `found` (a float test per value costs four times that).
+template <int FORM, typename IO>
+__device__ __forceinline__ void put16v(IO* row, int c, int cols, const float (&f)[kVec<IO>], uint32_t& found) {
+  constexpr int V = kVec<IO>;
+  u32x4_t q;
+  IO* e = reinterpret_cast<IO*>(&q);
+#pragma unroll
+  for (int k = 0; k < V; ++k) e[k] = from_f32<IO>(f[k]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) found |= nonfinite_bits<IO>(q[k]);
+  if (c + V <= cols) {
+    *reinterpret_cast<typename Vec16<sizeof(IO)>::type*>(row + c) = q;
+  } else if constexpr (FORM != kEven) {
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (c + k < cols) row[c + k] = e[k];
   }
 }
 
+// A row's sum as norm.hpp's row_sum, with one barrier where a row is more than
+// a wave: successive sums of a block alternate between two buffers.
+template <int TPR>
+struct RowSums {
+  static constexpr int kWaves = kNormThreads<TPR> / 64;
+  float (*sh)[kWaves];  // [2]
+  int turn = 0;
+  __device__ __forceinline__ float operator()(float v) {
+    v = wave_row_sum<TPR>(v);
+    if constexpr (TPR > 64) {
+      float* b = sh[turn];
+      turn ^= 1;
+      if ((threadIdx.x & 63) == 0) b[threadIdx.x >> 6] = v;
+      __syncthreads();
+      v = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) v += b[i];
+    }
+    return v;
+  }
+};
+
 template <typename IO, typename PT, int NV, int TPR, int FORM>
 __global__ void __launch_bounds__(kNormThreads<TPR>) k_resnorm_fwd(ResNormFwdArgs p) {
-  constexpr int V = kVec<IO>;
-  __shared__ float sh[kNormThreads<TPR> / 64];
+  constexpr int V = kVec<IO>, R = kNormRows<TPR>, T = kNormThreads<TPR>;
+  __shared__ float sums[2][T / 64];
+  __shared__ ParamRow<PT, NV, TPR, V> w_row, wb_row, gate_row;
   const int t = threadIdx.x % TPR;
   const float inv_n = 1.f / (float)p.cols;
-  auto in = [&](int c, int k) { return (FORM == kEven ? c : c + k) < p.cols; };  // column c + k is in the row
-  const PT *W = reinterpret_cast<const PT*>(p.w), *WB = reinterpret_cast<const PT*>(p.wb);
-  const int64_t stride = (int64_t)gridDim.x * kNormRows<TPR>;
+  auto col = [&](int i) { return (i * TPR + t) * V; };
+  const int64_t stride = (int64_t)gridDim.x * R;
+  RowSums<TPR> row_total{sums};
+  const bool shared_gate = !p.gate || (int64_t)p.gate_rows == p.rows;
+  u32x4_t rx[NV], rz[NV];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      rx[i] = issue16<FORM, IO>(reinterpret_cast<const IO*>(p.X) + row * p.ldx, col(i), p.cols);
+      if (p.Z) rz[i] = issue16<FORM, IO>(reinterpret_cast<const IO*>(p.Z) + row * p.ldz, col(i), p.cols);
+    }
+  };
+  int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / TPR;
+  if (row < p.rows) fetch(row);
+  w_row.fill(reinterpret_cast<const PT*>(p.w), p.cols, threadIdx.x, T);
+  if (p.Z) {
+    wb_row.fill(reinterpret_cast<const PT*>(p.wb), p.cols, threadIdx.x, T);
+    if (shared_gate) gate_row.fill(reinterpret_cast<const PT*>(p.gate), p.cols, threadIdx.x, T);
+  }
+  __syncthreads();
   bool bad = false;
+  uint32_t found = 0;
   // The trip count differs between the threads of a block only when a row is
   // at most a wave, and then no barrier is inside.
-  for (int64_t row = (int64_t)blockIdx.x * kNormRows<TPR> + threadIdx.x / TPR; row < p.rows; row += stride) {
+  for (; row < p.rows; row += stride) {
     const IO* x = reinterpret_cast<const IO*>(p.X) + row * p.ldx;
-    const IO* z = p.Z ? reinterpret_cast<const IO*>(p.Z) + row * p.ldz : nullptr;
-    const PT* gate = p.gate ? reinterpret_cast<const PT*>(p.gate) + (int64_t)((uint32_t)row / p.gate_rows) * p.cols : nullptr;
-    u32x4_t rx[NV], rz[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * V;
-      rx[i] = issue16<FORM, IO>(x, c, p.cols);
-      if (z) rz[i] = issue16<FORM, IO>(z, c, p.cols);
-    }
     float f[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * V;
-      unpack<IO>(settle16<FORM, IO>(rx[i], x, c, p.cols), f[i]);
-    }
-    if (z) {
-      float b[NV][V], q = 0.f, rb = 1.f;
+    for (int i = 0; i < NV; ++i) unpack<IO>(settle16<FORM, IO>(rx[i], x, col(i), p.cols), f[i]);
+    if (p.Z) {
+      const IO* z = reinterpret_cast<const IO*>(p.Z) + row * p.ldz;
+      float b[NV][V], gv[NV][V], q = 0.f, rb = 1.f;
+      if (!shared_gate) {
+        const PT* gate = reinterpret_cast<const PT*>(p.gate) + (int64_t)((uint32_t)row / p.gate_rows) * p.cols;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          Params<FORM, PT, V> g;
+          g.issue(gate, col(i), p.cols);
+          g.settle(gate, col(i), p.cols);
+#pragma unroll
+          for (int k = 0; k < V; ++k) gv[i][k] = g.get(k);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        unpack<IO>(settle16<FORM, IO>(rz[i], z, (i * TPR + t) * V, p.cols), b[i]);
+        unpack<IO>(settle16<FORM, IO>(rz[i], z, col(i), p.cols), b[i]);
 #pragma unroll
         for (int k = 0; k < V; ++k) q = fmaf(b[i][k], b[i][k], q);
       }
+      if (row + stride < p.rows) fetch(row + stride);
       if (p.norm_branch) {
-        const float mean = row_sum<TPR>(q, sh) * inv_n;
+        const float mean = row_total(q) * inv_n;
         rb = 1.f / sqrtf(mean + p.eps);
         // Squares past fp32 make rb 0, and s finite but not the formula's: reported.
         bad |= !(mean < __builtin_inff());
@@ -102,43 +188,39 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) k_resnorm_fwd(ResNormFwdArg
       IO* s = reinterpret_cast<IO*>(p.S) + row * p.lds;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * V;
-        float wv[V], gv[V];
-        param_values<FORM, PT, V>(WB, c, p.cols, wv);
-        param_values<FORM, PT, V>(gate, c, p.cols, gv);
+        const int c = col(i);
+        float wv[V];
+        wb_row.get(i, t, wv);
+        if (shared_gate) gate_row.get(i, t, gv[i]);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          f[i][k] = p.scale * f[i][k] + gv[k] * (b[i][k] * rb * wv[k]);
-          bad |= in(c, k) && !(fabsf(f[i][k]) < kRoundsToInf<IO>);
-        }
-        if (c < p.cols) store16v<FORM, IO>(s, c, p.cols, f[i]);
+        for (int k = 0; k < V; ++k) f[i][k] = p.scale * f[i][k] + gv[i][k] * (b[i][k] * rb * wv[k]);
+        if (c < p.cols) put16v<FORM, IO>(s, c, p.cols, f[i], found);
       }
+    } else if (row + stride < p.rows) {
+      fetch(row + stride);
     }
     if (!p.Y) continue;
+    // Past the row x, z and so f are zeros.
     float q = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < V; ++k) q = in((i * TPR + t) * V, k) ? fmaf(f[i][k], f[i][k], q) : q;
-    const float mean = row_sum<TPR>(q, sh) * inv_n, rs = 1.f / sqrtf(mean + p.eps);
+      for (int k = 0; k < V; ++k) q = fmaf(f[i][k], f[i][k], q);
+    const float mean = row_total(q) * inv_n, rs = 1.f / sqrtf(mean + p.eps);
     bad |= !(mean < __builtin_inff());
     if (t == 0 && p.rs) p.rs[row] = rs;
     IO* y = reinterpret_cast<IO*>(p.Y) + row * p.ldy;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * V;
-      if (c >= p.cols) continue;
+      const int c = col(i);
       float wv[V];
-      param_values<FORM, PT, V>(W, c, p.cols, wv);
+      w_row.get(i, t, wv);
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        f[i][k] = f[i][k] * rs * wv[k];
-        bad |= in(c, k) && !(fabsf(f[i][k]) < kRoundsToInf<IO>);
-      }
-      store16v<FORM, IO>(y, c, p.cols, f[i]);
+      for (int k = 0; k < V; ++k) f[i][k] = f[i][k] * rs * wv[k];
+      if (c < p.cols) put16v<FORM, IO>(y, c, p.cols, f[i], found);
     }
   }
-  if (p.d_status) report_status(p.d_status, p.status_bits, bad);
+  if (p.d_status) report_status(p.d_status, p.status_bits, bad || (found & kNonfiniteMask<IO>));
 }
 
 // Rows of less than a vector or too long for registers: three passes over the
@@ -219,218 +301,270 @@ struct ResNormBwdArgs {
   // for each.
   int64_t groups, group_rows;
   int split;
-  float* partial;               // [blocks][3][cols]: dw, dwb, and with split > 1 the segment's dgate
+  float* partial;               // [blocks][3][partial_stride]: dw, dwb, and with split > 1 the segment's dgate
   void* dgate;                  // with split == 1: written when a segment ends
   int want_w, want_wb;          // whether dw and dwb are wanted
   int want_gate;                // whether the segments' dgate is
+  int e_gated;                  // segments hold rows of several gates: want_gate is 0
   float* c_row;                 // [rows] (k_resnorm_*_long): mean_j(u shat)
   int32_t* d_status;
   int32_t status_bits;
 };
 
-// One array of column sums of a block's R rows, joined in their order; the
-// last row's threads hold the result.
+// One array of column sums of a block's R rows, joined in their order (the two
+// halves of a wave first): the threads of the first row hold the result.  `sh`
+// holds three rows; all threads of the block call it.
 template <int NV, int V, int TPR, int R>
-__device__ __forceinline__ void join_rows(float (&v)[NV][V], float* sh) {
+__device__ __forceinline__ void join_rows(float (&v)[NV][V], float (*sh)[NV * V * TPR]) {
+  if constexpr (TPR == 32) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const uint32_t u = __float_as_uint(v[i][k]);
+        const auto q = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        v[i][k] = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+      }
+  }
   if constexpr (R > 1) {
-    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    for (int j = 0; j < R; ++j) {
-      if (sub == j) {
+    static_assert(TPR <= 64, "several rows share a block of four waves");
+    const int wave = threadIdx.x >> 6, t = threadIdx.x % TPR;
+    __syncthreads();  // readers of an earlier call are done
+    if (wave > 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) sh[wave - 1][(i * V + k) * TPR + t] = v[i][k];
+    }
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int w = 0; w < 3; ++w)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int k = 0; k < V; ++k) {
-            float* q = sh + (i * V + k) * TPR + t;
-            if (j > 0) v[i][k] += *q;
-            *q = v[i][k];
-          }
-      }
-      __syncthreads();
+          for (int k = 0; k < V; ++k) v[i][k] += sh[w][(i * V + k) * TPR + t];
     }
   }
 }
 
+// A packed vector that the compiler may not look through: unpacked again in
+// each phase, it costs a few shifts; kept unpacked it would hold V registers
+// from one phase to the next.
+__device__ __forceinline__ void repack(u32x4_t& q) { asm volatile("" : "+v"(q)); }
+
+// Partial rows in the workspace are whole vectors.
+__host__ __device__ inline int64_t partial_stride(int64_t cols) { return (cols + 63) / 64 * 64; }
+
+template <int V>
+__device__ __forceinline__ void put_partial(float* row, int c, const float (&f)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; k += 4) *reinterpret_cast<f32x4*>(row + c + k) = f32x4{f[k], f[k + 1], f[k + 2], f[k + 3]};
+}
+
+// A row goes through three phases over its packed registers: the mean of
+// u shat; G, dx and the mean of a bhat; dz.  Two column sums live in registers
+// beside them, dw and e = sum G bhat.  While the gate is the same for all rows
+// of a segment, dgate is wb e and dwb gate e, added up in LDS when a segment
+// ends; where rows of one segment have gates of their own, e holds dwb itself.
 template <typename IO, typename PT, int NV, int TPR, int FORM>
-__global__ void __launch_bounds__(kNormThreads<TPR>) k_resnorm_bwd(ResNormBwdArgs p) {
-  constexpr int V = kVec<IO>, R = kNormRows<TPR>;
-  __shared__ float sh[kNormThreads<TPR> / 64];
-  __shared__ float join[R > 1 ? NV * V * TPR : 1];
+__global__ void __launch_bounds__(kNormThreads<TPR>, 2) k_resnorm_bwd(ResNormBwdArgs p) {
+  constexpr int V = kVec<IO>, R = kNormRows<TPR>, T = kNormThreads<TPR>, N = NV * TPR * V;
+  __shared__ float sums[2][T / 64];
+  __shared__ float join[R > 1 ? 3 : 1][R > 1 ? N : 1];
+  __shared__ alignas(16) float wb_sum[N];  // dwb of the segments done
+  __shared__ ParamRow<PT, NV, TPR, V> w_row, wb_row, gate_row;
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const float inv_n = 1.f / (float)p.cols;
-  auto in = [&](int c, int k) { return (FORM == kEven ? c : c + k) < p.cols; };
-  const PT *W = reinterpret_cast<const PT*>(p.w), *WB = reinterpret_cast<const PT*>(p.wb);
-  float dw[NV][V], dwb[NV][V], dg[NV][V];
+  auto col = [&](int i) { return (i * TPR + t) * V; };
+  auto row_of = [&](const void* base, int64_t row, int64_t ld) { return reinterpret_cast<const IO*>(base) + row * ld; };
+  RowSums<TPR> row_total{sums};
+  w_row.fill(reinterpret_cast<const PT*>(p.w), p.cols, threadIdx.x, T);
+  wb_row.fill(reinterpret_cast<const PT*>(p.wb), p.cols, threadIdx.x, T);
+  for (int c = threadIdx.x; c < N; c += T) wb_sum[c] = 0.f;
+  float dw[NV][V], e[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int k = 0; k < V; ++k) dw[i][k] = dwb[i][k] = dg[i][k] = 0.f;
+    for (int k = 0; k < V; ++k) dw[i][k] = e[i][k] = 0.f;
+  uint32_t found = 0;
   bool bad = false;
-  u32x4_t rd[NV], ry[NV], rS[NV], rz[NV];
-  auto row_of = [&](const void* base, int64_t row, int64_t ld) { return reinterpret_cast<const IO*>(base) + row * ld; };
-  auto fetch = [&](int64_t row) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + t) * V;
-      if (p.dS) rd[i] = issue16<FORM, IO>(row_of(p.dS, row, p.ldds), c, p.cols);
-      if (p.dY) {
-        ry[i] = issue16<FORM, IO>(row_of(p.dY, row, p.lddy), c, p.cols);
-        rS[i] = issue16<FORM, IO>(row_of(p.S, row, p.lds), c, p.cols);
-      }
-      if (p.Z) rz[i] = issue16<FORM, IO>(row_of(p.Z, row, p.ldz), c, p.cols);
-    }
-  };
   const int64_t segments = p.groups * p.split, step = (int64_t)p.split * R;
+  float* partial = p.partial + (int64_t)blockIdx.x * 3 * partial_stride(p.cols);
   for (int64_t seg = blockIdx.x; seg < segments; seg += gridDim.x) {
     const int64_t group = seg / p.split, end = (group + 1) * p.group_rows;
-    int64_t row = group * p.group_rows + (seg - group * p.split) * R + sub;
-    if (row < end) fetch(row);
-    for (; row < end; row += step) {
-      const PT* gate = p.gate ? reinterpret_cast<const PT*>(p.gate) + (int64_t)((uint32_t)row / p.gate_rows) * p.cols : nullptr;
-      float G[NV][V], b[NV][V];
+    if (!p.e_gated) {
+      // The segment's gate, for all its rows.
+      const int64_t g = p.gate ? (int64_t)((uint32_t)(end - 1) / p.gate_rows) : 0;
+      __syncthreads();
+      gate_row.fill(p.gate ? reinterpret_cast<const PT*>(p.gate) + g * p.cols : nullptr, p.cols, threadIdx.x, T);
+    }
+    __syncthreads();
+    for (int64_t row = group * p.group_rows + (seg - group * p.split) * R + sub; row < end; row += step) {
+      u32x4_t rd[NV], ry[NV], rS[NV], rz[NV];
+      Params<FORM, PT, V> rg[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * V;
+        if (p.dY) {
+          ry[i] = issue16<FORM, IO>(row_of(p.dY, row, p.lddy), col(i), p.cols);
+          rS[i] = issue16<FORM, IO>(row_of(p.S, row, p.lds), col(i), p.cols);
+        }
+        if (p.dS) rd[i] = issue16<FORM, IO>(row_of(p.dS, row, p.ldds), col(i), p.cols);
+        if (p.Z) rz[i] = issue16<FORM, IO>(row_of(p.Z, row, p.ldz), col(i), p.cols);
+      }
+      const PT* gate = p.e_gated ? reinterpret_cast<const PT*>(p.gate) + (int64_t)((uint32_t)row / p.gate_rows) * p.cols : nullptr;
+      if (p.e_gated) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) rg[i].issue(gate, col(i), p.cols);
+      }
+      const float rs = p.dY ? p.rs[row] : 0.f, rb = p.rb ? p.rb[row] : 1.f;
+      float m = 0.f;
+      if (p.dY) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float u[V], s[V], wv[V];
+          ry[i] = settle16<FORM, IO>(ry[i], row_of(p.dY, row, p.lddy), col(i), p.cols);
+          rS[i] = settle16<FORM, IO>(rS[i], row_of(p.S, row, p.lds), col(i), p.cols);
+          unpack<IO>(ry[i], u);
+          unpack<IO>(rS[i], s);
+          w_row.get(i, t, wv);
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            const float shat = s[k] * rs;
+            dw[i][k] = fmaf(u[k], shat, dw[i][k]);
+            m = fmaf(u[k] * wv[k], shat, m);
+          }
+          repack(ry[i]);
+          repack(rS[i]);
+        }
+        m = row_total(m) * inv_n;
+      }
+      float a[NV][V], m2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = col(i);
+        float G[V];
         if (p.dS) {
-          unpack<IO>(settle16<FORM, IO>(rd[i], row_of(p.dS, row, p.ldds), c, p.cols), G[i]);
+          unpack<IO>(settle16<FORM, IO>(rd[i], row_of(p.dS, row, p.ldds), c, p.cols), G);
         } else {
 #pragma unroll
-          for (int k = 0; k < V; ++k) G[i][k] = 0.f;
+          for (int k = 0; k < V; ++k) G[k] = 0.f;
         }
-        if (p.Z) unpack<IO>(settle16<FORM, IO>(rz[i], row_of(p.Z, row, p.ldz), c, p.cols), b[i]);
-      }
-      if (p.dY) {
-        const float rs = p.rs[row];
-        float u[NV][V], s[NV][V], m = 0.f;
+        if (p.dY) {
+          float u[V], s[V], wv[V];
+          unpack<IO>(ry[i], u);
+          unpack<IO>(rS[i], s);
+          w_row.get(i, t, wv);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = (i * TPR + t) * V;
-          float wv[V];
-          unpack<IO>(settle16<FORM, IO>(ry[i], row_of(p.dY, row, p.lddy), c, p.cols), u[i]);
-          unpack<IO>(settle16<FORM, IO>(rS[i], row_of(p.S, row, p.lds), c, p.cols), s[i]);
-          param_values<FORM, PT, V>(W, c, p.cols, wv);
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            s[i][k] *= rs;
-            dw[i][k] = fmaf(u[i][k], s[i][k], dw[i][k]);
-            u[i][k] *= wv[k];
-            m = fmaf(u[i][k], s[i][k], m);
-          }
+          for (int k = 0; k < V; ++k) G[k] += rs * (u[k] * wv[k] - s[k] * rs * m);
         }
-        if (row + step < end) fetch(row + step);
-        m = row_sum<TPR>(m, sh) * inv_n;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int k = 0; k < V; ++k) G[i][k] += rs * (u[i][k] - s[i][k] * m);
-      } else if (row + step < end) {
-        fetch(row + step);
-      }
-      if (p.dX) {
-        IO* dx = reinterpret_cast<IO*>(p.dX) + row * p.lddx;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int c = (i * TPR + t) * V;
-          if (c >= p.cols) continue;
+        if (p.dX && c < p.cols) {
           float o[V];
 #pragma unroll
-          for (int k = 0; k < V; ++k) {
-            o[k] = p.scale * G[i][k];
-            bad |= in(c, k) && !(fabsf(o[k]) < kRoundsToInf<IO>);
-          }
-          store16v<FORM, IO>(dx, c, p.cols, o);
+          for (int k = 0; k < V; ++k) o[k] = p.scale * G[k];
+          put16v<FORM, IO>(reinterpret_cast<IO*>(p.dX) + row * p.lddx, c, p.cols, o, found);
         }
-      }
-      if (!p.Z) continue;
-      const float rb = p.rb ? p.rb[row] : 1.f;
-      float m = 0.f;
+        if (!p.Z) continue;
+        float b[V], wv[V], gv[V];
+        rz[i] = settle16<FORM, IO>(rz[i], row_of(p.Z, row, p.ldz), c, p.cols);
+        unpack<IO>(rz[i], b);
+        wb_row.get(i, t, wv);
+        if (p.e_gated) {
+          rg[i].settle(gate, c, p.cols);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * V;
-        float wv[V], gv[V], o[V];
-        param_values<FORM, PT, V>(WB, c, p.cols, wv);
-        param_values<FORM, PT, V>(gate, c, p.cols, gv);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          // Past the row z is zero, and G some number that meets it only.
-          b[i][k] *= rb;
-          o[k] = G[i][k] * b[i][k] * wv[k];
-          dg[i][k] += o[k];
-          const float q = gv[k] * G[i][k];
-          dwb[i][k] = fmaf(q, b[i][k], dwb[i][k]);
-          G[i][k] = wv[k] * q;
-          m = fmaf(G[i][k], b[i][k], m);
+          for (int k = 0; k < V; ++k) gv[k] = rg[i].get(k);
+        } else {
+          gate_row.get(i, t, gv);
         }
         if (p.dgate_rows && c < p.cols) {
+          float o[V];
+          uint32_t off = 0;
 #pragma unroll
-          for (int k = 0; k < V; ++k) bad |= in(c, k) && !(fabsf(o[k]) < kRoundsToInf<PT>);
+          for (int k = 0; k < V; ++k) o[k] = G[k] * (b[k] * rb) * wv[k];
           PT* out = reinterpret_cast<PT*>(p.dgate_rows) + row * p.cols;
           if constexpr (sizeof(PT) == sizeof(IO)) {
-            store16v<FORM, PT>(out, c, p.cols, o);
+            put16v<FORM, PT>(out, c, p.cols, o, off);
           } else {
             // fp32 gates beside 16-bit data: two vectors.
             float half[2][4];
 #pragma unroll
             for (int k = 0; k < V; ++k) half[k / 4][k % 4] = o[k];
-            store16v<kRagged, PT>(out, c, p.cols, half[0]);
-            if (c + 4 < p.cols) store16v<kRagged, PT>(out, c + 4, p.cols, half[1]);
+            put16v<kRagged, PT>(out, c, p.cols, half[0], off);
+            if (c + 4 < p.cols) put16v<kRagged, PT>(out, c + 4, p.cols, half[1], off);
           }
+          bad |= (off & kNonfiniteMask<PT>) != 0;
         }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          // Past the row z is zero, and G some number that meets it only.
+          const float bhat = b[k] * rb, q = gv[k] * G[k];
+          e[i][k] = fmaf(p.e_gated ? q : G[k], bhat, e[i][k]);
+          a[i][k] = wv[k] * q;
+          m2 = fmaf(a[i][k], bhat, m2);
+        }
+        repack(rz[i]);
       }
-      m = p.rb ? row_sum<TPR>(m, sh) * inv_n : 0.f;
+      if (!p.Z) continue;
+      m2 = p.rb ? row_total(m2) * inv_n : 0.f;
       IO* dz = reinterpret_cast<IO*>(p.dZ) + row * p.lddz;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * V;
-        if (c >= p.cols) continue;
+        const int c = col(i);
+        float b[V];
+        unpack<IO>(rz[i], b);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          G[i][k] = rb * (G[i][k] - b[i][k] * m);
-          bad |= in(c, k) && !(fabsf(G[i][k]) < kRoundsToInf<IO>);
-        }
-        store16v<FORM, IO>(dz, c, p.cols, G[i]);
+        for (int k = 0; k < V; ++k) a[i][k] = rb * (a[i][k] - b[k] * rb * m2);
+        if (c < p.cols) put16v<FORM, IO>(dz, c, p.cols, a[i], found);
       }
     }
-    if (p.want_gate) {
-      // The segment's share of its gate row, or all of it.
-      join_rows<NV, V, TPR, R>(dg, join);
-      if (sub == R - 1) {
+    // The segment's end (once, after all rows, where e holds dwb itself).
+    if (!(p.want_gate || p.want_wb)) continue;
+    if (p.e_gated && seg + gridDim.x < segments) continue;
+    if constexpr (R > 1) join_rows<NV, V, TPR, R>(e, join);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      const int c = col(i);
+      if (sub == 0 && c < p.cols) {
+        float gv[V], wv[V], dg[V];
+        gate_row.get(i, t, gv);
+        wb_row.get(i, t, wv);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          wb_sum[c + k] += p.e_gated ? e[i][k] : gv[k] * e[i][k];
+          dg[k] = wv[k] * e[i][k];
+        }
+        if (p.want_gate && p.split > 1) {
+          put_partial(partial + 2 * partial_stride(p.cols), c, dg);
+        } else if (p.want_gate) {
 #pragma unroll
           for (int k = 0; k < V; ++k) {
-            const int c = (i * TPR + t) * V + k;
-            if (c >= p.cols) continue;
-            if (p.split > 1) {
-              p.partial[((int64_t)blockIdx.x * 3 + 2) * p.cols + c] = dg[i][k];
-            } else {
-              reinterpret_cast<PT*>(p.dgate)[group * p.cols + c] = from_f32<PT>(dg[i][k]);
-              bad |= !(fabsf(dg[i][k]) < kRoundsToInf<PT>);
-            }
+            if (c + k >= p.cols) continue;
+            reinterpret_cast<PT*>(p.dgate)[group * p.cols + c + k] = from_f32<PT>(dg[k]);
+            bad |= !(fabsf(dg[k]) < kRoundsToInf<PT>);
           }
+        }
       }
-      if constexpr (R > 1) __syncthreads();
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int k = 0; k < V; ++k) dg[i][k] = 0.f;
+      for (int k = 0; k < V; ++k) e[i][k] = 0.f;
     }
   }
-  if (p.d_status) report_status(p.d_status, p.status_bits, bad);
-  auto leave = [&](float (&v)[NV][V], int which) {
-    join_rows<NV, V, TPR, R>(v, join);
-    if (sub == R - 1) {
+  if (p.d_status) report_status(p.d_status, p.status_bits, bad || (found & kNonfiniteMask<IO>));
+  if constexpr (R > 1) {
+    if (p.want_w) join_rows<NV, V, TPR, R>(dw, join);
+  }
+  if (sub != 0) return;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int c = col(i);
+    if (c >= p.cols) continue;
+    if (p.want_w) put_partial(partial, c, dw[i]);
+    if (p.want_wb) {
+      float o[V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const int c = (i * TPR + t) * V + k;
-          if (c < p.cols) p.partial[((int64_t)blockIdx.x * 3 + which) * p.cols + c] = v[i][k];
-        }
+      for (int k = 0; k < V; ++k) o[k] = wb_sum[c + k];
+      put_partial(partial + partial_stride(p.cols), c, o);
     }
-    if constexpr (R > 1) __syncthreads();
-  };
-  if (p.want_w) leave(dw, 0);
-  if (p.want_wb) leave(dwb, 1);
+  }
 }
 
 // Rows of less than a vector or too long for registers: first each row's
@@ -492,15 +626,15 @@ __global__ void __launch_bounds__(256) k_resnorm_cols_long(ResNormBwdArgs p) {
     }
     if (!p.want_gate) continue;
     if (p.split > 1) {
-      p.partial[((int64_t)blockIdx.y * 3 + 2) * p.cols + c] = dg;
+      p.partial[((int64_t)blockIdx.y * 3 + 2) * partial_stride(p.cols) + c] = dg;
     } else {
       reinterpret_cast<PT*>(p.dgate)[group * p.cols + c] = from_f32<PT>(dg);
       bad |= !(fabsf(dg) < kRoundsToInf<PT>);
     }
   }
-  float* out = p.partial + (int64_t)blockIdx.y * 3 * p.cols;
+  float* out = p.partial + (int64_t)blockIdx.y * 3 * partial_stride(p.cols);
   if (p.want_w) out[c] = dw;
-  if (p.want_wb) out[p.cols + c] = dwb;
+  if (p.want_wb) out[partial_stride(p.cols) + c] = dwb;
   if (p.d_status) report_status(p.d_status, p.status_bits, bad);
 }
 
@@ -541,9 +675,10 @@ __global__ void __launch_bounds__(1024) k_resnorm_bwd_long(ResNormBwdArgs p) {
   if (p.d_status) report_status(p.d_status, p.status_bits, bad);
 }
 
-// The parameters' gradients from the blocks' partial rows, a block for 64
+// The parameters' gradients from the blocks' partial rows, a block for 32
 // columns of one of them: dw and dwb, from all partial rows, then the gate's
-// rows, each from the `split` rows of its own.
+// rows, each from the `split` rows of its own.  32 half-waves take every 32nd
+// partial row, all their loads in flight at once, and join in a fixed order.
 struct ResNormJoinArgs {
   const float* partial;
   int blocks, split, cols;
@@ -553,26 +688,27 @@ struct ResNormJoinArgs {
 };
 template <typename PT>
 __global__ void __launch_bounds__(1024) k_resnorm_join(ResNormJoinArgs p) {
-  __shared__ float sh[16][64];
-  const int slices = (p.cols + 63) / 64, output = blockIdx.x / slices, which = output < 2 ? output : 2;
-  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
-  const int c = (blockIdx.x % slices) * 64 + lane;
+  __shared__ float sh[32][33];
+  const int slices = (p.cols + 31) / 32, output = blockIdx.x / slices, which = output < 2 ? output : 2;
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int c = (blockIdx.x % slices) * 32 + lane;
   void* out = which == 0 ? p.dw : which == 1 ? p.dwb : p.dgate;
   if (!out) return;
   const int64_t group = which == 2 ? output - 2 : 0;
   const int first = which == 2 ? (int)group * p.split : 0, count = which == 2 ? p.split : p.blocks;
   float s = 0.f;
   if (c < p.cols) {
-    const float* src = p.partial + ((int64_t)first * 3 + which) * p.cols + c;
-#pragma unroll 8
-    for (int i = g; i < count; i += 16) s += src[(int64_t)i * 3 * p.cols];
+    const int64_t stride = partial_stride(p.cols);
+    const float* src = p.partial + ((int64_t)first * 3 + which) * stride + c;
+#pragma unroll 16
+    for (int i = g; i < count; i += 32) s += src[(int64_t)i * 3 * stride];
   }
   sh[g][lane] = s;
   __syncthreads();
   if (g == 0 && c < p.cols) {
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += sh[i][lane];
+    for (int i = 0; i < 32; ++i) s += sh[i][lane];
     reinterpret_cast<PT*>(out)[group * p.cols + c] = from_f32<PT>(s);
     if (p.d_status) report_status(p.d_status, p.status_bits, !(fabsf(s) < kRoundsToInf<PT>));
   }
