@@ -558,10 +558,11 @@ ns_status ns_linear_cross_entropy_backward(
  * operation rounded (so codes do not depend on who computes them); p is
  * rounded once to its type (an update below
  * half a step of a 16-bit p is lost: keep such parameters in fp32).  Tensors
- * must not overlap each other.  Non-finite new values of p, copy and fp32
- * moments are reported; with 8-bit moments a NaN stays in its element and an
- * infinite moment makes its whole block NaN.
- * Any number of tensors takes ceil(count / 48) launches.
+ * must not overlap each other.  Non-finite new values of p, copy and the
+ * moments are reported; an infinite second moment counts as 2^128 in the
+ * update.  With 8-bit moments a NaN stays in its element, an infinite m makes
+ * its whole block NaN, and roots end at 2^64.
+ * Up to 54 tensors go in one launch.
  */
 typedef struct ns_adamw_tensor {
   void* param;

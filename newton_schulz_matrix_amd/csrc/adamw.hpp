@@ -24,14 +24,19 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "norm.hpp"
+#include "xent.hpp"
 
 namespace nsk {
 
-constexpr int kAdamwItems = 48;                   // tensors of one launch: 3.6 KB of arguments
-constexpr int kAdamwThreads = 256, kAdamwEach = 8;  // elements of a thread: one 16-byte vector of a 16-bit type
-constexpr int kAdamwChunk = kAdamwThreads * kAdamwEach;
-constexpr int kStateBlock = 256;                  // elements that share a scale: 32 lanes of 8
+constexpr int kAdamwItems = 54;                   // tensors of one launch: 4 KB of arguments
+constexpr int kAdamwThreads = 256;
+constexpr int kStateBlock = 256;                  // elements that share a scale
+// 16 lanes take a block, each two groups of 8 elements half a block apart, so
+// that neighbours' 16-byte vectors lie side by side.  (32 lanes with a group
+// each spent a fifth more instructions per element, on addresses and on the
+// blocks' scales, and arithmetic was 70 % of the time.)
+constexpr int kAdamwGroups = 2, kAdamwLanes = kStateBlock / (8 * kAdamwGroups);
+constexpr int kAdamwChunk = kAdamwThreads * 8 * kAdamwGroups;
 constexpr float kCodeTop = 448.f;                 // the largest e4m3 number
 constexpr float kCodeLeast = 0x1p-9f;             // and the smallest positive one
 constexpr float kScaleLeast = 0x1p-100f;          // keeps 448 / top finite
@@ -59,6 +64,8 @@ struct AdamwArgs {
   int32_t* d_status;
   int32_t status_bits;
 };
+
+static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments");
 
 // Eight consecutive elements of a type known at run time, as raw vectors and
 // as floats; `left`: how many of them there are.  The type is the same for a
@@ -89,26 +96,30 @@ __device__ __forceinline__ void floats_of(const Eight& r, float (&f)[8]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) f[k] = to_f32<T>(reinterpret_cast<const T*>(&r.q[k / kVec<T>])[k % kVec<T>]);
 }
+// Returns nonfinite_bits of what was stored.
 template <typename T>
-__device__ __forceinline__ bool store_eight(T* d, int64_t left, const float (&f)[8]) {
+__device__ __forceinline__ uint32_t store_eight(T* d, int64_t left, const float (&f)[8]) {
   constexpr int N = 8 / kVec<T>;
   Eight r;
-  bool bad = false;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    reinterpret_cast<T*>(&r.q[k / kVec<T>])[k % kVec<T>] = from_f32<T>(f[k]);
-    bad |= k < left && !(fabsf(f[k]) < kRoundsToInf<T>);
-  }
+  for (int k = 0; k < 8; ++k) reinterpret_cast<T*>(&r.q[k / kVec<T>])[k % kVec<T>] = from_f32<T>(f[k]);
+  uint32_t found = 0;
   if (left >= 8) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) {
       *reinterpret_cast<typename Vec16<sizeof(T)>::type*>(d + i * kVec<T>) = r.q[i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) found |= nonfinite_bits<T>(r.q[i][k]);
+    }
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (k < left) d[k] = reinterpret_cast<const T*>(&r.q[k / kVec<T>])[k % kVec<T>];
+      if (k < left) {
+        d[k] = reinterpret_cast<const T*>(&r.q[k / kVec<T>])[k % kVec<T>];
+        found |= nonfinite_bits<T>(one_bits(d[k]));
+      }
   }
-  return bad;
+  return found & kNonfiniteMask<T>;
 }
 
 // Calls f(T{}) for an ns_dtype.
@@ -168,7 +179,7 @@ __device__ __forceinline__ Codes encode(const float (&f)[8], float inv) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     q[k] = f[k] * inv;
-    if (ROOT) q[k] = f[k] > 0.f && q[k] < kCodeLeast ? kCodeLeast : q[k];
+    if (ROOT) q[k] = f[k] > 0.f ? fmaxf(q[k], kCodeLeast) : f[k];
   }
   Codes c;
 #pragma unroll
@@ -179,20 +190,35 @@ __device__ __forceinline__ Codes encode(const float (&f)[8], float inv) {
   return c;
 }
 
-// Largest of 32 lanes' values (>= 0, NaN passed over), in every one of them.
+// Largest of 16 lanes' values (>= 0, NaN passed over), in every one of them.
 template <int CTRL>
 __device__ __forceinline__ float max_dpp(float v) {
   const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false);
   return fmaxf(v, __builtin_bit_cast(float, o));
 }
-__device__ __forceinline__ float half_wave_max(float v) {
+__device__ __forceinline__ float block_max(float v) {
+  static_assert(kAdamwLanes == 16, "a row of the data-parallel moves");
   v = max_dpp<0xB1>(v);
   v = max_dpp<0x4E>(v);
   v = max_dpp<0x141>(v);
-  v = max_dpp<0x140>(v);
-  const uint32_t u = __float_as_uint(v);
-  const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  return max_dpp<0x140>(v);
+}
+
+// The square root, rounded to nearest (for v >= 2^-100; codes and scales are
+// made of it, and equal moments give equal ones whoever computes them): the
+// hardware's reciprocal root, one Newton step for the root s and half its
+// reciprocal h, and the residual's last correction.  The compiler's own
+// sequence takes twice the instructions, for the range below.  An infinite
+// moment counts as the largest finite one, whose root is kRootTop.
+constexpr float kRootTop = 0x1.fffffep63f;
+__device__ __forceinline__ float root_of(float v) {
+  v = fminf(v, 0x1.fffffep127f);
+  const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));
+  float s = v * y, h = 0.5f * y;
+  const float r = fmaf(-h, s, 0.5f);
+  s = fmaf(s, r, s);
+  h = fmaf(h, r, h);
+  return fmaf(fmaf(-s, s, v), h, s);
 }
 
 // The moments' update, each operation rounded on its own (no fused
@@ -217,80 +243,98 @@ static __global__ void __launch_bounds__(kAdamwThreads) k_adamw(AdamwArgs a) {
   for (int step = 32; step > 0; step >>= 1)
     if (i + step < a.count && a.item[i + step].first <= (int)blockIdx.x) i += step;
   bool bad = false;
+  constexpr int kG = kAdamwGroups;
+  // A thread's place in a chunk: block, lane and with it the first group.
+  const int place = (int)threadIdx.x / kAdamwLanes * kStateBlock + (int)threadIdx.x % kAdamwLanes * 8;
+  constexpr int kApart = kAdamwLanes * 8;
   for (int chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
     while (i + 1 < a.count && a.item[i + 1].first <= chunk) ++i;
     const AdamwItem& it = a.item[i];
-    const int64_t e = (int64_t)(chunk - it.first) * kAdamwChunk + threadIdx.x * kAdamwEach;
-    const int64_t left = it.n - e;
+    const int64_t e0 = (int64_t)(chunk - it.first) * kAdamwChunk + place;
     const int pt = it.types & 15, gt = it.types >> 4 & 15, ct = it.types >> 8 & 15;
     const bool coded = it.scales != nullptr;
-    Eight rp{}, rg{}, rm{}, rv{};
-    Codes cm{}, cv{};
+    const int64_t block = e0 / kStateBlock, blocks = (it.n + kStateBlock - 1) / kStateBlock;
+    Eight rp[kG], rg[kG], rm[kG], rv[kG];
+    Codes cm[kG], cv[kG];
     float um = 0.f, uv = 0.f;
-    const int64_t block = e / kStateBlock, blocks = (it.n + kStateBlock - 1) / kStateBlock;
-    if (left > 0) {
-      of_type(gt, [&](auto t) { load_eight(reinterpret_cast<const decltype(t)*>(it.g) + e, left, rg); });
-      of_type(pt, [&](auto t) { load_eight(reinterpret_cast<const decltype(t)*>(it.p) + e, left, rp); });
-      if (coded) {
-        cm = load_codes(reinterpret_cast<const uint8_t*>(it.m) + e, left);
-        cv = load_codes(reinterpret_cast<const uint8_t*>(it.v) + e, left);
+    of_type(gt, [&](auto t) {
+#pragma unroll
+      for (int j = 0; j < kG; ++j) load_eight(reinterpret_cast<const decltype(t)*>(it.g) + e0 + j * kApart, it.n - e0 - j * kApart, rg[j]);
+    });
+    of_type(pt, [&](auto t) {
+#pragma unroll
+      for (int j = 0; j < kG; ++j) load_eight(reinterpret_cast<const decltype(t)*>(it.p) + e0 + j * kApart, it.n - e0 - j * kApart, rp[j]);
+    });
+    if (coded) {
+#pragma unroll
+      for (int j = 0; j < kG; ++j) {
+        cm[j] = load_codes(reinterpret_cast<const uint8_t*>(it.m) + e0 + j * kApart, it.n - e0 - j * kApart);
+        cv[j] = load_codes(reinterpret_cast<const uint8_t*>(it.v) + e0 + j * kApart, it.n - e0 - j * kApart);
+      }
+      if (block < blocks) {
         um = it.scales[block] * (1.f / kCodeTop);
         uv = it.scales[blocks + block] * (1.f / kCodeTop);
-      } else {
-        load_eight(reinterpret_cast<const float*>(it.m) + e, left, rm);
-        load_eight(reinterpret_cast<const float*>(it.v) + e, left, rv);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kG; ++j) {
+        load_eight(reinterpret_cast<const float*>(it.m) + e0 + j * kApart, it.n - e0 - j * kApart, rm[j]);
+        load_eight(reinterpret_cast<const float*>(it.v) + e0 + j * kApart, it.n - e0 - j * kApart, rv[j]);
       }
     }
-    float p[8], g[8], m[8], v[8], root[8];
-    of_type(pt, [&](auto t) { floats_of<decltype(t)>(rp, p); });
-    of_type(gt, [&](auto t) { floats_of<decltype(t)>(rg, g); });
-    if (coded) {
-      decode(cm, um, m);
-      decode(cv, uv, v);
+    const float lr = it.lr * lrs, keep = 1.f - lr * it.decay, lrc = lr * c1;
+    float m[kG][8], root[kG][8], tm = 0.f, tv = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= v[k];
-    } else {
-      floats_of<float>(rm, m);
-      floats_of<float>(rv, v);
-    }
-    const float lr = it.lr * lrs, keep = lr * it.decay;
+    for (int j = 0; j < kG; ++j) {
+      const int64_t e = e0 + j * kApart, left = it.n - e;
+      float p[8], g[8], v[8];
+      of_type(pt, [&](auto t) { floats_of<decltype(t)>(rp[j], p); });
+      of_type(gt, [&](auto t) { floats_of<decltype(t)>(rg[j], g); });
+      if (coded) {
+        decode(cm[j], um, m[j]);
+        decode(cv[j], uv, v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      g[k] *= gs;
-      next_moments(a.b1, a.a1, a.b2, a.a2, g[k], m[k], v[k]);
-      root[k] = sqrtf(v[k]);
-      p[k] = p[k] - keep * p[k] - lr * (c1 * m[k] / (root[k] * c2 + a.eps));
-    }
-    if (coded) {
-      // All 32 lanes of a block take part, those past the tensor's end with zeros.
-      float tm = 0.f, tv = 0.f;
+        for (int k = 0; k < 8; ++k) v[k] *= v[k];
+      } else {
+        floats_of<float>(rm[j], m[j]);
+        floats_of<float>(rv[j], v);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        tm = fmaxf(tm, fabsf(m[k]));
-        tv = fmaxf(tv, root[k]);
-        // An infinite second moment leaves p finite.
-        bad |= !(fabsf(m[k]) < __builtin_inff() && root[k] < __builtin_inff());
+        next_moments(a.b1, a.a1, a.b2, a.a2, g[k] * gs, m[j][k], v[k]);
+        root[j][k] = root_of(v[k]);
+        // The hardware's reciprocal is good to a step of fp32; only the step
+        // is made of it.
+        p[k] = fmaf(-lrc * m[j][k], __builtin_amdgcn_rcpf(fmaf(root[j][k], c2, a.eps)), p[k] * keep);
+        tm = fmaxf(tm, fabsf(m[j][k]));
+        tv = fmaxf(tv, root[j][k]);
       }
-      tm = fmaxf(half_wave_max(tm), kScaleLeast);
-      tv = fmaxf(half_wave_max(tv), kScaleLeast);
-      cm = encode<false>(m, 1.f / tm * kCodeTop);
-      cv = encode<true>(root, 1.f / tv * kCodeTop);
-      if (left > 0) {
-        store_codes(reinterpret_cast<uint8_t*>(it.m) + e, left, cm);
-        store_codes(reinterpret_cast<uint8_t*>(it.v) + e, left, cv);
-        if ((threadIdx.x & 31) == 0) {
-          it.scales[block] = tm;
-          it.scales[blocks + block] = tv;
-        }
+      if (left <= 0) continue;
+      if (!coded) {
+        bad |= (store_eight(reinterpret_cast<float*>(it.m) + e, left, m[j]) |
+                store_eight(reinterpret_cast<float*>(it.v) + e, left, v)) != 0;
       }
-    } else if (left > 0) {
-      bad |= store_eight(reinterpret_cast<float*>(it.m) + e, left, m);
-      bad |= store_eight(reinterpret_cast<float*>(it.v) + e, left, v);
-    }
-    if (left > 0) {
-      of_type(pt, [&](auto t) { bad |= store_eight(reinterpret_cast<decltype(t)*>(it.p) + e, left, p); });
+      of_type(pt, [&](auto t) { bad |= store_eight(reinterpret_cast<decltype(t)*>(it.p) + e, left, p) != 0; });
       if (it.copy)
-        of_type(ct, [&](auto t) { bad |= store_eight(reinterpret_cast<decltype(t)*>(it.copy) + e, left, p); });
+        of_type(ct, [&](auto t) { bad |= store_eight(reinterpret_cast<decltype(t)*>(it.copy) + e, left, p) != 0; });
+    }
+    if (!coded) continue;
+    // All lanes of a block take part, those past the tensor's end with zeros.
+    // An infinite moment may leave p finite; a NaN does not.
+    bad |= !(tm < __builtin_inff() && tv < kRootTop);
+    tm = fmaxf(block_max(tm), kScaleLeast);
+    tv = fmaxf(block_max(tv), kScaleLeast);
+    const float im = 1.f / tm * kCodeTop, iv = 1.f / tv * kCodeTop;
+#pragma unroll
+    for (int j = 0; j < kG; ++j) {
+      const int64_t e = e0 + j * kApart, left = it.n - e;
+      if (left <= 0) continue;
+      store_codes(reinterpret_cast<uint8_t*>(it.m) + e, left, encode<false>(m[j], im));
+      store_codes(reinterpret_cast<uint8_t*>(it.v) + e, left, encode<true>(root[j], iv));
+    }
+    if (threadIdx.x % kAdamwLanes == 0 && block < blocks) {
+      it.scales[block] = tm;
+      it.scales[blocks + block] = tv;
     }
   }
   if (a.d_status) report_status(a.d_status, a.status_bits, bad);

@@ -107,8 +107,10 @@ class _Set:
                 m64, v64 = _decode(m0, s0[0]), _decode(v0, s0[1]) ** 2
             p, m, v = oracle.adamw(_np(p0), _np(g0), m64, v64, rate, step, BETAS, EPS, wd, grad_scale)
             g = _np(g0) * grad_scale
-            # m: beta, the decoded moment (2), the scaled gradient (2),
-            # product and sum; v: the squares twice that.
+            # m: of the decoded moment 1 / 448, the unit and the product, then
+            # beta, product and sum (6); of the gradient its scaling, 1 - beta,
+            # product and sum (4); and 1 for the second order.  v: the squares
+            # of those, so at most 10, its root half of that and 1 of its own.
             em = 7 * U32 * (BETAS[0] * np.abs(m64) + (1 - BETAS[0]) * np.abs(g))
             root = np.sqrt(v / (1 - BETAS[1] ** step))
             update = np.abs(m) / (1 - BETAS[0] ** step) / (root + EPS)
@@ -127,7 +129,9 @@ class _Set:
                 continue
             for name, code, want, err, row in (("m", self.m[i], m, em, 0), ("root", self.v[i], np.sqrt(v), 7 * U32 * np.sqrt(v), 1)):
                 top = oracle.state_tops(want)
-                _close(self.scales[i][row], top, 9 * U32 * top, f"scale of {name}[{i}]")
+                # The largest of a block is off by no more than its elements
+                # are (m's two terms may cancel, so not relative to itself).
+                _close(self.scales[i][row], top, oracle.state_tops(err, least=0.0), f"scale of {name}[{i}]")
                 unit = np.repeat(top, 256)[:want.size].reshape(want.shape) / 448
                 # Half an e4m3 step, 2^-4 relative or half of 2^-9 below its
                 # normal numbers; positive roots down there go up, by 2^-9 at most.
