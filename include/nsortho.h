@@ -766,9 +766,9 @@ int64_t ns_plan_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab,
 /*
  * The same for ns_gated_mlp (backward == 0) or its gradients (backward == 1,
  * all of them), with the arguments of ns_gated_mlp_workspace_size.  Entries,
- * in launch order: prep<op> (copies, where there are any); up<op,rows x
- * columns of a tile of h> and products<op,edge> forward, dz<op,edge> and
- * products<op,edge> backward, join<op> and splits=S where y or dX is summed
+ * in launch order: prep<op> (copies, where there are any); up<op,tile>
+ * (rows x columns of h) and products<op,tile> forward, dz<op,tile> and
+ * products<op,tile> backward, join<op> and splits=S where y or dX is summed
  * from S parts; for a few rows dotup<op,rows,form> and
  * dotdown<op,rows,form>; zero<op> (gradients without rows).
  */

@@ -18,10 +18,6 @@ constexpr int64_t kMaxMlpInner = int64_t(1) << 40;
 // the weights.
 constexpr int64_t kMlpDotMost = 4, kMlpDotMostStaged = 8;
 
-// The projections' tiles: us per k-tile and fixed, as EdgeCost.
-template <int ES> constexpr EdgeCost kUpLargeCost = ES == 2 ? EdgeCost{0, 0.82, 4.0} : EdgeCost{0, 2.10, 3.5};
-template <int ES> constexpr EdgeCost kUpSmallCost = ES == 2 ? EdgeCost{0, 0.52, 3.0} : EdgeCost{0, 1.06, 2.5};
-
 struct MlpPlan {
   int64_t n = 0, d = 0, f = 0;
   int es = 2, bk = 64;
@@ -29,13 +25,18 @@ struct MlpPlan {
   bool stage_d = false, stage_f = false;  // operands of d or f columns need staging copies
   bool dot = false;
   // Forward.
-  bool up_large = false;
-  int64_t up_m = 0, up_cols = 0;       // tile of the projections: rows and columns of h
+  int up_tile = 0;                     // of the projections
   int64_t h_rows = 0, h_ld = 0;
-  // y forward, dz and the gradients backward.
-  int64_t edge = 0;
+  // y forward, the gradients backward: tile and its shape, splits of y or dx.
+  int tile = 0;
+  int64_t tm = 0, tn = 0;
   int splits = 1;
-  int64_t n_pad = 0, d_pad = 0, f_pad = 0, dt = 0;  // backward; dt: row stride of Wd^T
+  // Backward: dh's tiles; the rows and columns that they cover, which the
+  // gradients' contractions run over; d in whole 64s.
+  int dz_tile = 0;
+  int64_t n_pad = 0, f_pad = 0, d_pad = 0;
+  // Row strides of buffers that are n_pad, 2 f_pad and d_pad wide (see skewed).
+  int64_t t_ld = 0, z_ld = 0, d_ld = 0;
   // Buffers.
   char *Xs = nullptr, *Gs = nullptr, *Us = nullptr, *Ds = nullptr, *h = nullptr;
   char *Ys = nullptr, *dz = nullptr, *dzt = nullptr, *ht = nullptr, *WT = nullptr, *DT = nullptr, *XT = nullptr,
@@ -44,59 +45,131 @@ struct MlpPlan {
   size_t total = 0;
 };
 
+// The row stride of a workspace buffer: an odd number of k-tiles (128 bytes).
+// With rows a large power of two apart, a tile's rows meet in few memory
+// channels.
+int64_t skewed(int64_t width, int bk) {
+  const int64_t k = (width + bk - 1) / bk;
+  return (k % 2 ? k : k + 1) * bk;
+}
+
 bool mlp_shape_ok(int64_t n, int64_t d, int64_t f) {
   return n >= 0 && n <= kMaxMlpRows && d >= 1 && d <= kMaxMlpCols && f >= 1 && f <= kMaxMlpCols &&
          n <= kMaxMlpInner / f;
 }
 
-// y's edge and splits: few rows against a long contraction leave most compute
+int64_t tiles_of(int64_t size, int64_t edge) { return (size + edge - 1) / edge; }
+
+// Estimated times, as measured on MI355X: us per k-tile and fixed.  Tiles that
+// share a compute unit (dh's) take `alone` per k-tile while there is one for
+// each, and `ktile` for both of two.
+struct TileCost {
+  int tile;
+  TileShape shape;
+  double ktile, fixed, alone;
+};
+double tile_product_us(const TileCost& c, int64_t tiles, double ktiles) {
+  if (c.alone == 0) return product_us(EdgeCost{0, c.ktile, c.fixed}, tiles, ktiles);
+  if (tiles <= kXentGroups) return ktiles * c.alone + c.fixed;
+  return (double)tiles_of(tiles, 2 * kXentGroups) * (ktiles * c.ktile + c.fixed);
+}
+template <typename T>
+constexpr TileCost kUpCosts[3] = {{kTileLarge, up_shape<T>(kTileLarge), 0.82, 4.0, 0},
+                                  {kTileSmall, up_shape<T>(kTileSmall), 0.52, 3.0, 0},
+                                  {kTileShort, up_shape<T>(kTileShort), 0.36, 2.0, 0}};
+template <>
+constexpr TileCost kUpCosts<float>[3] = {{kTileLarge, up_shape<float>(kTileLarge), 2.10, 3.5, 0},
+                                         {kTileSmall, up_shape<float>(kTileSmall), 1.06, 2.5, 0},
+                                         {kTileSmall, up_shape<float>(kTileSmall), 1.06, 2.5, 0}};
+template <typename T>
+constexpr TileCost kDzCosts[2] = {{kTileLarge, dz_shape<T>(kTileLarge), 0.95, 12.0, 0.52},
+                                  {kTileSmall, dz_shape<T>(kTileSmall), 0.55, 7.0, 0.36}};
+template <>
+constexpr TileCost kDzCosts<float>[2] = {{kTileLarge, dz_shape<float>(kTileLarge), 3.90, 9.0, 2.10},
+                                         {kTileSmall, dz_shape<float>(kTileSmall), 1.00, 4.0, 0.53}};
+
+// The tile whose product of rows x cols over `ktiles` is estimated to end
+// first; `per`: right-hand rows a column.
+template <int N>
+const TileCost& best_tile(const TileCost (&costs)[N], int64_t rows, int64_t cols, int per, double ktiles) {
+  int best = 0;
+  double least = 1e300;
+  for (int i = 0; i < N; ++i) {
+    const TileShape& s = costs[i].shape;
+    const double us = tile_product_us(costs[i], tiles_of(rows, s.m) * tiles_of(cols, s.n / per), ktiles);
+    if (us < least) {
+      least = us;
+      best = i;
+    }
+  }
+  return costs[best];
+}
+
+// y's tile and splits: few rows against a long contraction leave most compute
 // units without a tile.
 struct MlpChoice {
-  int64_t edge = 0;
+  int tile = kTileSmall;
+  TileShape shape{};
   int splits = 1;
   double us = 1e300;
 };
-MlpChoice choose_down(const EdgeCost& c, int64_t n, int64_t d, int64_t ktiles) {
+template <typename T>
+MlpChoice choose_down(int64_t n, int64_t d, double ktiles) {
   MlpChoice best;
-  const int64_t m = (n + c.edge - 1) / c.edge, t = (d + c.edge - 1) / c.edge;
-  for (int s : kXentSplits) {
-    if (s > 1 && ktiles / s < 3) break;
-    // fp32 sums written and read, and a launch.
-    const double sums = s > 1 ? (double)s * m * t * c.edge * c.edge * 8.0 / 4.5e6 + 5.0 : 0.0;
-    const double us = product_us(c, m * t * s, (double)ktiles / s) + sums;
-    if (us < best.us) best = {c.edge, s, us};
+  const EdgeCost* edges = edge_costs(sizeof(T));
+  const TileCost costs[3] = {{kTileLarge, product_shape<T>(kTileLarge), edges[0].ktile, edges[0].fixed, 0},
+                             {kTileSmall, product_shape<T>(kTileSmall), edges[1].ktile, edges[1].fixed, 0},
+                             {kTileShort, product_shape<T>(kTileShort), 0.36, 1.5, 0}};
+  for (const TileCost& c : costs) {
+    if (c.tile == kTileShort && (sizeof(T) == 4 || n > c.shape.m)) continue;
+    const int64_t tiles = tiles_of(n, c.shape.m) * tiles_of(d, c.shape.n);
+    for (int s : kXentSplits) {
+      if (s > 1 && ktiles / s < 3) break;
+      // fp32 sums written and read, and a launch.
+      const double sums = s > 1 ? (double)s * n * tiles_of(d, c.shape.n) * c.shape.n * 8.0 / 4.5e6 + 5.0 : 0.0;
+      const double us = tile_product_us(c, tiles * s, ktiles / s) + sums;
+      if (us < best.us) best = {c.tile, c.shape, s, us};
+    }
   }
   return best;
 }
 
-MlpChoice choose_gradients(const EdgeCost& c, int64_t n, int64_t d, int64_t f, int64_t dk, int bk, bool dx, bool dw) {
-  const int64_t e = c.edge, m = (n + e - 1) / e, t = (d + e - 1) / e, ft = (f + e - 1) / e;
-  const double dz = product_us(c, m * ft, (double)dk / bk);
-  const double kw = (double)m * e / bk, kx = 2.0 * ft * e / bk;
+template <typename T>
+MlpChoice choose_gradients(int64_t n, int64_t d, int64_t f, double kw, double kx) {
   MlpChoice best;
-  for (int s : kXentSplits) {
-    if (s > 1 && (!dx || kx / s < 3)) break;
-    const double sums = s > 1 ? (double)s * m * t * e * e * 8.0 / 4.5e6 + 5.0 : 0.0;
-    const double us = dz + sums + grad_rounds(c, dw ? 3 * ft * t : 0, kw, dx ? m * t * s : 0, kx / s).us;
-    if (us < best.us) best = {e, s, us};
+  for (int i = 0; i < 2; ++i) {
+    const EdgeCost& c = edge_costs(sizeof(T))[i];
+    const int64_t e = c.edge, m = tiles_of(n, e), t = tiles_of(d, e), ft = tiles_of(f, e);
+    for (int s : kXentSplits) {
+      if (s > 1 && kx / s < 3) break;
+      const double sums = s > 1 ? (double)s * n * t * e * 8.0 / 4.5e6 + 5.0 : 0.0;
+      const double us = sums + grad_rounds(c, 3 * ft * t, kw, m * t * s, kx / s).us;
+      if (us < best.us) best = {i == 0 ? kTileLarge : kTileSmall, {(int)e, (int)e}, s, us};
+    }
   }
   return best;
 }
 
 // The same for what a call leaves out: workspaces are planned with both
 // gradients.
-MlpPlan mlp_plan(int64_t n, int64_t d, int64_t f, ns_dtype dtype, bool aligned, bool backward, void* ws) {
+template <typename T>
+MlpPlan mlp_plan_of(int64_t n, int64_t d, int64_t f, bool aligned, bool backward, void* ws) {
   MlpPlan p;
   p.n = n;
   p.d = d;
   p.f = f;
-  p.es = bytes_of(dtype);
+  p.es = sizeof(T);
   p.bk = kRowBytes / p.es;
   p.dk = round_to(d, p.bk);
   p.fk = round_to(f, p.bk);
   p.stage_d = !aligned || p.dk != d;
   p.stage_f = !aligned || p.fk != f;
-  const EdgeCost* costs = edge_costs(p.es);
+  auto take_choice = [&](const MlpChoice& best) {
+    p.tile = best.tile;
+    p.tm = best.shape.m;
+    p.tn = best.shape.n;
+    p.splits = best.splits;
+  };
   Carver c{reinterpret_cast<char*>(ws)};
   if (n == 0) return p;
   if (!backward) {
@@ -104,52 +177,48 @@ MlpPlan mlp_plan(int64_t n, int64_t d, int64_t f, ns_dtype dtype, bool aligned, 
     p.h_rows = n;
     p.h_ld = p.fk;
     if (!p.dot) {
-      auto us = [&](const EdgeCost& x, int64_t tm, int64_t cols) {
-        return product_us(x, ((n + tm - 1) / tm) * ((f + cols - 1) / cols), (double)p.dk / p.bk);
-      };
-      const bool half = p.es == 2;
-      const int64_t lm = half ? kUpLargeM<__bf16> : kUpLargeM<float>, lc = (half ? kUpLargeN<__bf16> : kUpLargeN<float>) / 2;
-      const int64_t sm = half ? kUpSmallM<__bf16> : kUpSmallM<float>, sc = (half ? kUpSmallN<__bf16> : kUpSmallN<float>) / 2;
-      p.up_large = us(half ? kUpLargeCost<2> : kUpLargeCost<4>, lm, lc) <= us(half ? kUpSmallCost<2> : kUpSmallCost<4>, sm, sc);
-      p.up_m = p.up_large ? lm : sm;
-      p.up_cols = p.up_large ? lc : sc;
-      p.h_rows = round_to(n, p.up_m);
-      p.h_ld = round_to(f, p.up_cols);
-      const MlpChoice large = choose_down(costs[0], n, d, p.fk / p.bk), small = choose_down(costs[1], n, d, p.fk / p.bk);
-      const MlpChoice& best = large.us <= small.us ? large : small;
-      p.edge = best.edge;
-      p.splits = best.splits;
+      const TileCost& up = best_tile(kUpCosts<T>, n, f, 2, (double)p.dk / p.bk);
+      p.up_tile = up.tile;
+      p.h_rows = round_to(n, up.shape.m);
+      p.h_ld = skewed(round_to(f, up.shape.n / 2), p.bk);
+      take_choice(choose_down<T>(n, d, (double)p.fk / p.bk));
       if (p.stage_d) {
         p.Xs = c.take<char>(n * p.dk * p.es);
         p.Gs = c.take<char>(f * p.dk * p.es);
         p.Us = c.take<char>(f * p.dk * p.es);
       }
       if (p.stage_f) p.Ds = c.take<char>(d * p.fk * p.es);
-      if (p.splits > 1) p.parts = c.take<float>(p.splits * round_to(n, p.edge) * round_to(d, p.edge));
+      if (p.splits > 1) p.parts = c.take<float>(p.splits * round_to(n, p.tm) * round_to(d, p.tn));
     }
     p.h = c.take<char>(p.h_rows * p.h_ld * p.es);
   } else {
-    const MlpChoice large = choose_gradients(costs[0], n, d, f, p.dk, p.bk, true, true);
-    const MlpChoice small = choose_gradients(costs[1], n, d, f, p.dk, p.bk, true, true);
-    const MlpChoice& best = large.us <= small.us ? large : small;
-    p.edge = best.edge;
-    p.splits = best.splits;
-    p.n_pad = round_to(n, p.edge);
-    p.d_pad = round_to(d, p.edge);
-    p.f_pad = round_to(f, p.edge);
-    p.dt = round_to(d, 64);
+    const TileCost& dz = best_tile(kDzCosts<T>, n, f, 1, (double)p.dk / p.bk);
+    p.dz_tile = dz.tile;
+    p.n_pad = round_to(n, dz.shape.m);
+    p.f_pad = round_to(f, dz.shape.n);
+    p.d_pad = round_to(d, 64);
+    p.t_ld = skewed(p.n_pad, p.bk);
+    p.z_ld = skewed(2 * p.f_pad, p.bk);
+    p.d_ld = skewed(p.d_pad, p.bk);
+    take_choice(choose_gradients<T>(n, d, f, (double)p.n_pad / p.bk, 2.0 * p.f_pad / p.bk));
     if (p.stage_d) p.Ys = c.take<char>(n * p.dk * p.es);
-    p.dz = c.take<char>(2 * p.n_pad * p.f_pad * p.es);
-    p.dzt = c.take<char>(2 * p.n_pad * p.f_pad * p.es);
-    p.ht = c.take<char>(p.n_pad * p.f_pad * p.es);
-    p.WT = c.take<char>(2 * p.d_pad * p.f_pad * p.es);
-    p.DT = c.take<char>(p.f_pad * p.dt * p.es);
-    p.XT = c.take<char>(p.d_pad * p.n_pad * p.es);
-    p.YT = c.take<char>(p.d_pad * p.n_pad * p.es);
-    if (p.splits > 1) p.parts = c.take<float>(p.splits * p.n_pad * p.d_pad);
+    p.dz = c.take<char>(p.n_pad * p.z_ld * p.es);
+    p.dzt = c.take<char>(2 * p.f_pad * p.t_ld * p.es);
+    p.ht = c.take<char>(p.f_pad * p.t_ld * p.es);
+    p.WT = c.take<char>(p.d_pad * p.z_ld * p.es);
+    p.DT = c.take<char>(p.f_pad * p.d_ld * p.es);
+    p.XT = c.take<char>(p.d_pad * p.t_ld * p.es);
+    p.YT = c.take<char>(p.d_pad * p.t_ld * p.es);
+    if (p.splits > 1) p.parts = c.take<float>(p.splits * round_to(n, p.tm) * round_to(d, p.tn));
   }
   p.total = c.used;
   return p;
+}
+
+MlpPlan mlp_plan(int64_t n, int64_t d, int64_t f, ns_dtype dtype, bool aligned, bool backward, void* ws) {
+  // bf16 and fp16 have the same tiles.
+  return dtype == NS_FP32 ? mlp_plan_of<float>(n, d, f, aligned, backward, ws)
+                          : mlp_plan_of<_Float16>(n, d, f, aligned, backward, ws);
 }
 
 // A call's launches as text (see ns_plan_gated_mlp); the length that it needs
@@ -168,10 +237,13 @@ int describe_mlp(const MlpPlan& p, ns_dtype dtype, bool backward, char* buf, siz
   const char* prep = backward || p.stage_d || p.stage_f ? "prep" : "";
   char first[32] = "";
   if (*prep) snprintf(first, sizeof first, "prep<%s> ", op);
-  if (!backward)
-    return snprintf(buf, len, "%sup<%s,%dx%d> products<%s,%d>%s", first, op, (int)p.up_m, (int)p.up_cols, op, (int)p.edge,
-                    split);
-  return snprintf(buf, len, "%sdz<%s,%d> products<%s,%d>%s", first, op, (int)p.edge, op, (int)p.edge, split);
+  const bool half = p.es == 2;
+  const TileShape up = half ? up_shape<_Float16>(p.up_tile) : up_shape<float>(p.up_tile);
+  const TileShape dz = half ? dz_shape<_Float16>(p.dz_tile) : dz_shape<float>(p.dz_tile);
+  const char* name = backward ? "dz" : "up";
+  const TileShape& shape = backward ? dz : up;
+  return snprintf(buf, len, "%s%s<%s,%dx%d> products<%s,%dx%d>%s", first, name, op, shape.m, shape.n / (backward ? 1 : 2), op,
+                  (int)p.tm, (int)p.tn, split);
 }
 
 // The products' copies take 16-byte chunks, swizzled by bits 4 to 6 of the
@@ -251,8 +323,9 @@ ns_status mlp_forward(const MlpPlan& p, const MlpIn& in, int act, void* Y, int64
   a.ktiles = (int)(p.dk / p.bk);
   a.n = p.n;
   a.f = p.f;
-  a.tiles_m = (int)(p.h_rows / p.up_m);
-  a.tiles_n = (int)(p.h_ld / p.up_cols);
+  const TileShape up_tile = up_shape<T>(p.up_tile);
+  a.tiles_m = (int)(p.h_rows / up_tile.m);
+  a.tiles_n = (int)tiles_of(p.f, up_tile.n / 2);
   a.h = p.h;
   a.ldh = p.h_ld;
   a.gate = gate;
@@ -262,9 +335,9 @@ ns_status mlp_forward(const MlpPlan& p, const MlpIn& in, int act, void* Y, int64
   a.act = act;
   a.d_status = d_status;
   a.status_bits = bits;
-  if (launch_mlp_up<T>(a, p.up_large, st) != hipSuccess) return NS_ERR_HIP;
+  if (launch_mlp_up<T>(a, p.up_tile, st) != hipSuccess) return NS_ERR_HIP;
   MlpGradArgs g{};
-  const int64_t tm = (p.n + p.edge - 1) / p.edge, tn = (p.d + p.edge - 1) / p.edge;
+  const int64_t tm = tiles_of(p.n, p.tm), tn = tiles_of(p.d, p.tn);
   g.x = MlpProduct{p.h, p.stage_f ? p.Ds : in.D, (int)tm, (int)tn, p.n, p.d, Y, ldy, p.n, (int)p.d};
   g.x_ldl = p.h_ld * es;
   g.x_ldr = (p.stage_f ? p.fk : in.ldd) * es;
@@ -273,8 +346,8 @@ ns_status mlp_forward(const MlpPlan& p, const MlpIn& in, int act, void* Y, int64
   g.parts = p.parts;
   g.d_status = d_status;
   g.status_bits = bits;
-  if (launch_mlp_products<T>(g, (int)p.edge, st) != hipSuccess) return NS_ERR_HIP;
-  return p.splits > 1 ? mlp_join<T>(p, tm * p.edge, tn * p.edge, Y, ldy, d_status, bits, st) : NS_OK;
+  if (launch_mlp_products<T>(g, p.tile, st) != hipSuccess) return NS_ERR_HIP;
+  return p.splits > 1 ? mlp_join<T>(p, tm * p.tm, tn * p.tn, Y, ldy, d_status, bits, st) : NS_OK;
 }
 
 struct MlpOut {
@@ -289,26 +362,27 @@ ns_status mlp_backward(const MlpPlan& p, const MlpIn& in, const void* dY, int64_
   constexpr int64_t es = sizeof(T);
   const bool dw = out.dG || out.dU || out.dD;
   MlpPrepArgs prep{};
-  prep.copy[0] = mlp_copy(dY, lddy, p.n, p.d, p.Ys, p.dk, dw ? p.YT : nullptr, p.n_pad, p.d_pad, p.n_pad);
-  prep.copy[1] = mlp_copy(in.D, in.ldd, p.d, p.f, nullptr, 0, p.DT, p.dt, p.f_pad, p.dt);
-  if (dw) prep.copy[2] = mlp_copy(in.X, in.ldx, p.n, p.d, nullptr, 0, p.XT, p.n_pad, p.d_pad, p.n_pad);
+  prep.copy[0] = mlp_copy(dY, lddy, p.n, p.d, p.Ys, p.dk, dw ? p.YT : nullptr, p.n_pad, p.d_pad, p.t_ld);
+  prep.copy[1] = mlp_copy(in.D, in.ldd, p.d, p.f, nullptr, 0, p.DT, p.d_pad, p.f_pad, p.d_ld);
+  if (dw) prep.copy[2] = mlp_copy(in.X, in.ldx, p.n, p.d, nullptr, 0, p.XT, p.n_pad, p.d_pad, p.t_ld);
   if (out.dX) {
-    prep.copy[3] = mlp_copy(in.G, in.ldg, p.f, p.d, nullptr, 0, p.WT, p.f_pad, p.d_pad, 2 * p.f_pad);
-    prep.copy[4] = mlp_copy(in.U, in.ldu, p.f, p.d, nullptr, 0, p.WT + p.f_pad * es, p.f_pad, p.d_pad, 2 * p.f_pad);
+    prep.copy[3] = mlp_copy(in.G, in.ldg, p.f, p.d, nullptr, 0, p.WT, p.f_pad, p.d_pad, p.z_ld);
+    prep.copy[4] = mlp_copy(in.U, in.ldu, p.f, p.d, nullptr, 0, p.WT + p.f_pad * es, p.f_pad, p.d_pad, p.z_ld);
   }
   ns_status s = mlp_prep<T>(prep, st);
   if (s != NS_OK) return s;
-  const int64_t tm = p.n_pad / p.edge, td = p.d_pad / p.edge, tf = p.f_pad / p.edge;
+  // The gradients' tiles are square.
+  const int64_t tm = tiles_of(p.n, p.tm), td = tiles_of(p.d, p.tm), tf = tiles_of(p.f, p.tm);
   MlpDzArgs a{};
   a.dY = p.stage_d ? p.Ys : dY;
   a.WT = p.DT;
   a.ldy = (p.stage_d ? p.dk : lddy) * es;
-  a.ldw = p.dt * es;
+  a.ldw = p.d_ld * es;
   a.ktiles = (int)(p.dk / p.bk);
   a.n = p.n;
   a.f = p.f;
-  a.tiles_m = (int)tm;
-  a.tiles_n = (int)tf;
+  a.tiles_m = (int)(p.n_pad / dz_shape<T>(p.dz_tile).m);
+  a.tiles_n = (int)(p.f_pad / dz_shape<T>(p.dz_tile).n);
   a.gate = gate;
   a.up = up;
   a.lds = lds;
@@ -316,39 +390,40 @@ ns_status mlp_backward(const MlpPlan& p, const MlpIn& in, const void* dY, int64_
   a.dz = p.dz;
   a.dzt = p.dzt;
   a.ht = p.ht;
-  a.n_pad = p.n_pad;
   a.f_pad = p.f_pad;
+  a.z_ld = p.z_ld;
+  a.t_ld = p.t_ld;
   a.act = act;
-  if (launch_mlp_dz<T>(a, (int)p.edge, st) != hipSuccess) return NS_ERR_HIP;
+  if (launch_mlp_dz<T>(a, p.dz_tile, st) != hipSuccess) return NS_ERR_HIP;
   MlpGradArgs g{};
   int tiles = 0;
   if (out.dG) tiles += (int)(tf * td);
   g.w[0] = MlpProduct{p.dzt, p.XT, (int)tf, (int)td, p.f_pad, p.d_pad, out.dG, out.lddg, p.f, (int)p.d};
   g.w_tiles[0] = tiles;
   if (out.dU) tiles += (int)(tf * td);
-  g.w[1] = MlpProduct{p.dzt + p.f_pad * p.n_pad * es, p.XT, (int)tf, (int)td, p.f_pad, p.d_pad, out.dU, out.lddu, p.f,
+  g.w[1] = MlpProduct{p.dzt + p.f_pad * p.t_ld * es, p.XT, (int)tf, (int)td, p.f_pad, p.d_pad, out.dU, out.lddu, p.f,
                       (int)p.d};
   g.w_tiles[1] = tiles;
   if (out.dD) tiles += (int)(tf * td);
   g.w[2] = MlpProduct{p.YT, p.ht, (int)td, (int)tf, p.d_pad, p.f_pad, out.dD, out.lddd, p.d, (int)p.f};
   g.w_tiles[2] = tiles;
-  g.w_ld = p.n_pad * es;
+  g.w_ld = p.t_ld * es;
   g.w_ktiles = (int)(p.n_pad / p.bk);
   g.splits = p.splits;
   if (out.dX) {
     g.x = MlpProduct{p.dz, p.WT, (int)tm, (int)td, p.n, p.d_pad, out.dX, out.lddx, p.n, (int)p.d};
-    g.x_ldl = g.x_ldr = 2 * p.f_pad * es;
+    g.x_ldl = g.x_ldr = p.z_ld * es;
     g.x_ktiles = (int)(2 * p.f_pad / p.bk);
     g.parts = p.parts;
     const EdgeCost* costs = edge_costs(p.es);
-    g.extra = grad_rounds(costs[p.edge == costs[0].edge ? 0 : 1], tiles, (double)g.w_ktiles, tm * td * p.splits,
+    g.extra = grad_rounds(costs[p.tile == kTileLarge ? 0 : 1], tiles, (double)g.w_ktiles, tm * td * p.splits,
                           (double)g.x_ktiles / p.splits)
                   .extra;
   }
   g.d_status = d_status;
   g.status_bits = bits;
-  if (launch_mlp_products<T>(g, (int)p.edge, st) != hipSuccess) return NS_ERR_HIP;
-  return out.dX && p.splits > 1 ? mlp_join<T>(p, p.n_pad, p.d_pad, out.dX, out.lddx, d_status, bits, st) : NS_OK;
+  if (launch_mlp_products<T>(g, p.tile, st) != hipSuccess) return NS_ERR_HIP;
+  return out.dX && p.splits > 1 ? mlp_join<T>(p, tm * p.tm, td * p.tm, out.dX, out.lddx, d_status, bits, st) : NS_OK;
 }
 
 bool stride_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxMlpStride; }

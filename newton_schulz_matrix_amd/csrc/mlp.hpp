@@ -290,6 +290,76 @@ __global__ void __launch_bounds__(kThreads, 1) k_mlp_up(MlpUpArgs p) {
 }
 
 // ---------------------------------------------------------------------------
+// One tile of a product whose epilogue moves as many bytes as its k-tiles:
+// two work-groups share a compute unit, with two LDS stages each, so that one
+// multiplies while the other loads and stores.  (dh as a stream of 192 x 192
+// tiles, stream.hpp, whose one work-group does nothing else meanwhile, spent
+// 640 of 1480 us on the epilogue at 8192 x 4096 x 14336; so do pairs of 128
+// tiles there, but at 16384 x 768 x 2048 the backward pass takes 475 us
+// instead of 528.  The projections' product, whose epilogue is shorter, lost
+// by it: 1.60 -> 1.82 ms.)  Stages, fragments and steps are products.hpp's; the
+// operands' resources end with their last valid rows as in stream.hpp.
+// ---------------------------------------------------------------------------
+template <int ROWS>
+__device__ __forceinline__ void limit_rows(DmaLoader<ROWS>& l, const char* base, int64_t ld, int rows, uint32_t row_bytes) {
+  const int left = rows - l.wave_row0;
+  const uint32_t rec = left <= 0 ? 0 : (uint32_t)((left < ROWS / 4 ? left : ROWS / 4) - 1) * (uint32_t)ld + row_bytes;
+  l.rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base) + l.wave_row0 * ld, (short)0, (int)rec, 0x00020000);
+}
+
+template <typename T, int TM, int TN>
+__device__ __forceinline__ void pair_tile(const StreamTile& tile, int64_t ldl, int64_t ldr, Acc<T, TM, TN>& acc) {
+  constexpr int FM = TM / 64, FN = TN / 64, kOffR = TM * kRowBytes;
+  using S = Stages<TM, TN, 2>;
+  static_assert(S::kCount == 2 && (TM + TN) * kRowBytes <= S::kBytes, "two stages of a tile");
+  const int w = threadIdx.x >> 6;
+  FragAddr fa;
+  fa.init((w >> 1) * (TM / 2), (w & 1) * (TN / 2));
+  DmaLoader<TM> la;
+  DmaLoader<TN> lb;
+  la.init(tile.L, ldl);
+  lb.init(tile.R, ldr);
+  const uint32_t row_bytes = (uint32_t)(tile.kts * kRowBytes);
+  limit_rows(la, tile.L, ldl, tile.rows_l, row_bytes);
+  limit_rows(lb, tile.R, ldr, tile.rows_r, row_bytes);
+  const int last = tile.kts - 1;
+  auto copy = [&](int kt, char* D) {
+    la.issue(kt < last ? kt : last, D);
+    lb.issue(kt < last ? kt : last, D + kOffR);
+  };
+  acc_zero(acc);
+  copy(0, S::s0());
+  copy(1, S::s1());
+  __builtin_amdgcn_s_waitcnt(wait_vm(TM / 32 + TN / 32));
+  lds_barrier();
+  FragSets<FM, FN> fs;
+  load_frags<FM, FN>(S::s0(), S::s0() + kOffR, fa, 0, fs.f0);
+  load_frags<FM, FN>(S::s0(), S::s0() + kOffR, fa, 1, fs.f1);
+  load_frags<FM, FN>(S::s0(), S::s0() + kOffR, fa, 2, fs.f2);
+  load_frags<FM, FN>(S::s0(), S::s0() + kOffR, fa, 3, fs.f3);
+  mma_frags<T, FM, FN>(fs.f0, acc.v);
+  mma_frags<T, FM, FN>(fs.f1, acc.v);
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+  lds_barrier();
+  // Step t: k-tile t + 2 into the stage of k-tile t, fragments of k-tile
+  // t + 1.  Two steps at a time, so that each names its stages.
+  auto step = [&](int t, char* D, const char* P) {
+    const int kt = t + 2 < last ? t + 2 : last;
+    pipe_step<T, TM, TN, 2>(nullptr, nullptr, la, lb, kt, 0, D, P, fa, fs, acc.v, [](int, const char*, const FragAddr&) {});
+  };
+  int t = 0;
+  for (; t + 2 <= last; t += 2) {
+    step(t, S::s0(), S::s1());
+    step(t + 1, S::s1(), S::s0());
+  }
+  if (t < last) step(t, S::s0(), S::s1());
+  mma_frags<T, FM, FN>(fs.f2, acc.v);
+  mma_frags<T, FM, FN>(fs.f3, acc.v);
+  // The last, repeated copies must land before the LDS is given away.
+  __builtin_amdgcn_s_waitcnt(0);
+}
+
+// ---------------------------------------------------------------------------
 // Backward: dh and what follows from it.
 // ---------------------------------------------------------------------------
 struct MlpDzArgs {
@@ -301,10 +371,10 @@ struct MlpDzArgs {
   const void *gate, *up;   // n x f, row stride lds
   int64_t lds;
   int save32;              // they are fp32 and not T
-  void* dz;                // n_pad x 2 f_pad: da, db
-  void* dzt;               // 2 f_pad x n_pad
-  void* ht;                // f_pad x n_pad
-  int64_t n_pad, f_pad;
+  void* dz;                // n_pad x 2 f_pad: da, db; row stride z_ld
+  void* dzt;               // 2 f_pad x n_pad, row stride t_ld
+  void* ht;                // f_pad x n_pad, row stride t_ld
+  int64_t f_pad, z_ld, t_ld;
   int act;
 };
 
@@ -327,17 +397,9 @@ __device__ __forceinline__ f32x4 load_quad(const T* s) {
 template <typename T, int TM, int TN>
 struct MlpDzEpilogue {
   using A = Acc<T, TM, TN>;
-  // Per 32 x 32 block, every one executed by every wave: 12 transposed ones,
-  // and in rows 4 of 16 bits or 8 of fp32.
-  static constexpr int kStores = A::FM * A::FN * (sizeof(T) == 2 ? 16 : 20);
   const MlpDzArgs& p;
-  const TileRun& run;
   LanePlace<TM, TN> at;
-  __device__ __forceinline__ void load(int) {}
-  __device__ __forceinline__ void settle() {}
-  __device__ __forceinline__ void store(int j, A& acc) {
-    int tm, tn;
-    grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+  __device__ __forceinline__ void store(int tm, int tn, A& acc) {
     const int64_t row0 = (int64_t)tm * TM + at.wr, col0 = (int64_t)tn * TN + at.wc;
     // Rows and columns of this wave's part that exist.
     const int rows = (int)(p.n - row0 < TM / 2 ? p.n - row0 : TM / 2), cols = (int)(p.f - col0 < TN / 2 ? p.f - col0 : TN / 2);
@@ -348,8 +410,8 @@ struct MlpDzEpilogue {
       for (int fm = 0; fm < A::FM; ++fm) {
         const int r = fm * 32 + at.lr;
         const int64_t in = (row0 + r) * p.lds + col0 + 4 * at.h;
-        T* dz = reinterpret_cast<T*>(p.dz) + (row0 + r) * 2 * p.f_pad + col0;
-        const int64_t t = (col0 + 4 * at.h + q) * p.n_pad + row0 + fm * 32 + i4;
+        T* dz = reinterpret_cast<T*>(p.dz) + (row0 + r) * p.z_ld + col0;
+        const int64_t t = (col0 + 4 * at.h + q) * p.t_ld + row0 + fm * 32 + i4;
         T *dzt = reinterpret_cast<T*>(p.dzt) + t, *ht = reinterpret_cast<T*>(p.ht) + t;
 #pragma unroll
         for (int fn = 0; fn < A::FN; ++fn) {
@@ -394,9 +456,9 @@ struct MlpDzEpilogue {
             }
           put_padded<T>(dz + 32 * fn, at.h, da);
           put_padded<T>(dz + p.f_pad + 32 * fn, at.h, db);
-          put_transposed<T>(dzt + (int64_t)(32 * fn) * p.n_pad, p.n_pad, da);
-          put_transposed<T>(dzt + (p.f_pad + 32 * fn) * p.n_pad, p.n_pad, db);
-          put_transposed<T>(ht + (int64_t)(32 * fn) * p.n_pad, p.n_pad, h);
+          put_transposed<T>(dzt + (int64_t)(32 * fn) * p.t_ld, p.t_ld, da);
+          put_transposed<T>(dzt + (p.f_pad + 32 * fn) * p.t_ld, p.t_ld, db);
+          put_transposed<T>(ht + (int64_t)(32 * fn) * p.t_ld, p.t_ld, h);
         }
       }
     });
@@ -404,19 +466,16 @@ struct MlpDzEpilogue {
 };
 
 template <typename T, int TM, int TN>
-__global__ void __launch_bounds__(kThreads, 1) k_mlp_dz(MlpDzArgs p) {
-  const TileRun run(p.tiles_m * p.tiles_n);
-  stream_tiles<T, TM, TN>(
-      run.count, p.ldy, p.ldw, (uint32_t)(p.ktiles * kRowBytes),
-      [&](int j) {
-        int tm, tn;
-        grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
-        const int64_t row0 = (int64_t)tm * TM;
-        return StreamTile{reinterpret_cast<const char*>(p.dY) + row0 * p.ldy,
-                          reinterpret_cast<const char*>(p.WT) + (int64_t)tn * TN * p.ldw,
-                          (int)(p.n - row0 < TM ? p.n - row0 : TM), TN, 0, p.ktiles};
-      },
-      MlpDzEpilogue<T, TM, TN>{p, run});
+__global__ void __launch_bounds__(kThreads, 2) k_mlp_dz(MlpDzArgs p) {
+  int tm, tn;
+  grouped_tile(xcd_order(blockIdx.x, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, tm, tn);
+  const int64_t row0 = (int64_t)tm * TM;
+  const StreamTile tile{reinterpret_cast<const char*>(p.dY) + row0 * p.ldy,
+                        reinterpret_cast<const char*>(p.WT) + (int64_t)tn * TN * p.ldw,
+                        (int)(p.n - row0 < TM ? p.n - row0 : TM), TN, 0, p.ktiles};
+  Acc<T, TM, TN> acc;
+  pair_tile<T, TM, TN>(tile, p.ldy, p.ldw, acc);
+  MlpDzEpilogue<T, TM, TN>{p}.store(tm, tn, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -525,13 +584,16 @@ struct SplitEpilogue {
     float* out = p.parts + ((int64_t)(i / per) * p.x.tiles_m * TM + (int64_t)tm * TM + at.wr + at.lr) * ld + tn * TN +
                  at.wc + 4 * at.h;
 #pragma unroll
-    for (int fm = 0; fm < A::FM; ++fm)
+    for (int fm = 0; fm < A::FM; ++fm) {
+      // Rows past the result are not summed either.
+      if ((int64_t)tm * TM + at.wr + at.lr + fm * 32 >= p.x.rows) continue;
 #pragma unroll
       for (int fn = 0; fn < A::FN; ++fn)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           *reinterpret_cast<f32x4*>(out + (int64_t)fm * 32 * ld + fn * 32 + 8 * g) =
               f32x4{acc.v[fm][fn][4 * g], acc.v[fm][fn][4 * g + 1], acc.v[fm][fn][4 * g + 2], acc.v[fm][fn][4 * g + 3]};
+    }
   }
 };
 
@@ -760,37 +822,68 @@ namespace nsr {
 
 using namespace nsk;
 
-// Tiles of the projections' product, whose right-hand rows are two columns
-// each: rows of the larger and the smaller one, right-hand rows of both.  The
-// other products have xent.hpp's square tiles.
-template <typename T> inline constexpr int kUpLargeM = 128;
-template <typename T> inline constexpr int kUpLargeN = sizeof(T) == 2 ? 256 : 128;
-template <typename T> inline constexpr int kUpSmallM = sizeof(T) == 2 ? 128 : 64;
-template <typename T> inline constexpr int kUpSmallN = 128;
+// Tiles, rows by right-hand rows.  The projections' right-hand rows are two a
+// column.  16-bit products have short ones beside them, for few rows.
+enum MlpTile { kTileLarge = 0, kTileSmall = 1, kTileShort = 2 };
+struct TileShape {
+  int m, n;
+};
+template <typename T>
+constexpr TileShape up_shape(int tile) {
+  if (sizeof(T) == 4) return tile == kTileLarge ? TileShape{128, 128} : TileShape{64, 128};
+  return tile == kTileLarge ? TileShape{128, 256} : tile == kTileSmall ? TileShape{128, 128} : TileShape{64, 128};
+}
+template <typename T>
+constexpr TileShape dz_shape(int tile) {
+  if (sizeof(T) == 4) return tile == kTileLarge ? TileShape{128, 128} : TileShape{64, 64};
+  return tile == kTileLarge ? TileShape{128, 128} : TileShape{64, 128};
+}
+template <typename T>
+constexpr TileShape product_shape(int tile) {
+  return tile == kTileLarge   ? TileShape{kXentLarge<T>, kXentLarge<T>}
+         : tile == kTileSmall ? TileShape{kXentSmall<T>, kXentSmall<T>}
+                              : TileShape{64, 128};
+}
 
-template <typename T> hipError_t launch_mlp_up(const MlpUpArgs& a, bool large, hipStream_t s);
-template <typename T> hipError_t launch_mlp_dz(const MlpDzArgs& a, int edge, hipStream_t s);
-template <typename T> hipError_t launch_mlp_products(const MlpGradArgs& a, int edge, hipStream_t s);
+template <typename T> hipError_t launch_mlp_up(const MlpUpArgs& a, int tile, hipStream_t s);
+template <typename T> hipError_t launch_mlp_dz(const MlpDzArgs& a, int tile, hipStream_t s);
+template <typename T> hipError_t launch_mlp_products(const MlpGradArgs& a, int tile, hipStream_t s);
 template <typename T> hipError_t launch_mlp_dot_up(const MlpDotUpArgs& a, hipStream_t s);
 template <typename T> hipError_t launch_mlp_dot_down(const MlpDotDownArgs& a, hipStream_t s);
 
+#define NS_MLP_TILE(K, SHAPE, TILE, GRID) \
+  hipLaunchKernelGGL((K<T, SHAPE<T>(TILE).m, SHAPE<T>(TILE).n>), GRID, dim3(kThreads), 0, s, a)
 template <typename T>
-hipError_t mlp_up_of(const MlpUpArgs& a, bool large, hipStream_t s) {
-  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-  if (large)
-    NS_XENT_LAUNCH(k_mlp_up, kUpLargeM<T>, kUpLargeN<T>, tiles, a);
+hipError_t mlp_up_of(const MlpUpArgs& a, int tile, hipStream_t s) {
+  const dim3 grid = xent_grid((int64_t)a.tiles_m * a.tiles_n);
+  if (tile == kTileLarge)
+    NS_MLP_TILE(k_mlp_up, up_shape, kTileLarge, grid);
+  else if (tile == kTileSmall || sizeof(T) == 4)
+    NS_MLP_TILE(k_mlp_up, up_shape, kTileSmall, grid);
   else
-    NS_XENT_LAUNCH(k_mlp_up, kUpSmallM<T>, kUpSmallN<T>, tiles, a);
+    NS_MLP_TILE(k_mlp_up, up_shape, kTileShort, grid);
   return hipGetLastError();
 }
 template <typename T>
-hipError_t mlp_dz_of(const MlpDzArgs& a, int edge, hipStream_t s) {
-  NS_XENT_EDGE(k_mlp_dz, (int64_t)a.tiles_m * a.tiles_n, a);
+hipError_t mlp_dz_of(const MlpDzArgs& a, int tile, hipStream_t s) {
+  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n));
+  if (tile == kTileLarge)
+    NS_MLP_TILE(k_mlp_dz, dz_shape, kTileLarge, grid);
+  else
+    NS_MLP_TILE(k_mlp_dz, dz_shape, kTileSmall, grid);
+  return hipGetLastError();
 }
 template <typename T>
-hipError_t mlp_products_of(const MlpGradArgs& a, int edge, hipStream_t s) {
-  const int64_t tiles = a.w_tiles[kMlpProducts - 1] + (int64_t)a.x.tiles_m * a.x.tiles_n * a.splits;
-  NS_XENT_EDGE(k_mlp_products, tiles, a);
+hipError_t mlp_products_of(const MlpGradArgs& a, int tile, hipStream_t s) {
+  const dim3 grid = xent_grid(a.w_tiles[kMlpProducts - 1] + (int64_t)a.x.tiles_m * a.x.tiles_n * a.splits);
+  if (tile == kTileLarge) {
+    NS_MLP_TILE(k_mlp_products, product_shape, kTileLarge, grid);
+  } else if (tile == kTileSmall) {
+    NS_MLP_TILE(k_mlp_products, product_shape, kTileSmall, grid);
+  } else {
+    if constexpr (sizeof(T) == 2) NS_MLP_TILE(k_mlp_products, product_shape, kTileShort, grid);
+  }
+  return hipGetLastError();
 }
 #define NS_MLP_DOT(K, N, FORM) hipLaunchKernelGGL((K<T, N, FORM>), grid, dim3(256), 0, s, a)
 #define NS_MLP_DOTS(K, COLS)                                                      \
@@ -821,26 +914,26 @@ hipError_t mlp_dot_down_of(const MlpDotDownArgs& a, hipStream_t s) {
   NS_MLP_DOTS(k_mlp_dot_down, a.f);
 }
 
-#define NS_MLP_LAUNCHERS(T)                                                        \
-  template <>                                                                      \
-  hipError_t launch_mlp_up<T>(const MlpUpArgs& a, bool large, hipStream_t s) {     \
-    return mlp_up_of<T>(a, large, s);                                              \
-  }                                                                                \
-  template <>                                                                      \
-  hipError_t launch_mlp_dz<T>(const MlpDzArgs& a, int edge, hipStream_t s) {       \
-    return mlp_dz_of<T>(a, edge, s);                                               \
-  }                                                                                \
-  template <>                                                                      \
-  hipError_t launch_mlp_products<T>(const MlpGradArgs& a, int edge, hipStream_t s) { \
-    return mlp_products_of<T>(a, edge, s);                                         \
-  }                                                                                \
-  template <>                                                                      \
-  hipError_t launch_mlp_dot_up<T>(const MlpDotUpArgs& a, hipStream_t s) {          \
-    return mlp_dot_up_of<T>(a, s);                                                 \
-  }                                                                                \
-  template <>                                                                      \
-  hipError_t launch_mlp_dot_down<T>(const MlpDotDownArgs& a, hipStream_t s) {      \
-    return mlp_dot_down_of<T>(a, s);                                               \
+#define NS_MLP_LAUNCHERS(T)                                                          \
+  template <>                                                                        \
+  hipError_t launch_mlp_up<T>(const MlpUpArgs& a, int tile, hipStream_t s) {         \
+    return mlp_up_of<T>(a, tile, s);                                                 \
+  }                                                                                  \
+  template <>                                                                        \
+  hipError_t launch_mlp_dz<T>(const MlpDzArgs& a, int tile, hipStream_t s) {         \
+    return mlp_dz_of<T>(a, tile, s);                                                 \
+  }                                                                                  \
+  template <>                                                                        \
+  hipError_t launch_mlp_products<T>(const MlpGradArgs& a, int tile, hipStream_t s) { \
+    return mlp_products_of<T>(a, tile, s);                                           \
+  }                                                                                  \
+  template <>                                                                        \
+  hipError_t launch_mlp_dot_up<T>(const MlpDotUpArgs& a, hipStream_t s) {            \
+    return mlp_dot_up_of<T>(a, s);                                                   \
+  }                                                                                  \
+  template <>                                                                        \
+  hipError_t launch_mlp_dot_down<T>(const MlpDotDownArgs& a, hipStream_t s) {        \
+    return mlp_dot_down_of<T>(a, s);                                                 \
   }
 
 }  // namespace nsr

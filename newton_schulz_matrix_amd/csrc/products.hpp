@@ -348,7 +348,8 @@ struct FragSets {
 template <int NM, int NR, int NV, int I>
 __device__ __forceinline__ void schedule_half() {
   if constexpr (I < NR) {
-    __builtin_amdgcn_sched_group_barrier(0x008, (I + 1) * NM / NR - I * NM / NR, 0);
+    constexpr int m = (I + 1) * NM / NR - I * NM / NR;
+    if constexpr (m > 0) __builtin_amdgcn_sched_group_barrier(0x008, m, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     constexpr int v = (I + 1) * NV / NR - I * NV / NR;
     if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x020, v, 0);
@@ -363,7 +364,6 @@ __device__ __forceinline__ void schedule_step() {
   constexpr int NM = 2 * FM * FN * (sizeof(T) == 4 ? 4 : 1);      // MFMAs per half
   constexpr int NV = TM / 32 + TN / 32;                           // copies per step
   constexpr int NV1 = Stages<TM, TN, G>::kCount == 3 ? (NV + 1) / 2 : NV;
-  static_assert(NM >= NR, "at least one MFMA per read");
   schedule_half<NM, NR, NV1, 0>();
   schedule_half<NM, NR, NV - NV1, 0>();
 }

@@ -19,6 +19,6 @@ MLP_CASES = [
     # The larger tiles, work-groups with several of them, each of more k-tiles
     # than the three LDS stages hold.
     (1003, 520, 1407, ALL), (1500, 264, 3001, HALF), (5000, 776, 264, HALF), (5000, 1000, 2800, ("bf16",)),
-    (4000, 200, 3001, ("fp32",)), (4000, 776, 264, ("fp32",)),
+    (4000, 200, 3001, ("fp32",)), (4000, 776, 264, ("fp32",)), (1500, 64, 3001, ("fp32",)),
 ]
 MLP_RUNS = [(n, d, f, t) for n, d, f, types in MLP_CASES for t in types]

@@ -10,18 +10,21 @@ import pytest
 from newton_schulz_matrix_amd import build as nsbuild
 from test_training_waits import HIPCC, _steps
 
-# And the vector stores that their waits count on at a tile's border, per
-# 32 x 32 block of a wave: of h 2 in 16 bits and 4 in fp32 (for half the
-# blocks, beside twice as many of a and b, which are not counted on), of da,
-# db and h 16 and 20.
-KERNELS = [("k_mlp_up<__bf16, 128, 256>(MlpUpArgs)", 4 * (2 + 4)), ("k_mlp_up<float, 64, 128>(MlpUpArgs)", 4 + 8),
-           ("k_mlp_dz<_Float16, 192, 192>(MlpDzArgs)", 9 * 16), ("k_mlp_dz<float, 64, 64>(MlpDzArgs)", 20),
-           ("k_mlp_products<__bf16, 192, 192>(MlpGradArgs)", 0)]
+# And the vector stores that the streams' waits count on at a tile's border,
+# per 32 x 32 block of a wave: of h 2 in 16 bits and 4 in fp32 (for half the
+# blocks, beside twice as many of a and b, which are not counted on).  dh's
+# tiles are no stream.  Barriers and copies: at least three steps' (two for dh).
+KERNELS = [("k_mlp_up<__bf16, 128, 256>(MlpUpArgs)", 4 * (2 + 4), 7, 36),
+           ("k_mlp_up<_Float16, 64, 128>(MlpUpArgs)", 2 + 4, 7, 18),
+           ("k_mlp_up<float, 64, 128>(MlpUpArgs)", 4 + 8, 7, 18),
+           ("k_mlp_dz<_Float16, 128, 128>(MlpDzArgs)", 4 * 16, 4, 24), ("k_mlp_dz<__bf16, 64, 128>(MlpDzArgs)", 2 * 16, 4, 18),
+           ("k_mlp_dz<float, 64, 64>(MlpDzArgs)", 20, 4, 12),
+           ("k_mlp_products<__bf16, 192, 192>(MlpGradArgs)", 0, 7, 36), ("k_mlp_products<__bf16, 64, 128>(MlpGradArgs)", 0, 7, 18)]
 
 
 @pytest.mark.skipif(HIPCC is None, reason="hipcc not found")
-@pytest.mark.parametrize("kernel,stores", KERNELS)
-def test_every_barrier_behind_copies_has_a_wait_that_waits(kernel, stores, tmp_path):
+@pytest.mark.parametrize("kernel,stores,barriers,copies", KERNELS)
+def test_every_barrier_behind_copies_has_a_wait_that_waits(kernel, stores, barriers, copies, tmp_path):
     src = tmp_path / "one.hip"
     src.write_text(f'#include "mlp.hpp"\nnamespace nsk {{ template __global__ void {kernel}; }}\n')
     got = subprocess.run([HIPCC, *nsbuild.HIP_FLAGS, "-I", nsbuild.CSRC, "-I", nsbuild.INCLUDE, "-S", "--cuda-device-only",
@@ -30,7 +33,7 @@ def test_every_barrier_behind_copies_has_a_wait_that_waits(kernel, stores, tmp_p
     # None of the stores is merged with another or left out.
     assert len(re.findall(r"^\s*global_store_dwordx[24]\b", got.stdout, re.M)) >= stores
     steps = _steps(got.stdout)
-    assert sum(k == "barrier" for k, _ in steps) >= 7 and sum(k == "copy" for k, _ in steps) >= 36
+    assert sum(k == "barrier" for k, _ in steps) >= barriers and sum(k == "copy" for k, _ in steps) >= copies
     waited, seen = True, 0
     for kind, count in steps:
         if kind == "copy":
