@@ -10,31 +10,35 @@ that the library could not use.
 from __future__ import annotations
 
 import ctypes
-import struct
-from itertools import chain
-from operator import attrgetter
+import importlib
 from typing import List, Optional, Sequence, Tuple, Union
 
 import torch
 
 from . import _binding as B
 from ._binding import NSError, dtype_code, lib
-from ._training import (_call, _device, _output, _output_like, _param, _per_row, _ptr,
-                        _rows, _same_device, _status_ptr, _workspace_args)
+from ._training import (_call, _current_device, _device, _output, _output_like, _param, _per_row, _ptr,
+                        _raw_stream, _rows, _same_device, _status_ptr, _workspace_args)
+
+_MARSHAL = None
+
+
+def _marshal():
+    """The host module that checks the arguments of small calls (csrc/marshal.cpp)."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        try:
+            _MARSHAL = importlib.import_module("._marshal", __package__)
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is not built for this Python and torch; run "
+                               "`python -m newton_schulz_matrix_amd.build` first") from e
+    return _MARSHAL
+
 
 # ---------------------------------------------------------------------------
 # AdamW.
 # ---------------------------------------------------------------------------
 STATE_BLOCK = 256  # elements of an 8-bit moment that share a scale
-
-_TENSOR_FORMAT = "6Qq2f4i"  # ns_adamw_tensor
-_TENSOR = struct.Struct("=" + _TENSOR_FORMAT)
-
-_MOMENT_TYPES = {torch.float32: False, torch.float8_e4m3fn: True}
-
-_data_ptr, _numel, _size = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.size
-_get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
-_dtype = attrgetter("dtype")
 
 
 def adamw_states(params: Sequence[torch.Tensor], bits: int = 32):
@@ -57,14 +61,6 @@ def adamw_states(params: Sequence[torch.Tensor], bits: int = 32):
     return m, v, scales
 
 
-def _per_tensor(value, count: int, name: str) -> Sequence[float]:
-    if isinstance(value, (int, float)):
-        return (value,) * count
-    if len(value) != count:
-        raise ValueError(f"{name} must be one number or one per tensor")
-    return value
-
-
 def _scalar(t: Optional[torch.Tensor], dtype: torch.dtype, device: torch.device,
             name: str) -> Optional[int]:
     if t is None:
@@ -74,26 +70,6 @@ def _scalar(t: Optional[torch.Tensor], dtype: torch.dtype, device: torch.device,
     if t.device != device or t.numel() != 1:
         raise ValueError(f"{name} must hold one element on {device}")
     return t.data_ptr()
-
-
-def _scales_ptr(scales: Optional[torch.Tensor], numel: int, coded: bool, device: torch.device) -> int:
-    if (scales is not None) != coded:
-        raise ValueError("scales go with float8_e4m3fn moments, one tensor each")
-    if scales is None:
-        return 0
-    if (scales.dtype != torch.float32 or scales.numel() != 2 * -(-numel // STATE_BLOCK) or scales.device != device
-            or not scales.is_contiguous()):
-        raise ValueError(f"scales must be contiguous float32 tensors [2, ceil(numel / {STATE_BLOCK})] on {device}")
-    return scales.data_ptr()
-
-
-def _copy_ptr(copy: Optional[torch.Tensor], param: torch.Tensor, device: torch.device) -> int:
-    if copy is None:
-        return 0
-    if (copy.dtype not in B._DTYPE_CODE or copy.shape != param.shape or copy.device != device
-            or not copy.is_contiguous()):
-        raise ValueError("copies must be contiguous bf16, fp16 or fp32 tensors of their parameter's shape")
-    return copy.data_ptr()
 
 
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
@@ -121,59 +97,17 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     factors of all gradients and of all learning rates.
     """
     count = len(params)
-    if not (len(grads) == len(m) == len(v) == count):
-        raise ValueError("params, grads, m and v must have one entry per tensor")
-    for name, given in (("scales", scales), ("copies", copies)):
-        if given is not None and len(given) != count:
-            raise ValueError(f"{name} must have one entry (or None) per tensor")
-    rates = _per_tensor(lr, count, "lr")
-    decays = _per_tensor(weight_decay, count, "weight_decay")
     if count == 0:
         return
     device = _device(params[0])
-    # Whole lists at a time: a step over 50 vectors takes 5 us on the device,
-    # and checking them one by one took 90 here.
-    here = {device.index}
-    for name, tensors in (("params", params), ("grads", grads), ("m", m), ("v", v)):
-        if set(map(_get_device, tensors)) != here:
-            raise ValueError(f"{name} must be on {device}")
-        if not all(map(_is_contiguous, tensors)):
-            raise ValueError(f"{name} must be contiguous")
-    numels = list(map(_numel, params))
-    if list(map(_size, grads)) != list(map(_size, params)):
-        raise ValueError("grads must have their parameters' shapes")
-    if list(map(_numel, m)) != numels or list(map(_numel, v)) != numels:
-        raise ValueError("m and v must have as many elements as their parameters")
-    ptypes, gtypes = (list(map(B._DTYPE_CODE.get, map(_dtype, tensors))) for tensors in (params, grads))
-    if None in ptypes or None in gtypes:
-        raise TypeError("params and grads must be bf16, fp16 or fp32")
-    mtypes = list(map(_dtype, m))
-    coded = list(map(_MOMENT_TYPES.get, mtypes))
-    if None in coded or list(map(_dtype, v)) != mtypes:
-        raise TypeError("m and v must both be float32 or both float8_e4m3fn")
-    zeros = [0] * count
-    ps, pc, ctypes_ = zeros, zeros, zeros
-    if scales is not None or True in coded:
-        given = scales if scales is not None else [None] * count
-        ps = [_scales_ptr(s, n, c, device) for s, n, c in zip(given, numels, coded)]
-    if copies is not None:
-        pc = [_copy_ptr(c, p, device) for c, p in zip(copies, params)]
-        ctypes_ = [0 if c is None else B._DTYPE_CODE[c.dtype] for c in copies]
-    pp, pg, pm, pv = (list(map(_data_ptr, tensors)) for tensors in (params, grads, m, v))
-    written = [ptr for column in (pp, pm, pv, ps, pc) if column is not zeros for ptr in column if ptr]
-    if 0 in numels:
-        written = [ptr for column in (pp, pm, pv, ps, pc) for ptr, n in zip(column, numels) if ptr and n]
-    if len(set(written)) != len(written):
-        raise ValueError("a tensor is given twice")
-    table = bytearray(struct.pack("=" + _TENSOR_FORMAT * count, *chain.from_iterable(
-        zip(pp, pg, pm, pv, ps, pc, numels, rates, decays, ptypes, gtypes, ctypes_, zeros))))
+    table = _marshal().adamw_table(params, grads, m, v, scales, copies, lr, weight_decay)
     if isinstance(step, torch.Tensor):
         step_ptr, step = _scalar(step, torch.int32, device, "step"), 0
     else:
         step_ptr = None
         if step < 1:
             raise ValueError("step must be 1 or more")
-    _call("ns_adamw_step", device, (ctypes.c_char * len(table)).from_buffer(table), count,
+    _call("ns_adamw_step", device, table, count,
           betas[0], betas[1], eps, int(step), step_ptr,
           _scalar(grad_scale, torch.float32, device, "grad_scale"),
           _scalar(lr_scale, torch.float32, device, "lr_scale"),
@@ -217,6 +151,9 @@ def _param_dtype(x: torch.Tensor, **params: Optional[torch.Tensor]) -> torch.dty
     return x.dtype if dtype is None else dtype
 
 
+_RESIDUAL_NORM = None  # the entry point's address
+
+
 def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None,
                   gate: Optional[torch.Tensor] = None, scale: float = 1.0,
                   branch_weight: Optional[torch.Tensor] = None,
@@ -242,36 +179,20 @@ def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None,
     stream) may be ``residual`` and ``out_norm`` may be ``branch``.
     """
     device = _device(residual)
-    rows, cols, ldx = _rows(residual, "residual")
-    code = dtype_code(residual.dtype)
-    if branch is None:
-        if gate is not None or branch_weight is not None or out is not None or scale != 1.0:
-            raise ValueError("gate, branch_weight, out and scale go with a branch")
-        if not norm_out:
-            raise ValueError("nothing to compute")
-    ldz = _like(branch, residual, device, "branch") if branch is not None else 0
-    groups = _gate_groups(gate, residual, rows, cols)
-    _param(branch_weight, residual, cols, "branch_weight")
-    _param(weight, residual, cols, "weight")
-    pcode = dtype_code(_param_dtype(residual, gate=gate, branch_weight=branch_weight, weight=weight))
-    stream, normed, lds, ldy = residual, None, 0, 0
-    if branch is not None:
-        stream, lds = _output_like(out, residual, cols, device, "out")
-    if norm_out:
-        normed, ldy = _output_like(out_norm, residual, cols, device, "out_norm")
-    rb = rs = None
-    if stats:
-        lead = (rows,) if residual.dim() == 2 else residual.shape[:-1]
-        if branch is not None and norm_branch:
-            rb = torch.empty(lead, dtype=torch.float32, device=device)
-        if norm_out:
-            rs = torch.empty(lead, dtype=torch.float32, device=device) if rb is None else torch.empty_like(rb)
-    _call("ns_residual_norm", device,
-          residual.data_ptr(), ldx, _ptr(branch), ldz, rows, cols, code, _ptr(gate), groups,
-          _ptr(branch_weight), _ptr(weight), pcode, scale, 1 if norm_branch else 0, eps,
-          stream.data_ptr() if branch is not None else None, lds, _ptr(normed), ldy, _ptr(rb), _ptr(rs),
-          _status_ptr(status, device))
-    return stream, normed, rb, rs
+    global _RESIDUAL_NORM
+    if _RESIDUAL_NORM is None:
+        _RESIDUAL_NORM = ctypes.cast(lib().ns_residual_norm, ctypes.c_void_p).value
+    index = device.index
+    args = (_RESIDUAL_NORM, residual, branch, gate, scale, branch_weight, weight, norm_branch, norm_out, eps, stats,
+            out, out_norm, None if status is None else _status_ptr(status, device), _raw_stream(index))
+    if index == _current_device():
+        got = _marshal().residual_norm(*args)
+    else:
+        with torch.cuda.device(device):
+            got = _marshal().residual_norm(*args)
+    if type(got) is int:
+        B._check(got, "ns_residual_norm")
+    return got
 
 
 def residual_norm_workspace_size(rows: int, cols: int) -> int:

@@ -34,6 +34,23 @@ HIP_FLAGS = [
 ]
 
 
+MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
+
+
+def marshal_command() -> list:
+    """Compiles the host module that checks the arguments of small calls
+    against this Python and this torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    includes = [flag for path in include_paths() for flag in ("-isystem", path)]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *includes,
+            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", MARSHAL_PATH + ".tmp",
+            "-L", os.path.join(torch.__path__[0], "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc",
                  shutil.which("hipcc")):
@@ -43,7 +60,8 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False, extra_flags=None) -> str:
-    """Compile every HIP source and link libnsortho.so next to this file."""
+    """Compile every HIP source and link libnsortho.so, and the host module,
+    next to this file."""
     cc = hipcc()
     objs = []
     procs = []
@@ -56,11 +74,15 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         procs.append((subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                        stderr=subprocess.STDOUT), src))
         objs.append(obj)
+    cmd = marshal_command()
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    procs.append((subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), "marshal.cpp"))
     for p, src in procs:
         out, _ = p.communicate()
         text = out.decode(errors="replace")
         if p.returncode != 0:
-            raise RuntimeError(f"hipcc failed on {src}:\n{text}")
+            raise RuntimeError(f"the compiler failed on {src}:\n{text}")
         if verbose and text.strip():
             print(text, flush=True)
     tmp = LIB_PATH + ".tmp"
@@ -71,6 +93,7 @@ def build(verbose: bool = False, extra_flags=None) -> str:
     if res.returncode != 0:
         raise RuntimeError("link failed:\n" + res.stdout.decode(errors="replace"))
     os.replace(tmp, LIB_PATH)
+    os.replace(MARSHAL_PATH + ".tmp", MARSHAL_PATH)
     for obj in objs:
         os.remove(obj)
     return LIB_PATH

@@ -5,6 +5,7 @@ dereferenced)."""
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import pytest
@@ -13,12 +14,12 @@ import torch
 import oracle
 import newton_schulz_matrix_amd as nsa
 from newton_schulz_matrix_amd import _binding as B
-from newton_schulz_matrix_amd import _block
 
 built = pytest.mark.skipif(not os.path.exists(B.LIB_PATH), reason="libnsortho.so not built")
 
 INV, DT, WSP = 1, 2, 3
 PTR = 1 << 20  # stands for a device pointer
+ENTRY = struct.Struct("=6Qq2f4i")  # ns_adamw_tensor
 
 
 # ---------------------------------------------------------------------------
@@ -44,9 +45,9 @@ def test_oracle_adamw_against_closed_forms():
 def _adamw(beta1=0.9, beta2=0.95, eps=1e-8, step=1, d_step=None, count=1, table=True, **kw):
     e = dict(param=PTR, grad=PTR, m=PTR, v=PTR, scales=0, copy=0, numel=10, lr=1e-3, wd=0.1, pt=0, gt=0, ct=0, zero=0)
     e.update(kw)
-    raw = bytearray(_block._TENSOR.pack(*(e[k] or 0 for k in ("param", "grad", "m", "v", "scales", "copy", "numel", "lr",
+    raw = bytearray(ENTRY.pack(*(e[k] or 0 for k in ("param", "grad", "m", "v", "scales", "copy", "numel", "lr",
                                                               "wd", "pt", "gt", "ct", "zero"))))
-    arr = (ctypes.c_char * len(raw)).from_buffer(raw) if table else None
+    arr = bytes(raw) if table else None
     return B.lib().ns_adamw_step(arr, count, beta1, beta2, eps, step, d_step, None, None, None, None)
 
 
@@ -71,7 +72,7 @@ def test_adamw_table_entry_has_the_headers_layout():
     names = [line.split()[-1].rstrip(";").lstrip("*") for line in body.splitlines()[1:] if line.strip()]
     assert names == ["param", "grad", "exp_avg", "exp_avg_sq", "scales", "copy", "numel", "lr", "weight_decay",
                      "param_dtype", "grad_dtype", "copy_dtype", "reserved"]
-    assert _block._TENSOR.size == 6 * 8 + 8 + 2 * 4 + 4 * 4
+    assert ENTRY.size == 6 * 8 + 8 + 2 * 4 + 4 * 4
 
 
 def test_adamw_states_and_host_tensors():
