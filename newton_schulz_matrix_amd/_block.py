@@ -17,8 +17,7 @@ import torch
 
 from . import _binding as B
 from ._binding import NSError, dtype_code, lib
-from ._training import (_call, _current_device, _device, _output, _output_like, _param, _per_row, _ptr,
-                        _raw_stream, _rows, _same_device, _status_ptr, _workspace_args)
+from ._training import _call, _current_device, _device, _raw_stream, _status_ptr
 
 _MARSHAL = None
 
@@ -33,6 +32,31 @@ def _marshal():
             raise RuntimeError("_marshal.so is not built for this Python and torch; run "
                                "`python -m newton_schulz_matrix_amd.build` first") from e
     return _MARSHAL
+
+
+_ADDRESS = {}  # the entry points' addresses
+
+
+def _address(name: str) -> int:
+    got = _ADDRESS.get(name)
+    if got is None:
+        got = _ADDRESS[name] = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+    return got
+
+
+def _run(name: str, device: torch.device, status: Optional[torch.Tensor], *args):
+    """Checks the arguments of an entry point in the host module and calls it
+    on the current stream of ``device``, which is made the current device."""
+    args += (None if status is None else _status_ptr(status, device), _raw_stream(device.index))
+    fn = getattr(_marshal(), name[3:])
+    if device.index == _current_device():
+        got = fn(_address(name), *args)
+    else:
+        with torch.cuda.device(device):
+            got = fn(_address(name), *args)
+    if type(got) is int:
+        B._check(got, name)
+    return got
 
 
 # ---------------------------------------------------------------------------
@@ -118,42 +142,6 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
 # Norms before and after a block.
 # ---------------------------------------------------------------------------
 
-def _like(t: torch.Tensor, x: torch.Tensor, device: torch.device, name: str) -> int:
-    """The row stride of a tensor of x's shape and dtype."""
-    if t.shape != x.shape or t.dtype != x.dtype:
-        raise ValueError(f"{name} must have the shape and dtype of the other tensors")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return _rows(t, name)[2]
-
-
-def _gate_groups(gate: Optional[torch.Tensor], x: torch.Tensor, rows: int, cols: int) -> int:
-    if gate is None:
-        return 0
-    if gate.dtype != x.dtype and gate.dtype != torch.float32:
-        raise TypeError("gate must have the data's dtype or float32")
-    if gate.device != x.device or not gate.is_contiguous() or gate.dim() < 1 or gate.shape[-1] != cols:
-        raise ValueError(f"gate must be a contiguous tensor on {x.device} whose last axis has {cols} elements")
-    groups = gate.numel() // cols
-    if groups < 1 or (rows and (groups > rows or rows % groups)):
-        raise ValueError("gate must have rows that divide the data's")
-    return groups
-
-
-def _param_dtype(x: torch.Tensor, **params: Optional[torch.Tensor]) -> torch.dtype:
-    """The one type of the gate and the weights (x's without any)."""
-    dtype = None
-    for p in params.values():
-        if p is not None:
-            if dtype is not None and p.dtype != dtype:
-                raise TypeError(f"{', '.join(params)} must have the same dtype")
-            dtype = p.dtype
-    return x.dtype if dtype is None else dtype
-
-
-_RESIDUAL_NORM = None  # the entry point's address
-
-
 def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None,
                   gate: Optional[torch.Tensor] = None, scale: float = 1.0,
                   branch_weight: Optional[torch.Tensor] = None,
@@ -178,21 +166,8 @@ def residual_norm(residual: torch.Tensor, branch: Optional[torch.Tensor] = None,
     ``residual`` itself, which is returned as the stream.  ``out`` (the
     stream) may be ``residual`` and ``out_norm`` may be ``branch``.
     """
-    device = _device(residual)
-    global _RESIDUAL_NORM
-    if _RESIDUAL_NORM is None:
-        _RESIDUAL_NORM = ctypes.cast(lib().ns_residual_norm, ctypes.c_void_p).value
-    index = device.index
-    args = (_RESIDUAL_NORM, residual, branch, gate, scale, branch_weight, weight, norm_branch, norm_out, eps, stats,
-            out, out_norm, None if status is None else _status_ptr(status, device), _raw_stream(index))
-    if index == _current_device():
-        got = _marshal().residual_norm(*args)
-    else:
-        with torch.cuda.device(device):
-            got = _marshal().residual_norm(*args)
-    if type(got) is int:
-        B._check(got, "ns_residual_norm")
-    return got
+    return _run("ns_residual_norm", _device(residual), status, residual, branch, gate, scale, branch_weight, weight,
+                norm_branch, norm_out, eps, stats, out, out_norm)
 
 
 def residual_norm_workspace_size(rows: int, cols: int) -> int:
@@ -221,48 +196,9 @@ def residual_norm_backward(dstream: Optional[torch.Tensor], dnormed: Optional[to
     dresidual and may be ``dstream``; ``out_branch`` receives dbranch and may
     be ``dnormed``.
     """
-    device = _device(stream)
-    rows, cols, lds = _rows(stream, "stream")
-    code = dtype_code(stream.dtype)
-    if dstream is None and dnormed is None:
-        raise ValueError("dstream or dnormed must be given")
-    ldds = _like(dstream, stream, device, "dstream") if dstream is not None else 0
-    lddy = _like(dnormed, stream, device, "dnormed") if dnormed is not None else 0
-    if dnormed is not None:
-        if rstd is None:
-            raise ValueError("dnormed needs rstd")
-        _per_row(rstd, rows, device, "rstd")
-    elif weight is not None:
-        raise ValueError("weight goes with dnormed")
-    if branch is None:
-        if gate is not None or branch_weight is not None or branch_rstd is not None or scale != 1.0:
-            raise ValueError("gate, branch_weight, branch_rstd and scale go with a branch")
-        if out_branch is not None:
-            raise ValueError("out_branch goes with a branch")
-    ldz = _like(branch, stream, device, "branch") if branch is not None else 0
-    if branch_rstd is not None:
-        _per_row(branch_rstd, rows, device, "branch_rstd")
-    groups = _gate_groups(gate, stream, rows, cols)
-    _param(branch_weight, stream, cols, "branch_weight")
-    _param(weight, stream, cols, "weight")
-    pcode = dtype_code(_param_dtype(stream, gate=gate, branch_weight=branch_weight, weight=weight))
-    dres, lddx = _output_like(out, stream, cols, device, "out")
-    dbranch, lddz = (_output_like(out_branch, stream, cols, device, "out_branch") if branch is not None
-                     else (None, 0))
-
-    def grad_of(p):
-        return torch.empty_like(p, requires_grad=False) if params and p is not None else None
-
-    dgate, dwb, dw = grad_of(gate), grad_of(branch_weight), grad_of(weight)
-    wptr, wbytes, keep = _workspace_args(
-        int(lib().ns_residual_norm_workspace_size(rows, cols)), device, workspace,
-        "ns_residual_norm_workspace_size")
-    _call("ns_residual_norm_backward", device,
-          _ptr(dstream), ldds, _ptr(dnormed), lddy, stream.data_ptr(), lds, _ptr(branch), ldz, rows, cols, code,
-          _ptr(branch_rstd), _ptr(rstd), _ptr(gate), groups, _ptr(branch_weight), _ptr(weight), pcode, scale,
-          dres.data_ptr(), lddx, _ptr(dbranch), lddz, _ptr(dgate), _ptr(dwb), _ptr(dw),
-          _status_ptr(status, device), wptr, wbytes)
-    return dres, dbranch, dgate, dwb, dw
+    return _run("ns_residual_norm_backward", _device(stream), status, _address("ns_residual_norm_workspace_size"),
+                dstream, dnormed, stream, branch, branch_rstd, rstd, gate, scale, branch_weight, weight, params, out,
+                out_branch, workspace)
 
 
 # ---------------------------------------------------------------------------
@@ -276,25 +212,6 @@ def _activation(name: str) -> int:
         return _ACTIVATIONS[name]
     except KeyError:
         raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}") from None
-
-
-def _weights(x: torch.Tensor, cols: int, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor):
-    """(inner, their row strides) of a block's matrices."""
-    device = x.device
-    if w_gate.dim() != 2 or w_up.dim() != 2 or w_down.dim() != 2:
-        raise ValueError("w_gate, w_up and w_down must be 2-D")
-    inner, _, ldg = _rows(w_gate, "w_gate")
-    if inner < 1 or w_gate.shape[1] != cols or w_up.shape != w_gate.shape or tuple(w_down.shape) != (cols, inner):
-        raise ValueError("w_gate and w_up must be [inner, cols] and w_down [cols, inner]")
-    if not (w_gate.dtype == w_up.dtype == w_down.dtype == x.dtype):
-        raise ValueError("the weights must have x's dtype")
-    _same_device(device, w_gate=w_gate, w_up=w_up, w_down=w_down)
-    return inner, ldg, _rows(w_up, "w_up")[2], _rows(w_down, "w_down")[2]
-
-
-def _aligned(*operands) -> bool:
-    """Whether (tensor, row stride) pairs start on 16 bytes and step by whole 128."""
-    return all(t.data_ptr() % 16 == 0 and ld * t.element_size() % 128 == 0 for t, ld in operands)
 
 
 def gated_mlp_workspace_size(rows: int, cols: int, inner: int, dtype: torch.dtype = torch.bfloat16,
@@ -332,27 +249,17 @@ def gated_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     which halves their memory and doubles the gradients' rounding error.
     With ``save=False`` they are None.
     """
-    device = _device(x)
-    rows, cols, ldx = _rows(x, "x")
-    code, act = dtype_code(x.dtype), _activation(activation)
-    inner, ldg, ldu, ldd = _weights(x, cols, w_gate, w_up, w_down)
-    y, ldy = _output_like(out, x, cols, device, "out")
-    gate = up = None
-    stype = save if isinstance(save, torch.dtype) else torch.float32
-    if stype not in (torch.float32, x.dtype):
+    device, act = _device(x), _activation(activation)
+    if save is True:
+        save = torch.float32
+    if save is False:
+        save = None
+    elif save != torch.float32 and save != x.dtype:
         raise TypeError("save must be True, False, torch.float32 or x's dtype")
-    if save:
-        gate = torch.empty(tuple(x.shape[:-1]) + (inner,), dtype=stype, device=device)
-        up = torch.empty_like(gate)
-    aligned = ldg == ldu and _aligned((x, ldx), (w_gate, ldg), (w_up, ldu), (w_down, ldd))
-    wptr, wbytes, keep = _workspace_args(
-        int(lib().ns_gated_mlp_workspace_size(rows, cols, inner, code, 1 if aligned else 0, 0)), device, workspace,
-        "ns_gated_mlp_workspace_size")
-    _call("ns_gated_mlp", device,
-          x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd, rows, cols, inner,
-          code, act, y.data_ptr(), ldy, _ptr(gate), _ptr(up), inner, dtype_code(stype), _status_ptr(status, device),
-          wptr, wbytes)
-    return y, gate, up
+    else:
+        save = save == torch.float32
+    return _run("ns_gated_mlp", device, status, _address("ns_gated_mlp_workspace_size"), x, w_gate, w_up, w_down, act,
+                save, out, workspace)
 
 
 def gated_mlp_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
@@ -368,33 +275,6 @@ def gated_mlp_backward(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, 
     workspace holds the gradients of gate and up twice, h, and transposed
     copies of x, dy and the weights.
     """
-    device = _device(x)
-    rows, cols, ldx = _rows(x, "x")
-    code, act = dtype_code(x.dtype), _activation(activation)
-    inner, ldg, ldu, ldd = _weights(x, cols, w_gate, w_up, w_down)
-    lddy = _like(dy, x, device, "dy")
-    shape = tuple(x.shape[:-1]) + (inner,)
-    for name, t in (("gate", gate), ("up", up)):
-        if tuple(t.shape) != shape or t.dtype != gate.dtype or t.device != device:
-            raise ValueError(f"{name} must have shape {shape}, gate's dtype and device {device}")
-    if gate.dtype not in (torch.float32, x.dtype):
-        raise TypeError("gate and up must be float32 or have x's dtype")
-    lds = _rows(gate, "gate")[2]
-    if _rows(up, "up")[2] != lds:
-        raise ValueError("gate and up must have the same row stride")
-    dx = dwg = dwu = dwd = None
-    lddx, lddg, lddu, lddd = cols, cols, cols, inner
-    if need_dx:
-        dx, lddx = _output_like(out_dx, x, cols, device, "out_dx")
-    if need_dw:
-        dwg, lddg = _output(out_dw_gate, w_gate.shape, x.dtype, device, "out_dw_gate")
-        dwu, lddu = _output(out_dw_up, w_up.shape, x.dtype, device, "out_dw_up")
-        dwd, lddd = _output(out_dw_down, w_down.shape, x.dtype, device, "out_dw_down")
-    wptr, wbytes, keep = _workspace_args(
-        int(lib().ns_gated_mlp_workspace_size(rows, cols, inner, code, 1 if _aligned((dy, lddy)) else 0, 1)), device,
-        workspace, "ns_gated_mlp_workspace_size")
-    _call("ns_gated_mlp_backward", device,
-          dy.data_ptr(), lddy, x.data_ptr(), ldx, w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, w_down.data_ptr(), ldd,
-          gate.data_ptr(), up.data_ptr(), lds, dtype_code(gate.dtype), rows, cols, inner, code, act, _ptr(dx), lddx, _ptr(dwg), lddg,
-          _ptr(dwu), lddu, _ptr(dwd), lddd, _status_ptr(status, device), wptr, wbytes)
-    return dx, dwg, dwu, dwd
+    return _run("ns_gated_mlp_backward", _device(x), status, _address("ns_gated_mlp_workspace_size"), x, w_gate, w_up,
+                w_down, dy, gate, up, _activation(activation), need_dx, need_dw, out_dx, out_dw_gate, out_dw_up,
+                out_dw_down, workspace)
