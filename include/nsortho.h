@@ -665,13 +665,14 @@ ns_status ns_residual_norm_backward(
  *   rows <= 2^22, cols and inner <= 2^20, rows * inner <= 2^40, row strides
  *            <= 2^23.
  *   workspace   ns_gated_mlp_workspace_size(rows, cols, inner, dtype,
- *            aligned, 0) bytes, 256-byte aligned; aligned is 1 when X, Wg, Wu
- *            and Wd start on 16-byte boundaries, their row strides are
- *            multiples of 128 bytes and ldwg == ldwu, else 0 (the operands
- *            are then copied, as they are when cols or inner is not a
- *            multiple of 64, or 32 in fp32).
- * The products accumulate in fp32; h is formed in fp32 and rounded to dtype,
- * being an operand itself.
+ *            aligned, 0) bytes, 256-byte aligned.  aligned is 1 when those
+ *            operands start on 16-byte boundaries and have row strides of
+ *            whole 128 bytes whose rows are whole 128 bytes: X, Wg and Wu
+ *            (with ldwg == ldwu) if cols is a multiple of 64 (32 in fp32), Wd
+ *            if inner is.  The others are copied in any case, and with
+ *            aligned 0 all are.
+ * The products accumulate in fp32; h is formed in fp32 and rounded to dtype
+ * where it is a matrix instruction's operand (with a few rows it is not).
  */
 typedef enum { NS_SILU = 0, NS_GELU = 1, NS_GELU_TANH = 2, NS_RELU = 3 } ns_activation;
 

@@ -216,9 +216,10 @@ def _activation(name: str) -> int:
 
 def gated_mlp_workspace_size(rows: int, cols: int, inner: int, dtype: torch.dtype = torch.bfloat16,
                              aligned: bool = True, backward: bool = False) -> int:
-    """``aligned``: x and the weights (backward: dy) start on 16-byte
-    boundaries, their row strides are multiples of 128 bytes and w_gate's and
-    w_up's are the same."""
+    """``aligned``: the operands whose rows are whole 128 bytes (x, w_gate and
+    w_up by cols, w_down by inner; backward: dy) start on 16-byte boundaries,
+    their row strides are multiples of 128 bytes and w_gate's and w_up's are
+    the same."""
     return int(lib().ns_gated_mlp_workspace_size(rows, cols, inner, dtype_code(dtype), 1 if aligned else 0,
                                                  1 if backward else 0))
 

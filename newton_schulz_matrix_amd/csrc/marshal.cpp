@@ -544,8 +544,10 @@ PyObject* gated_mlp(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     up = at::empty(sizes, b.x.options().dtype(type));
     st_code = dtype_of(gate);
   }
-  const bool even = b.ldg == b.ldu && aligned(b.x, b.r.ld) && aligned(b.wg, b.ldg) && aligned(b.wu, b.ldu) &&
-                    aligned(b.wd, b.ldd);
+  const int64_t ktile = 128 / (int64_t)b.x.element_size();
+  const bool even = (b.r.cols % ktile || (b.ldg == b.ldu && aligned(b.x, b.r.ld) && aligned(b.wg, b.ldg) &&
+                                          aligned(b.wu, b.ldu))) &&
+                    (b.inner % ktile || aligned(b.wd, b.ldd));
   const size_t need = query(b.r.rows, b.r.cols, b.inner, (ns_dtype)b.dt, even, 0);
   if (need == 0) return PyLong_FromLong(NS_ERR_INVALID_ARG);
   Workspace ws;

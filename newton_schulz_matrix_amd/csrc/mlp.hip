@@ -31,6 +31,9 @@ struct MlpPlan {
   int tile = 0;
   int64_t tm = 0, tn = 0;
   int splits = 1;
+  // The copies that the projections (dh's product) do not read go along with
+  // their tiles.
+  bool side = false;
   // Backward: dh's tiles; the rows and columns that they cover, which the
   // gradients' contractions run over; d in whole 64s.
   int dz_tile = 0;
@@ -88,6 +91,8 @@ template <>
 constexpr TileCost kDzCosts<float>[2] = {{kTileLarge, dz_shape<float>(kTileLarge), 3.90, 9.0, 2.10},
                                          {kTileSmall, dz_shape<float>(kTileSmall), 1.00, 4.0, 0.53}};
 
+constexpr double kCopyUs = 0.8;  // of a 64 x 64 tile
+
 // The tile whose product of rows x cols over `ktiles` is estimated to end
 // first; `per`: right-hand rows a column.
 template <int N>
@@ -103,6 +108,18 @@ const TileCost& best_tile(const TileCost (&costs)[N], int64_t rows, int64_t cols
     }
   }
   return costs[best];
+}
+
+// Whether `copies` 64 x 64 tiles of copies go along with a product's tiles of
+// so many us on `slots` places for a work-group: where the idle ones get
+// through them in that time.  (A launch of its own moves them faster, eight
+// work-groups a compute unit, but nothing else runs meanwhile.  Along,
+// 1003 x 2048 x 1407 in fp16 takes 33.5 us forward instead of 42.0 and
+// 128 x 2048 x 5461 91.4 us backward instead of 99.3; with copies counted at
+// 0.3 us, where there are few idle places for many, 128 x 2048 x 5461 takes
+// 53.3 us forward instead of 42.2.)
+bool goes_along(int64_t copies, int64_t tiles, int64_t slots, double us) {
+  return copies > 0 && tiles < slots && (double)copies * kCopyUs <= (double)(slots - tiles) * us;
 }
 
 // y's tile and splits: few rows against a long contraction leave most compute
@@ -187,10 +204,14 @@ MlpPlan mlp_plan_of(int64_t n, int64_t d, int64_t f, bool aligned, bool backward
         p.Gs = c.take<char>(f * p.dk * p.es);
         p.Us = c.take<char>(f * p.dk * p.es);
       }
-      if (p.stage_f) p.Ds = c.take<char>(d * p.fk * p.es);
+      if (p.stage_f) {
+        p.Ds = c.take<char>(d * p.fk * p.es);
+        p.side = goes_along(tiles_of(d, 64) * tiles_of(p.fk, 64), tiles_of(n, up.shape.m) * tiles_of(f, up.shape.n / 2),
+                            kXentGroups, (double)p.dk / p.bk * up.ktile + up.fixed);
+      }
       if (p.splits > 1) p.parts = c.take<float>(p.splits * round_to(n, p.tm) * round_to(d, p.tn));
     }
-    p.h = c.take<char>(p.h_rows * p.h_ld * p.es);
+    p.h = c.take<char>(p.h_rows * p.h_ld * (p.dot ? 4 : p.es));
   } else {
     const TileCost& dz = best_tile(kDzCosts<T>, n, f, 1, (double)p.dk / p.bk);
     p.dz_tile = dz.tile;
@@ -201,6 +222,9 @@ MlpPlan mlp_plan_of(int64_t n, int64_t d, int64_t f, bool aligned, bool backward
     p.z_ld = skewed(2 * p.f_pad, p.bk);
     p.d_ld = skewed(p.d_pad, p.bk);
     take_choice(choose_gradients<T>(n, d, f, (double)p.n_pad / p.bk, 2.0 * p.f_pad / p.bk));
+    const int64_t d64 = p.d_pad / 64, n64 = tiles_of(p.n_pad, 64), f64 = tiles_of(p.f_pad, 64);
+    p.side = goes_along((p.stage_d ? 1 : 2) * n64 * d64 + 2 * f64 * d64, p.n_pad / dz.shape.m * (p.f_pad / dz.shape.n),
+                        2 * kXentGroups, (double)p.dk / p.bk * dz.alone + dz.fixed);
     if (p.stage_d) p.Ys = c.take<char>(n * p.dk * p.es);
     p.dz = c.take<char>(p.n_pad * p.z_ld * p.es);
     p.dzt = c.take<char>(2 * p.f_pad * p.t_ld * p.es);
@@ -234,16 +258,15 @@ int describe_mlp(const MlpPlan& p, ns_dtype dtype, bool backward, char* buf, siz
   }
   char split[32] = "";
   if (p.splits > 1) snprintf(split, sizeof split, " join<%s> splits=%d", op, p.splits);
-  const char* prep = backward || p.stage_d || p.stage_f ? "prep" : "";
   char first[32] = "";
-  if (*prep) snprintf(first, sizeof first, "prep<%s> ", op);
+  if (backward || p.stage_d || (p.stage_f && !p.side)) snprintf(first, sizeof first, "prep<%s> ", op);
   const bool half = p.es == 2;
   const TileShape up = half ? up_shape<_Float16>(p.up_tile) : up_shape<float>(p.up_tile);
   const TileShape dz = half ? dz_shape<_Float16>(p.dz_tile) : dz_shape<float>(p.dz_tile);
   const char* name = backward ? "dz" : "up";
   const TileShape& shape = backward ? dz : up;
-  return snprintf(buf, len, "%s%s<%s,%dx%d> products<%s,%dx%d>%s", first, name, op, shape.m, shape.n / (backward ? 1 : 2), op,
-                  (int)p.tm, (int)p.tn, split);
+  return snprintf(buf, len, "%s%s<%s,%dx%d%s> products<%s,%dx%d>%s", first, name, op, shape.m, shape.n / (backward ? 1 : 2),
+                  p.side ? ",copies" : "", op, (int)p.tm, (int)p.tn, split);
 }
 
 // The products' copies take 16-byte chunks, swizzled by bits 4 to 6 of the
@@ -273,8 +296,7 @@ XentCopyArgs mlp_copy(const void* src, int64_t ld, int64_t rows, int64_t cols, c
 
 template <typename T>
 ns_status mlp_prep(const MlpPrepArgs& a, hipStream_t st) {
-  int64_t blocks = 0;
-  for (const XentCopyArgs& c : a.copy) blocks += c.blocks();
+  const int64_t blocks = a.blocks();
   if (blocks == 0) return NS_OK;
   if (blocks >= int64_t(1) << 31) return NS_ERR_INVALID_ARG;
   hipLaunchKernelGGL((k_mlp_prep<T>), dim3((unsigned)blocks), dim3(256), 0, st, a);
@@ -301,20 +323,21 @@ ns_status mlp_forward(const MlpPlan& p, const MlpIn& in, int act, void* Y, int64
   const int32_t bits = (int32_t)(NS_ERR_NONFINITE | NS_STATUS_AT_OUTPUT);
   constexpr int64_t es = sizeof(T);
   if (p.dot) {
-    const MlpDotUpArgs a{in.X, in.G, in.U, in.ldx, in.ldg, in.ldu, p.n,      p.f, (int)p.d, p.h,
+    float* h = reinterpret_cast<float*>(p.h);
+    const MlpDotUpArgs a{in.X, in.G, in.U, in.ldx, in.ldg, in.ldu, p.n, p.f, (int)p.d, h,
                          p.h_ld, gate, up, lds,    save32, act,    d_status, bits};
     if (launch_mlp_dot_up<T>(a, st) != hipSuccess) return NS_ERR_HIP;
-    const MlpDotDownArgs b{p.h, in.D, p.h_ld, in.ldd, p.n, p.d, (int)p.f, Y, ldy, d_status, bits};
+    const MlpDotDownArgs b{h, in.D, p.h_ld, in.ldd, p.n, p.d, (int)p.f, Y, ldy, d_status, bits};
     return launch_mlp_dot_down<T>(b, st) == hipSuccess ? NS_OK : NS_ERR_HIP;
   }
   MlpPrepArgs prep{};
   prep.copy[0] = mlp_copy(in.X, in.ldx, p.n, p.d, p.Xs, p.dk, nullptr, 0, 0, 0);
   prep.copy[1] = mlp_copy(in.G, in.ldg, p.f, p.d, p.Gs, p.dk, nullptr, 0, 0, 0);
   prep.copy[2] = mlp_copy(in.U, in.ldu, p.f, p.d, p.Us, p.dk, nullptr, 0, 0, 0);
-  prep.copy[3] = mlp_copy(in.D, in.ldd, p.d, p.f, p.Ds, p.fk, nullptr, 0, 0, 0);
+  MlpUpArgs a{};
+  (p.side ? a.side : prep).copy[3] = mlp_copy(in.D, in.ldd, p.d, p.f, p.Ds, p.fk, nullptr, 0, 0, 0);
   ns_status s = mlp_prep<T>(prep, st);
   if (s != NS_OK) return s;
-  MlpUpArgs a{};
   a.X = p.stage_d ? p.Xs : in.X;
   a.G = p.stage_d ? p.Gs : in.G;
   a.U = p.stage_d ? p.Us : in.U;
@@ -362,18 +385,19 @@ ns_status mlp_backward(const MlpPlan& p, const MlpIn& in, const void* dY, int64_
   constexpr int64_t es = sizeof(T);
   const bool dw = out.dG || out.dU || out.dD;
   MlpPrepArgs prep{};
-  prep.copy[0] = mlp_copy(dY, lddy, p.n, p.d, p.Ys, p.dk, dw ? p.YT : nullptr, p.n_pad, p.d_pad, p.t_ld);
+  MlpDzArgs a{};
+  MlpPrepArgs& side = p.side ? a.side : prep;
+  (p.stage_d ? prep : side).copy[0] = mlp_copy(dY, lddy, p.n, p.d, p.Ys, p.dk, dw ? p.YT : nullptr, p.n_pad, p.d_pad, p.t_ld);
   prep.copy[1] = mlp_copy(in.D, in.ldd, p.d, p.f, nullptr, 0, p.DT, p.d_pad, p.f_pad, p.d_ld);
-  if (dw) prep.copy[2] = mlp_copy(in.X, in.ldx, p.n, p.d, nullptr, 0, p.XT, p.n_pad, p.d_pad, p.t_ld);
+  if (dw) side.copy[2] = mlp_copy(in.X, in.ldx, p.n, p.d, nullptr, 0, p.XT, p.n_pad, p.d_pad, p.t_ld);
   if (out.dX) {
-    prep.copy[3] = mlp_copy(in.G, in.ldg, p.f, p.d, nullptr, 0, p.WT, p.f_pad, p.d_pad, p.z_ld);
-    prep.copy[4] = mlp_copy(in.U, in.ldu, p.f, p.d, nullptr, 0, p.WT + p.f_pad * es, p.f_pad, p.d_pad, p.z_ld);
+    side.copy[3] = mlp_copy(in.G, in.ldg, p.f, p.d, nullptr, 0, p.WT, p.f_pad, p.d_pad, p.z_ld);
+    side.copy[4] = mlp_copy(in.U, in.ldu, p.f, p.d, nullptr, 0, p.WT + p.f_pad * es, p.f_pad, p.d_pad, p.z_ld);
   }
   ns_status s = mlp_prep<T>(prep, st);
   if (s != NS_OK) return s;
   // The gradients' tiles are square.
   const int64_t tm = tiles_of(p.n, p.tm), td = tiles_of(p.d, p.tm), tf = tiles_of(p.f, p.tm);
-  MlpDzArgs a{};
   a.dY = p.stage_d ? p.Ys : dY;
   a.WT = p.DT;
   a.ldy = (p.stage_d ? p.dk : lddy) * es;
@@ -457,8 +481,11 @@ ns_status ns_gated_mlp(const void* X, int64_t ldx, const void* Wg, int64_t ldwg,
   if (!known(dtype) || !(save_dtype == dtype || save_dtype == NS_FP32)) return NS_ERR_UNSUPPORTED_DTYPE;
   if (rows == 0) return NS_OK;
   if (!X || !Wg || !Wu || !Wd || !Y || !gate != !up) return NS_ERR_INVALID_ARG;
-  const bool aligned = operand_aligned(X, ldx, dtype) && operand_aligned(Wg, ldwg, dtype) &&
-                       operand_aligned(Wu, ldwu, dtype) && operand_aligned(Wd, ldwd, dtype) && ldwg == ldwu;
+  // An operand whose rows are no whole k-tiles is copied wherever it starts.
+  const int64_t bk = kRowBytes / bytes_of(dtype);
+  const bool aligned = (cols % bk || (operand_aligned(X, ldx, dtype) && operand_aligned(Wg, ldwg, dtype) &&
+                                      operand_aligned(Wu, ldwu, dtype) && ldwg == ldwu)) &&
+                       (inner % bk || operand_aligned(Wd, ldwd, dtype));
   const MlpPlan p = mlp_plan(rows, cols, inner, dtype, aligned, false, workspace);
   if (!workspace_ok(workspace, workspace_bytes, p.total)) return NS_ERR_WORKSPACE;
   const MlpIn in{X, Wg, Wu, Wd, ldx, ldwg, ldwu, ldwd};

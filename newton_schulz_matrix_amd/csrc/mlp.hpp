@@ -75,23 +75,33 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 }
 
 // ---------------------------------------------------------------------------
-// Copies of operands, padded or transposed, all in one launch (xent.hpp's
-// 64 x 64 tiles).
+// Copies of operands, padded or transposed, in 64 x 64 tiles (xent.hpp): all
+// in one launch, or those that the projections' (dh's) tiles do not read
+// beside these, where they leave compute units idle.
 // ---------------------------------------------------------------------------
 constexpr int kMlpCopies = 5;
 struct MlpPrepArgs {
   XentCopyArgs copy[kMlpCopies];
+  __host__ __device__ int64_t blocks() const {
+    int64_t n = 0;
+    for (const XentCopyArgs& c : copy) n += c.blocks();
+    return n;
+  }
 };
 template <typename T>
-__global__ void __launch_bounds__(256) k_mlp_prep(MlpPrepArgs p) {
-  int64_t b = blockIdx.x;
+__device__ __forceinline__ void mlp_copy_block(const MlpPrepArgs& p, int64_t b, T* tile) {
 #pragma unroll
   for (int i = 0; i < kMlpCopies; ++i) {
     const int64_t blocks = p.copy[i].blocks();
     if (b >= 0 && b < blocks)
-      xent_copy_tile<T>(p.copy[i], XentRowArgs{}, (int)(b / p.copy[i].tiles_c), (int)(b % p.copy[i].tiles_c));
+      xent_copy_tile<T>(p.copy[i], XentRowArgs{}, (int)(b / p.copy[i].tiles_c), (int)(b % p.copy[i].tiles_c), tile);
     b -= blocks;
   }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) k_mlp_prep(MlpPrepArgs p) {
+  __shared__ __attribute__((aligned(16))) T tile[kCopyTile<T>];
+  mlp_copy_block<T>(p, blockIdx.x, tile);
 }
 
 // ---------------------------------------------------------------------------
@@ -181,6 +191,7 @@ struct MlpUpArgs {
   int act;
   int32_t* d_status;
   int32_t status_bits;
+  MlpPrepArgs side;        // copies that go along
 };
 
 // Leaves one wave's a and b for the backward pass; returns whether any is not
@@ -268,7 +279,17 @@ struct UpEpilogue {
 
 template <typename T, int TM, int TN>
 __global__ void __launch_bounds__(kThreads, 1) k_mlp_up(MlpUpArgs p) {
-  const TileRun run(p.tiles_m * p.tiles_n);
+  const int tiles = p.tiles_m * p.tiles_n;
+  if ((int)blockIdx.x >= tiles) {
+    // A work-group beyond the tiles (mlp_up_of).
+    const int64_t blocks = p.side.blocks();
+    for (int64_t b = blockIdx.x - tiles; b < blocks; b += gridDim.x - tiles) {
+      mlp_copy_block<T>(p.side, b, reinterpret_cast<T*>(Stages<TM, TN>::s0()));
+      __syncthreads();
+    }
+    return;
+  }
+  const TileRun run(tiles, (int)gridDim.x < tiles ? (int)gridDim.x : tiles);
   // Wave w copies TN / 4 right-hand rows of a tile: even waves rows of Wg,
   // odd ones rows of Wu, for the columns of the waves w / 2 and w / 2 + 2.
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -376,6 +397,7 @@ struct MlpDzArgs {
   void* ht;                // f_pad x n_pad, row stride t_ld
   int64_t f_pad, z_ld, t_ld;
   int act;
+  MlpPrepArgs side;        // copies that go along
 };
 
 // Four columns of a caller's row as floats, at any alignment.
@@ -467,8 +489,11 @@ struct MlpDzEpilogue {
 
 template <typename T, int TM, int TN>
 __global__ void __launch_bounds__(kThreads, 2) k_mlp_dz(MlpDzArgs p) {
+  const int tiles = p.tiles_m * p.tiles_n;
+  if ((int)blockIdx.x >= tiles)
+    return mlp_copy_block<T>(p.side, blockIdx.x - tiles, reinterpret_cast<T*>(Stages<TM, TN, 2>::s0()));
   int tm, tn;
-  grouped_tile(xcd_order(blockIdx.x, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, tm, tn);
+  grouped_tile(xcd_order(blockIdx.x, tiles), p.tiles_m, p.tiles_n, tm, tn);
   const int64_t row0 = (int64_t)tm * TM;
   const StreamTile tile{reinterpret_cast<const char*>(p.dY) + row0 * p.ldy,
                         reinterpret_cast<const char*>(p.WT) + (int64_t)tn * TN * p.ldw,
@@ -676,7 +701,7 @@ struct MlpDotUpArgs {
   const void *X, *G, *U;
   int64_t ldx, ldg, ldu, n, f;  // elements
   int d;
-  void* h;                      // n x ldh
+  float* h;                     // n x ldh, not rounded: it costs nothing here
   int64_t ldh;
   void *gate, *up;              // n x f, row stride lds, or null
   int64_t lds;
@@ -686,9 +711,25 @@ struct MlpDotUpArgs {
   int32_t status_bits;
 };
 
-// acc[r][i] = the wave's share of w[r] . x[i] over columns c0, c0 + step, ...
-template <typename T, int R, int N, int FORM>
-__device__ __forceinline__ void dot_rows(const T* const (&w)[R], const T* x, int64_t ldx, int n, int cols, int first,
+// A vector's worth of T's of an fp32 row.
+template <int FORM, typename T>
+__device__ __forceinline__ void load_floats(const float* row, int c, int cols, float (&v)[kVec<T>]) {
+  u32x4_t raw[kVec<T> / 4];
+#pragma unroll
+  for (int q = 0; q < kVec<T> / 4; ++q) raw[q] = issue16<FORM, float>(row, c + 4 * q, cols);
+#pragma unroll
+  for (int q = 0; q < kVec<T> / 4; ++q) {
+    float part[4];
+    unpack<float>(settle16<FORM, float>(raw[q], row, c + 4 * q, cols), part);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[4 * q + k] = part[k];
+  }
+}
+
+// acc[r][i] = the wave's share of w[r] . x[i] over columns c0, c0 + step, ...;
+// X is T or float.
+template <typename T, int R, int N, int FORM, typename X>
+__device__ __forceinline__ void dot_rows(const T* const (&w)[R], const X* x, int64_t ldx, int n, int cols, int first,
                                          int step, float (&acc)[R][N]) {
   constexpr int V = kVec<T>;
   const int lane = threadIdx.x & 63;
@@ -706,8 +747,11 @@ __device__ __forceinline__ void dot_rows(const T* const (&w)[R], const T* x, int
     float h[N][V];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const T* row = x + (i < n ? i : 0) * ldx;
-      unpack<T>(settle16<FORM, T>(issue16<FORM, T>(row, c, cols), row, c, cols), h[i]);
+      const X* row = x + (i < n ? i : 0) * ldx;
+      if constexpr (std::is_same_v<X, T>)
+        unpack<T>(settle16<FORM, T>(issue16<FORM, T>(row, c, cols), row, c, cols), h[i]);
+      else
+        load_floats<FORM, T>(row, c, cols, h[i]);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -754,7 +798,7 @@ __global__ void __launch_bounds__(256) k_mlp_dot_up(MlpDotUpArgs p) {
   if (lane < C * N && row < p.n && c < p.f) {
     float h = 0.f;
     with_act(p.act, [&](auto act) { h = Act<decltype(act)::value>(a).value * b; });
-    reinterpret_cast<T*>(p.h)[row * p.ldh + c] = from_f32<T>(h);
+    p.h[row * p.ldh + c] = h;
     if (p.gate) {
       auto save = [&](auto s) {
         using S = decltype(s);
@@ -772,7 +816,8 @@ __global__ void __launch_bounds__(256) k_mlp_dot_up(MlpDotUpArgs p) {
 }
 
 struct MlpDotDownArgs {
-  const void *h, *W;
+  const float* h;
+  const void* W;
   int64_t ldh, ldw, n, d;  // elements
   int f;
   void* y;
@@ -793,7 +838,7 @@ __global__ void __launch_bounds__(256) k_mlp_dot_down(MlpDotDownArgs p) {
 #pragma unroll
   for (int r = 0; r < R; ++r) w[r] = reinterpret_cast<const T*>(p.W) + (c0 + r < p.d ? c0 + r : p.d - 1) * p.ldw;
   float acc[R][N];
-  dot_rows<T, R, N, FORM>(w, reinterpret_cast<const T*>(p.h), p.ldh, (int)p.n, p.f, wave * 64 * V, 4 * 64 * V, acc);
+  dot_rows<T, R, N, FORM>(w, p.h, p.ldh, (int)p.n, p.f, wave * 64 * V, 4 * 64 * V, acc);
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -855,7 +900,9 @@ template <typename T> hipError_t launch_mlp_dot_down(const MlpDotDownArgs& a, hi
   hipLaunchKernelGGL((K<T, SHAPE<T>(TILE).m, SHAPE<T>(TILE).n>), GRID, dim3(kThreads), 0, s, a)
 template <typename T>
 hipError_t mlp_up_of(const MlpUpArgs& a, int tile, hipStream_t s) {
-  const dim3 grid = xent_grid((int64_t)a.tiles_m * a.tiles_n);
+  // With copies the tiles are fewer than the compute units; the others take
+  // the copies.
+  const dim3 grid = a.side.blocks() > 0 ? dim3(kXentGroups) : xent_grid((int64_t)a.tiles_m * a.tiles_n);
   if (tile == kTileLarge)
     NS_MLP_TILE(k_mlp_up, up_shape, kTileLarge, grid);
   else if (tile == kTileSmall || sizeof(T) == 4)
@@ -866,7 +913,7 @@ hipError_t mlp_up_of(const MlpUpArgs& a, int tile, hipStream_t s) {
 }
 template <typename T>
 hipError_t mlp_dz_of(const MlpDzArgs& a, int tile, hipStream_t s) {
-  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n));
+  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n + a.side.blocks()));
   if (tile == kTileLarge)
     NS_MLP_TILE(k_mlp_dz, dz_shape, kTileLarge, grid);
   else

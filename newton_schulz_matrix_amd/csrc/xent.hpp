@@ -131,10 +131,11 @@ __device__ __forceinline__ void xent_rows_block(const XentRowArgs& p, int block)
 // of H, which may hold anything (padding positions): the transposed H has
 // zeros there.
 template <typename T>
-__device__ __forceinline__ void xent_copy_tile(const XentCopyArgs& p, const XentRowArgs& rows, int tr, int tc) {
+constexpr int kCopyTile = 64 * (64 + kVec<T>);  // elements of LDS that a tile takes, 16-byte aligned
+template <typename T>
+__device__ __forceinline__ void xent_copy_tile(const XentCopyArgs& p, const XentRowArgs& rows, int tr, int tc, T* tile) {
   constexpr int V = kVec<T>, C = 64 / V;  // vectors per tile row
   constexpr int kStride = 64 + V;
-  __shared__ __attribute__((aligned(16))) T tile[64 * kStride];
   const int64_t r0 = (int64_t)tr * 64;
   const int c0 = tc * 64;
   typedef typename Vec16<sizeof(T)>::type vec_t;
@@ -197,7 +198,8 @@ __global__ void __launch_bounds__(256) k_xent_prep(XentPrepArgs p) {
   b -= p.row_blocks;
   const XentCopyArgs& c = b < p.h.blocks() ? p.h : p.w;
   if (b >= p.h.blocks()) b -= p.h.blocks();
-  xent_copy_tile<T>(c, p.rows, (int)(b / c.tiles_c), (int)(b % c.tiles_c));
+  __shared__ __attribute__((aligned(16))) T tile[kCopyTile<T>];
+  xent_copy_tile<T>(c, p.rows, (int)(b / c.tiles_c), (int)(b % c.tiles_c), tile);
 }
 
 // rows x cols zeros (dW when there is no row).
@@ -231,15 +233,16 @@ struct XentArgs {
   int64_t ldz;
 };
 
-// The tiles of one work-group of a persistent grid: every gridDim.x-th of the
-// list, offset so that work-groups of one XCD run neighbours.
+// The tiles of one of the first `groups` work-groups of a persistent grid:
+// every groups-th of the list, offset so that work-groups of one XCD run
+// neighbours.
 struct TileRun {
-  int first, count;
-  __device__ __forceinline__ explicit TileRun(int total) {
-    first = xcd_order(blockIdx.x, gridDim.x);
-    count = first < total ? (total - first + (int)gridDim.x - 1) / (int)gridDim.x : 0;
+  int groups, first, count;
+  __device__ __forceinline__ explicit TileRun(int total, int groups = (int)gridDim.x) : groups(groups) {
+    first = xcd_order(blockIdx.x, groups);
+    count = first < total ? (total - first + groups - 1) / groups : 0;
   }
-  __device__ __forceinline__ int at(int j) const { return first + j * (int)gridDim.x; }
+  __device__ __forceinline__ int at(int j) const { return first + j * groups; }
 };
 
 // The logits' tiles, for the forward pass and for dz.

@@ -20,5 +20,8 @@ MLP_CASES = [
     # than the three LDS stages hold.
     (1003, 520, 1407, ALL), (1500, 264, 3001, HALF), (5000, 776, 264, HALF), (5000, 1000, 2800, ("bf16",)),
     (4000, 200, 3001, ("fp32",)), (4000, 776, 264, ("fp32",)), (1500, 64, 3001, ("fp32",)),
+    # Copies in a launch of their own, as the tiles leave too few compute
+    # units to them.
+    (513, 1, 14336, HALF), (513, 1, 2048, HALF), (1003, 1, 14336, ("fp16",)), (8192, 1, 1407, ("fp32",)),
 ]
 MLP_RUNS = [(n, d, f, t) for n, d, f, types in MLP_CASES for t in types]
