@@ -51,6 +51,16 @@ bool tensor_of(PyObject* o, at::Tensor& t, const char* name) {
   return true;
 }
 
+// The same without a reference of its own, for lists of many tensors whose
+// sequence holds them.
+const at::Tensor* borrowed(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) {
+    fail(PyExc_TypeError, std::string(name) + " must be a tensor");
+    return nullptr;
+  }
+  return &THPVariable_Unpack(o);
+}
+
 // A Python sequence, held.
 struct Sequence {
   PyObject* fast = nullptr;
@@ -115,12 +125,12 @@ PyObject* adamw_table(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   ns_adamw_tensor* table = reinterpret_cast<ns_adamw_tensor*>(PyBytes_AS_STRING(out));
   std::vector<const void*> written;
   written.reserve(5 * count);
-  at::Tensor p, g, m, v, s, c;
   at::Device device(at::kCPU);
   for (Py_ssize_t i = 0; i < count; ++i) {
-    if (!tensor_of(params.at(i), p, "params") || !tensor_of(grads.at(i), g, "grads") || !tensor_of(ms.at(i), m, "m") ||
-        !tensor_of(vs.at(i), v, "v"))
-      return nullptr;
+    const at::Tensor *pp = borrowed(params.at(i), "params"), *gp = pp ? borrowed(grads.at(i), "grads") : nullptr,
+                     *mp = gp ? borrowed(ms.at(i), "m") : nullptr, *vp = mp ? borrowed(vs.at(i), "v") : nullptr;
+    if (!vp) return nullptr;
+    const at::Tensor &p = *pp, &g = *gp, &m = *mp, &v = *vp;
     if (i == 0) device = p.device();
     const at::Tensor* all[] = {&p, &g, &m, &v};
     for (const at::Tensor* t : all) {
@@ -144,19 +154,21 @@ PyObject* adamw_table(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     if ((so != Py_None) != coded)
       return fail(PyExc_ValueError, "scales go with float8_e4m3fn moments, one tensor each");
     if (coded) {
-      if (!tensor_of(so, s, "scales")) return nullptr;
-      if (s.scalar_type() != at::kFloat || s.numel() != 2 * ((n + kStateBlock - 1) / kStateBlock) ||
-          s.device() != device || !s.is_contiguous())
+      const at::Tensor* s = borrowed(so, "scales");
+      if (!s) return nullptr;
+      if (s->scalar_type() != at::kFloat || s->numel() != 2 * ((n + kStateBlock - 1) / kStateBlock) ||
+          s->device() != device || !s->is_contiguous())
         return fail(PyExc_ValueError, "scales must be contiguous float32 tensors [2, ceil(numel / 256)] on the device");
-      e.scales = static_cast<float*>(s.data_ptr());
+      e.scales = static_cast<float*>(s->data_ptr());
     }
     PyObject* co = args[5] == Py_None ? Py_None : copies.at(i);
     if (co != Py_None) {
-      if (!tensor_of(co, c, "copies")) return nullptr;
-      const int ct = dtype_of(c);
-      if (ct < 0 || c.sizes() != p.sizes() || c.device() != device || !c.is_contiguous())
+      const at::Tensor* c = borrowed(co, "copies");
+      if (!c) return nullptr;
+      const int ct = dtype_of(*c);
+      if (ct < 0 || c->sizes() != p.sizes() || c->device() != device || !c->is_contiguous())
         return fail(PyExc_ValueError, "copies must be contiguous bf16, fp16 or fp32 tensors of their parameter's shape");
-      e.copy = c.data_ptr();
+      e.copy = c->data_ptr();
       e.copy_dtype = (ns_dtype)ct;
     }
     e.param = p.data_ptr();

@@ -64,6 +64,8 @@ ns_status ns_adamw_step(const ns_adamw_tensor* tensors, int64_t count, double be
       if (t.numel == 0) continue;
       const int64_t more = (t.numel + kAdamwChunk - 1) / kAdamwChunk;
       if (chunks + more >= int64_t(1) << 31 && a.count > 0) break;
+      a.types[a.count] = (int32_t)t.param_dtype | (int32_t)t.grad_dtype << 4 | (t.copy ? (int32_t)t.copy_dtype : 0) << 8;
+      a.first[a.count] = (int32_t)chunks;
       AdamwItem& o = a.item[a.count++];
       o.p = t.param;
       o.g = t.grad;
@@ -74,8 +76,6 @@ ns_status ns_adamw_step(const ns_adamw_tensor* tensors, int64_t count, double be
       o.n = t.numel;
       o.lr = t.lr;
       o.decay = t.weight_decay;
-      o.types = (int32_t)t.param_dtype | (int32_t)t.grad_dtype << 4 | (t.copy ? (int32_t)t.copy_dtype : 0) << 8;
-      o.first = (int32_t)chunks;
       chunks += more;
     }
     if (a.count == 0) break;
