@@ -604,7 +604,8 @@ ns_status ns_adamw_step(const ns_adamw_tensor* tensors, int64_t count,
  *   branch_weight, weight   cols elements, or NULL (ones).  Gate and weights
  *            have param_dtype (dtype or NS_FP32).
  *   S, Y     rows x cols, row strides lds and ldy; Y may be NULL (no second
- *            norm).  S may be X and Y may be Z, with equal strides.
+ *            norm).  S may be X and Y may be Z, with equal strides; S and Y
+ *            may not be the same.
  *   branch_rstd, rstd   rows floats each, for the backward pass; either may
  *            be NULL.
  *   rows < 2^31, 1 <= cols <= 2^24; eps >= 0 and finite; scale finite.
@@ -634,8 +635,8 @@ ns_status ns_residual_norm(const void* X, int64_t ldx, const void* Z,
  *   Z, branch_rstd   as given to and written by ns_residual_norm;
  *            branch_rstd NULL if the block's output was not normed.
  *   dX may be NULL; dgate, dbranch_weight and dweight (param_dtype) too.
- *   dX may be dS and dZ may be dY, with equal strides.  With no rows the
- *   parameters' gradients are zeros.
+ *   dX may be dS and dZ may be dY, with equal strides; dX and dZ may not be
+ *   the same.  With no rows the parameters' gradients are zeros.
  *   workspace   ns_residual_norm_workspace_size(rows, cols) bytes, 256-byte
  *            aligned.
  */
@@ -695,7 +696,8 @@ ns_status ns_gated_mlp(const void* X, int64_t ldx, const void* Wg,
  *     dX = da Wg + db Wu,  dWg = da^T X,  dWu = db^T X,  dWd = dY^T h
  *   gate, up   a and b as written by ns_gated_mlp, in save_dtype; h is made
  *            of them again.
- *   dX, dWg, dWu, dWd   any may be NULL.
+ *   dX, dWg, dWu, dWd   any may be NULL; no two may be the same.  dX may be
+ *            dY or X.
  *   workspace   ns_gated_mlp_workspace_size(rows, cols, inner, dtype,
  *            aligned, 1) bytes; aligned is 1 when dY starts on a 16-byte
  *            boundary and its row stride is a multiple of 128 bytes.

@@ -298,7 +298,7 @@ template <typename T>
 ns_status mlp_prep(const MlpPrepArgs& a, hipStream_t st) {
   const int64_t blocks = a.blocks();
   if (blocks == 0) return NS_OK;
-  if (blocks >= int64_t(1) << 31) return NS_ERR_INVALID_ARG;
+  if (blocks >= int64_t(1) << 24) return NS_ERR_INVALID_ARG;  // a launch may not have 2^32 threads
   hipLaunchKernelGGL((k_mlp_prep<T>), dim3((unsigned)blocks), dim3(256), 0, st, a);
   return launched();
 }
@@ -488,6 +488,7 @@ ns_status ns_gated_mlp(const void* X, int64_t ldx, const void* Wg, int64_t ldwg,
                        (inner % bk || operand_aligned(Wd, ldwd, dtype));
   const MlpPlan p = mlp_plan(rows, cols, inner, dtype, aligned, false, workspace);
   if (!workspace_ok(workspace, workspace_bytes, p.total)) return NS_ERR_WORKSPACE;
+  if (gate && gate == up) return NS_ERR_INVALID_ARG;
   const MlpIn in{X, Wg, Wu, Wd, ldx, ldwg, ldwu, ldwd};
   return with_type(dtype, [&](auto io) {
     return mlp_forward<decltype(io)>(p, in, (int)activation, Y, ldy, gate, up, ldg,
@@ -527,6 +528,10 @@ ns_status ns_gated_mlp_backward(const void* dY, int64_t lddy, const void* X, int
   const MlpPlan p = mlp_plan(rows, cols, inner, dtype, operand_aligned(dY, lddy, dtype), true, workspace);
   if (!workspace_ok(workspace, workspace_bytes, p.total)) return NS_ERR_WORKSPACE;
   if (!dX && !dWg && !dWu && !dWd) return NS_OK;
+  const void* outs[] = {dX, dWg, dWu, dWd};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (outs[i] && outs[i] == outs[j]) return NS_ERR_INVALID_ARG;
   const MlpIn in{X, Wg, Wu, Wd, ldx, ldwg, ldwu, ldwd};
   const MlpOut out{dX, dWg, dWu, dWd, lddx, lddwg, lddwu, lddwd};
   return with_type(dtype, [&](auto io) {

@@ -100,8 +100,7 @@ struct ResNormBwdRun {
 
 bool resnorm_shape_ok(int64_t rows, int64_t cols, int64_t groups) {
   if (!(rows >= 0 && rows < (int64_t(1) << 31) && cols >= 1 && cols <= kMaxResNormCols)) return false;
-  // Without rows the gate's gradient is zeros, by a block for each 32 columns.
-  if (rows == 0) return groups >= 0 && groups < (int64_t(1) << 30) / ((cols + 31) / 32) - 2;
+  if (rows == 0) return groups >= 0 && groups < (int64_t(1) << 31);  // zeros for the gate's gradient
   return groups == 0 || (groups > 0 && groups <= rows && rows % groups == 0);
 }
 
@@ -138,7 +137,7 @@ ns_status ns_residual_norm(const void* X, int64_t ldx, const void* Z, int64_t ld
   if (rows == 0) return NS_OK;
   // Without a block's output there is only the second norm.
   if (!Z && (gate || branch_weight || S || scale != 1.f || !Y)) return NS_ERR_INVALID_ARG;
-  if (!X || (Z && !S)) return NS_ERR_INVALID_ARG;
+  if (!X || (Z && !S) || (S && S == Y)) return NS_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   ResNormFwdArgs a{};
   a.X = X;
@@ -201,6 +200,7 @@ ns_status ns_residual_norm_backward(const void* dS, int64_t ldds, const void* dY
     return NS_OK;
   }
   if (!workspace_ok(workspace, workspace_bytes, ns_residual_norm_workspace_size(rows, cols))) return NS_ERR_WORKSPACE;
+  if (rows > 0 && dX && dX == dZ) return NS_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   ResNormBwdArgs a{};
   a.dS = dS;
@@ -261,10 +261,11 @@ ns_status ns_residual_norm_backward(const void* dS, int64_t ldds, const void* dY
     // unless the caller says so.
     const bool join_gate = a.want_gate && (rows == 0 || cut.split > 1);
     if (dweight || dbranch_weight || join_gate) {
-      const ResNormJoinArgs j{a.partial, (int)cut.blocks, rows > 0 ? cut.split : 0, (int)cols, dweight, dbranch_weight,
-                              join_gate ? dgate : nullptr, d_status, a.status_bits};
       const int64_t outputs = 2 + (join_gate ? groups : 0);
-      hipLaunchKernelGGL((k_resnorm_join<PT>), dim3((unsigned)((cols + 31) / 32 * outputs)), dim3(1024), 0, st, j);
+      const ResNormJoinArgs j{a.partial, (int)cut.blocks, rows > 0 ? cut.split : 0, (int)cols, outputs, dweight,
+                              dbranch_weight, join_gate ? dgate : nullptr, d_status, a.status_bits};
+      hipLaunchKernelGGL((k_resnorm_join<PT>),
+                         dim3((unsigned)((cols + 31) / 32), (unsigned)std::min<int64_t>(outputs, 4096)), dim3(1024), 0, st, j);
     }
     return launched();
   });

@@ -277,3 +277,16 @@ def test_block_calls_refuse_host_tensors():
                  lambda: nsa.residual_norm(x, x), lambda: nsa.residual_norm_backward(x, None, x)):
         with pytest.raises(ValueError, match="device tensor"):
             call()
+
+
+@built
+def test_results_in_one_place_are_refused():
+    # Addresses that nothing is launched on: each call ends at the check.
+    a, b = PTR, PTR + 4096
+    assert _norm(S=a, Y=a) == INV
+    assert _norm_back(dX=b, dZ=b) == INV
+    assert _mlp(gate=a, up=a, nb=1 << 40) == INV
+    for same in (("dX", "dG"), ("dX", "dD"), ("dG", "dU"), ("dU", "dD")):
+        outs = dict(dX=a, dG=a + 256, dU=a + 512, dD=a + 768)
+        outs[same[1]] = outs[same[0]]
+        assert _mlp_back(nb=1 << 40, **outs) == INV, same

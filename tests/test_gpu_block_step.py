@@ -318,3 +318,62 @@ def test_axes_of_any_number_and_single_columns():
     assert bool(((dx.double() - want).abs() <= 8 * U32 * want.abs()).all())
     s, h, rb, r = nsa.residual_norm(x, x.clone(), weight=torch.ones(1, device=dev))
     assert s.shape == h.shape == x.shape and r.shape == (9,)
+
+
+@pytest.mark.parametrize("n,d,f", [(3, 72, 130), (60, 96, 200), (300, 128, 256)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_feed_forward_results_written_over_inputs(n, d, f, dtype):
+    dev = _dev()
+    g = torch.Generator().manual_seed(n)
+
+    def make(*shape):
+        return torch.randn(*shape, generator=g).to(dtype).to(dev)
+
+    x, dy, wg, wu, wd = make(n, d), make(n, d), make(f, d), make(f, d), make(d, f)
+    y, a, b = nsa.gated_mlp(x, wg, wu, wd)
+    over = x.clone()
+    assert nsa.gated_mlp(over, wg, wu, wd, out=over)[0] is over and torch.equal(over, y)
+    want = nsa.gated_mlp_backward(dy, x, wg, wu, wd, a, b)
+    over = [t.clone() for t in (dy, wg, wu, wd)]
+    got = nsa.gated_mlp_backward(over[0], x, *over[1:], a, b, out_dx=over[0], out_dw_gate=over[1], out_dw_up=over[2],
+                                 out_dw_down=over[3])
+    assert all(p is q for p, q in zip(got, over)) and all(torch.equal(p, q) for p, q in zip(got, want))
+    over = x.clone()
+    assert torch.equal(nsa.gated_mlp_backward(dy, over, wg, wu, wd, a, b, need_dw=False, out_dx=over)[0], want[0])
+    # One matrix in both places.
+    y, a, b = nsa.gated_mlp(x, wg, wg, wd)
+    assert torch.equal(a, b)
+
+
+def test_gates_of_many_wide_rows():
+    # 256 rows of a gate, each of 2^20 columns, are summed over 2 rows each.
+    dev = _dev()
+    rows, cols, groups = 512, 1 << 20, 256
+    g = torch.Generator(device=dev).manual_seed(4)
+
+    def make(*shape):
+        return torch.randn(*shape, device=dev, generator=g).bfloat16()
+
+    x, z, ds, dy, gate = make(rows, cols), make(rows, cols), make(rows, cols), make(rows, cols), make(groups, cols)
+    s, y, rb, rs = nsa.residual_norm(x, z, gate=gate)
+    dgate = nsa.residual_norm_backward(ds, dy, s, z, rb, rs, gate=gate)[2]
+    for i in range(0, groups, 32):
+        c = slice(2 * i, 2 * i + 64)
+        r64, shat = rs[c].double()[:, None], s[c].double() * rs[c].double()[:, None]
+        u = dy[c].double()
+        top = ds[c].double() + r64 * (u - shat * (u * shat).mean(1, keepdim=True))
+        bhat = z[c].double() * rb[c].double()[:, None]
+        want = (top * bhat).view(32, 2, cols).sum(1)
+        size = ((top.abs() + 1) * bhat.abs()).view(32, 2, cols).sum(1)
+        # Rounded once to bf16; top to its mean, a sum of 2^20 terms taken by
+        # 1024 threads, of 1024 steps and 20 more.
+        assert bool(((dgate[i:i + 32].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1056 * U32 * size).all())
+
+
+def test_a_large_gate_without_rows():
+    dev = _dev()
+    gate = torch.ones(5000, 65536, dtype=torch.bfloat16, device=dev)
+    none = torch.empty(0, 65536, dtype=torch.bfloat16, device=dev)
+    r = torch.empty(0, device=dev)
+    got = nsa.residual_norm_backward(none, none, none, none, r, r, gate=gate, weight=gate[0])
+    assert got[2].shape == gate.shape and not bool(got[2].any()) and not bool(got[4].any())
