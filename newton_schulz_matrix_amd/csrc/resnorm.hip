@@ -18,6 +18,7 @@ constexpr int64_t kResNormFwdThreads = 256 * 2048;
 // and the gate's gradient: two per compute unit (16384 x 768: one 56 us, two
 // 43, four 52, for the partial rows), or the one that fits.
 constexpr int64_t kResNormParts = 512;
+constexpr int64_t kMaxJoinRows = 32768;  // of a launch's second dimension
 
 // Calls f.template run<NV, TPR>() for a row width: rows of up to 128 vectors
 // share a block, whose waves hold one or two each; wider ones have a block of
@@ -261,11 +262,14 @@ ns_status ns_residual_norm_backward(const void* dS, int64_t ldds, const void* dY
     // unless the caller says so.
     const bool join_gate = a.want_gate && (rows == 0 || cut.split > 1);
     if (dweight || dbranch_weight || join_gate) {
+      ResNormJoinArgs j{a.partial, (int)cut.blocks, rows > 0 ? cut.split : 0, (int)cols, 0, dweight, dbranch_weight,
+                        join_gate ? dgate : nullptr, d_status, a.status_bits};
+      // More than one launch only for a gate that has no rows to sum over.
       const int64_t outputs = 2 + (join_gate ? groups : 0);
-      const ResNormJoinArgs j{a.partial, (int)cut.blocks, rows > 0 ? cut.split : 0, (int)cols, outputs, dweight,
-                              dbranch_weight, join_gate ? dgate : nullptr, d_status, a.status_bits};
-      hipLaunchKernelGGL((k_resnorm_join<PT>),
-                         dim3((unsigned)((cols + 31) / 32), (unsigned)std::min<int64_t>(outputs, 4096)), dim3(1024), 0, st, j);
+      for (; j.first < outputs; j.first += kMaxJoinRows)
+        hipLaunchKernelGGL((k_resnorm_join<PT>),
+                           dim3((unsigned)((cols + 31) / 32), (unsigned)std::min(outputs - j.first, kMaxJoinRows)), dim3(1024),
+                           0, st, j);
     }
     return launched();
   });

@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(1024) k_resnorm_bwd_long(ResNormBwdArgs p) {
 struct ResNormJoinArgs {
   const float* partial;
   int blocks, split, cols;
-  int64_t outputs;         // rows: dw, dwb, those of dgate
+  int64_t first;           // the launch's first row of dw, dwb and those of dgate
   void *dw, *dwb, *dgate;  // null: not wanted
   int32_t* d_status;
   int32_t status_bits;
@@ -692,30 +692,27 @@ __global__ void __launch_bounds__(1024) k_resnorm_join(ResNormJoinArgs p) {
   __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  for (int64_t output = blockIdx.y; output < p.outputs; output += gridDim.y) {
-    const int which = output < 2 ? (int)output : 2;
-    void* out = which == 0 ? p.dw : which == 1 ? p.dwb : p.dgate;
-    if (!out) continue;
-    const int64_t group = which == 2 ? output - 2 : 0;
-    const int64_t first = group * p.split;
-    const int count = which == 2 ? p.split : p.blocks;
-    float s = 0.f;
-    if (c < p.cols) {
-      const int64_t stride = partial_stride(p.cols);
-      const float* src = p.partial + (first * 3 + which) * stride + c;
+  const int64_t output = p.first + blockIdx.y;
+  const int which = output < 2 ? (int)output : 2;
+  void* out = which == 0 ? p.dw : which == 1 ? p.dwb : p.dgate;
+  if (!out) return;
+  const int64_t group = which == 2 ? output - 2 : 0, first = group * p.split;
+  const int count = which == 2 ? p.split : p.blocks;
+  float s = 0.f;
+  if (c < p.cols) {
+    const int64_t stride = partial_stride(p.cols);
+    const float* src = p.partial + (first * 3 + which) * stride + c;
 #pragma unroll 16
-      for (int i = g; i < count; i += 32) s += src[(int64_t)i * 3 * stride];
-    }
-    sh[g][lane] = s;
-    __syncthreads();
-    if (g == 0 && c < p.cols) {
-      s = 0.f;
+    for (int i = g; i < count; i += 32) s += src[(int64_t)i * 3 * stride];
+  }
+  sh[g][lane] = s;
+  __syncthreads();
+  if (g == 0 && c < p.cols) {
+    s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s += sh[i][lane];
-      reinterpret_cast<PT*>(out)[group * p.cols + c] = from_f32<PT>(s);
-      if (p.d_status) report_status(p.d_status, p.status_bits, !(fabsf(s) < kRoundsToInf<PT>));
-    }
-    __syncthreads();
+    for (int i = 0; i < 32; ++i) s += sh[i][lane];
+    reinterpret_cast<PT*>(out)[group * p.cols + c] = from_f32<PT>(s);
+    if (p.d_status) report_status(p.d_status, p.status_bits, !(fabsf(s) < kRoundsToInf<PT>));
   }
 }
 
