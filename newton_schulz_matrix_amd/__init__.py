@@ -7,8 +7,9 @@ coefficient schedules (fitted on the host, run through the per-step
 coefficient arrays) and a whole Muon step (momentum, orthogonalization,
 weight update).  Beside it stand the operators that give the parameters Muon
 leaves out their gradients: embedding, layer norm and the output projection's
-softmax cross entropy, forward and backward.  The HIP
-library does all the work; this package only marshals arguments.
+softmax cross entropy, forward and backward; and the rest of a block's step:
+the gated feed-forward block, the norms around it, and AdamW over many tensors.
+The HIP library does all the work; this package only marshals arguments.
 """
 
 from .flops import gram_flops, ns_flops, standard_flops

@@ -5,7 +5,9 @@
 //
 // Bound by memory: every element of p, g, m and v is read once and p, m and v
 // are written once, 22 bytes an element with 16-bit p and g and fp32 moments,
-// 10 with 8-bit moments.
+// 10 with 8-bit moments.  Measured (MI355X): 38.6M fp32 masters with bf16
+// gradients and copies 214 us (5.0 TB/s), 524M bf16 parameters with 8-bit
+// moments 1120 us (4.7), as a copy of that size; 50 vectors of 768 6 us.
 //
 // The tensors come as a table in the kernel's arguments (no copy to the
 // device, no workspace), so a launch takes up to kAdamwItems of them, cut into

@@ -22,9 +22,15 @@
 // themselves: half a step per term of the sums, of the size of the result's
 // own rounding.  a and b are left for backward in fp32 (or, at half the
 // memory, rounded to the operands' type, which doubles the gradients' error:
-// 0.0035 against 0.0024 relative in bf16, results alone rounded 0.0017).
+// 0.0035 against 0.0023 relative in bf16, results alone rounded 0.0017).
 //
-// A few rows go without tiles: a wave reads whole rows of the weights.
+// A few rows go without tiles: a wave reads whole rows of the weights, and h
+// stays in fp32.
+//
+// Measured (MI355X): 8192 x 4096 x 14336 in bf16 2.43 ms forward (1190
+// TFLOP/s), 2.67 with a and b left, 5.47 backward (1055); 1003 x 2048 x 1407 in
+// fp16 33, 38 and 86 us; 300 x 1000 x 2731 in fp32 73, 74 and 130 us; one row of
+// 4096 x 14336 in bf16 65 us (5.4 TB/s), 48 rows 77.
 #pragma once
 
 #include <hip/hip_runtime.h>

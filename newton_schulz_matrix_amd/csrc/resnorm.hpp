@@ -17,6 +17,10 @@
 // NV vectors of 16 bytes of each operand.  Statistics and sums are fp32; s, y
 // and the gradients are rounded once, when stored: y comes from the stream
 // before its rounding, so it carries one rounding and not two.
+//
+// Measured (MI355X): forward 8192 x 4096 in bf16 46 us (5.8 TB/s with its inputs
+// in the cache, 55 us and 4.9 without); backward 16384 x 768 with fp32
+// parameters 38 us (4.0 TB/s) and 5 for the join, 5003 x 1001 in fp32 30 and 4.
 #pragma once
 
 #include <hip/hip_runtime.h>
