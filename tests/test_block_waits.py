@@ -13,11 +13,13 @@ from test_training_waits import HIPCC, _steps
 # And the vector stores that the streams' waits count on at a tile's border,
 # per 32 x 32 block of a wave: of h 2 in 16 bits and 4 in fp32 (for half the
 # blocks, beside twice as many of a and b, which are not counted on).  dh's
-# tiles are no stream.  Barriers and copies: at least three steps' (two for dh).
+# tiles are no stream (4 of da and db in rows, 12 of the transposed results, which
+# in its large 16-bit tile leave 32 columns of 64 rows at a time).  Barriers and
+# copies: at least three steps' (two for dh).
 KERNELS = [("k_mlp_up<__bf16, 128, 256>(MlpUpArgs)", 4 * (2 + 4), 7, 36),
            ("k_mlp_up<_Float16, 64, 128>(MlpUpArgs)", 2 + 4, 7, 18),
            ("k_mlp_up<float, 64, 128>(MlpUpArgs)", 4 + 8, 7, 18),
-           ("k_mlp_dz<_Float16, 128, 128>(MlpDzArgs)", 4 * 16, 4, 24), ("k_mlp_dz<__bf16, 64, 128>(MlpDzArgs)", 2 * 16, 4, 18),
+           ("k_mlp_dz<_Float16, 128, 128>(MlpDzArgs)", 4 * 4 + 2 * 12, 5, 24), ("k_mlp_dz<__bf16, 64, 128>(MlpDzArgs)", 2 * 16, 4, 18),
            ("k_mlp_dz<float, 64, 64>(MlpDzArgs)", 20, 4, 12),
            ("k_mlp_products<__bf16, 192, 192>(MlpGradArgs)", 0, 7, 36), ("k_mlp_products<__bf16, 64, 128>(MlpGradArgs)", 0, 7, 18)]
 
