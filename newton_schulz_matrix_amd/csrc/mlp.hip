@@ -85,7 +85,7 @@ constexpr TileCost kUpCosts<float>[3] = {{kTileLarge, up_shape<float>(kTileLarge
                                          {kTileSmall, up_shape<float>(kTileSmall), 1.06, 2.5, 0},
                                          {kTileSmall, up_shape<float>(kTileSmall), 1.06, 2.5, 0}};
 template <typename T>
-constexpr TileCost kDzCosts[2] = {{kTileLarge, dz_shape<T>(kTileLarge), 0.95, 12.0, 0.52},
+constexpr TileCost kDzCosts[2] = {{kTileLarge, dz_shape<T>(kTileLarge), 0.95, 6.0, 0.52},
                                   {kTileSmall, dz_shape<T>(kTileSmall), 0.55, 7.0, 0.36}};
 template <>
 constexpr TileCost kDzCosts<float>[2] = {{kTileLarge, dz_shape<float>(kTileLarge), 3.90, 9.0, 2.10},

@@ -28,7 +28,7 @@
 // stays in fp32.
 //
 // Measured (MI355X): 8192 x 4096 x 14336 in bf16 2.43 ms forward (1190
-// TFLOP/s), 2.67 with a and b left, 5.47 backward (1055); 1003 x 2048 x 1407 in
+// TFLOP/s), 2.67 with a and b left, 5.29 backward (1092); 1003 x 2048 x 1407 in
 // fp16 33, 38 and 86 us; 300 x 1000 x 2731 in fp32 73, 74 and 130 us; one row of
 // 4096 x 14336 in bf16 65 us (5.4 TB/s), 48 rows 77.
 #pragma once
@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mlp_up(MlpUpArgs p) {
 // two work-groups share a compute unit, with two LDS stages each, so that one
 // multiplies while the other loads and stores.  (dh as a stream of 192 x 192
 // tiles, stream.hpp, whose one work-group does nothing else meanwhile, spent
-// 640 of 1480 us on the epilogue at 8192 x 4096 x 14336; so do pairs of 128
-// tiles there, but at 16384 x 768 x 2048 the backward pass takes 475 us
+// 640 of 1480 us on the epilogue at 8192 x 4096 x 14336; pairs of 128 tiles
+// take 1345 us, and at 16384 x 768 x 2048 the backward pass takes 453 us
 // instead of 528.  The projections' product, whose epilogue is shorter, lost
 // by it: 1.60 -> 1.82 ms.)  Stages, fragments and steps are products.hpp's; the
 // operands' resources end with their last valid rows as in stream.hpp.

@@ -22,6 +22,6 @@ MLP_CASES = [
     (4000, 200, 3001, ("fp32",)), (4000, 776, 264, ("fp32",)), (1500, 64, 3001, ("fp32",)),
     # Copies in a launch of their own, as the tiles leave too few compute
     # units to them.
-    (513, 1, 14336, HALF), (513, 1, 2048, HALF), (1003, 1, 14336, ("fp16",)), (8192, 1, 1407, ("fp32",)),
+    (513, 1, 14336, HALF), (1, 1000, 14336, HALF), (513, 1, 2048, HALF), (1003, 1, 14336, ("fp16",)), (8192, 1, 1407, ("fp32",)),
 ]
 MLP_RUNS = [(n, d, f, t) for n, d, f, types in MLP_CASES for t in types]
