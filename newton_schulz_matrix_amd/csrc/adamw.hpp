@@ -211,10 +211,13 @@ __device__ __forceinline__ float block_max(float v) {
 // hardware's reciprocal root, one Newton step for the root s and half its
 // reciprocal h, and the residual's last correction.  The compiler's own
 // sequence takes twice the instructions, for the range below.  An infinite
-// moment counts as the largest finite one, whose root is kRootTop.
+// moment counts as the largest finite one, whose root is kRootTop.  A NaN
+// stays one (fminf would make it the largest number, whose root would become
+// the scale of the whole block): the maxima of a block pass it over, and its
+// code is e4m3's NaN.
 constexpr float kRootTop = 0x1.fffffep63f;
 __device__ __forceinline__ float root_of(float v) {
-  v = fminf(v, 0x1.fffffep127f);
+  v = v > 0x1.fffffep127f ? 0x1.fffffep127f : v;
   const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));
   float s = v * y, h = 0.5f * y;
   const float r = fmaf(-h, s, 0.5f);

@@ -1,0 +1,59 @@
+"""AdamW where its states run out of range: a NaN gradient among 8-bit
+moments."""
+
+import pytest
+import torch
+
+from newton_schulz_matrix_amd import _binding as B
+from test_gpu_adamw import DTYPES, _Set, _dev
+
+pytestmark = pytest.mark.gpu
+
+NAN_CODE = 0x7F  # e4m3's NaN but for its sign
+
+
+def _codes(t):
+    return t.view(torch.uint8)
+
+
+@pytest.mark.parametrize("place", [0, 255, 600, 767, 999])
+@pytest.mark.parametrize("ptype", ["bf16", "fp32"])
+def test_a_nan_stays_in_its_element(place, ptype):
+    # Two runs that differ in one element of one gradient, whose moments are
+    # zeros, so that without the NaN it has no share in its block's scales.
+    dev = _dev()
+    print(f"adamw nan at {place} {ptype}", flush=True)
+    sets = [_Set([(1000,)], [DTYPES[ptype]], [torch.float32], (8,), dev, seed=2) for _ in range(2)]
+    other = torch.ones(1000, dtype=torch.bool, device=dev)
+    other[place] = False
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    for s, value in zip(sets, (0.0, float("nan"))):
+        _codes(s.m[0])[place] = 0
+        _codes(s.v[0])[place] = 0
+        s.g[0][place] = value
+        st.zero_()
+        s.step(status=st)
+        assert int(st.item()) == (B.NS_ERR_NONFINITE | B.STATUS_AT_OUTPUT if value else 0)
+    plain, hit = sets
+    for step in (7, 8, 9):
+        assert torch.equal(plain.scales[0], hit.scales[0])
+        for a, b in ((plain.p[0], hit.p[0]), (_codes(plain.m[0]), _codes(hit.m[0])), (_codes(plain.v[0]), _codes(hit.v[0]))):
+            assert torch.equal(a[other], b[other])
+        assert torch.isnan(hit.p[0][place])
+        assert int(_codes(hit.m[0])[place]) & 0x7F == NAN_CODE and int(_codes(hit.v[0])[place]) & 0x7F == NAN_CODE
+        # What follows moves the others as ever.
+        before = plain.p[0].clone()
+        for s in sets:
+            s.g[0].copy_(s.before[0][1]).mul_(0.5)
+            s.step(step=step + 1)
+        assert (plain.p[0] != before)[other].float().mean().item() > 0.5
+
+
+def test_a_nan_second_moment_in_fp32_is_not_a_large_one():
+    dev = _dev()
+    s = _Set([(700,)], [torch.float32], [torch.float32], (32,), dev)
+    s.v[0][300] = float("nan")
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    s.step(status=st)
+    assert int(st.item()) == B.NS_ERR_NONFINITE | B.STATUS_AT_OUTPUT
+    assert torch.isnan(s.p[0][300]) and int(torch.isnan(s.p[0]).sum()) == 1
