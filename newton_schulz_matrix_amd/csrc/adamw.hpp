@@ -206,16 +206,16 @@ __device__ __forceinline__ float block_max(float v) {
   return max_dpp<0x140>(v);
 }
 
-// The square root, rounded to nearest (for v >= 2^-100; codes and scales are
-// made of it, and equal moments give equal ones whoever computes them): the
-// hardware's reciprocal root, one Newton step for the root s and half its
-// reciprocal h, and the residual's last correction.  The compiler's own
-// sequence takes twice the instructions, for the range below.  An infinite
+// The square root, rounded to nearest (codes and scales are made of it, and
+// equal moments give equal ones whoever computes them): the hardware's
+// reciprocal root, one Newton step for the root s and half its reciprocal h,
+// and the residual's last correction.  The compiler's own sequence takes twice
+// the instructions, for moments of 2^-100 and more and zero.  An infinite
 // moment counts as the largest finite one, whose root is kRootTop.  A NaN
 // stays one (fminf would make it the largest number, whose root would become
 // the scale of the whole block): the maxima of a block pass it over, and its
 // code is e4m3's NaN.
-constexpr float kRootTop = 0x1.fffffep63f;
+constexpr float kRootTop = 0x1.fffffep63f, kRootLeast = 0x1p-100f;
 __device__ __forceinline__ float root_of(float v) {
   v = v > 0x1.fffffep127f ? 0x1.fffffep127f : v;
   const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));
@@ -225,6 +225,11 @@ __device__ __forceinline__ float root_of(float v) {
   h = fmaf(h, r, h);
   return fmaf(fmaf(-s, s, v), h, s);
 }
+// Of a moment below kRootLeast, whose residual would fall among the subnormal
+// numbers and which the reciprocal root does not take below 2^-126.  Only where
+// the least of eight moments is one (or zero), which costs 6 us of 1123 at 524M
+// 8-bit moments; scaling every moment costs 20.
+__device__ __forceinline__ float root_of_small(float v) { return root_of(v * 0x1p64f) * 0x1p-32f; }
 
 // The moments' update, each operation rounded on its own (no fused
 // multiply-adds): a code is then what its formula in fp32 gives, whoever
@@ -295,6 +300,7 @@ static __global__ void __launch_bounds__(kAdamwThreads) k_adamw(AdamwArgs a) {
     for (int j = 0; j < kG; ++j) {
       const int64_t e = e0 + j * kApart, left = it.n - e;
       float p[8], g[8], v[8];
+      float least = 1.f;
       of_type(pt, [&](auto t) { floats_of<decltype(t)>(rp[j], p); });
       of_type(gt, [&](auto t) { floats_of<decltype(t)>(rg[j], g); });
       if (coded) {
@@ -310,6 +316,15 @@ static __global__ void __launch_bounds__(kAdamwThreads) k_adamw(AdamwArgs a) {
       for (int k = 0; k < 8; ++k) {
         next_moments(a.b1, a.a1, a.b2, a.a2, g[k] * gs, m[j][k], v[k]);
         root[j][k] = root_of(v[k]);
+        least = fminf(least, v[k]);
+      }
+      if (least < kRootLeast) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (v[k] < kRootLeast) root[j][k] = root_of_small(v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
         // The hardware's reciprocal is good to a step of fp32; only the step
         // is made of it.
         p[k] = fmaf(-lrc * m[j][k], __builtin_amdgcn_rcpf(fmaf(root[j][k], c2, a.eps)), p[k] * keep);

@@ -1,11 +1,13 @@
 """AdamW where its states run out of range: a NaN gradient among 8-bit
-moments."""
+moments, and second moments below the smallest normal number."""
 
+import numpy as np
 import pytest
 import torch
 
+import newton_schulz_matrix_amd as nsa
 from newton_schulz_matrix_amd import _binding as B
-from test_gpu_adamw import DTYPES, _Set, _dev
+from test_gpu_adamw import DTYPES, U32, _Set, _dev
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +59,25 @@ def test_a_nan_second_moment_in_fp32_is_not_a_large_one():
     s.step(status=st)
     assert int(st.item()) == B.NS_ERR_NONFINITE | B.STATUS_AT_OUTPUT
     assert torch.isnan(s.p[0][300]) and int(torch.isnan(s.p[0]).sum()) == 1
+
+
+def test_second_moments_below_the_normal_numbers():
+    # g = 0 and betas of a half: v is exactly halved.  Without eps the step is
+    # lr m / sqrt(v), by the root's half step, its correction factor's and
+    # product's (1 each, c2 is 1 here), the reciprocal's step (2 halves), lr c1 m
+    # (2) and the sum.
+    dev = _dev()
+    rng = np.random.default_rng(1)
+    bits = np.concatenate([2 ** np.arange(23), [3, 5, 7, 1000, 0x7FFFFF, 0x3FFFFF], rng.integers(1, 1 << 22, 300),
+                           0x00800000 * np.arange(1, 60) + rng.integers(0, 1 << 23, 59)]).astype(np.uint32)
+    half = bits.view(np.float32)
+    v0 = (half.astype(np.float64) * 2).astype(np.float32)
+    m0 = (2 * np.sqrt(half.astype(np.float64)) * rng.uniform(0.5, 2.0, half.size)).astype(np.float32)
+    p, g = torch.zeros(half.size, device=dev), torch.zeros(half.size, device=dev)
+    m, v = torch.from_numpy(m0).to(dev), torch.from_numpy(v0).to(dev)
+    nsa.adamw_step([p], [g], [m], [v], lr=1.0, step=2000, betas=(0.5, 0.5), eps=0.0, weight_decay=0.0)
+    assert np.array_equal(v.cpu().numpy(), half)
+    want = -(m0.astype(np.float64) / 2) / np.sqrt(half.astype(np.float64))
+    off = np.abs(p.cpu().double().numpy() - want) / np.abs(want)
+    print(f"small moments: worst {off.max() / U32:.2f} half steps of fp32", flush=True)
+    assert off.max() <= 8 * U32
