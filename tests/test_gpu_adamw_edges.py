@@ -1,5 +1,7 @@
 """AdamW where its states run out of range: a NaN gradient among 8-bit
-moments, and second moments below the smallest normal number."""
+moments, second moments below the smallest normal number, and codes and
+scales that are the documented fp32 formula's to the bit.
+"""
 
 import numpy as np
 import pytest
@@ -7,7 +9,7 @@ import torch
 
 import newton_schulz_matrix_amd as nsa
 from newton_schulz_matrix_amd import _binding as B
-from test_gpu_adamw import DTYPES, U32, _Set, _dev
+from test_gpu_adamw import BETAS, DTYPES, U32, _Set, _dev
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +83,51 @@ def test_second_moments_below_the_normal_numbers():
     off = np.abs(p.cpu().double().numpy() - want) / np.abs(want)
     print(f"small moments: worst {off.max() / U32:.2f} half steps of fp32", flush=True)
     assert off.max() <= 8 * U32
+
+
+def _formula(g, cm, cv, scales, betas):
+    """Codes and scales after a step, one rounded fp32 operation at a time."""
+    f = np.float32
+    b1, a1, b2, a2 = f(betas[0]), f(1.0 - betas[0]), f(betas[1]), f(1.0 - betas[1])
+    n = g.size
+    unit = np.repeat(scales * (f(1) / f(448)), 256, axis=1)[:, :n]
+    with np.errstate(under="ignore"):
+        m, r = cm * unit[0], cv * unit[1]
+        v = r * r
+        m = b1 * m + a1 * g
+        v = b2 * v + a2 * g * g
+        root = np.sqrt(v)
+        tops, codes = [], []
+        for x in (m, root):
+            top = np.maximum(np.abs(np.pad(x, (0, -n % 256))).reshape(-1, 256).max(1), f(2.0 ** -100))
+            inv = f(1) / top * f(448)
+            q = x * np.repeat(inv, 256)[:n]
+            if x is root:
+                q = np.where(root > 0, np.maximum(q, f(2.0 ** -9)), q)
+            assert q.dtype == np.float32 and top.dtype == np.float32
+            tops.append(top)
+            codes.append(torch.from_numpy(q).to(torch.float8_e4m3fn).view(torch.uint8))
+    return codes, np.stack(tops)
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -40, 2.0 ** -66, 2.0 ** -72, 2.0 ** 40])
+@pytest.mark.parametrize("gtype", list(DTYPES))
+@pytest.mark.parametrize("n", [1, 255, 256, 1003, 50001])
+def test_codes_and_scales_are_the_formulas_to_the_bit(n, gtype, size):
+    dev = _dev()
+    if gtype == "fp16" and size != 1.0:
+        pytest.skip("beyond fp16's numbers")
+    s = _Set([(n,)], [torch.float32], [DTYPES[gtype]], (8,), dev, seed=n)
+    s.scales[0].mul_(size)
+    s.g[0].mul_(size)
+    if n > 300:
+        s.g[0][:256] = 0  # a block that only decays
+    c = [t.float().cpu().numpy() for t in (s.g[0], s.m[0], s.v[0])]
+    scales = s.scales[0].cpu().numpy()
+    for step in range(1, 4):
+        codes, tops = _formula(*c, scales, BETAS)
+        s.step(step=step)
+        assert np.array_equal(s.scales[0].cpu().numpy(), tops)
+        assert torch.equal(_codes(s.m[0]).cpu(), codes[0]) and torch.equal(_codes(s.v[0]).cpu(), codes[1])
+        c[1:] = [t.float().cpu().numpy() for t in (s.m[0], s.v[0])]
+        scales = tops
