@@ -60,7 +60,10 @@ struct Act {
       constexpr float c = 0.79788456080286536f, k = 0.044715f;
       const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-2.f * kLog2e * c * a * fmaf(k * a, a, 1.f)));
       value = a * s;
-      slope = s * fmaf(2.f * a * (1.f - s), c * fmaf(3.f * k * a, a, 1.f), 1.f);
+      // From |a| = 16 on s is 0 or 1 and so is the slope, but a^3 may be
+      // infinite, which times that 0 would be a NaN.  A NaN stays one.
+      const float t = a < -16.f ? -16.f : a > 16.f ? 16.f : a;
+      slope = s * fmaf(2.f * t * (1.f - s), c * fmaf(3.f * k * t, t, 1.f), 1.f);
     } else {
       value = a < 0.f ? 0.f : a;  // a NaN stays one
       slope = a > 0.f ? 1.f : 0.f;
