@@ -7,13 +7,13 @@
 // A Python extension module (host code only).  It reads tensors through
 // torch's C++ interface, raises the same exceptions as the Python checks
 // beside it, and calls the library through the addresses that the Python
-// side passes.
+// side passes.  Other threads have the interpreter while it allocates or the
+// library runs: either may wait for the device.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -30,6 +30,17 @@ constexpr int64_t kStateBlock = 256;  // elements of an 8-bit moment that share 
 PyObject* fail(PyObject* type, const std::string& what) {
   PyErr_SetString(type, what.c_str());
   return nullptr;
+}
+
+// What f() gives, the interpreter left to other threads meanwhile: f touches no
+// Python object.
+template <class F>
+auto unlocked(F&& f) {
+  struct Released {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+  } released;
+  return f();
 }
 
 // The ns_dtype of a tensor; -1 for another type.
@@ -241,12 +252,14 @@ bool like(const at::Tensor& t, const at::Tensor& x, const char* name, int64_t& l
   return shaped(t, x.sizes(), x.scalar_type(), x, name, ld);
 }
 
-// The tensor to write, given or made, and its row stride.
+// The tensor to write if it is given (else it is made later), and its row stride.
 bool output(PyObject* o, at::Tensor& t, at::IntArrayRef sizes, const at::Tensor& x, const char* name, int64_t& ld) {
   if (o != Py_None) return tensor_of(o, t, name) && shaped(t, sizes, x.scalar_type(), x, name, ld);
-  t = at::empty(sizes, x.options());
   ld = sizes.back();
   return true;
+}
+void make(at::Tensor& t, at::IntArrayRef sizes, const at::Tensor& x) {
+  if (!t.defined()) t = at::empty(sizes, x.options());
 }
 
 // A parameter of x's type or float32, of one type with those before it
@@ -309,26 +322,26 @@ bool per_row(PyObject* o, at::Tensor& t, const at::Tensor& x, const Rows& r, con
   return true;
 }
 
-// A workspace of the caller's or of torch's, 256-byte aligned.
+// A workspace of the caller's, or of torch's once it is made, 256-byte aligned.
 struct Workspace {
   at::Tensor held;
   void* ptr = nullptr;
   size_t bytes = 0;
-  bool take(PyObject* o, size_t need, const at::Tensor& x) {
-    if (o == Py_None) {
-      held = at::empty({(int64_t)need + 256}, x.options().dtype(at::kByte));
-    } else {
-      if (!tensor_of(o, held, "workspace")) return false;
-      if (held.device() != x.device() || !held.is_contiguous()) {
-        fail(PyExc_ValueError, "workspace must be contiguous and on the data's device");
-        return false;
-      }
+  bool check(PyObject* o, const at::Tensor& x) {
+    if (o == Py_None) return true;
+    if (!tensor_of(o, held, "workspace")) return false;
+    if (held.device() != x.device() || !held.is_contiguous()) {
+      fail(PyExc_ValueError, "workspace must be contiguous and on the data's device");
+      return false;
     }
+    return true;
+  }
+  void take(size_t need, const at::Tensor& x) {
+    if (!held.defined()) held = at::empty({(int64_t)need + 256}, x.options().dtype(at::kByte));
     const uintptr_t at = reinterpret_cast<uintptr_t>(held.data_ptr());
     const size_t pad = (size_t)(-at & 255), all = (size_t)held.numel() * held.element_size();
     ptr = reinterpret_cast<void*>(at + pad);
     bytes = all > pad ? all - pad : 0;
-    return true;
   }
 };
 
@@ -361,7 +374,9 @@ using ResidualNorm = ns_status (*)(const void*, int64_t, const void*, int64_t, i
 PyObject* residual_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
   if (nargs != 15) return fail(PyExc_TypeError, "residual_norm takes 15 arguments");
-  const ResidualNorm fn = reinterpret_cast<ResidualNorm>(PyLong_AsVoidPtr(args[0]));
+  const auto fn = address<ResidualNorm>(args[0]);
+  const auto status = address<int32_t*>(args[13]);
+  const auto stream = address<void*>(args[14]);
   at::Tensor x, z, gate, wb, w, s, y, rb, rs;
   if (!tensor_of(args[1], x, "residual")) return nullptr;
   Rows r;
@@ -385,14 +400,16 @@ PyObject* residual_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   if (args[6] != Py_None && !weight_of(args[6], w, x, r, pt, "weight")) return nullptr;
   if (has_z && !output(args[11], s, x.sizes(), x, "out", lds)) return nullptr;
   if (norm_out && !output(args[12], y, x.sizes(), x, "out_norm", ldy)) return nullptr;
-  const auto lead = x.sizes().slice(0, x.dim() - 1);
-  if (stats && has_z && norm_branch) rb = at::empty(lead, x.options().dtype(at::kFloat));
-  if (stats && norm_out) rs = at::empty(lead, x.options().dtype(at::kFloat));
-  const ns_status st = fn(x.data_ptr(), r.ld, data(z), ldz, r.rows, r.cols, (ns_dtype)dt, data(gate), groups, data(wb),
-                          data(w), (ns_dtype)(pt < 0 ? dt : pt), (float)scale, norm_branch, (float)eps, data(s), lds,
-                          data(y), ldy, static_cast<float*>(data(rb)), static_cast<float*>(data(rs)),
-                          address<int32_t*>(args[13]), address<void*>(args[14]));
-  if (PyErr_Occurred()) return nullptr;
+  const ns_status st = unlocked([&] {
+    const auto lead = x.sizes().slice(0, x.dim() - 1);
+    if (has_z) make(s, x.sizes(), x);
+    if (norm_out) make(y, x.sizes(), x);
+    if (stats && has_z && norm_branch) rb = at::empty(lead, x.options().dtype(at::kFloat));
+    if (stats && norm_out) rs = at::empty(lead, x.options().dtype(at::kFloat));
+    return fn(x.data_ptr(), r.ld, data(z), ldz, r.rows, r.cols, (ns_dtype)dt, data(gate), groups, data(wb), data(w),
+              (ns_dtype)(pt < 0 ? dt : pt), (float)scale, norm_branch, (float)eps, data(s), lds, data(y), ldy,
+              static_cast<float*>(data(rb)), static_cast<float*>(data(rs)), status, stream);
+  });
   if (st != NS_OK) return PyLong_FromLong(st);
   PyObject* out = PyTuple_New(4);
   if (!out) return nullptr;
@@ -419,6 +436,8 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t na
   if (nargs != 18) return fail(PyExc_TypeError, "residual_norm_backward takes 18 arguments");
   const auto fn = address<ResidualNormBackward>(args[0]);
   const auto query = address<WorkspaceSize2>(args[1]);
+  const auto status = address<int32_t*>(args[16]);
+  const auto handle = address<void*>(args[17]);
   at::Tensor ds, dy, s, z, rb, rs, gate, wb, w, dx, dz, dgate, dwb, dw;
   if (!tensor_of(args[4], s, "stream")) return nullptr;
   Rows r;
@@ -452,21 +471,22 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t na
   if (args[11] != Py_None && !weight_of(args[11], w, s, r, pt, "weight")) return nullptr;
   if (!output(args[13], dx, s.sizes(), s, "out", lddx)) return nullptr;
   if (has_z && !output(args[14], dz, s.sizes(), s, "out_branch", lddz)) return nullptr;
-  if (params) {
-    if (gate.defined()) dgate = at::empty(gate.sizes(), gate.options());
-    if (wb.defined()) dwb = at::empty(wb.sizes(), wb.options());
-    if (w.defined()) dw = at::empty(w.sizes(), w.options());
-  }
   const size_t need = query(r.rows, r.cols);
   if (need == 0) return PyLong_FromLong(NS_ERR_INVALID_ARG);
   Workspace ws;
-  if (!ws.take(args[15], need, s)) return nullptr;
-  const ns_status st =
-      fn(data(ds), ldds, data(dy), lddy, s.data_ptr(), r.ld, data(z), ldz, r.rows, r.cols, (ns_dtype)dt,
-         static_cast<float*>(data(rb)), static_cast<float*>(data(rs)), data(gate), groups, data(wb), data(w),
-         (ns_dtype)(pt < 0 ? dt : pt), (float)scale, dx.data_ptr(), lddx, data(dz), lddz, data(dgate), data(dwb), data(dw),
-         address<int32_t*>(args[16]), ws.ptr, ws.bytes, address<void*>(args[17]));
-  if (PyErr_Occurred()) return nullptr;
+  if (!ws.check(args[15], s)) return nullptr;
+  const ns_status st = unlocked([&] {
+    make(dx, s.sizes(), s);
+    if (has_z) make(dz, s.sizes(), s);
+    if (params && gate.defined()) make(dgate, gate.sizes(), gate);
+    if (params && wb.defined()) make(dwb, wb.sizes(), wb);
+    if (params && w.defined()) make(dw, w.sizes(), w);
+    ws.take(need, s);
+    return fn(data(ds), ldds, data(dy), lddy, s.data_ptr(), r.ld, data(z), ldz, r.rows, r.cols, (ns_dtype)dt,
+              static_cast<float*>(data(rb)), static_cast<float*>(data(rs)), data(gate), groups, data(wb), data(w),
+              (ns_dtype)(pt < 0 ? dt : pt), (float)scale, dx.data_ptr(), lddx, data(dz), lddz, data(dgate), data(dwb),
+              data(dw), status, ws.ptr, ws.bytes, handle);
+  });
   if (st != NS_OK) return PyLong_FromLong(st);
   PyObject* out = PyTuple_New(5);
   if (!out) return nullptr;
@@ -541,6 +561,8 @@ PyObject* gated_mlp(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   if (nargs != 12) return fail(PyExc_TypeError, "gated_mlp takes 12 arguments");
   const auto fn = address<GatedMlp>(args[0]);
   const auto query = address<MlpWorkspaceSize>(args[1]);
+  const auto status = address<int32_t*>(args[10]);
+  const auto stream = address<void*>(args[11]);
   Block b;
   if (!b.read(args + 2)) return nullptr;
   const auto act = (ns_activation)PyLong_AsLong(args[6]);
@@ -549,13 +571,9 @@ PyObject* gated_mlp(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   int64_t ldy = 0;
   if (!output(args[8], y, b.x.sizes(), b.x, "out", ldy)) return nullptr;
   int st_code = NS_FP32;
-  if (args[7] != Py_None) {
-    const auto type = args[7] == Py_True ? at::kFloat : b.x.scalar_type();
-    const auto sizes = b.hidden();
-    gate = at::empty(sizes, b.x.options().dtype(type));
-    up = at::empty(sizes, b.x.options().dtype(type));
-    st_code = dtype_of(gate);
-  }
+  const bool saved = args[7] != Py_None;
+  const auto save_type = args[7] == Py_True ? at::kFloat : b.x.scalar_type();
+  if (saved) st_code = save_type == at::kFloat ? (int)NS_FP32 : b.dt;
   const int64_t ktile = 128 / (int64_t)b.x.element_size();
   const bool even = (b.r.cols % ktile || (b.ldg == b.ldu && aligned(b.x, b.r.ld) && aligned(b.wg, b.ldg) &&
                                           aligned(b.wu, b.ldu))) &&
@@ -563,12 +581,19 @@ PyObject* gated_mlp(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   const size_t need = query(b.r.rows, b.r.cols, b.inner, (ns_dtype)b.dt, even, 0);
   if (need == 0) return PyLong_FromLong(NS_ERR_INVALID_ARG);
   Workspace ws;
-  if (!ws.take(args[9], need, b.x)) return nullptr;
-  const ns_status st = fn(b.x.data_ptr(), b.r.ld, b.wg.data_ptr(), b.ldg, b.wu.data_ptr(), b.ldu, b.wd.data_ptr(), b.ldd,
-                          b.r.rows, b.r.cols, b.inner, (ns_dtype)b.dt, act, y.data_ptr(), ldy, data(gate), data(up),
-                          b.inner, (ns_dtype)st_code, address<int32_t*>(args[10]), ws.ptr, ws.bytes,
-                          address<void*>(args[11]));
-  if (PyErr_Occurred()) return nullptr;
+  if (!ws.check(args[9], b.x)) return nullptr;
+  const ns_status st = unlocked([&] {
+    make(y, b.x.sizes(), b.x);
+    if (saved) {
+      const auto sizes = b.hidden();
+      gate = at::empty(sizes, b.x.options().dtype(save_type));
+      up = at::empty(sizes, b.x.options().dtype(save_type));
+    }
+    ws.take(need, b.x);
+    return fn(b.x.data_ptr(), b.r.ld, b.wg.data_ptr(), b.ldg, b.wu.data_ptr(), b.ldu, b.wd.data_ptr(), b.ldd, b.r.rows,
+              b.r.cols, b.inner, (ns_dtype)b.dt, act, y.data_ptr(), ldy, data(gate), data(up), b.inner, (ns_dtype)st_code,
+              status, ws.ptr, ws.bytes, stream);
+  });
   if (st != NS_OK) return PyLong_FromLong(st);
   PyObject* out = PyTuple_New(3);
   if (!out) return nullptr;
@@ -588,6 +613,8 @@ PyObject* gated_mlp_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs)
   if (nargs != 19) return fail(PyExc_TypeError, "gated_mlp_backward takes 19 arguments");
   const auto fn = address<GatedMlpBackward>(args[0]);
   const auto query = address<MlpWorkspaceSize>(args[1]);
+  const auto status = address<int32_t*>(args[17]);
+  const auto stream = address<void*>(args[18]);
   Block b;
   if (!b.read(args + 2)) return nullptr;
   at::Tensor dy, gate, up, dx, dwg, dwu, dwd;
@@ -612,13 +639,20 @@ PyObject* gated_mlp_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs)
   const size_t need = query(b.r.rows, b.r.cols, b.inner, (ns_dtype)b.dt, aligned(dy, lddy), 1);
   if (need == 0) return PyLong_FromLong(NS_ERR_INVALID_ARG);
   Workspace ws;
-  if (!ws.take(args[16], need, b.x)) return nullptr;
-  const ns_status st =
-      fn(dy.data_ptr(), lddy, b.x.data_ptr(), b.r.ld, b.wg.data_ptr(), b.ldg, b.wu.data_ptr(), b.ldu, b.wd.data_ptr(),
-         b.ldd, gate.data_ptr(), up.data_ptr(), lds, (ns_dtype)dtype_of(gate), b.r.rows, b.r.cols, b.inner,
-         (ns_dtype)b.dt, act, data(dx), lddx, data(dwg), lddg, data(dwu), lddu, data(dwd), lddd,
-         address<int32_t*>(args[17]), ws.ptr, ws.bytes, address<void*>(args[18]));
-  if (PyErr_Occurred()) return nullptr;
+  if (!ws.check(args[16], b.x)) return nullptr;
+  const ns_status st = unlocked([&] {
+    if (need_dx) make(dx, b.x.sizes(), b.x);
+    if (need_dw) {
+      make(dwg, b.wg.sizes(), b.x);
+      make(dwu, b.wu.sizes(), b.x);
+      make(dwd, b.wd.sizes(), b.x);
+    }
+    ws.take(need, b.x);
+    return fn(dy.data_ptr(), lddy, b.x.data_ptr(), b.r.ld, b.wg.data_ptr(), b.ldg, b.wu.data_ptr(), b.ldu,
+              b.wd.data_ptr(), b.ldd, gate.data_ptr(), up.data_ptr(), lds, (ns_dtype)dtype_of(gate), b.r.rows, b.r.cols,
+              b.inner, (ns_dtype)b.dt, act, data(dx), lddx, data(dwg), lddg, data(dwu), lddu, data(dwd), lddd, status,
+              ws.ptr, ws.bytes, stream);
+  });
   if (st != NS_OK) return PyLong_FromLong(st);
   PyObject* out = PyTuple_New(4);
   if (!out) return nullptr;

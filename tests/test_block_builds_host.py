@@ -1,0 +1,40 @@
+"""Host side of the block's operators: calls of the host module leave the
+interpreter to other threads."""
+
+import ctypes
+import importlib
+import os
+
+import pytest
+import torch
+
+from newton_schulz_matrix_amd import _binding as B
+
+built = pytest.mark.skipif(not os.path.exists(B.LIB_PATH), reason="libnsortho.so not built")
+
+
+@built
+def test_calls_of_the_host_module_leave_the_interpreter_to_other_threads():
+    # In place of an entry point stands Python's own question whether the
+    # calling thread holds the interpreter's lock: 1 would come back as a
+    # status, 0 as the call's results.
+    marshal = importlib.import_module("newton_schulz_matrix_amd._marshal")
+    held = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    assert ctypes.pythonapi.PyGILState_Check() == 1
+
+    def address(name):
+        return ctypes.cast(getattr(B.lib(), name), ctypes.c_void_p).value
+
+    x, w, stat = torch.zeros(6, 8), torch.zeros(8), torch.zeros(6)
+    got = marshal.residual_norm(held, x, x, None, 1.0, None, w, True, True, 1e-6, True, None, None, None, 0)
+    assert isinstance(got, tuple) and got[0].shape == (6, 8) and got[3].shape == (6,)
+    got = marshal.residual_norm_backward(held, address("ns_residual_norm_workspace_size"), x, x, x, x, stat, stat, None, 1.0,
+                                         None, w, True, None, None, None, None, 0)
+    assert isinstance(got, tuple) and got[4].shape == (8,)
+    wide, down = torch.zeros(16, 8), torch.zeros(8, 16)
+    size = address("ns_gated_mlp_workspace_size")
+    y, gate, up = marshal.gated_mlp(held, size, x, wide, wide, down, 0, True, None, None, None, 0)
+    assert y.shape == (6, 8) and gate.shape == up.shape == (6, 16)
+    got = marshal.gated_mlp_backward(held, size, x, wide, wide, down, x, gate, up, 0, True, True, None, None, None, None, None,
+                                     None, 0)
+    assert isinstance(got, tuple) and got[1].shape == (16, 8)
