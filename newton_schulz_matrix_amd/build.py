@@ -1,10 +1,14 @@
-"""Build libnsortho.so (HIP, gfx950) in-tree with hipcc.
+"""Build libnsortho.so (HIP, gfx950) in-tree with hipcc, and the host module
+that the package's block calls go through with g++ against this torch.
 
-Usage: ``python -m newton_schulz_matrix_amd.build`` or ``build()``.
+Usage: ``python -m newton_schulz_matrix_amd.build`` or ``build()``; for C
+programs ``python newton_schulz_matrix_amd/build.py --library``, which needs
+neither g++ nor torch.
 """
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -59,45 +63,59 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build libnsortho)")
 
 
-def build(verbose: bool = False, extra_flags=None) -> str:
-    """Compile every HIP source and link libnsortho.so, and the host module,
-    next to this file."""
+def _start(cmd: list, verbose: bool) -> subprocess.Popen:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish(proc: subprocess.Popen, what: str, verbose: bool) -> None:
+    text = proc.communicate()[0].decode(errors="replace")
+    if proc.returncode != 0:
+        raise RuntimeError(f"{what}:\n{text}")
+    if verbose and text.strip():
+        print(text, flush=True)
+
+
+def build_library(verbose: bool = False, extra_flags=None) -> str:
+    """Compile every HIP source and link libnsortho.so next to this file: all
+    that a C program needs, with hipcc alone."""
     cc = hipcc()
-    objs = []
-    procs = []
-    for src in SOURCES:
-        obj = os.path.join(CSRC, os.path.splitext(src)[0] + ".o")
-        cmd = [cc, *HIP_FLAGS, *(extra_flags or []), "-I", INCLUDE, "-c",
-               os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                       stderr=subprocess.STDOUT), src))
-        objs.append(obj)
-    cmd = marshal_command()
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    procs.append((subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), "marshal.cpp"))
-    for p, src in procs:
-        out, _ = p.communicate()
-        text = out.decode(errors="replace")
-        if p.returncode != 0:
-            raise RuntimeError(f"the compiler failed on {src}:\n{text}")
-        if verbose and text.strip():
-            print(text, flush=True)
+    objs = [os.path.join(CSRC, os.path.splitext(src)[0] + ".o") for src in SOURCES]
+    procs = [_start([cc, *HIP_FLAGS, *(extra_flags or []), "-I", INCLUDE, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
+             for src, obj in zip(SOURCES, objs)]
+    for proc, src in zip(procs, SOURCES):
+        _finish(proc, f"the compiler failed on {src}", verbose)
     tmp = LIB_PATH + ".tmp"
-    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if res.returncode != 0:
-        raise RuntimeError("link failed:\n" + res.stdout.decode(errors="replace"))
+    _finish(_start([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs], verbose), "link failed", verbose)
     os.replace(tmp, LIB_PATH)
-    os.replace(MARSHAL_PATH + ".tmp", MARSHAL_PATH)
     for obj in objs:
         os.remove(obj)
     return LIB_PATH
 
 
+def build_marshal(verbose: bool = False) -> str:
+    """Compile the host module next to this file; this takes g++ (or CXX),
+    Python's headers and torch."""
+    _finish(_start(marshal_command(), verbose), "the compiler failed on marshal.cpp", verbose)
+    os.replace(MARSHAL_PATH + ".tmp", MARSHAL_PATH)
+    return MARSHAL_PATH
+
+
+def build(verbose: bool = False, extra_flags=None) -> str:
+    """The library, then the host module, which is left out where there is no
+    torch to load it.  Where it cannot be built this raises, with the library
+    in place for C programs and for every call that does not go through it."""
+    path = build_library(verbose, extra_flags)
+    if importlib.util.find_spec("torch") is None:
+        print("no torch: the host module of the package's block calls is left out", file=sys.stderr)
+        return path
+    try:
+        build_marshal(verbose)
+    except Exception as e:
+        raise RuntimeError(f"{path} is built, but the host module of the package's block calls is not: {e}") from e
+    return path
+
+
 if __name__ == "__main__":
-    print(build(verbose="-v" in sys.argv))
+    print((build_library if "--library" in sys.argv else build)(verbose="-v" in sys.argv))

@@ -1,14 +1,17 @@
 """Host side of the block's operators: calls of the host module leave the
-interpreter to other threads."""
+interpreter to other threads, and the library is built where the host module
+cannot be."""
 
 import ctypes
 import importlib
+import importlib.util
 import os
 
 import pytest
 import torch
 
 from newton_schulz_matrix_amd import _binding as B
+from newton_schulz_matrix_amd import build as nsbuild
 
 built = pytest.mark.skipif(not os.path.exists(B.LIB_PATH), reason="libnsortho.so not built")
 
@@ -38,3 +41,36 @@ def test_calls_of_the_host_module_leave_the_interpreter_to_other_threads():
     got = marshal.gated_mlp_backward(held, size, x, wide, wide, down, x, gate, up, 0, True, True, None, None, None, None, None,
                                      None, 0)
     assert isinstance(got, tuple) and got[1].shape == (16, 8)
+
+
+def _small_build(monkeypatch, tmp_path):
+    """The build's paths in a folder of their own, with the shortest source."""
+    try:
+        nsbuild.hipcc()
+    except RuntimeError:
+        pytest.skip("hipcc not found")
+    monkeypatch.setattr(nsbuild, "SOURCES", ["optim.hip"])
+    monkeypatch.setattr(nsbuild, "LIB_PATH", str(tmp_path / "libnsortho.so"))
+    monkeypatch.setattr(nsbuild, "MARSHAL_PATH", str(tmp_path / "_marshal.so"))
+
+
+def test_the_library_is_built_without_a_host_compiler(monkeypatch, tmp_path):
+    _small_build(monkeypatch, tmp_path)
+    monkeypatch.setenv("CXX", "/bin/false")
+    with pytest.raises(RuntimeError, match="is built, but the host module"):
+        nsbuild.build()
+    assert hasattr(ctypes.CDLL(nsbuild.LIB_PATH), "ns_adamw_step") and not os.path.exists(nsbuild.MARSHAL_PATH)
+    os.remove(nsbuild.LIB_PATH)
+    monkeypatch.setenv("CXX", "no such compiler")
+    with pytest.raises(RuntimeError, match="is built, but the host module"):
+        nsbuild.build()
+    assert os.path.exists(nsbuild.LIB_PATH)
+    os.remove(nsbuild.LIB_PATH)
+    assert nsbuild.build_library() == nsbuild.LIB_PATH and os.path.exists(nsbuild.LIB_PATH)
+
+
+def test_the_library_is_built_without_torch(monkeypatch, tmp_path):
+    _small_build(monkeypatch, tmp_path)
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name: None)
+    assert nsbuild.build() == nsbuild.LIB_PATH
+    assert os.path.exists(nsbuild.LIB_PATH) and not os.path.exists(nsbuild.MARSHAL_PATH)
