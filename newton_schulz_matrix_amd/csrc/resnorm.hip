@@ -52,6 +52,15 @@ bool resnorm_by_element(int64_t cols) {
   return cols < kVec<IO> || cols > kResNormRegisterCols;
 }
 
+// Rows of less than a vector that a block sums columns over at a time, each of
+// up to 256 / kResNormNarrow columns.
+constexpr int kResNormNarrow = 32;
+template <typename IO>
+constexpr bool resnorm_narrow(int64_t cols) {
+  static_assert(kVec<IO> <= 256 / kResNormNarrow, "a block's columns");
+  return cols < kVec<IO>;
+}
+
 // Rows that a block works on at a time, and the blocks of the backward pass.
 struct ResNormBlocks {
   int rows;
@@ -65,7 +74,7 @@ struct ResNormBlocksOf {
 };
 template <typename IO, typename PT>
 ResNormBlocks resnorm_blocks(int64_t cols) {
-  if (resnorm_by_element<IO>(cols)) return {1, kResNormParts};
+  if (resnorm_by_element<IO>(cols)) return {resnorm_narrow<IO>(cols) ? kResNormNarrow : 1, kResNormParts};
   return resnorm_form<IO, PT>(cols, ResNormBlocksOf{});
 }
 
@@ -250,9 +259,14 @@ ns_status ns_residual_norm_backward(const void* dS, int64_t ldds, const void* dY
       if (resnorm_by_element<IO>(cols)) {
         const dim3 grid((unsigned)std::min(rows, kMaxBlocks));
         if (dY) hipLaunchKernelGGL((k_resnorm_rows_long<IO, PT>), grid, dim3(1024), 0, st, a);
-        if (a.want_w || a.want_wb || a.want_gate)
-          hipLaunchKernelGGL((k_resnorm_cols_long<IO, PT>), dim3((unsigned)((cols + 255) / 256), (unsigned)cut.blocks),
-                             dim3(256), 0, st, a);
+        if (a.want_w || a.want_wb || a.want_gate) {
+          const unsigned parts = (unsigned)cut.blocks;
+          if (resnorm_narrow<IO>(cols))
+            hipLaunchKernelGGL((k_resnorm_cols_long<IO, PT, kResNormNarrow>), dim3(1, parts), dim3(256), 0, st, a);
+          else
+            hipLaunchKernelGGL((k_resnorm_cols_long<IO, PT, 1>), dim3((unsigned)((cols + 255) / 256), parts), dim3(256), 0,
+                               st, a);
+        }
         if (dX || dZ) hipLaunchKernelGGL((k_resnorm_bwd_long<IO, PT>), grid, dim3(1024), 0, st, a);
       } else {
         resnorm_form<IO, PT>(cols, ResNormBwdRun<IO, PT>{a, cut.blocks, st});

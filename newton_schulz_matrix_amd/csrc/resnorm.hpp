@@ -610,35 +610,76 @@ __global__ void __launch_bounds__(1024) k_resnorm_rows_long(ResNormBwdArgs p) {
   }
 }
 
-template <typename IO, typename PT>
+// A sum of up to millions of terms by one thread: runs of kSumRun terms, whose
+// totals are added up apart, so that its error grows with the runs and their
+// number and not with the number of terms (one running sum of terms of one
+// sign is off by a step of itself for each, and ends to grow at 2^24 of them).
+constexpr int kSumRun = 256;
+struct LongSum {
+  float total = 0.f, run = 0.f;
+  __device__ __forceinline__ void add(float a, float b) { run = fmaf(a, b, run); }
+  __device__ __forceinline__ void fold() {
+    total += run;
+    run = 0.f;
+  }
+  __device__ __forceinline__ float value() const { return total + run; }
+};
+
+// R rows of a segment at a time, 256 / R columns a block: rows of less than a
+// vector share a block, and their sums are joined in LDS in their order.
+template <typename IO, typename PT, int R>
 __global__ void __launch_bounds__(256) k_resnorm_cols_long(ResNormBwdArgs p) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.cols) return;
+  constexpr int C = 256 / R;
+  __shared__ float sh[R > 1 ? R : 1][C];
+  const int sub = threadIdx.x / C, c = blockIdx.x * C + threadIdx.x % C;
+  const bool in = c < p.cols;
+  // The sum of all rows' values, in the first one's threads.
+  auto joined = [&](float v) {
+    if constexpr (R > 1) {
+      __syncthreads();
+      sh[sub][threadIdx.x % C] = v;
+      __syncthreads();
+      v = 0.f;
+      if (sub == 0)
+        for (int i = 0; i < R; ++i) v += sh[i][threadIdx.x % C];
+    }
+    return v;
+  };
   const ResNormElement<IO, PT> e{p};
-  float dw = 0.f, dwb = 0.f;
+  LongSum dw, dwb;
+  int terms = 0;
   bool bad = false;
-  const int64_t segments = p.groups * p.split;
+  const int64_t segments = p.groups * p.split, step = (int64_t)p.split * R;
   for (int64_t seg = blockIdx.y; seg < segments; seg += gridDim.y) {
     const int64_t group = seg / p.split, end = (group + 1) * p.group_rows;
-    float dg = 0.f;
-    for (int64_t row = group * p.group_rows + (seg - group * p.split); row < end; row += p.split) {
-      if (p.dY) dw = fmaf(e.at(p.dY, row * p.lddy + c), e.shat(row, c), dw);
+    LongSum dg;
+    for (int64_t row = group * p.group_rows + (seg - group * p.split) * R + sub; in && row < end; row += step) {
+      if (++terms == kSumRun) {
+        terms = 0;
+        dw.fold();
+        dwb.fold();
+        dg.fold();
+      }
+      if (p.dY) dw.add(e.at(p.dY, row * p.lddy + c), e.shat(row, c));
       if (!p.Z) continue;
       const float g = e.grad(row, c, p.dY ? p.c_row[row] : 0.f), b = e.bhat(row, c);
-      dg = fmaf(g, b * e.param(p.wb, c), dg);
-      dwb = fmaf(e.gate(row, c) * g, b, dwb);
+      dg.add(g, b * e.param(p.wb, c));
+      dwb.add(e.gate(row, c) * g, b);
     }
     if (!p.want_gate) continue;
+    const float sum = joined(dg.value());
+    if (!in || sub > 0) continue;
     if (p.split > 1) {
-      p.partial[((int64_t)blockIdx.y * 3 + 2) * partial_stride(p.cols) + c] = dg;
+      p.partial[((int64_t)blockIdx.y * 3 + 2) * partial_stride(p.cols) + c] = sum;
     } else {
-      reinterpret_cast<PT*>(p.dgate)[group * p.cols + c] = from_f32<PT>(dg);
-      bad |= !(fabsf(dg) < kRoundsToInf<PT>);
+      reinterpret_cast<PT*>(p.dgate)[group * p.cols + c] = from_f32<PT>(sum);
+      bad |= !(fabsf(sum) < kRoundsToInf<PT>);
     }
   }
+  const float w = joined(dw.value()), wb = joined(dwb.value());
   float* out = p.partial + (int64_t)blockIdx.y * 3 * partial_stride(p.cols);
-  if (p.want_w) out[c] = dw;
-  if (p.want_wb) out[partial_stride(p.cols) + c] = dwb;
+  if (in && sub == 0 && p.want_w) out[c] = w;
+  if (in && sub == 0 && p.want_wb) out[partial_stride(p.cols) + c] = wb;
   if (p.d_status) report_status(p.d_status, p.status_bits, bad);
 }
 
