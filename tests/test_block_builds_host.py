@@ -1,10 +1,11 @@
-"""Host side of the block's operators: calls of the host module leave the
-interpreter to other threads, and the library is built where the host module
-cannot be."""
+"""Host side of the block's operators: the norms' cases reach every kernel
+build, calls of the host module leave the interpreter to other threads, and
+the library is built where the host module cannot be."""
 
 import ctypes
 import importlib
 import importlib.util
+import itertools
 import os
 
 import pytest
@@ -12,8 +13,19 @@ import torch
 
 from newton_schulz_matrix_amd import _binding as B
 from newton_schulz_matrix_amd import build as nsbuild
+from resnorm_cases import MORE_WIDTHS, build_of
 
 built = pytest.mark.skipif(not os.path.exists(B.LIB_PATH), reason="libnsortho.so not built")
+
+
+def test_the_widths_reach_every_build_of_the_residual_norms():
+    from test_gpu_residual_norm import WIDTHS
+    types = [(2, 2), (2, 4), (4, 4)]
+    every = {(t, build_of(c, *t)) for c, t in itertools.product(range(1, 8200), types)}
+    covered = {(t, build_of(c, *t)) for c, t in itertools.product(WIDTHS + MORE_WIDTHS, types)}
+    assert every - covered == set()
+    # Element by element: less than a vector, and too long.
+    assert any(c < 4 for c in WIDTHS) and any(c > 8192 for c in WIDTHS)
 
 
 @built

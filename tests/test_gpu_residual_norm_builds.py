@@ -1,12 +1,21 @@
-"""The residual norms' column sums over millions of narrow rows."""
+"""The residual norms' kernel builds that test_gpu_residual_norm.py's widths
+leave out, and column sums over millions of narrow rows."""
 
 import pytest
 import torch
 
 import newton_schulz_matrix_amd as nsa
-from test_gpu_residual_norm import U32, _dev
+from resnorm_cases import MORE_WIDTHS
+from test_gpu_residual_norm import TYPES, U32, _check, _dev
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("cols", MORE_WIDTHS)
+@pytest.mark.parametrize("dtype,pdtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 40, 1100])
+def test_matches_the_oracle_at_more_widths(rows, cols, dtype, pdtype):
+    _check(rows, cols, dtype, pdtype, 2 if rows > 1 else 1, seed=cols + rows)
 
 
 @pytest.mark.parametrize("cols", [1, 3])
