@@ -673,7 +673,10 @@ ns_status ns_residual_norm_backward(
  *            if inner is.  The others are copied in any case, and with
  *            aligned 0 all are.
  * The products accumulate in fp32; h is formed in fp32 and rounded to dtype
- * where it is a matrix instruction's operand (with a few rows it is not).
+ * where it is a matrix instruction's operand (with a few rows it is not).  In
+ * fp16 a row of h whose largest magnitude is not between 2^-10 and 65504 is held
+ * times a power of two that takes it to 2^14, and its y is taken back by that:
+ * y is finite and as exact as others where its own values are fp16's.
  */
 typedef enum { NS_SILU = 0, NS_GELU = 1, NS_GELU_TANH = 2, NS_RELU = 3 } ns_activation;
 
@@ -702,7 +705,9 @@ ns_status ns_gated_mlp(const void* X, int64_t ldx, const void* Wg,
  *            aligned, 1) bytes; aligned is 1 when dY starts on a 16-byte
  *            boundary and its row stride is a multiple of 128 bytes.
  * da, db and h are rounded to dtype, being operands; all products accumulate
- * in fp32.  No row is left out: a row of dY that is zero adds nothing to the
+ * in fp32.  In fp16 they are held times powers of two as h is above: for dX a
+ * row's da and db, for the weights' gradients, which add up over the rows, all
+ * da and db, and all h.  No row is left out: a row of dY that is zero adds nothing to the
  * weights' gradients as long as its rows of X, gate and up are finite.
  * With no rows the weights' gradients are zeros.
  */
@@ -771,7 +776,8 @@ int64_t ns_plan_linear_cross_entropy(int64_t rows, int64_t cols, int64_t vocab,
  * all of them), with the arguments of ns_gated_mlp_workspace_size.  Entries,
  * in launch order: prep<op> (copies, where there are any); up<op,tile>
  * (rows x columns of h) and products<op,tile> forward, dz<op,tile> and
- * products<op,tile> backward, join<op> and splits=S where y or dX is summed
+ * products<op,tile> backward, between the two in fp16 again<op,tile> (ends at
+ * once unless operands are out of fp16's range), join<op> and splits=S where y or dX is summed
  * from S parts; for a few rows dotup<op,rows,form> and
  * dotdown<op,rows,form>; zero<op> (gradients without rows).
  */

@@ -45,6 +45,9 @@ struct MlpPlan {
   char *Ys = nullptr, *dz = nullptr, *dzt = nullptr, *ht = nullptr, *WT = nullptr, *DT = nullptr, *XT = nullptr,
        *YT = nullptr;
   float* parts = nullptr;
+  HeldRange* range = nullptr;  // fp16 (ranged)
+  UpRange seen{};
+  bool ranged = false;
   size_t total = 0;
 };
 
@@ -170,7 +173,7 @@ MlpChoice choose_gradients(int64_t n, int64_t d, int64_t f, double kw, double kx
 // The same for what a call leaves out: workspaces are planned with both
 // gradients.
 template <typename T>
-MlpPlan mlp_plan_of(int64_t n, int64_t d, int64_t f, bool aligned, bool backward, void* ws) {
+MlpPlan mlp_plan_of(int64_t n, int64_t d, int64_t f, bool ranged, bool aligned, bool backward, void* ws) {
   MlpPlan p;
   p.n = n;
   p.d = d;
@@ -212,6 +215,7 @@ MlpPlan mlp_plan_of(int64_t n, int64_t d, int64_t f, bool aligned, bool backward
       if (p.splits > 1) p.parts = c.take<float>(p.splits * round_to(n, p.tm) * round_to(d, p.tn));
     }
     p.h = c.take<char>(p.h_rows * p.h_ld * (p.dot ? 4 : p.es));
+    p.ranged = ranged && !p.dot;
   } else {
     const TileCost& dz = best_tile(kDzCosts<T>, n, f, 1, (double)p.dk / p.bk);
     p.dz_tile = dz.tile;
@@ -234,6 +238,14 @@ MlpPlan mlp_plan_of(int64_t n, int64_t d, int64_t f, bool aligned, bool backward
     p.XT = c.take<char>(p.d_pad * p.t_ld * p.es);
     p.YT = c.take<char>(p.d_pad * p.t_ld * p.es);
     if (p.splits > 1) p.parts = c.take<float>(p.splits * round_to(n, p.tm) * round_to(d, p.tn));
+    p.ranged = ranged;
+  }
+  if (p.ranged) {
+    p.range = reinterpret_cast<HeldRange*>(c.take<uint32_t>(kRangeWords + n));
+    if (!backward) {
+      p.seen.outside = c.take<uint32_t>(kXentGroups * (kThreads / 64));
+      p.seen.parts = c.take<uint32_t>(2 * tiles_of(f, up_shape<T>(p.up_tile).n / 2) * n);
+    }
   }
   p.total = c.used;
   return p;
@@ -241,8 +253,8 @@ MlpPlan mlp_plan_of(int64_t n, int64_t d, int64_t f, bool aligned, bool backward
 
 MlpPlan mlp_plan(int64_t n, int64_t d, int64_t f, ns_dtype dtype, bool aligned, bool backward, void* ws) {
   // bf16 and fp16 have the same tiles.
-  return dtype == NS_FP32 ? mlp_plan_of<float>(n, d, f, aligned, backward, ws)
-                          : mlp_plan_of<_Float16>(n, d, f, aligned, backward, ws);
+  return dtype == NS_FP32 ? mlp_plan_of<float>(n, d, f, false, aligned, backward, ws)
+                          : mlp_plan_of<_Float16>(n, d, f, dtype == NS_FP16, aligned, backward, ws);
 }
 
 // A call's launches as text (see ns_plan_gated_mlp); the length that it needs
@@ -265,8 +277,11 @@ int describe_mlp(const MlpPlan& p, ns_dtype dtype, bool backward, char* buf, siz
   const TileShape dz = half ? dz_shape<_Float16>(p.dz_tile) : dz_shape<float>(p.dz_tile);
   const char* name = backward ? "dz" : "up";
   const TileShape& shape = backward ? dz : up;
-  return snprintf(buf, len, "%s%s<%s,%dx%d%s> products<%s,%dx%d>%s", first, name, op, shape.m, shape.n / (backward ? 1 : 2),
-                  p.side ? ",copies" : "", op, (int)p.tm, (int)p.tn, split);
+  char tile[16], again[32] = "";
+  snprintf(tile, sizeof tile, "%dx%d", shape.m, shape.n / (backward ? 1 : 2));
+  if (p.ranged) snprintf(again, sizeof again, "again<%s,%s> ", op, tile);
+  return snprintf(buf, len, "%s%s<%s,%s%s> %sproducts<%s,%dx%d>%s", first, name, op, tile, p.side ? ",copies" : "", again, op,
+                  (int)p.tm, (int)p.tn, split);
 }
 
 // The products' copies take 16-byte chunks, swizzled by bits 4 to 6 of the
@@ -296,7 +311,7 @@ XentCopyArgs mlp_copy(const void* src, int64_t ld, int64_t rows, int64_t cols, c
 
 template <typename T>
 ns_status mlp_prep(const MlpPrepArgs& a, hipStream_t st) {
-  const int64_t blocks = a.blocks();
+  const int64_t blocks = a.blocks() + a.zero_blocks();
   if (blocks == 0) return NS_OK;
   if (blocks >= int64_t(1) << 24) return NS_ERR_INVALID_ARG;  // a launch may not have 2^32 threads
   hipLaunchKernelGGL((k_mlp_prep<T>), dim3((unsigned)blocks), dim3(256), 0, st, a);
@@ -358,7 +373,14 @@ ns_status mlp_forward(const MlpPlan& p, const MlpIn& in, int act, void* Y, int64
   a.act = act;
   a.d_status = d_status;
   a.status_bits = bits;
-  if (launch_mlp_up<T>(a, p.up_tile, st) != hipSuccess) return NS_ERR_HIP;
+  a.range = p.range;
+  a.seen = p.seen;
+  if (launch_mlp_up<T>(a, p.up_tile, false, st) != hipSuccess) return NS_ERR_HIP;
+  if (p.ranged) {
+    // a and b are saved and the copies made.
+    a.gate = a.up = nullptr;
+    if (launch_mlp_up<T>(a, p.up_tile, true, st) != hipSuccess) return NS_ERR_HIP;
+  }
   MlpGradArgs g{};
   const int64_t tm = tiles_of(p.n, p.tm), tn = tiles_of(p.d, p.tn);
   g.x = MlpProduct{p.h, p.stage_f ? p.Ds : in.D, (int)tm, (int)tn, p.n, p.d, Y, ldy, p.n, (int)p.d};
@@ -367,6 +389,7 @@ ns_status mlp_forward(const MlpPlan& p, const MlpIn& in, int act, void* Y, int64
   g.x_ktiles = (int)(p.fk / p.bk);
   g.splits = p.splits;
   g.parts = p.parts;
+  g.range = p.range;
   g.d_status = d_status;
   g.status_bits = bits;
   if (launch_mlp_products<T>(g, p.tile, st) != hipSuccess) return NS_ERR_HIP;
@@ -394,6 +417,10 @@ ns_status mlp_backward(const MlpPlan& p, const MlpIn& in, const void* dY, int64_
     side.copy[3] = mlp_copy(in.G, in.ldg, p.f, p.d, nullptr, 0, p.WT, p.f_pad, p.d_pad, p.z_ld);
     side.copy[4] = mlp_copy(in.U, in.ldu, p.f, p.d, nullptr, 0, p.WT + p.f_pad * es, p.f_pad, p.d_pad, p.z_ld);
   }
+  if (p.ranged) {
+    prep.zero = reinterpret_cast<uint32_t*>(p.range);
+    prep.zeros = kRangeWords + p.n;
+  }
   ns_status s = mlp_prep<T>(prep, st);
   if (s != NS_OK) return s;
   // The gradients' tiles are square.
@@ -418,7 +445,9 @@ ns_status mlp_backward(const MlpPlan& p, const MlpIn& in, const void* dY, int64_
   a.z_ld = p.z_ld;
   a.t_ld = p.t_ld;
   a.act = act;
-  if (launch_mlp_dz<T>(a, p.dz_tile, st) != hipSuccess) return NS_ERR_HIP;
+  a.range = p.range;
+  if (launch_mlp_dz<T>(a, p.dz_tile, false, st) != hipSuccess) return NS_ERR_HIP;
+  if (p.ranged && launch_mlp_dz<T>(a, p.dz_tile, true, st) != hipSuccess) return NS_ERR_HIP;
   MlpGradArgs g{};
   int tiles = 0;
   if (out.dG) tiles += (int)(tf * td);
@@ -434,6 +463,7 @@ ns_status mlp_backward(const MlpPlan& p, const MlpIn& in, const void* dY, int64_
   g.w_ld = p.t_ld * es;
   g.w_ktiles = (int)(p.n_pad / p.bk);
   g.splits = p.splits;
+  g.range = p.range;
   if (out.dX) {
     g.x = MlpProduct{p.dz, p.WT, (int)tm, (int)td, p.n, p.d_pad, out.dX, out.lddx, p.n, (int)p.d};
     g.x_ldl = g.x_ldr = p.z_ld * es;

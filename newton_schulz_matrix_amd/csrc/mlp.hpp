@@ -24,6 +24,11 @@
 // memory, rounded to the operands' type, which doubles the gradients' error:
 // 0.0035 against 0.0023 relative in bf16, results alone rounded 0.0017).
 //
+// fp16 operands may lie outside the type's numbers where the results do not
+// (see HeldRange): each product's epilogue also looks for the largest of what it
+// leaves, and where that does not fit, the same tiles are made again in other
+// units, which the next products' results are taken back by.
+//
 // A few rows go without tiles: a wave reads whole rows of the weights, and h
 // stays in fp32.
 //
@@ -35,6 +40,8 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "xent.hpp"
 
@@ -84,6 +91,85 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 }
 
 // ---------------------------------------------------------------------------
+// The range of fp16 operands.
+//
+// h, da and db in fp16 are infinite past 65504 and lose digits below 2^-14, with
+// x, weights and results well inside: |a|, |b| of 300 do for one, a dy of 1e-6
+// for the other.  So they are held times a power of two, 2^held_exp, by which
+// the products' fp32 results are taken back: h for y and da, db for dx in units
+// of their row (a row's result does not depend on the others), for the weights'
+// gradients, which add up over rows, in one unit each of da and db and of h.
+// The unit is 1 while the largest magnitude is between 2^-10, from where on
+// values of a sixteenth of it still have all their digits, and 65504; outside it
+// takes that magnitude to [2^14, 2^15).
+//
+// The largest is known only when all tiles are made, so they are first made
+// with the unit 1, which is nearly always right, and each wave leaves the
+// largest magnitudes that it saw; a second launch of the same kernel then ends
+// at once, or makes those tiles again that need it.  (1003 x 2048 x 1407: 2.7 us
+// forward and 4.3 backward, of which the launches take 5; 8192 x 4096 x 14336
+// 12 of 2440 and 25 of 5500.  Made again, all tiles: 25 and 32 us, 2.1 and 1.3 ms.)
+// ---------------------------------------------------------------------------
+template <typename T>
+constexpr bool kRanged = __is_same(T, _Float16);
+
+// Magnitudes of finite numbers as integers of the same order, infinities and
+// NaN below all of them: they go into their own results only.
+constexpr uint32_t kKeyZero = 0x01000000u;
+__device__ __forceinline__ uint32_t range_key(float v) { return (__float_as_uint(v) << 1) + kKeyZero; }
+constexpr uint32_t key_of(float v) { return (__builtin_bit_cast(uint32_t, v) << 1) + kKeyZero; }
+constexpr uint32_t kKeyLeast = key_of(0x1p-10f), kKeyMost = key_of(65504.f);
+__device__ __forceinline__ bool out_of_range(uint32_t key) { return key > kKeyZero && (key < kKeyLeast || key > kKeyMost); }
+__device__ __forceinline__ int held_exp(uint32_t key) {
+  if (!out_of_range(key)) return 0;
+  // The magnitude is m 2^e with m in [1/2, 1).
+  const int e = 15 - __builtin_amdgcn_frexp_expf(__uint_as_float((key - kKeyZero) >> 1));
+  return e < 126 ? e : 126;
+}
+__device__ __forceinline__ float scaled(float v, int e) { return __builtin_amdgcn_ldexpf(v, e); }
+
+// What the waves saw and the units that follow from it, in the workspace.
+// Backward it is cleared before the tiles, and their waves take part in the
+// maxima; forward, where a launch to clear it would cost as much as the check,
+// each wave leaves its own parts (UpRange) and the second launch joins them.
+constexpr int kRangeSlots = 64;  // words that the maxima of all are spread over (one took all atomics in turn)
+struct HeldRange {
+  uint32_t outside;        // whether any part of a row is out of range
+  int32_t dz_exp, h_exp;   // held_exp of all da and db and of all h, left by the second launch
+  uint32_t unused[61];
+  uint32_t dz[kRangeSlots], h[kRangeSlots];
+  uint32_t row[1];         // of each row of h (forward) or of da and db
+};
+constexpr int64_t kRangeWords = (sizeof(HeldRange) / 4) - 1;
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// Ends a maximum here: left to the compiler it waits for its last term, with all
+// the others kept in registers (49 of them spilled in dh's large tile).
+__device__ __forceinline__ void settle_key(uint32_t& key) { asm volatile("" : "+v"(key)); }
+// A row's part, whose two halves are in lanes lr and lr + 32.
+__device__ __forceinline__ uint32_t row_part(uint32_t key) {
+  const auto p = __builtin_amdgcn_permlane32_swap(key, key, false, false);
+  return max_u32(p[0], p[1]);
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp_u32(uint32_t v) {
+  return max_u32(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max_dpp_u32<0xB1>(v);
+  v = max_dpp_u32<0x4E>(v);
+  v = max_dpp_u32<0x141>(v);
+  v = max_dpp_u32<0x140>(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return row_part(max_u32(p[0], p[1]));
+}
+// held_exp of the largest of a wave's keys; nothing is moved between lanes
+// where it is in range.
+__device__ __forceinline__ int wave_held_exp(uint32_t key) {
+  if (!__any(key > kKeyMost) && (__any(key >= kKeyLeast) || !__any(key > kKeyZero))) return 0;
+  return __builtin_amdgcn_readfirstlane(held_exp(wave_max(key)));
+}
+
+// ---------------------------------------------------------------------------
 // Copies of operands, padded or transposed, in 64 x 64 tiles (xent.hpp): all
 // in one launch, or those that the projections' (dh's) tiles do not read
 // beside these, where they leave compute units idle.
@@ -91,6 +177,9 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 constexpr int kMlpCopies = 5;
 struct MlpPrepArgs {
   XentCopyArgs copy[kMlpCopies];
+  uint32_t* zero;  // words to clear (k_mlp_prep), in blocks behind the copies'
+  int64_t zeros;
+  __host__ __device__ int64_t zero_blocks() const { return (zeros + 1023) / 1024; }
   __host__ __device__ int64_t blocks() const {
     int64_t n = 0;
     for (const XentCopyArgs& c : copy) n += c.blocks();
@@ -110,6 +199,16 @@ __device__ __forceinline__ void mlp_copy_block(const MlpPrepArgs& p, int64_t b, 
 template <typename T>
 __global__ void __launch_bounds__(256) k_mlp_prep(MlpPrepArgs p) {
   __shared__ __attribute__((aligned(16))) T tile[kCopyTile<T>];
+  if constexpr (kRanged<T>) {
+    const int64_t copies = p.blocks();
+    if (blockIdx.x >= copies) {
+      const int64_t first = (blockIdx.x - copies) * 1024 + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (first + 256 * i < p.zeros) p.zero[first + 256 * i] = 0u;
+      return;
+    }
+  }
   mlp_copy_block<T>(p, blockIdx.x, tile);
 }
 
@@ -186,6 +285,12 @@ __device__ __forceinline__ void put_transposed(T* col, int64_t ld, const f32x4 (
 // ---------------------------------------------------------------------------
 // Forward: both projections and the activation.
 // ---------------------------------------------------------------------------
+// What the waves of the first launch leave (fp16): whether a part of a row was
+// out of range, for each wave, and the largest magnitudes of each part.
+struct UpRange {
+  uint32_t* outside;       // [waves]
+  uint32_t* parts;         // [2 tiles_n][n]
+};
 struct MlpUpArgs {
   const void *X, *G, *U;   // n x k, f x k, f x k, rows of whole k-tiles
   int64_t ldx, ldw;        // row strides in bytes
@@ -200,6 +305,8 @@ struct MlpUpArgs {
   int act;
   int32_t* d_status;
   int32_t status_bits;
+  HeldRange* range;        // fp16
+  UpRange seen;
   MlpPrepArgs side;        // copies that go along
 };
 
@@ -229,14 +336,18 @@ __device__ __forceinline__ bool save_projections(const f32x16 (&acc)[FM][2 * FH]
   return found & kNonfiniteMask<S>;
 }
 
-template <typename T, int TM, int TN>
+template <typename T, int TM, int TN, bool AGAIN>
 struct UpEpilogue {
   using A = Acc<T, TM, TN>;
   static constexpr int FH = A::FN / 2;  // 32-column blocks of a, then as many of b
   static constexpr int kStores = A::FM * FH * (sizeof(T) == 2 ? 2 : 4);
   const MlpUpArgs& p;
   const TileRun& run;
+  const uint32_t* row_keys;  // AGAIN: of the tile's rows, in LDS
+  bool outside = false;      // whether the wave saw a part of a row that is out of range
   LanePlace<TM, TN> at;
+  __device__ __forceinline__ UpEpilogue(const MlpUpArgs& p, const TileRun& run, const uint32_t* row_keys)
+      : p(p), run(run), row_keys(row_keys) {}
   __device__ __forceinline__ void load(int) {}
   __device__ __forceinline__ void settle() {}
   __device__ __forceinline__ void store(int j, A& acc) {
@@ -271,6 +382,9 @@ struct UpEpilogue {
 #pragma unroll
       for (int fm = 0; fm < A::FM; ++fm) {
         T* row = reinterpret_cast<T*>(p.h) + (row0 + fm * 32) * p.ldh + col0;
+        uint32_t key = 0;
+        int unit = 0;
+        if constexpr (AGAIN) unit = held_exp(row_keys[at.wr + at.lr + fm * 32]);
 #pragma unroll
         for (int fn = 0; fn < FH; ++fn) {
           f32x4 v[4];
@@ -278,27 +392,29 @@ struct UpEpilogue {
           for (int g = 0; g < 4; ++g)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
+            {
               v[g][e] = Act<decltype(act)::value>(acc.v[fm][fn][4 * g + e]).value * acc.v[fm][fn + FH][4 * g + e];
+              if constexpr (AGAIN)
+                v[g][e] = scaled(v[g][e], unit);
+              else if constexpr (kRanged<T>)
+                key = max_u32(key, range_key(v[g][e]));
+            }
+          if constexpr (kRanged<T> && !AGAIN) settle_key(key);
           put_padded<T>(row + 32 * fn, at.h, v);
+        }
+        if constexpr (kRanged<T> && !AGAIN) {
+          const int64_t r = row0 + fm * 32;
+          key = row_part(key);
+          if (r < p.n && at.h == 0) p.seen.parts[(2 * tn + (at.wc > 0)) * p.n + r] = key;
+          outside |= __any(r < p.n && out_of_range(key));
         }
       }
     });
   }
 };
 
-template <typename T, int TM, int TN>
-__global__ void __launch_bounds__(kThreads, 1) k_mlp_up(MlpUpArgs p) {
-  const int tiles = p.tiles_m * p.tiles_n;
-  if ((int)blockIdx.x >= tiles) {
-    // A work-group beyond the tiles (mlp_up_of).
-    const int64_t blocks = p.side.blocks();
-    for (int64_t b = blockIdx.x - tiles; b < blocks; b += gridDim.x - tiles) {
-      mlp_copy_block<T>(p.side, b, reinterpret_cast<T*>(Stages<TM, TN>::s0()));
-      __syncthreads();
-    }
-    return;
-  }
-  const TileRun run(tiles, (int)gridDim.x < tiles ? (int)gridDim.x : tiles);
+template <typename T, int TM, int TN, class Epilogue>
+__device__ __forceinline__ void up_tiles(const MlpUpArgs& p, const TileRun& run, Epilogue& epilogue) {
   // Wave w copies TN / 4 right-hand rows of a tile: even waves rows of Wg,
   // odd ones rows of Wu, for the columns of the waves w / 2 and w / 2 + 2.
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -316,7 +432,71 @@ __global__ void __launch_bounds__(kThreads, 1) k_mlp_up(MlpUpArgs p) {
                           (int)(p.n - row0 < TM ? p.n - row0 : TM), own + (int)(left < TN / 4 ? left : TN / 4), 0,
                           p.ktiles};
       },
-      UpEpilogue<T, TM, TN>{p, run});
+      epilogue);
+}
+
+// The second launch (fp16): joins what the waves of the first saw, and makes
+// those tiles again that have a row out of range, in its unit.
+template <typename T, int TM, int TN>
+__device__ __forceinline__ void up_again(const MlpUpArgs& p) {
+  __shared__ uint32_t row_keys[TM];
+  const int tiles = p.tiles_m * p.tiles_n;
+  const TileRun run(tiles);
+  uint32_t seen = 0;
+  for (int i = threadIdx.x; i < (int)gridDim.x * (kThreads / 64); i += kThreads) seen |= p.seen.outside[i];
+  const bool outside = __syncthreads_or(seen != 0);
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.range->outside = outside;
+  if (!outside) return;
+  for (int j = 0; j < run.count; ++j) {
+    int tm, tn;
+    grouped_tile(run.at(j), p.tiles_m, p.tiles_n, tm, tn);
+    // Each row's parts, shared by kThreads / TM threads.
+    const int r = threadIdx.x % TM;
+    const int64_t row = (int64_t)tm * TM + r;
+    if ((int)threadIdx.x < TM) row_keys[r] = 0;
+    __syncthreads();
+    uint32_t key = 0;
+    if (row < p.n) {
+#pragma unroll 16
+      for (int i = threadIdx.x / TM; i < 2 * p.tiles_n; i += kThreads / TM) key = max_u32(key, p.seen.parts[i * p.n + row]);
+      atomicMax(&row_keys[r], key);
+    }
+    __syncthreads();
+    key = row_keys[r];
+    if (tn == 0 && (int)threadIdx.x < TM && row < p.n) p.range->row[row] = key;
+    if (!__syncthreads_or(out_of_range(key))) continue;
+    TileRun one = run;
+    one.first = run.at(j);
+    one.count = 1;
+    UpEpilogue<T, TM, TN, true> epilogue(p, one, row_keys);
+    up_tiles<T, TM, TN>(p, one, epilogue);
+    // All waves have read the keys.
+    __syncthreads();
+  }
+}
+
+template <typename T, int TM, int TN, bool AGAIN = false>
+__global__ void __launch_bounds__(kThreads, 1) k_mlp_up(MlpUpArgs p) {
+  if constexpr (AGAIN) {
+    up_again<T, TM, TN>(p);
+  } else {
+    const int tiles = p.tiles_m * p.tiles_n;
+    if ((int)blockIdx.x >= tiles) {
+      // A work-group beyond the tiles (mlp_up_of).
+      const int64_t blocks = p.side.blocks();
+      for (int64_t b = blockIdx.x - tiles; b < blocks; b += gridDim.x - tiles) {
+        mlp_copy_block<T>(p.side, b, reinterpret_cast<T*>(Stages<TM, TN>::s0()));
+        __syncthreads();
+      }
+      return;
+    }
+    const TileRun run(tiles, (int)gridDim.x < tiles ? (int)gridDim.x : tiles);
+    UpEpilogue<T, TM, TN, false> epilogue(p, run, nullptr);
+    up_tiles<T, TM, TN>(p, run, epilogue);
+    if constexpr (kRanged<T>) {
+      if ((threadIdx.x & 63) == 0) p.seen.outside[blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)] = epilogue.outside;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -406,6 +586,7 @@ struct MlpDzArgs {
   void* ht;                // f_pad x n_pad, row stride t_ld
   int64_t f_pad, z_ld, t_ld;
   int act;
+  HeldRange* range;        // fp16
   MlpPrepArgs side;        // copies that go along
 };
 
@@ -425,7 +606,7 @@ __device__ __forceinline__ f32x4 load_quad(const T* s) {
   }
 }
 
-template <typename T, int TM, int TN>
+template <typename T, int TM, int TN, bool AGAIN>
 struct MlpDzEpilogue {
   using A = Acc<T, TM, TN>;
   // A wave with 64 rows of 16-bit results turns 32 columns of them in LDS, so
@@ -448,12 +629,23 @@ struct MlpDzEpilogue {
   int64_t row0, col0;
   int rows, cols;  // of this wave's part that exist
   bool whole;
+  // The largest of each row's part of da and db and of h, as keys; AGAIN: the
+  // units of the rows, of all da and db and of all h.
+  uint32_t row_key[A::FM], h_key = 0;
+  int row_exp[A::FM], dz_exp = 0, h_exp = 0;
   __device__ __forceinline__ MlpDzEpilogue(const MlpDzArgs& p, int tm, int tn) : p(p) {
     row0 = (int64_t)tm * TM + at.wr;
     col0 = (int64_t)tn * TN + at.wc;
     rows = (int)(p.n - row0 < TM / 2 ? p.n - row0 : TM / 2);
     cols = (int)(p.f - col0 < TN / 2 ? p.f - col0 : TN / 2);
     whole = rows == TM / 2 && cols == TN / 2;
+#pragma unroll
+    for (int fm = 0; fm < A::FM; ++fm) {
+      row_key[fm] = 0;
+      row_exp[fm] = 0;
+      if constexpr (AGAIN)
+        if (fm * 32 + at.lr < rows) row_exp[fm] = held_exp(p.range->row[row0 + fm * 32 + at.lr]);
+    }
   }
   __device__ __forceinline__ bool exists(int fm, int fn, int g, int e) const {
     return fm * 32 + at.lr < rows && 32 * fn + 8 * g + 4 * at.h + e < cols;
@@ -486,7 +678,7 @@ struct MlpDzEpilogue {
       load(T{});
   }
   template <int ACT>
-  __device__ __forceinline__ void make(A& acc, int fm, int fn, Block& o) const {
+  __device__ __forceinline__ void make(A& acc, int fm, int fn, Block& o) {
     Saved v;
     fetch(fm, fn, v);
     if (!whole) {
@@ -506,10 +698,53 @@ struct MlpDzEpilogue {
         o.da[g][e] = dh * v.b[g][e] * s.slope;
         o.db[g][e] = dh * s.value;
         o.h[g][e] = s.value * v.b[g][e];
+        if constexpr (kRanged<T> && !AGAIN) {
+          row_key[fm] = max_u32(row_key[fm], max_u32(range_key(o.da[g][e]), range_key(o.db[g][e])));
+          h_key = max_u32(h_key, range_key(o.h[g][e]));
+        }
       }
+    if constexpr (kRanged<T> && !AGAIN) {
+      settle_key(row_key[fm]);
+      settle_key(h_key);
+    }
     T* dz = reinterpret_cast<T*>(p.dz) + (row0 + fm * 32 + at.lr) * p.z_ld + col0 + 32 * fn;
-    put_padded<T>(dz, at.h, o.da);
-    put_padded<T>(dz + p.f_pad, at.h, o.db);
+    if constexpr (AGAIN) {
+      f32x4 in_row[2][4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          in_row[0][g][e] = scaled(o.da[g][e], row_exp[fm]);
+          in_row[1][g][e] = scaled(o.db[g][e], row_exp[fm]);
+          o.da[g][e] = scaled(o.da[g][e], dz_exp);
+          o.db[g][e] = scaled(o.db[g][e], dz_exp);
+          o.h[g][e] = scaled(o.h[g][e], h_exp);
+        }
+      put_padded<T>(dz, at.h, in_row[0]);
+      put_padded<T>(dz + p.f_pad, at.h, in_row[1]);
+    } else {
+      put_padded<T>(dz, at.h, o.da);
+      put_padded<T>(dz + p.f_pad, at.h, o.db);
+    }
+  }
+  // What the wave saw, once all its blocks are made.
+  __device__ __forceinline__ void leave_keys() const {
+    uint32_t key = 0;
+    bool outside = false;
+#pragma unroll
+    for (int fm = 0; fm < A::FM; ++fm) {
+      const uint32_t part = row_part(row_key[fm]);
+      const bool valid = fm * 32 + at.lr < rows;
+      if (valid && at.h == 0) atomicMax(&p.range->row[row0 + fm * 32 + at.lr], part);
+      outside |= __any(valid && out_of_range(part));
+      key = max_u32(key, part);
+    }
+    const uint32_t dz = wave_max(key), h = wave_max(h_key);
+    if ((threadIdx.x & 63) == 0) {
+      if (outside) atomicOr(&p.range->outside, 1u);
+      atomicMax(&p.range->dz[blockIdx.x % kRangeSlots], dz);
+      atomicMax(&p.range->h[blockIdx.x % kRangeSlots], h);
+    }
   }
   // lds: the wave's own 3 x 32 rows of kTurnLd.
   __device__ __forceinline__ void store(A& acc, T* lds) {
@@ -568,20 +803,15 @@ struct MlpDzEpilogue {
   }
 };
 
-template <typename T, int TM, int TN>
-__global__ void __launch_bounds__(kThreads, 2) k_mlp_dz(MlpDzArgs p) {
-  const int tiles = p.tiles_m * p.tiles_n;
-  if ((int)blockIdx.x >= tiles)
-    return mlp_copy_block<T>(p.side, blockIdx.x - tiles, reinterpret_cast<T*>(Stages<TM, TN, 2>::s0()));
-  int tm, tn;
-  grouped_tile(xcd_order(blockIdx.x, tiles), p.tiles_m, p.tiles_n, tm, tn);
+template <typename T, int TM, int TN, bool AGAIN>
+__device__ __forceinline__ void dz_tile(const MlpDzArgs& p, int tm, int tn, int dz_exp, int h_exp) {
   const int64_t row0 = (int64_t)tm * TM;
   const StreamTile tile{reinterpret_cast<const char*>(p.dY) + row0 * p.ldy,
                         reinterpret_cast<const char*>(p.WT) + (int64_t)tn * TN * p.ldw,
                         (int)(p.n - row0 < TM ? p.n - row0 : TM), TN, 0, p.ktiles};
   Acc<T, TM, TN> acc;
   pair_tile<T, TM, TN>(tile, p.ldy, p.ldw, acc);
-  using Epilogue = MlpDzEpilogue<T, TM, TN>;
+  using Epilogue = MlpDzEpilogue<T, TM, TN, AGAIN>;
   char* lds = nullptr;
   if constexpr (Epilogue::kTurn) {
     // All waves' copies have landed and their reads are over.
@@ -591,7 +821,50 @@ __global__ void __launch_bounds__(kThreads, 2) k_mlp_dz(MlpDzArgs p) {
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     lds = (w & 1 ? S::s1() : S::s0()) + (w >> 1) * (96 * Epilogue::kTurnLd * sizeof(T));
   }
-  Epilogue(p, tm, tn).store(acc, reinterpret_cast<T*>(lds));
+  Epilogue epilogue(p, tm, tn);
+  epilogue.dz_exp = dz_exp;
+  epilogue.h_exp = h_exp;
+  epilogue.store(acc, reinterpret_cast<T*>(lds));
+  if constexpr (kRanged<T> && !AGAIN) epilogue.leave_keys();
+}
+
+// The second launch (fp16): leaves the units of all da and db and of all h for
+// the products, and makes those tiles again that are out of range.
+template <typename T, int TM, int TN>
+__device__ __forceinline__ void dz_again(const MlpDzArgs& p) {
+  static_assert(kRangeSlots == 64, "a lane each");
+  const int lane = threadIdx.x & 63;
+  const uint32_t dz_key = p.range->dz[lane], h_key = p.range->h[lane], outside = p.range->outside;
+  const int dz_exp = wave_held_exp(dz_key), h_exp = wave_held_exp(h_key);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.range->dz_exp = dz_exp;
+    p.range->h_exp = h_exp;
+  }
+  const bool all = dz_exp != 0 || h_exp != 0;
+  if (!all && !outside) return;
+  const int tiles = p.tiles_m * p.tiles_n;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    int tm, tn;
+    grouped_tile(xcd_order(t, tiles), p.tiles_m, p.tiles_n, tm, tn);
+    const int64_t row = (int64_t)tm * TM + threadIdx.x;
+    const bool mine = (int)threadIdx.x < TM && row < p.n && out_of_range(p.range->row[row]);
+    // Also a barrier behind the reads of the tile before.
+    if (__syncthreads_or(mine) || all) dz_tile<T, TM, TN, true>(p, tm, tn, dz_exp, h_exp);
+  }
+}
+
+template <typename T, int TM, int TN, bool AGAIN = false>
+__global__ void __launch_bounds__(kThreads, 2) k_mlp_dz(MlpDzArgs p) {
+  if constexpr (AGAIN) {
+    dz_again<T, TM, TN>(p);
+  } else {
+    const int tiles = p.tiles_m * p.tiles_n;
+    if ((int)blockIdx.x >= tiles)
+      return mlp_copy_block<T>(p.side, blockIdx.x - tiles, reinterpret_cast<T*>(Stages<TM, TN, 2>::s0()));
+    int tm, tn;
+    grouped_tile(xcd_order(blockIdx.x, tiles), p.tiles_m, p.tiles_n, tm, tn);
+    dz_tile<T, TM, TN, false>(p, tm, tn, 0, 0);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -618,9 +891,20 @@ struct MlpGradArgs {
   int x_ktiles, splits;
   float* parts;               // splits > 1: [splits][x.tiles_m TM][x.tiles_n TN]
   int extra;                  // DhRun's
+  const HeldRange* range;     // fp16: of x's rows and, with w, of its operands
   int32_t* d_status;
   int32_t status_bits;
 };
+
+// An accumulator's values times a power of two, per 32 rows.
+template <typename T, int TM, int TN>
+__device__ __forceinline__ void take_back(Acc<T, TM, TN>& acc, int fm, int held) {
+  using A = Acc<T, TM, TN>;
+#pragma unroll
+  for (int fn = 0; fn < A::FN; ++fn)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc.v[fm][fn][e] = scaled(acc.v[fm][fn][e], -held);
+}
 
 template <typename T, int TM, int TN>
 __device__ __forceinline__ void product_store(const MlpProduct& o, int tm, int tn, const LanePlace<TM, TN>& at,
@@ -673,11 +957,19 @@ struct WeightEpilogue {
   static constexpr int kStores = 0;  // rows and columns past the result store nothing
   const MlpGradArgs& p;
   const TileRun& run;
+  int dz_exp, h_exp;  // fp16
   LanePlace<TM, TN> at;
   __device__ __forceinline__ void load(int) {}
   __device__ __forceinline__ void settle() {}
   __device__ __forceinline__ void store(int j, Acc<T, TM, TN>& acc) {
     const WeightTile t(p, run.at(j));
+    if constexpr (kRanged<T>) {
+      const int held = t.which == 2 ? h_exp : dz_exp;
+      if (held != 0) {
+#pragma unroll
+        for (int fm = 0; fm < Acc<T, TM, TN>::FM; ++fm) take_back<T, TM, TN>(acc, fm, held);
+      }
+    }
     product_store<T, TM, TN>(p.w[t.which], t.tm, t.tn, at, acc, p.d_status, p.status_bits);
   }
 };
@@ -688,6 +980,7 @@ struct SplitEpilogue {
   static constexpr int kStores = 0;
   const MlpGradArgs& p;
   const DhRun& run;
+  bool outside;  // fp16: whether rows have units of their own
   LanePlace<TM, TN> at;
   __device__ __forceinline__ void load(int) {}
   __device__ __forceinline__ void settle() {}
@@ -695,6 +988,14 @@ struct SplitEpilogue {
     const int per = p.x.tiles_m * p.x.tiles_n, i = run.at(j);
     int tm, tn;
     grouped_tile(i % per, p.x.tiles_m, p.x.tiles_n, tm, tn);
+    if constexpr (kRanged<T>) {
+      if (outside) {
+        const int64_t row = (int64_t)tm * TM + at.wr + at.lr;
+#pragma unroll
+        for (int fm = 0; fm < A::FM; ++fm)
+          take_back<T, TM, TN>(acc, fm, row + fm * 32 < p.x.rows ? held_exp(p.range->row[row + fm * 32]) : 0);
+      }
+    }
     if (p.splits == 1) return product_store<T, TM, TN>(p.x, tm, tn, at, acc, p.d_status, p.status_bits);
     const int64_t ld = (int64_t)p.x.tiles_n * TN;
     float* out = p.parts + ((int64_t)(i / per) * p.x.tiles_m * TM + (int64_t)tm * TM + at.wr + at.lr) * ld + tn * TN +
@@ -716,6 +1017,15 @@ struct SplitEpilogue {
 template <typename T, int TM, int TN>
 __global__ void __launch_bounds__(kThreads, 1) k_mlp_products(MlpGradArgs p) {
   const int w_tiles = p.w_tiles[kMlpProducts - 1];
+  bool outside = false;
+  int dz_exp = 0, h_exp = 0;
+  if constexpr (kRanged<T>) {
+    outside = p.range->outside != 0;
+    if (w_tiles > 0) {
+      dz_exp = p.range->dz_exp;
+      h_exp = p.range->h_exp;
+    }
+  }
   if (w_tiles > 0) {
     const TileRun run(w_tiles);
     stream_tiles<T, TM, TN>(
@@ -724,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mlp_products(MlpGradArgs p) {
           const WeightTile t(p, run.at(j));
           return product_tile<T, TM, TN>(p.w[t.which], p.w_ld, p.w_ld, t.tm, t.tn, 0, p.w_ktiles);
         },
-        WeightEpilogue<T, TM, TN>{p, run});
+        WeightEpilogue<T, TM, TN>{p, run, dz_exp, h_exp});
     // All reads of the stages are over before they are filled again.
     lds_barrier();
   }
@@ -740,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mlp_products(MlpGradArgs p) {
         const int kt1 = (int)((int64_t)p.x_ktiles * (split + 1) / p.splits);
         return product_tile<T, TM, TN>(p.x, p.x_ldl, p.x_ldr, tm, tn, kt0, kt1 - kt0);
       },
-      SplitEpilogue<T, TM, TN>{p, run});
+      SplitEpilogue<T, TM, TN>{p, run, outside});
 }
 
 // The splits' sum, rounded: a thread per 16 bytes of a row.
@@ -981,34 +1291,51 @@ constexpr TileShape product_shape(int tile) {
                               : TileShape{64, 128};
 }
 
-template <typename T> hipError_t launch_mlp_up(const MlpUpArgs& a, int tile, hipStream_t s);
-template <typename T> hipError_t launch_mlp_dz(const MlpDzArgs& a, int tile, hipStream_t s);
+// again: the second launch for operands out of range (fp16).
+template <typename T> hipError_t launch_mlp_up(const MlpUpArgs& a, int tile, bool again, hipStream_t s);
+template <typename T> hipError_t launch_mlp_dz(const MlpDzArgs& a, int tile, bool again, hipStream_t s);
 template <typename T> hipError_t launch_mlp_products(const MlpGradArgs& a, int tile, hipStream_t s);
 template <typename T> hipError_t launch_mlp_dot_up(const MlpDotUpArgs& a, hipStream_t s);
 template <typename T> hipError_t launch_mlp_dot_down(const MlpDotDownArgs& a, hipStream_t s);
 
 #define NS_MLP_TILE(K, SHAPE, TILE, GRID) \
   hipLaunchKernelGGL((K<T, SHAPE<T>(TILE).m, SHAPE<T>(TILE).n>), GRID, dim3(kThreads), 0, s, a)
-template <typename T>
-hipError_t mlp_up_of(const MlpUpArgs& a, int tile, hipStream_t s) {
-  // With copies the tiles are fewer than the compute units; the others take
-  // the copies.
-  const dim3 grid = a.side.blocks() > 0 ? dim3(kXentGroups) : xent_grid((int64_t)a.tiles_m * a.tiles_n);
+#define NS_MLP_PASS(K, SHAPE, TILE, AGAIN, GRID) \
+  hipLaunchKernelGGL((K<T, SHAPE<T>(TILE).m, SHAPE<T>(TILE).n, AGAIN>), GRID, dim3(kThreads), 0, s, a)
+template <typename T, bool AGAIN>
+void mlp_up_pass(const MlpUpArgs& a, int tile, dim3 grid, hipStream_t s) {
   if (tile == kTileLarge)
-    NS_MLP_TILE(k_mlp_up, up_shape, kTileLarge, grid);
+    NS_MLP_PASS(k_mlp_up, up_shape, kTileLarge, AGAIN, grid);
   else if (tile == kTileSmall || sizeof(T) == 4)
-    NS_MLP_TILE(k_mlp_up, up_shape, kTileSmall, grid);
+    NS_MLP_PASS(k_mlp_up, up_shape, kTileSmall, AGAIN, grid);
   else
-    NS_MLP_TILE(k_mlp_up, up_shape, kTileShort, grid);
-  return hipGetLastError();
+    NS_MLP_PASS(k_mlp_up, up_shape, kTileShort, AGAIN, grid);
 }
 template <typename T>
-hipError_t mlp_dz_of(const MlpDzArgs& a, int tile, hipStream_t s) {
-  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n + a.side.blocks()));
+hipError_t mlp_up_of(const MlpUpArgs& a, int tile, bool again, hipStream_t s) {
+  const dim3 tiles = xent_grid((int64_t)a.tiles_m * a.tiles_n);
+  // With copies the tiles are fewer than the compute units; the others take
+  // the copies.
+  if (!again) mlp_up_pass<T, false>(a, tile, a.side.blocks() > 0 ? dim3(kXentGroups) : tiles, s);
+  if constexpr (kRanged<T>) {
+    if (again) mlp_up_pass<T, true>(a, tile, tiles, s);
+  }
+  return hipGetLastError();
+}
+template <typename T, bool AGAIN>
+void mlp_dz_pass(const MlpDzArgs& a, int tile, dim3 grid, hipStream_t s) {
   if (tile == kTileLarge)
-    NS_MLP_TILE(k_mlp_dz, dz_shape, kTileLarge, grid);
+    NS_MLP_PASS(k_mlp_dz, dz_shape, kTileLarge, AGAIN, grid);
   else
-    NS_MLP_TILE(k_mlp_dz, dz_shape, kTileSmall, grid);
+    NS_MLP_PASS(k_mlp_dz, dz_shape, kTileSmall, AGAIN, grid);
+}
+template <typename T>
+hipError_t mlp_dz_of(const MlpDzArgs& a, int tile, bool again, hipStream_t s) {
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  if (!again) mlp_dz_pass<T, false>(a, tile, dim3((unsigned)(tiles + a.side.blocks())), s);
+  if constexpr (kRanged<T>) {
+    if (again) mlp_dz_pass<T, true>(a, tile, dim3((unsigned)std::min<int64_t>(tiles, 2 * kXentGroups)), s);
+  }
   return hipGetLastError();
 }
 template <typename T>
@@ -1054,12 +1381,12 @@ hipError_t mlp_dot_down_of(const MlpDotDownArgs& a, hipStream_t s) {
 
 #define NS_MLP_LAUNCHERS(T)                                                          \
   template <>                                                                        \
-  hipError_t launch_mlp_up<T>(const MlpUpArgs& a, int tile, hipStream_t s) {         \
-    return mlp_up_of<T>(a, tile, s);                                                 \
+  hipError_t launch_mlp_up<T>(const MlpUpArgs& a, int tile, bool again, hipStream_t s) { \
+    return mlp_up_of<T>(a, tile, again, s);                                          \
   }                                                                                  \
   template <>                                                                        \
-  hipError_t launch_mlp_dz<T>(const MlpDzArgs& a, int tile, hipStream_t s) {         \
-    return mlp_dz_of<T>(a, tile, s);                                                 \
+  hipError_t launch_mlp_dz<T>(const MlpDzArgs& a, int tile, bool again, hipStream_t s) { \
+    return mlp_dz_of<T>(a, tile, again, s);                                          \
   }                                                                                  \
   template <>                                                                        \
   hipError_t launch_mlp_products<T>(const MlpGradArgs& a, int tile, hipStream_t s) { \
