@@ -7,7 +7,7 @@
 // are written once, 22 bytes an element with 16-bit p and g and fp32 moments,
 // 10 with 8-bit moments.  Measured (MI355X): 38.6M fp32 masters with bf16
 // gradients and copies 214 us (5.0 TB/s), 524M bf16 parameters with 8-bit
-// moments 1120 us (4.7), as a copy of that size; 50 vectors of 768 6 us.
+// moments 1123 us (4.7), as a copy of that size; 50 vectors of 768 6 us.
 //
 // The tensors come as a table in the kernel's arguments (no copy to the
 // device, no workspace), so a launch takes up to kAdamwItems of them, cut into
@@ -227,8 +227,9 @@ __device__ __forceinline__ float root_of(float v) {
 }
 // Of a moment below kRootLeast, whose residual would fall among the subnormal
 // numbers and which the reciprocal root does not take below 2^-126.  Only where
-// the least of eight moments is one (or zero), which costs 6 us of 1123 at 524M
-// 8-bit moments; scaling every moment costs 20.
+// the least of eight moments but zeros is one, which costs 6 us of 1123 at 524M
+// 8-bit moments; scaling every moment costs 20, and going there for zeros took
+// 1237 us where most moments are (rows of an embedding that no token met).
 __device__ __forceinline__ float root_of_small(float v) { return root_of(v * 0x1p64f) * 0x1p-32f; }
 
 // The moments' update, each operation rounded on its own (no fused
@@ -319,9 +320,18 @@ static __global__ void __launch_bounds__(kAdamwThreads) k_adamw(AdamwArgs a) {
         least = fminf(least, v[k]);
       }
       if (least < kRootLeast) {
+        // Zeros, whose root is right, wrap to the top.
+        uint32_t key = ~0u;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (v[k] < kRootLeast) root[j][k] = root_of_small(v[k]);
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t u = __float_as_uint(v[k]) - 1u;
+          key = u < key ? u : key;
+        }
+        if (key < __float_as_uint(kRootLeast) - 1u) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (v[k] < kRootLeast) root[j][k] = root_of_small(v[k]);
+        }
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
