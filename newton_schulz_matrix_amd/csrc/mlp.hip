@@ -117,7 +117,7 @@ const TileCost& best_tile(const TileCost (&costs)[N], int64_t rows, int64_t cols
 // so many us on `slots` places for a work-group: where the idle ones get
 // through them in that time.  (A launch of its own moves them faster, eight
 // work-groups a compute unit, but nothing else runs meanwhile.  Along,
-// 1003 x 2048 x 1407 in fp16 takes 33.5 us forward instead of 42.0 and
+// 1003 x 2048 x 1407 in fp16, without its second launch, takes 33.5 us forward instead of 42.0 and
 // 128 x 2048 x 5461 91.4 us backward instead of 99.3; with copies counted at
 // 0.3 us, where there are few idle places for many, 128 x 2048 x 5461 takes
 // 53.3 us forward instead of 42.2.)

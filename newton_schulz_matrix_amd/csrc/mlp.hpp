@@ -20,9 +20,11 @@
 //
 // h, da and db are rounded to the operands' type, because they are operands
 // themselves: half a step per term of the sums, of the size of the result's
-// own rounding.  a and b are left for backward in fp32 (or, at half the
-// memory, rounded to the operands' type, which doubles the gradients' error:
-// 0.0035 against 0.0023 relative in bf16, results alone rounded 0.0017).
+// own rounding (bf16 results 0.0023 off instead of 0.0017).  Held as two numbers
+// of that type each they would double the matrix work of y, dx and all weights'
+// gradients.  a and b are left for backward in fp32 (or, at half the
+// memory, rounded to the operands' type, which takes the gradients' error to
+// 0.0035 in bf16).
 //
 // fp16 operands may lie outside the type's numbers where the results do not
 // (see HeldRange): each product's epilogue also looks for the largest of what it
@@ -33,8 +35,8 @@
 // stays in fp32.
 //
 // Measured (MI355X): 8192 x 4096 x 14336 in bf16 2.43 ms forward (1190
-// TFLOP/s), 2.67 with a and b left, 5.29 backward (1092); 1003 x 2048 x 1407 in
-// fp16 33, 38 and 86 us; 300 x 1000 x 2731 in fp32 73, 74 and 130 us; one row of
+// TFLOP/s), 2.7 with a and b left, 5.3 backward (1090); 1003 x 2048 x 1407 in
+// fp16 34, 38 and 86 us; 300 x 1000 x 2731 in fp32 73, 74 and 130 us; one row of
 // 4096 x 14336 in bf16 65 us (5.4 TB/s), 48 rows 77.
 #pragma once
 

@@ -20,7 +20,9 @@
 //
 // Measured (MI355X): forward 8192 x 4096 in bf16 46 us (5.8 TB/s with its inputs
 // in the cache, 55 us and 4.9 without); backward 16384 x 768 with fp32
-// parameters 38 us (4.0 TB/s) and 5 for the join, 5003 x 1001 in fp32 30 and 4.
+// parameters 38 us (4.0 TB/s) and 5 for the join, 5003 x 1001 in fp32 30 and 4,
+// 8192 x 4096 in bf16 102 both (3.9 TB/s).  The norm alone, 8192 x 4096: 27 us
+// forward (5.0 TB/s), 45 backward (4.4).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -228,8 +230,8 @@ __global__ void __launch_bounds__(kNormThreads<TPR>) k_resnorm_fwd(ResNormFwdArg
 }
 
 // Rows of less than a vector or too long for registers: three passes over the
-// row, the later two served by the cache.  S may be X and Y may be Z: the
-// last pass reads an element and then writes it.
+// row, the later two served by the cache (4096 x 16384 in bf16 508 us, 1.1 TB/s).
+// S may be X and Y may be Z: the last pass reads an element and then writes it.
 template <typename IO, typename PT>
 __global__ void __launch_bounds__(1024) k_resnorm_fwd_long(ResNormFwdArgs p) {
   __shared__ float sh[16];
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(kNormThreads<TPR>, 2) k_resnorm_bwd(ResNormBwd
 
 // Rows of less than a vector or too long for registers: first each row's
 // mean_j(u shat), then the column sums from it, then dx and dz (which may be
-// written over ds and dy).
+// written over ds and dy).  4096 x 16384 in bf16 1240 us, 0.65 TB/s.
 template <typename IO, typename PT>
 struct ResNormElement {
   const ResNormBwdArgs& p;
