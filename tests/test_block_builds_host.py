@@ -11,6 +11,7 @@ import os
 import pytest
 import torch
 
+import newton_schulz_matrix_amd as nsa
 from newton_schulz_matrix_amd import _binding as B
 from newton_schulz_matrix_amd import build as nsbuild
 from resnorm_cases import MORE_WIDTHS, build_of
@@ -26,6 +27,19 @@ def test_the_widths_reach_every_build_of_the_residual_norms():
     assert every - covered == set()
     # Element by element: less than a vector, and too long.
     assert any(c < 4 for c in WIDTHS) and any(c > 8192 for c in WIDTHS)
+
+
+@built
+def test_the_range_cases_reach_every_fp16_build_of_the_gated_mlp():
+    from test_gpu_gated_mlp_range import SHAPES
+
+    def builds(sizes, aligned):
+        return {(e, backward) for n, d, f in sizes for backward in (False, True)
+                for e in nsa.plan_gated_mlp(n, d, f, torch.float16, aligned, backward) if e.startswith(("again", "products", "join"))}
+
+    sweep = itertools.product([5, 9, 48, 129, 300, 513, 1003, 3000, 8192, 20000], [1, 64, 77, 768, 4096], [1, 64, 203, 1407, 2048, 14336])
+    every = set().union(*(builds([size], aligned) for size in sweep for aligned in (True, False)))
+    assert every and every - builds(SHAPES, True) == set()
 
 
 @built

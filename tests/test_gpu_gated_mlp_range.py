@@ -52,7 +52,10 @@ def test_activations_of_any_finite_number(act, dtype):
 # fp16: the products' own operands h, da and db beyond the type's numbers.
 # ---------------------------------------------------------------------------
 TINY = 2.0 ** -25
-SHAPES = [(5, 64, 128), (9, 72, 136), (40, 192, 320), (48, 256, 1411), (130, 128, 256), (300, 200, 703), (700, 264, 512), (1003, 520, 1407)]
+# The last three: several tiles a work-group in each launch, and the largest
+# tiles (tests/test_block_builds_host.py checks that every fp16 build is reached).
+SHAPES = [(5, 64, 128), (9, 72, 136), (40, 192, 320), (48, 256, 1411), (130, 128, 256), (300, 200, 703), (700, 264, 512), (1003, 520, 1407),
+          (3000, 264, 3001), (3000, 1536, 264), (700, 264, 3001)]
 
 
 def _unit(peak):
@@ -176,8 +179,10 @@ def test_fp16_gradients_of_operands_past_the_type(n, d, f, kind):
               "dwg": sums([(o["da"].T, dae.T, x)], n, o["dwg"]), "dwu": sums([(o["db"].T, dbe.T, x)], n, o["dwu"]),
               "dwd": sums([(o["h"].T, he.T, dy)], n, o["dwd"].T).T}
     for g, name in zip(got, ("dx", "dwg", "dwu", "dwd")):
-        fits = np.abs(o[name]) < 65000  # results past the type are infinite, as they should be
-        assert fits.mean() > 0.9, name
+        # Results past the type are infinite, as they should be; of the oracle's
+        # more than half are within it (0.61 of dw_gate at 3000 x 1536 x 264).
+        fits = np.abs(o[name]) < 65000
+        assert fits.mean() > 0.5, name
         _close(g[torch.from_numpy(fits).to(dev)], o[name][fits], bounds[name][fits], name)
     assert int(st.item()) == 0 or not all((np.abs(o[k]) < 65000).all() for k in ("dx", "dwg", "dwu", "dwd"))
     dx, *_ = nsa.gated_mlp_backward(t["dy"], t["x"], t["wg"], t["wu"], t["wd"], gate, up, activation=act, need_dw=False)
@@ -227,3 +232,25 @@ def test_fp16_range_captured_and_replayed():
         got = [o.clone() for o in out]
         want = step()
         assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(got, want)), kind
+
+
+def test_fp16_range_on_two_streams():
+    dev = _dev()
+    sets = [_range_inputs(300, 200, 703, dev, kind, seed=i) for i, kind in enumerate(("large row", "small dy"))]
+
+    def step(t):
+        w = (t["wg"], t["wu"], t["wd"])
+        y, gate, up = nsa.gated_mlp(t["x"], *w)
+        return (y, gate, up) + nsa.gated_mlp_backward(t["dy"], t["x"], *w, gate, up)
+
+    want = [step(t) for t in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for k, t in enumerate(sets):
+            with torch.cuda.stream(streams[k]):
+                got.append((k, step(t)))
+    torch.cuda.synchronize()
+    for k, out in got:
+        assert all(torch.equal(p, q) for p, q in zip(out, want[k]))
