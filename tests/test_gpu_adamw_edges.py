@@ -110,13 +110,12 @@ def _formula(g, cm, cv, scales, betas):
     return codes, np.stack(tops)
 
 
-@pytest.mark.parametrize("size", [1.0, 2.0 ** -40, 2.0 ** -66, 2.0 ** -72, 2.0 ** 40])
-@pytest.mark.parametrize("gtype", list(DTYPES))
+# The other sizes are beyond fp16's numbers.
+@pytest.mark.parametrize("gtype,size", [(t, 1.0) for t in DTYPES] + [(t, 2.0 ** e) for t in ("bf16", "fp32")
+                                                                      for e in (-72, -66, -40, 40)])
 @pytest.mark.parametrize("n", [1, 255, 256, 1003, 50001])
 def test_codes_and_scales_are_the_formulas_to_the_bit(n, gtype, size):
     dev = _dev()
-    if gtype == "fp16" and size != 1.0:
-        pytest.skip("beyond fp16's numbers")
     s = _Set([(n,)], [torch.float32], [DTYPES[gtype]], (8,), dev, seed=n)
     s.scales[0].mul_(size)
     s.g[0].mul_(size)
